@@ -477,6 +477,35 @@ MOE_API int moe_forward_grouped_fp8b(const void* x, const float* logits, const f
                                      int f, int E, int top_k, int n_group, int topk_group, float scale, void* out,
                                      void* workspace, size_t workspace_bytes, moe_stream_t stream);
 
+/* ---------------------------------------------------------------------------------------------
+ * Training: the operators that one training step of an MoE block adds to the forward steps above.
+ * K, N, f and d here are multiples of 8 (not of 64); M and T are any number of rows, 0 included.
+ * ------------------------------------------------------------------------------------------- */
+
+/* Grouped products.  Row segment e is rows offsets[e] .. offsets[e+1]-1 (moe_permute's offsets; a
+ * segment may be empty).  bf16 operands, fp32 accumulation, one rounding when out is bf16.
+ *   moe_grouped_mm        out[r] = a[r] . b[e]      b [E,K,N]           (transpose_b = 0)
+ *                         out[r] = a[r] . b[e]^T    b [E,N,K]           (transpose_b = 1: the input
+ *                         gradient, with a the gradient of the product's output and b its weights)
+ *     a [M,K] bf16;  out [M,N] bf16, or fp32 with out_fp32 = 1; rows outside the segments untouched.
+ *   moe_grouped_mm_wgrad  out[e] = sum over the rows r of segment e of a[r]^T . g[r], the weight
+ *                         gradient; an empty segment's is zero.  accumulate = 1 (fp32 only) adds to
+ *                         out instead.
+ *     a [M,K], g [M,N] bf16;  out [E,K,N] bf16 or fp32.
+ * K and N multiples of 8 in [8, 65536], 1 <= E <= 256; a, b, g, out and workspace 16-byte aligned.
+ * workspace: moe_grouped_mm_workspace_size(mode, ...) bytes with mode 0 (transpose_b = 0), 1
+ * (transpose_b = 1) or 2 (wgrad); with it a reduction whose tiles cannot fill the GPU is split into
+ * slices that are added in a fixed order (one launch more, same result on every run).  0 bytes means
+ * the shape is never split; NULL never splits.  status: device int32 or NULL (MOE_STATUS_BAD_OFFSETS:
+ * nothing is written; MOE_STATUS_WAIT_TIMEOUT). */
+MOE_API size_t moe_grouped_mm_workspace_size(int mode, int M, int K, int N, int E);
+MOE_API int moe_grouped_mm(const void* a, const void* b, const int32_t* offsets, int M, int K, int N, int E,
+                           int transpose_b, void* out, int out_fp32, void* workspace, size_t workspace_bytes,
+                           int32_t* status, moe_stream_t stream);
+MOE_API int moe_grouped_mm_wgrad(const void* a, const void* g, const int32_t* offsets, int M, int K, int N, int E,
+                                 void* out, int out_fp32, int accumulate, void* workspace, size_t workspace_bytes,
+                                 int32_t* status, moe_stream_t stream);
+
 /* Reads (synchronously: cudaMemcpy) a device status word — a stage call's `status` pointer, or
  * the workspace of moe_forward — into *code (0 = no device-side error).  With
  * status_or_workspace = NULL it reads the status word of moe_forward_noalloc's fixed array on the

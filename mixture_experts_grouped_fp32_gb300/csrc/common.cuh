@@ -30,7 +30,7 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
 }
 
 // Kernels of the layer, as bits of the programmatic-launch mask.
-enum PdlKernel { kPdlRoute = 1, kPdlPermute = 2, kPdlGateUp = 4, kPdlDown = 8, kPdlCombine = 16, kPdlQuant = 32 };
+enum PdlKernel { kPdlRoute = 1, kPdlPermute = 2, kPdlGateUp = 4, kPdlDown = 8, kPdlCombine = 16, kPdlQuant = 32, kPdlTrain = 64 };
 
 // Whether a kernel is launched with the programmatic-stream-serialization attribute (see
 // pdl_wait).  The environment variable MOE_PDL, a bit mask of PdlKernel, overrides the default.
@@ -195,6 +195,32 @@ bool make_tensor_map_u8(CUtensorMap* m, const void* base, uint64_t cols, uint64_
 // Blocked FP8 weight codes (rows x K in 8 KB blocks of 64 rows x 128 K, see moe.h): a box of
 // box_rows (a multiple of 64) rows x 128 K codes.
 bool make_tensor_map_w8(CUtensorMap* m, const void* base, uint64_t K, uint64_t rows, uint32_t box_rows);
+
+// Grouped products of the training path (grouped_mm.cu).
+enum GroupedMmMode {
+    kMmForward = 0,  // out [M, N]: rows of segment e times B[e] [K, N]
+    kMmTransB = 1,   // out [M, N]: rows of segment e times B[e]^T, B [E, N, K]
+    kMmWgrad = 2     // out [E, K, N]: A[segment e]^T G[segment e]
+};
+struct GroupedMmArgs {
+    const void* A;  // [M, K] bf16
+    const void* B;  // weights (modes 0, 1) or G [M, N] bf16 (mode 2)
+    const int32_t* offsets;
+    int M, K, N, E;
+    void* out;       // bf16, or fp32 with out_f32
+    bool out_f32;
+    bool accumulate;  // mode 2, fp32: out += instead of out =
+    int ksplit;       // slices of the reduction; > 1 needs `partial`
+    float* partial;   // [ksplit, out elements] fp32
+    int32_t* status;
+};
+// Slices of the reduction that a call of this shape uses (1 = no split).
+int grouped_mm_ksplit(int mode, int M, int K, int N, int E, int num_sms);
+cudaError_t launch_grouped_mm(int mode, const GroupedMmArgs& a, int num_sms, cudaStream_t s, const char** why);
+// 3-D bf16 tensor map over [d2, rows, cols] (cols contiguous), box = [1, box_rows, 64 cols],
+// 128-byte swizzle.
+bool make_tensor_map_bf16_3d(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows, uint64_t d2,
+                             uint32_t box_rows);
 
 // FP8 quantisation (fp8.cu).  Rows: row r of the bf16 [*, C] matrix a (row src[r] when src is
 // given, src values checked against src_rows) -> E4M3 codes q [R, C] and scale [R].  Weights:

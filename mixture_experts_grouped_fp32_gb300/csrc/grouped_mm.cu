@@ -1,0 +1,603 @@
+// grouped_mm.cu — the grouped products of the training path on SM pairs (tcgen05 cta_group::2):
+//
+//   kMmForward  C[r] = A[r] . B[e]      for the rows r of segment e   (B [E, K, N])
+//   kMmTransB   C[r] = A[r] . B[e]^T                                  (B [E, N, K]: input gradient)
+//   kMmWgrad    D[e] (+)= sum_{r in segment e} A[r]^T . G[r]          (weight gradient, D [E, K, N])
+//
+// bf16 operands, fp32 accumulation in tensor memory, one rounding at the store (or none: fp32 out).
+//
+// One orientation for all three: the output's contiguous index n is the UMMA M dimension (256 per CTA
+// pair, 128 per CTA: "features") and the output's row index is the UMMA N dimension ("rows").
+//   * A ragged segment then costs N = its rows rounded up to 32, not a 256-row tile: a segment of c
+//     rows is cut into ceil(c / 256) tiles of equal size.
+//   * In tensor memory a lane is a feature and a column is an output row, so for each output row the
+//     32 lanes of a warp hold 32 consecutive outputs: the epilogue's plain stores are coalesced
+//     (64 bytes of bf16 or 128 of fp32 per warp) without a pass through shared memory, and rows past
+//     a segment's end are simply not stored.
+// For the weight gradient the features are G's columns, the rows are A's columns and the reduction
+// runs over the segment's rows.
+//
+// Shared-memory stage of each CTA (64 deep along the reduction, 128-byte swizzle as TMA writes it):
+//   F (16 KB)  128 features.  kMmTransB: K-major, one box of 128 rows x 64 K.  Otherwise MN-major: two
+//              boxes of 64 features x 64 deep, 8 KB apart.
+//   R (16 KB)  this CTA's half of the tile's rows, at most 128.  Weight gradient: MN-major, two boxes
+//              as for F.  Otherwise K-major: one 128-row box, or as many 32-row boxes as needed.
+// Six stages; two 256-column accumulators, so that one tile's epilogue overlaps the next tile's
+// products.
+//
+// The weight gradient's last block along a segment's rows holds rows of the next segment.  They are
+// zeroed in shared memory in both operands (zeroing one would let an infinity in the other through as
+// NaN): that block's copies complete on a barrier of the CTA's own, a warp zeroes the rows past the
+// end up to the next multiple of 16 (one UMMA step; later steps are not issued) and then arrives on
+// the stage's `full` barrier.  Every other block goes from the copy to the tensor cores directly.
+//
+// Work items (expert, group of up to 8 row tiles, feature tile, row tile, slice of the reduction) are
+// numbered in this order and dealt round-robin to a persistent grid of CTA pairs: the row tiles of a
+// group run together and share the feature operand through L2, and groups of 8 keep the rows
+// re-read per feature tile few when a segment is long.
+//
+// Synchronisation across the pair is that of the layer's SM-pair kernel: full[s] lives in CTA 0 and
+// counts both CTAs' copies, empty[s] and tfull[a] are arrived on in both CTAs by CTA 0's multicast
+// commits, tempty[a] lives in CTA 0.  Every wait is bounded and reports MOE_STATUS_WAIT_TIMEOUT.
+#include "common.cuh"
+#include "tcgen05.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int BK = 64;
+constexpr int UMMA_K = 16;
+constexpr int TILE_F = 256;                      // features per pair
+constexpr int TILE_R = 256;                      // output rows per tile, at most
+constexpr int BOX_BYTES = 64 * BK * 2;           // 8 KB
+constexpr int F_BYTES = 128 * BK * 2;            // 16 KB
+constexpr int R_BYTES = 128 * BK * 2;            // 16 KB
+constexpr int STAGE_BYTES = F_BYTES + R_BYTES;   // 32 KB per CTA
+constexpr int ROW_BOX = 32;
+constexpr int ROW_BOX_BYTES = ROW_BOX * BK * 2;  // 4 KB
+constexpr int STAGES = 6;
+constexpr int ACC_COLS = 256;
+constexpr int NUM_ACC = 2;
+constexpr int TMEM_COLS = NUM_ACC * ACC_COLS;
+constexpr int GROUP_R = 8;  // row tiles that run together
+constexpr int MAX_E = 256;
+constexpr int MAX_SPLIT = 16;
+constexpr uint16_t BOTH_CTAS = 0x3;
+// Warps: 0 copies, 1 tensor memory and MMAs, 2-5 epilogue, 6 zeroes segment ends (weight gradient).
+constexpr int kFixWarp = 6;
+constexpr int SMEM_BYTES = 232448;
+
+struct Ctl {
+    uint64_t full[STAGES];
+    uint64_t empty[STAGES];
+    uint64_t tail[STAGES];  // weight gradient: copies of a segment's last block, per CTA
+    uint64_t tfull[NUM_ACC];
+    uint64_t tempty[NUM_ACC];
+    uint64_t drain;
+    uint32_t tmem_base;
+    int abort_flag;
+    int total_items;
+    int seg[MAX_E + 1];
+    int item_start[MAX_E + 1];
+};
+static_assert(STAGES * STAGE_BYTES + 1024 + sizeof(Ctl) <= SMEM_BYTES, "shared memory budget");
+
+// Tiles along the output rows of expert e, and rows per tile (a multiple of 32).
+template <int MODE>
+__device__ __forceinline__ int row_tiles(int cnt, int K) {
+    return ((MODE == kMmWgrad ? K : cnt) + TILE_R - 1) / TILE_R;
+}
+
+struct Item {
+    int e, f0;          // expert, first feature of the pair's tile
+    int r0, rows;       // first output row (of the segment, or of the expert's [K, N]) and how many
+    int ntok;           // UMMA N: rows rounded up to 32
+    int red0, red1;     // reduction range in blocks of 64
+    int red_rows;       // weight gradient: rows of the segment
+    int slice;
+};
+
+template <int MODE>
+__device__ __forceinline__ Item decode_item(const Ctl& c, int K, int E, int f_tiles, int ksplit, int i) {
+    int lo = 0, hi = E;  // item_start[lo] <= i < item_start[lo + 1]
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (c.item_start[mid] <= i) lo = mid; else hi = mid;
+    }
+    Item it;
+    it.e = lo;
+    const int cnt = c.seg[lo + 1] - c.seg[lo];
+    const int total = MODE == kMmWgrad ? K : cnt;
+    const int rt = row_tiles<MODE>(cnt, K);
+    int j = i - c.item_start[lo];
+    it.slice = j % ksplit;
+    j /= ksplit;
+    const int per_group = GROUP_R * f_tiles;
+    const int g = j / per_group;
+    j -= g * per_group;
+    const int gr = min(GROUP_R, rt - g * GROUP_R);
+    const int ft = j / gr;
+    const int r = g * GROUP_R + (j - ft * gr);
+    it.f0 = ft * TILE_F;
+    const int per = (((total + rt - 1) / rt) + 31) & ~31;  // equal tiles; the last one may be shorter
+    it.r0 = r * per;
+    it.rows = min(per, total - it.r0);  // may be <= 0 after the rounding to 32
+    it.ntok = (max(it.rows, 1) + 31) & ~31;
+    it.red_rows = cnt;
+    const int nkb = ((MODE == kMmWgrad ? cnt : K) + BK - 1) / BK;
+    it.red0 = static_cast<int>(static_cast<long long>(nkb) * it.slice / ksplit);
+    it.red1 = it.rows > 0 ? static_cast<int>(static_cast<long long>(nkb) * (it.slice + 1) / ksplit) : it.red0;
+    return it;
+}
+
+__device__ __forceinline__ void raise_abort(Ctl& c, int32_t* status) {
+    *reinterpret_cast<volatile int*>(&c.abort_flag) = 1;
+    flag_status(status, MOE_STATUS_WAIT_TIMEOUT);
+}
+
+template <typename T>
+__device__ __forceinline__ T cvt_out(float v);
+template <>
+__device__ __forceinline__ float cvt_out<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ __nv_bfloat16 cvt_out<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+
+// tmF: the feature operand (weights [E, K, N] / [E, N, K], or G [M, N] as one matrix); tmR, tmR32: the
+// row operand A [M, K] (boxes of 128 and of 32 rows; weight gradient: boxes of 64 rows).
+template <int MODE, typename OUT>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MODE == kMmWgrad ? 224 : 192, 1)
+grouped_mm_kernel(const __grid_constant__ CUtensorMap tmF, const __grid_constant__ CUtensorMap tmR,
+                  const __grid_constant__ CUtensorMap tmR32, const int32_t* __restrict__ offsets, int M, int K, int N,
+                  int E, int ksplit, int accumulate, OUT* __restrict__ out, int32_t* __restrict__ status) {
+    constexpr bool WGRAD = MODE == kMmWgrad;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = ptx::smem_u32(smem_raw);
+    uint8_t* tiles = smem_raw + (((raw + 1023u) & ~1023u) - raw);
+    Ctl& c = *reinterpret_cast<Ctl*>(tiles + STAGES * STAGE_BYTES);
+    const volatile int* abort_flag = &c.abort_flag;
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int rank = static_cast<int>(ptx::cluster_ctarank());
+    const bool leader = rank == 0;
+    const int pair_id = blockIdx.x >> 1, num_pairs = gridDim.x >> 1;
+    const int f_tiles = (N + TILE_F - 1) / TILE_F;
+
+    if (tid == 0) {
+        for (int s = 0; s < STAGES; ++s) {
+            // Weight gradient: one arrival of each CTA (its producer's, or its zeroing warp's).
+            ptx::mbar_init(&c.full[s], WGRAD ? 2 : 1);
+            ptx::mbar_init(&c.empty[s], 1);
+            ptx::mbar_init(&c.tail[s], 1);
+        }
+        for (int a = 0; a < NUM_ACC; ++a) {
+            ptx::mbar_init(&c.tfull[a], 1);
+            ptx::mbar_init(&c.tempty[a], 8);
+        }
+        ptx::mbar_init(&c.drain, 1);
+        c.abort_flag = 0;
+        ptx::fence_mbar_init();
+        ptx::fence_proxy_async_smem();
+    }
+    if (warp == 0 && lane == 0) {
+        ptx::prefetch_tensormap(&tmF);
+        ptx::prefetch_tensormap(&tmR);
+        if (!WGRAD) ptx::prefetch_tensormap(&tmR32);
+    }
+    if (warp == 1) {
+        ptx::tmem_alloc_pair(&c.tmem_base, TMEM_COLS);
+        ptx::tmem_relinquish_pair();
+    }
+    pdl_wait();
+    pdl_trigger();
+    if (warp == 2) {
+        // Check the offsets and number the work items (8 experts per lane).
+        for (int e = lane; e <= E; e += 32) c.seg[e] = __ldg(offsets + e);
+        __syncwarp();
+        bool ok = true;
+        for (int e = lane; e < E; e += 32) ok = ok && c.seg[e] <= c.seg[e + 1];
+        if (lane == 0) ok = ok && c.seg[0] >= 0 && c.seg[E] <= M;
+        ok = __all_sync(0xffffffffu, ok);
+        const int per = (E + 31) / 32;
+        const int e0 = min(E, lane * per), e1 = min(E, e0 + per);
+        auto items = [&](int e) {
+            const int cnt = c.seg[e + 1] - c.seg[e];
+            // An empty segment's weight gradient is zero: written, or left as it is when added to.
+            if (WGRAD && cnt == 0 && accumulate) return 0;
+            return row_tiles<MODE>(cnt, K) * f_tiles * ksplit;
+        };
+        int sum = 0;
+        if (ok)
+            for (int e = e0; e < e1; ++e) sum += items(e);
+        int incl = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += v;
+        }
+        int run = incl - sum;
+        for (int e = e0; e < e1; ++e) {
+            c.item_start[e] = run;
+            if (ok) run += items(e);
+        }
+        if (lane == 31) {
+            c.item_start[E] = incl;
+            c.total_items = incl;
+        }
+        if (!ok && lane == 0 && leader) flag_status(status, MOE_STATUS_BAD_OFFSETS);
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::cluster_sync();  // both CTAs' barriers exist before any cross-CTA arrive or copy
+    ptx::tc_fence_after();
+
+    const uint32_t tmem_base = c.tmem_base;
+    const int total = c.total_items;
+    uint32_t fill_parity[STAGES];
+    int filled_mask = 0;
+
+    if (warp == 0 && lane == 0) {
+        // ------------------------------ copies (both CTAs) ------------------------------
+        const uint64_t pol_r = WGRAD ? ptx::policy_evict_normal() : ptx::policy_evict_last();
+        const uint64_t pol_f = ptx::policy_evict_normal();
+        int stage = 0;
+        uint32_t phase = 0;
+        bool aborted = false;
+        for (int i = pair_id; i < total && !aborted; i += num_pairs) {
+            const Item it = decode_item<MODE>(c, K, E, f_tiles, ksplit, i);
+            const int half = it.ntok >> 1;
+            const int f = it.f0 + 128 * rank;           // this CTA's features
+            const int seg0 = c.seg[it.e];
+            const int rb = (half + ROW_BOX - 1) / ROW_BOX;
+            const uint32_t row_bytes = half == 128 ? R_BYTES : rb * ROW_BOX_BYTES;
+            const uint32_t cta_bytes = F_BYTES + (WGRAD ? R_BYTES : row_bytes);
+            for (int kb = it.red0; kb < it.red1; ++kb) {
+                if (!ptx::mbar_wait(&c.empty[stage], phase ^ 1u, abort_flag)) {
+                    raise_abort(c, status);
+                    aborted = true;
+                    break;
+                }
+                uint8_t* sf = tiles + stage * STAGE_BYTES;
+                uint8_t* sr = sf + F_BYTES;
+                const uint32_t full_leader = ptx::map_to_cta(ptx::smem_u32(&c.full[stage]), 0);
+                if (WGRAD) {
+                    const int row = seg0 + kb * BK;
+                    const int r = it.r0 + rank * half;  // this CTA's output rows = columns of A
+                    if ((kb + 1) * BK > it.red_rows && (it.red_rows & 15)) {
+                        // The segment's last block, with rows to be zeroed: its copies complete here.
+                        ptx::mbar_arrive_expect_tx(&c.tail[stage], cta_bytes);
+                        ptx::tma_load_2d(sf, &tmF, &c.tail[stage], f, row, pol_f);
+                        ptx::tma_load_2d(sf + BOX_BYTES, &tmF, &c.tail[stage], f + 64, row, pol_f);
+                        ptx::tma_load_2d(sr, &tmR, &c.tail[stage], r, row, pol_r);
+                        ptx::tma_load_2d(sr + BOX_BYTES, &tmR, &c.tail[stage], r + 64, row, pol_r);
+                    } else {
+                        if (leader) ptx::mbar_arrive_expect_tx(&c.full[stage], 2u * cta_bytes);
+                        else ptx::mbar_arrive_cluster(full_leader);
+                        ptx::tma_load_2d_pair(sf, &tmF, full_leader, f, row, pol_f);
+                        ptx::tma_load_2d_pair(sf + BOX_BYTES, &tmF, full_leader, f + 64, row, pol_f);
+                        ptx::tma_load_2d_pair(sr, &tmR, full_leader, r, row, pol_r);
+                        ptx::tma_load_2d_pair(sr + BOX_BYTES, &tmR, full_leader, r + 64, row, pol_r);
+                    }
+                } else {
+                    if (leader) ptx::mbar_arrive_expect_tx(&c.full[stage], 2u * cta_bytes);
+                    const int row = seg0 + it.r0 + rank * half;
+                    if (half == 128) {
+                        ptx::tma_load_2d_pair(sr, &tmR, full_leader, kb * BK, row, pol_r);
+                    } else {
+                        for (int q = 0; q < rb; ++q)
+                            ptx::tma_load_2d_pair(sr + q * ROW_BOX_BYTES, &tmR32, full_leader, kb * BK,
+                                                  row + q * ROW_BOX, pol_r);
+                    }
+                    if (MODE == kMmTransB) {
+                        ptx::tma_load_3d_pair(sf, &tmF, full_leader, kb * BK, f, it.e, pol_f);
+                    } else {
+                        ptx::tma_load_3d_pair(sf, &tmF, full_leader, f, kb * BK, it.e, pol_f);
+                        ptx::tma_load_3d_pair(sf + BOX_BYTES, &tmF, full_leader, f + 64, kb * BK, it.e, pol_f);
+                    }
+                }
+                fill_parity[stage] = phase;
+                filled_mask |= 1 << stage;
+                if (++stage == STAGES) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            }
+        }
+    } else if (warp == 1 && lane == 0 && leader) {
+        // ------------------------------ pair MMAs (CTA 0) ------------------------------
+        int stage = 0;
+        uint32_t phase = 0, acc = 0, acc_phase = 0;
+        bool aborted = false;
+        for (int i = pair_id; i < total && !aborted; i += num_pairs) {
+            const Item it = decode_item<MODE>(c, K, E, f_tiles, ksplit, i);
+            if (it.red0 >= it.red1) continue;  // nothing to reduce: the epilogue stores zeros
+            const uint32_t idesc = ptx::idesc_bf16_f32(TILE_F, static_cast<uint32_t>(it.ntok),
+                                                       /*a_mn=*/MODE == kMmTransB ? 0 : 1, /*b_mn=*/WGRAD ? 1 : 0);
+            if (!ptx::mbar_wait(&c.tempty[acc], acc_phase ^ 1u, abort_flag)) {
+                raise_abort(c, status);
+                break;
+            }
+            ptx::tc_fence_after();
+            const uint32_t d_tmem = tmem_base + acc * ACC_COLS;
+            for (int kb = it.red0; kb < it.red1; ++kb) {
+                if (!ptx::mbar_wait(&c.full[stage], phase, abort_flag)) {
+                    raise_abort(c, status);
+                    aborted = true;
+                    break;
+                }
+                ptx::tc_fence_after();
+                const uint32_t sf = ptx::smem_u32(tiles + stage * STAGE_BYTES);
+                // MN-major: 64-wide boxes 8 KB apart, 16 deep = 2 KB.  K-major: 16 deep = 32 bytes.
+                const uint64_t f_desc = ptx::smem_desc_sw128(sf, MODE == kMmTransB ? 16 : BOX_BYTES, 1024);
+                const uint64_t r_desc = ptx::smem_desc_sw128(sf + F_BYTES, WGRAD ? BOX_BYTES : 16, 1024);
+                constexpr uint64_t f_step = (MODE == kMmTransB ? 32 : 2048) >> 4;
+                constexpr uint64_t r_step = (WGRAD ? 2048 : 32) >> 4;
+                const int steps = WGRAD ? min(BK / UMMA_K, (it.red_rows - kb * BK + UMMA_K - 1) / UMMA_K) : BK / UMMA_K;
+#pragma unroll
+                for (int kk = 0; kk < BK / UMMA_K; ++kk)
+                    if (kk < steps)
+                        ptx::mma_bf16_ss_pair(d_tmem, f_desc + kk * f_step, r_desc + kk * r_step, idesc,
+                                              (kb != it.red0 || kk != 0) ? 1u : 0u);
+                ptx::mma_commit_pair(&c.empty[stage], BOTH_CTAS);
+                if (++stage == STAGES) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            }
+            if (aborted) break;
+            ptx::mma_commit_pair(&c.tfull[acc], BOTH_CTAS);
+            if (++acc == NUM_ACC) {
+                acc = 0;
+                acc_phase ^= 1u;
+            }
+        }
+    } else if (WGRAD && warp == kFixWarp) {
+        // ------------------- zero the rows past a segment's end (both CTAs) -------------------
+        int stage = 0;
+        uint32_t parity = 0;  // bit s: parity of tail[s]'s next phase
+        bool aborted = false;
+        for (int i = pair_id; i < total && !aborted; i += num_pairs) {
+            const Item it = decode_item<MODE>(c, K, E, f_tiles, ksplit, i);
+            const int n = it.red1 - it.red0;
+            if (n > 0 && it.red1 * BK > it.red_rows && (it.red_rows & 15)) {
+                const int st = (stage + n - 1) % STAGES;
+                const bool ok =
+                    __all_sync(0xffffffffu, ptx::mbar_wait(&c.tail[st], (parity >> st) & 1u, abort_flag));
+                if (!ok) {
+                    if (lane == 0) raise_abort(c, status);
+                    aborted = true;
+                    break;
+                }
+                parity ^= 1u << st;
+                const int z0 = it.red_rows - (it.red1 - 1) * BK;  // first row to zero, in [1, 63]
+                const int z1 = (z0 + UMMA_K - 1) & ~(UMMA_K - 1);
+                uint8_t* s0 = tiles + st * STAGE_BYTES;
+                for (int b = 0; b < STAGE_BYTES / BOX_BYTES; ++b)
+                    for (int o = z0 * 128 + lane * 16; o < z1 * 128; o += 512)
+                        *reinterpret_cast<uint4*>(s0 + b * BOX_BYTES + o) = make_uint4(0, 0, 0, 0);
+                ptx::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive_cluster(ptx::map_to_cta(ptx::smem_u32(&c.full[st]), 0));
+            }
+            stage = (stage + n) % STAGES;
+        }
+    } else if (warp >= 2 && warp < 6) {
+        // ------------------------------ epilogue (both CTAs) ------------------------------
+        const int quarter = warp & 3;  // this warp's tensor-memory lanes: 32 quarter .. + 31
+        uint32_t acc = 0, acc_phase = 0;
+        const size_t slice_elems = WGRAD ? static_cast<size_t>(E) * K * N : static_cast<size_t>(M) * N;
+        for (int i = pair_id; i < total; i += num_pairs) {
+            const Item it = decode_item<MODE>(c, K, E, f_tiles, ksplit, i);
+            const bool any = it.red0 < it.red1;
+            if (any) {
+                if (!ptx::mbar_wait(&c.tfull[acc], acc_phase, abort_flag)) {
+                    raise_abort(c, status);
+                    break;
+                }
+                ptx::tc_fence_after();
+            }
+            const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + acc * ACC_COLS;
+            const int n = it.f0 + 128 * rank + 32 * quarter + lane;
+            const size_t row0 = WGRAD ? static_cast<size_t>(it.e) * K + it.r0 : static_cast<size_t>(c.seg[it.e]) + it.r0;
+            OUT* dst = out + it.slice * slice_elems + row0 * N + n;
+#pragma unroll 1
+            for (int j0 = 0; j0 < it.rows; j0 += 32, dst += static_cast<size_t>(32) * N) {
+                uint32_t v[32];
+                if (any) {
+                    ptx::tmem_ld_32x32b_x32(taddr + j0, v);
+                    ptx::tmem_ld_wait();
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) v[j] = 0u;
+                }
+                const int nr = it.rows - j0;
+                if (n < N) {
+                    if constexpr (WGRAD && sizeof(OUT) == 4) {
+                        if (accumulate) {
+                            float old[32];
+#pragma unroll
+                            for (int j = 0; j < 32; ++j)
+                                old[j] = j < nr ? static_cast<float>(dst[static_cast<size_t>(j) * N]) : 0.0f;
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) + old[j]);
+                        }
+                    }
+                    if (nr >= 32) {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            dst[static_cast<size_t>(j) * N] = cvt_out<OUT>(__uint_as_float(v[j]));
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            if (j < nr) dst[static_cast<size_t>(j) * N] = cvt_out<OUT>(__uint_as_float(v[j]));
+                    }
+                }
+            }
+            if (any) {
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive_cluster(ptx::map_to_cta(ptx::smem_u32(&c.tempty[acc]), 0));
+                if (++acc == NUM_ACC) {
+                    acc = 0;
+                    acc_phase ^= 1u;
+                }
+            }
+        }
+    }
+
+    // ------------------------------ teardown ------------------------------
+    ptx::tc_fence_before();
+    __syncthreads();
+    if (warp == 0 && lane == 0 && c.abort_flag) {
+        if (leader) {
+            for (int s = 0; s < STAGES; ++s)
+                if (filled_mask & (1 << s)) ptx::mbar_wait_ns(&c.full[s], fill_parity[s], 100000000ull);
+        }
+        const uint64_t t0 = ptx::globaltimer_ns();  // give this CTA's own copies time to land
+        while (ptx::globaltimer_ns() - t0 < 1000000ull) {
+        }
+    }
+    if (warp == 1 && lane == 0 && leader) {
+        ptx::mma_commit_pair(&c.drain, 0x1);  // all pair MMAs issued by this thread have completed
+        ptx::mbar_wait_ns(&c.drain, 0, 100000000ull);
+    }
+    __syncthreads();
+    ptx::cluster_sync();  // neither CTA frees tensor memory or exits while the pair MMAs may run
+    ptx::tc_fence_after();
+    if (warp == 1) ptx::tmem_dealloc_pair(tmem_base, TMEM_COLS);
+    ptx::cluster_sync();
+}
+
+// Joins the slices of a split reduction: out = sum over s of partial[s], in slice order.  Rows outside
+// [offsets[0], offsets[E]) are not touched (modes with row output); a bad segmentation touches nothing.
+template <typename OUT>
+__global__ void __launch_bounds__(256)
+grouped_mm_join_kernel(const float4* __restrict__ partial, const int32_t* __restrict__ offsets, int M, int N, int E,
+                       size_t n4, int ksplit, int by_row, int accumulate, OUT* __restrict__ out) {
+    pdl_wait();
+    pdl_trigger();
+    size_t lo = 0, hi = n4;
+    if (by_row) {
+        const int r0 = __ldg(offsets), r1 = __ldg(offsets + E);
+        if (r0 < 0 || r1 > M || r0 > r1) return;
+        lo = static_cast<size_t>(r0) * N / 4;
+        hi = static_cast<size_t>(r1) * N / 4;
+    }
+    for (size_t i = lo + static_cast<size_t>(blockIdx.x) * 256 + threadIdx.x; i < hi;
+         i += static_cast<size_t>(gridDim.x) * 256) {
+        float4 a = __ldcg(partial + i);
+        for (int s = 1; s < ksplit; ++s) {
+            const float4 b = __ldcg(partial + s * n4 + i);
+            a.x += b.x; a.y += b.y; a.z += b.z; a.w += b.w;
+        }
+        if constexpr (sizeof(OUT) == 4) {
+            float4* o = reinterpret_cast<float4*>(out) + i;
+            if (accumulate) {
+                const float4 b = *o;
+                a.x += b.x; a.y += b.y; a.z += b.z; a.w += b.w;
+            }
+            *o = a;
+        } else {
+            reinterpret_cast<uint2*>(out)[i] = make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w));
+        }
+    }
+}
+
+template <int MODE, typename OUT>
+cudaError_t launch_mode(const GroupedMmArgs& a, OUT* out, int ksplit, int accumulate, int num_sms, cudaStream_t s,
+                        const char** why) {
+    static bool attr_set[64] = {};
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (dev < 64 && !attr_set[dev]) {
+        cudaError_t e = cudaFuncSetAttribute(grouped_mm_kernel<MODE, OUT>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
+        if (e != cudaSuccess) {
+            *why = "cudaFuncSetAttribute(max dynamic shared memory) failed";
+            return e;
+        }
+        attr_set[dev] = true;
+    }
+    CUtensorMap mF, mR, mR32;
+    bool ok;
+    if (MODE == kMmWgrad)
+        ok = make_tensor_map_bf16(&mF, a.B, a.N, a.M, BK) && make_tensor_map_bf16(&mR, a.A, a.K, a.M, BK);
+    else
+        ok = make_tensor_map_bf16(&mR, a.A, a.K, a.M, 128) && make_tensor_map_bf16(&mR32, a.A, a.K, a.M, ROW_BOX) &&
+             (MODE == kMmTransB ? make_tensor_map_bf16_3d(&mF, a.B, a.K, a.N, a.E, 128)
+                                : make_tensor_map_bf16_3d(&mF, a.B, a.N, a.K, a.E, BK));
+    if (MODE == kMmWgrad) mR32 = mR;
+    if (!ok) {
+        *why = "cuTensorMapEncodeTiled failed (driver entry point missing or bad operand)";
+        return cudaErrorInvalidValue;
+    }
+    return launch_k(kPdlTrain, grouped_mm_kernel<MODE, OUT>, dim3(num_sms & ~1), dim3(MODE == kMmWgrad ? 224 : 192),
+                    SMEM_BYTES, s, mF, mR, mR32, a.offsets, a.M, a.K, a.N, a.E, ksplit, accumulate, out, a.status);
+}
+
+template <int MODE>
+cudaError_t launch_any(const GroupedMmArgs& a, int num_sms, cudaStream_t s, const char** why) {
+    if (a.ksplit > 1) {
+        cudaError_t e = launch_mode<MODE, float>(a, a.partial, a.ksplit, 0, num_sms, s, why);
+        if (e != cudaSuccess) return e;
+        const size_t n4 = (MODE == kMmWgrad ? static_cast<size_t>(a.E) * a.K : static_cast<size_t>(a.M)) * a.N / 4;
+        const size_t want = (n4 + 255) / 256, most = static_cast<size_t>(num_sms) * 8;
+        const dim3 grid(static_cast<unsigned>(want < most ? want : most));
+        const int by_row = MODE != kMmWgrad, acc = a.accumulate ? 1 : 0;
+        *why = "slice join";
+        const float4* p = reinterpret_cast<const float4*>(a.partial);
+        if (a.out_f32)
+            return launch_k(kPdlTrain, grouped_mm_join_kernel<float>, grid, dim3(256), 0, s, p, a.offsets, a.M, a.N,
+                            a.E, n4, a.ksplit, by_row, acc, static_cast<float*>(a.out));
+        return launch_k(kPdlTrain, grouped_mm_join_kernel<__nv_bfloat16>, grid, dim3(256), 0, s, p, a.offsets, a.M,
+                        a.N, a.E, n4, a.ksplit, by_row, acc, static_cast<__nv_bfloat16*>(a.out));
+    }
+    const int acc = a.accumulate ? 1 : 0;
+    return a.out_f32 ? launch_mode<MODE, float>(a, static_cast<float*>(a.out), 1, acc, num_sms, s, why)
+                     : launch_mode<MODE, __nv_bfloat16>(a, static_cast<__nv_bfloat16*>(a.out), 1, acc, num_sms, s, why);
+}
+
+}  // namespace
+
+// The reduction is split when its tiles would leave most CTA pairs idle (serving a few tokens, or the
+// weight gradient of few experts over many rows).  Tiles are bounded above from the shape alone (the
+// row counts are on the device).  Among the slice counts that leave each slice at least 16 blocks of 64
+// and add at most a quarter to the bytes moved, the one with the fullest last round is taken.
+int grouped_mm_ksplit(int mode, int M, int K, int N, int E, int num_sms) {
+    const long long pairs = num_sms / 2;
+    const long long f_tiles = (N + TILE_F - 1) / TILE_F;
+    const long long active = M < E ? M : E;
+    long long tiles, blocks, out_elems, bytes;
+    if (mode == kMmWgrad) {
+        tiles = E * f_tiles * ((K + TILE_R - 1) / TILE_R);
+        blocks = M / E / BK;
+        out_elems = static_cast<long long>(E) * K * N;
+        bytes = 2ll * M * (K + N) + 4 * out_elems;
+    } else {
+        const long long long_tiles = M / TILE_R;
+        tiles = f_tiles * (active > long_tiles ? active : long_tiles);
+        blocks = K / BK;
+        out_elems = static_cast<long long>(M) * N;
+        bytes = 2ll * M * K + 2ll * active * K * N;
+    }
+    if (tiles * 4 > pairs * 3 || tiles == 0) return 1;
+    int best = 1;
+    double best_eff = 0.0;
+    for (int s = 1; s <= MAX_SPLIT; ++s) {
+        if (s > 1 && (blocks / s < 16 || 8ll * s * out_elems * 4 > bytes)) break;
+        const long long rounds = (tiles * s + pairs - 1) / pairs;
+        const double eff = static_cast<double>(tiles * s) / static_cast<double>(rounds * pairs);
+        if (eff > best_eff * 1.02) {
+            best_eff = eff;
+            best = s;
+        }
+    }
+    return best;
+}
+
+cudaError_t launch_grouped_mm(int mode, const GroupedMmArgs& a, int num_sms, cudaStream_t s, const char** why) {
+    if (mode == kMmForward) return launch_any<kMmForward>(a, num_sms, s, why);
+    if (mode == kMmTransB) return launch_any<kMmTransB>(a, num_sms, s, why);
+    return launch_any<kMmWgrad>(a, num_sms, s, why);
+}
+
+}  // namespace moe

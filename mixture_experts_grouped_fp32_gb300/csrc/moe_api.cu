@@ -5,12 +5,12 @@
 #include <cstdio>
 #include <mutex>
 
+#include "api.cuh"
 #include "common.cuh"
 
 namespace moe {
-namespace {
 
-thread_local char g_err[512] = "";
+static thread_local char g_err[512] = "";
 
 int fail(int code, const char* fmt, ...) {
     va_list ap;
@@ -24,6 +24,8 @@ int ok() {
     g_err[0] = '\0';
     return MOE_OK;
 }
+
+namespace {
 
 constexpr int kMaxE = 256, kMaxK = 8, kMaxDim = 65536;
 
@@ -49,6 +51,8 @@ struct DevInfo {
 };
 std::mutex g_dev_mu;
 DevInfo g_dev[64];
+
+}  // namespace
 
 // Current device must be compute capability 10.3; fills the SM count.
 int check_device(int* num_sms) {
@@ -77,15 +81,13 @@ int launched(cudaError_t e, const char* what) {
     return ok();
 }
 
-}  // namespace
-
 // Default: every launch but the permute's.  Measured on GB300 (ms per layer, all five = 0.4197 at
 // Mixtral T=32 against 0.4277 with none; but a programmatic permute launch costs the DeepSeek-
 // shaped layer 0.09 ms: 2.545 with only that bit against 2.454 with none).
 bool pdl_enabled(int kernel_bit) {
     static const int mask = [] {
         const char* v = std::getenv("MOE_PDL");
-        return v ? std::atoi(v) : (kPdlRoute | kPdlGateUp | kPdlDown | kPdlCombine | kPdlQuant);
+        return v ? std::atoi(v) : (kPdlRoute | kPdlGateUp | kPdlDown | kPdlCombine | kPdlQuant | kPdlTrain);
     }();
     return (mask & kernel_bit) != 0;
 }

@@ -77,6 +77,9 @@ _SIGS = {
                                  _SZ, _P], _I),
     "moe_forward_grouped_fp8b": ([_P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, ctypes.c_float, _P, _P,
                                   _SZ, _P], _I),
+    "moe_grouped_mm_workspace_size": ([_I, _I, _I, _I, _I], _SZ),
+    "moe_grouped_mm": ([_P, _P, _P, _I, _I, _I, _I, _I, _P, _I, _P, _SZ, _P, _P], _I),
+    "moe_grouped_mm_wgrad": ([_P, _P, _P, _I, _I, _I, _I, _P, _I, _I, _P, _SZ, _P, _P], _I),
 }
 
 WS_FIELDS = ("status", "idx", "w", "counts", "offsets", "src", "dest", "x_perm", "h", "y_perm", "total")
@@ -827,4 +830,89 @@ def forward_grouped_fp8(x, logits, bias, w8_gate_up, s_gate_up, w8_down, s_down,
     _call("moe_forward_grouped_fp8b" if blocks else "moe_forward_grouped_fp8", _ptr(x), _ptr(logits), _ptr(bias),
           _ptr(w8_gate_up), _ptr(s_gate_up), _ptr(w8_down), _ptr(s_down), T, d, f2 // 2, E, top_k, n_group,
           topk_group, float(scale), _ptr(out), _ptr(workspace), workspace.numel(), _stream(stream))
+    return out
+
+
+# ---------------------------------------------------------------------------------------------
+# Training: grouped products and their gradients.
+# ---------------------------------------------------------------------------------------------
+def _empty(shape, dtype, device, stream):
+    """torch.empty on the stream that the call runs on, so that the allocator orders its reuse there."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _shaped(t: torch.Tensor, shape: tuple, name: str) -> None:
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+
+
+def _out(out, shape, dtype, device, stream, name="out"):
+    if out is None:
+        return _empty(shape, dtype, device, stream)
+    _dev(out, dtype, name)
+    _shaped(out, tuple(shape), name)
+    return out
+
+
+def grouped_mm_workspace_size(mode: int, M: int, K: int, N: int, E: int) -> int:
+    """Bytes of workspace of a grouped product (mode 0: plain, 1: transpose_b, 2: weight gradient)."""
+    return int(load().moe_grouped_mm_workspace_size(mode, M, K, N, E))
+
+
+def _mm_args(mode, M, K, N, E, out, out_dtype, shape, workspace, device, stream):
+    if out is not None:
+        out_dtype = out.dtype
+    if out_dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"out must be bfloat16 or float32, got {out_dtype}")
+    out = _out(out, shape, out_dtype, device, stream)
+    if workspace is None:
+        need = grouped_mm_workspace_size(mode, M, K, N, E)
+        if need:
+            workspace = _empty(need, torch.uint8, device, stream)
+    return out, int(out_dtype == torch.float32), workspace, 0 if workspace is None else workspace.nbytes
+
+
+def grouped_mm(a, b, offsets, transpose_b: bool = False, out=None, out_dtype=torch.bfloat16, workspace=None,
+               status=None, stream=None):
+    """Products grouped by expert: out[r] = a[r] @ b[e] for the rows r of segment e of ``offsets`` [E+1]
+    int32, with b [E, K, N]; or a[r] @ b[e].T with ``transpose_b`` and b [E, N, K].  a [M, K] and b are
+    bf16; out [M, N] is bf16 or fp32.  Rows outside the segments are left as they are."""
+    _dev(a, torch.bfloat16, "a")
+    _dev(b, torch.bfloat16, "b")
+    _dev(offsets, torch.int32, "offsets")
+    if a.dim() != 2 or b.dim() != 3:
+        raise ValueError("a must be [M, K] and b [E, K, N] (or [E, N, K] with transpose_b)")
+    M, K = a.shape
+    E, N = b.shape[0], b.shape[1 if transpose_b else 2]
+    _shaped(b, (E, N, K) if transpose_b else (E, K, N), "b")
+    _shaped(offsets, (E + 1,), "offsets")
+    out, f32, workspace, nbytes = _mm_args(1 if transpose_b else 0, M, K, N, E, out, out_dtype, (M, N), workspace,
+                                           a.device, stream)
+    _call("moe_grouped_mm", _ptr(a), _ptr(b), _ptr(offsets), M, K, N, E, int(transpose_b), _ptr(out), f32,
+          _ptr(workspace), nbytes, _ptr(status), _stream(stream))
+    return out
+
+
+def grouped_mm_wgrad(a, g, offsets, out=None, out_dtype=torch.float32, accumulate: bool = False, workspace=None,
+                     status=None, stream=None):
+    """Weight gradient of a grouped product: out[e] = a[rows of e].T @ g[rows of e], [E, K, N] fp32 or
+    bf16, zero for an empty segment; with ``accumulate`` (fp32 ``out`` given) it is added to out."""
+    _dev(a, torch.bfloat16, "a")
+    _dev(g, torch.bfloat16, "g")
+    _dev(offsets, torch.int32, "offsets")
+    if a.dim() != 2 or g.dim() != 2 or offsets.dim() != 1:
+        raise ValueError("a must be [M, K], g [M, N] and offsets [E + 1]")
+    M, K = a.shape
+    N, E = g.shape[1], offsets.shape[0] - 1
+    _shaped(g, (M, N), "g")
+    if accumulate and out is None:
+        raise ValueError("accumulate adds to out: give out")
+    out, f32, workspace, nbytes = _mm_args(2, M, K, N, E, out, out_dtype, (E, K, N), workspace, a.device, stream)
+    _call("moe_grouped_mm_wgrad", _ptr(a), _ptr(g), _ptr(offsets), M, K, N, E, _ptr(out), f32, int(accumulate),
+          _ptr(workspace), nbytes, _ptr(status), _stream(stream))
     return out

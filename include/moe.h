@@ -506,6 +506,76 @@ MOE_API int moe_grouped_mm_wgrad(const void* a, const void* g, const int32_t* of
                                  void* out, int out_fp32, int accumulate, void* workspace, size_t workspace_bytes,
                                  int32_t* status, moe_stream_t stream);
 
+/* SwiGLU with a weight per row.  gu [M,2f] bf16: gate columns g first, then u (moe_grouped_mm of the
+ * permuted rows and w_gate_up); s = 1 / (1 + exp(-g)).
+ *   moe_swiglu           h = w g s u                  w [M] fp32, or NULL for 1;  h [M,f] bf16 out
+ *   moe_swiglu_backward  dgu = [w dh u s (1 + g (1 - s)) | w dh g s]   dh [M,f] bf16 in, dgu [M,2f] out
+ *                        dw[r] = sum over the row of dh g s u          fp32 [M] out, or NULL
+ *                        h as moe_swiglu's                             bf16 [M,f] out, or NULL
+ * With w the routing weight of each permuted row, the layer's combine is a plain sum (moe_combine with
+ * weights 1) and dw is the routing weights' gradient.  f a multiple of 8 in [8, 65536]; gu, dh, dgu and
+ * h 16-byte aligned.  The outputs must not overlap the inputs. */
+MOE_API int moe_swiglu(const void* gu, const float* w, int M, int f, void* h, moe_stream_t stream);
+MOE_API int moe_swiglu_backward(const void* gu, const void* dh, const float* w, int M, int f, void* dgu, float* dw,
+                                void* h, moe_stream_t stream);
+
+/* Norms after and before a block, with the block's gate and the residual scale:
+ *   y = res * x + (gate * tgate[t]) * (w_post * h / rms(h));   n = w_pre * y / rms(y)
+ *   rms(a) = sqrt(mean over the row of a^2 + eps)
+ * x, y [T,d]: the residual stream, bf16, or fp32 with x_fp32 = 1;  h [T,d] bf16: the block's output;
+ * n [T,d] bf16: the next block's input, from y before its rounding;  w_pre, w_post, gate, res [d] and
+ * tgate [T] fp32.
+ *   h NULL (before the first block): y = x is not written, and w_post, gate, tgate, res must be NULL.
+ *   w_pre and n NULL (after the last block): no n.   y NULL: not written.
+ *   gate, tgate, res NULL: 1.
+ * d a multiple of 8 in [8, 65536]; every pointer 16-byte aligned (tgate, dtgate 4-byte); eps >= 0.
+ * The outputs must not overlap the inputs, except that y may be x (in place). */
+MOE_API int moe_block_norm(const void* x, int x_fp32, const void* h, const float* w_pre, const float* w_post,
+                           const float* gate, const float* tgate, const float* res, int T, int d, float eps, void* y,
+                           void* n, moe_stream_t stream);
+
+/* Its gradient, from dy [T,d] (type of x; NULL = 0) and dn [T,d] bf16 (NULL = 0):
+ *   dx [T,d] (type of x), dh [T,d] bf16 (with h);  dw_pre (with dn), dw_post, dgate, dres (with h) [d] and
+ *   dtgate [T] (with tgate), fp32: sums over rows resp. columns, in a fixed order.  A NULL gradient of a
+ *   vector is not written; all are written, not added to.
+ * y is recomputed from x and h, so it need not be kept.  workspace: 16-byte aligned,
+ * moe_block_norm_backward_workspace_size(T, d) bytes. */
+MOE_API size_t moe_block_norm_backward_workspace_size(int T, int d);
+MOE_API int moe_block_norm_backward(const void* x, int x_fp32, const void* h, const void* dy, const void* dn,
+                                    const float* w_pre, const float* w_post, const float* gate, const float* tgate,
+                                    const float* res, int T, int d, float eps, void* dx, void* dh, float* dw_pre,
+                                    float* dw_post, float* dgate, float* dtgate, float* dres, void* workspace,
+                                    size_t workspace_bytes, moe_stream_t stream);
+
+/* One tensor of an AdamW step: device pointers, n elements (0: skipped). */
+typedef struct {
+    void* param;      /* fp32 or bf16, updated in place */
+    const void* grad; /* fp32 or bf16 */
+    void* m;          /* first moment: fp32, or E4M3 codes with 8-bit states */
+    void* v;          /* second moment: fp32; with 8-bit states E4M3 codes of its root */
+    float* m_scale;   /* 8-bit states: [ceil(n / 256)] scales, one per 256 elements; else NULL */
+    float* v_scale;
+    void* copy;       /* bf16 copy of the new parameter, or NULL */
+    long long n;
+} moe_adamw_tensor;
+
+/* One AdamW step over `count` tensors (a host array, read during the call).  With g' = c g:
+ *   m = beta1 m + (1 - beta1) g';   v = beta2 v + (1 - beta2) g'^2;
+ *   p = p (1 - lr weight_decay) - lr / (1 - beta1^t) * m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
+ * in fp32, each operation rounded by itself.  state_bits 32: m and v fp32.  state_bits 8: blocks of 256
+ * elements; m = code * m_scale, m_scale = max|m| / 448; sqrt(v) = code * v_scale likewise, where a root
+ * that is not zero has at least the code of 2^-9; a block whose maximum is below 2^-100 has codes 0 and
+ * scale 1 (so zeroed codes and any finite scales are a fresh state); a block with a NaN or an infinity
+ * becomes NaN.  The step uses the new moments before their rounding.
+ *   t = step (>= 1), or the int32 at the device pointer step_dev if that is not NULL;  c = 1 and lr as
+ *   given, or with factors (device fp32 [2], or NULL) c = factors[0] (for gradient clipping or loss
+ *   scales) and lr * factors[1] (for a schedule): a captured graph then replays later steps.
+ * Any element alignment works; tensors whose pieces are 16-byte aligned (8-bit codes: 8-byte) run
+ * faster.  One launch for up to 400 tensors.  param_bf16 / grad_bf16: types of all tensors. */
+MOE_API int moe_adamw_step(const moe_adamw_tensor* tensors, int count, int param_bf16, int grad_bf16, int state_bits,
+                           double lr, double beta1, double beta2, double eps, double weight_decay, int step,
+                           const int32_t* step_dev, const float* factors, moe_stream_t stream);
+
 /* Reads (synchronously: cudaMemcpy) a device status word — a stage call's `status` pointer, or
  * the workspace of moe_forward — into *code (0 = no device-side error).  With
  * status_or_workspace = NULL it reads the status word of moe_forward_noalloc's fixed array on the

@@ -222,6 +222,37 @@ cudaError_t launch_grouped_mm(int mode, const GroupedMmArgs& a, int num_sms, cud
 bool make_tensor_map_bf16_3d(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows, uint64_t d2,
                              uint32_t box_rows);
 
+// SwiGLU with a weight per row, and its gradient (swiglu.cu).  f a multiple of 8.
+cudaError_t launch_swiglu(const __nv_bfloat16* gu, const float* w, int M, int f, __nv_bfloat16* h, int num_sms,
+                          cudaStream_t s);
+cudaError_t launch_swiglu_backward(const __nv_bfloat16* gu, const __nv_bfloat16* dh, const float* w, int M, int f,
+                                   __nv_bfloat16* dgu, float* dw, __nv_bfloat16* h, int num_sms, cudaStream_t s);
+
+// Norms around a block (block_norm.cu).  d a multiple of 8; x, y, dy, dx fp32 with x_fp32, else bf16.
+struct BlockNormArgs {
+    bool x_fp32;
+    const void* x;
+    const __nv_bfloat16* h;  // null: y = x
+    const float *w_pre, *w_post, *gate, *tgate, *res;
+    int T, d;
+    float eps;
+    void* y;            // forward
+    __nv_bfloat16* n;
+    const void* dy;     // backward
+    const __nv_bfloat16* dn;
+    void* dx;
+    __nv_bfloat16* dh;
+    float *dw_pre, *dw_post, *dgate, *dtgate, *dres;
+    float* partial;     // [block_norm_blocks(T), 3, d]
+};
+int block_norm_blocks(int T);
+cudaError_t launch_block_norm(const BlockNormArgs& a, bool backward_pass, int num_sms, cudaStream_t s);
+
+// AdamW (adamw.cu).  corr1 = 1 - beta1^t, corr2 = sqrt(1 - beta2^t).
+cudaError_t launch_adamw(const moe_adamw_tensor* ts, int count, bool p_bf16, bool g_bf16, bool eight, double lr,
+                         double beta1, double beta2, double eps, double wd, double corr1, double corr2,
+                         const int32_t* step_dev, const float* factors, int num_sms, cudaStream_t s);
+
 // FP8 quantisation (fp8.cu).  Rows: row r of the bf16 [*, C] matrix a (row src[r] when src is
 // given, src values checked against src_rows) -> E4M3 codes q [R, C] and scale [R].  Weights:
 // W [E, K, N] bf16 -> Wq codes, transposed and blocked ([E, N/64, K/128, 64, 128]: code (e, n, k) at

@@ -1,0 +1,58 @@
+// train_util.cuh — vectors of eight values and reductions, shared by the training kernels.
+#pragma once
+
+#include "common.cuh"
+
+namespace moe {
+
+// Eight consecutive values, loaded and stored as 16-byte words (bf16: one, fp32: two).
+struct Vec8 {
+    float v[8];
+};
+__device__ __forceinline__ void unpack_bf16x2(uint32_t u, float& lo, float& hi) {
+    lo = __uint_as_float(u << 16);
+    hi = __uint_as_float(u & 0xffff0000u);
+}
+__device__ __forceinline__ Vec8 unpack8(const uint4& q) {
+    Vec8 r;
+    unpack_bf16x2(q.x, r.v[0], r.v[1]);
+    unpack_bf16x2(q.y, r.v[2], r.v[3]);
+    unpack_bf16x2(q.z, r.v[4], r.v[5]);
+    unpack_bf16x2(q.w, r.v[6], r.v[7]);
+    return r;
+}
+__device__ __forceinline__ uint4 pack8(const Vec8& a) {
+    return make_uint4(pack_bf16x2(a.v[0], a.v[1]), pack_bf16x2(a.v[2], a.v[3]), pack_bf16x2(a.v[4], a.v[5]),
+                      pack_bf16x2(a.v[6], a.v[7]));
+}
+// Vector i of an array of eights.  The data of these kernels is read once: no reuse in L1.
+__device__ __forceinline__ Vec8 load8(const __nv_bfloat16* p, size_t i) {
+    return unpack8(__ldcs(reinterpret_cast<const uint4*>(p) + i));
+}
+__device__ __forceinline__ Vec8 load8(const float* p, size_t i) {
+    const float4 a = __ldcs(reinterpret_cast<const float4*>(p) + 2 * i);
+    const float4 b = __ldcs(reinterpret_cast<const float4*>(p) + 2 * i + 1);
+    return Vec8{{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}};
+}
+// The same for vectors that every row reads again (weights): cached.
+__device__ __forceinline__ Vec8 load8_cached(const float* p, size_t i) {
+    const float4 a = __ldg(reinterpret_cast<const float4*>(p) + 2 * i);
+    const float4 b = __ldg(reinterpret_cast<const float4*>(p) + 2 * i + 1);
+    return Vec8{{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}};
+}
+__device__ __forceinline__ void store8(__nv_bfloat16* p, size_t i, const Vec8& a) {
+    reinterpret_cast<uint4*>(p)[i] = pack8(a);
+}
+__device__ __forceinline__ void store8(float* p, size_t i, const Vec8& a) {
+    float4* q = reinterpret_cast<float4*>(p) + 2 * i;
+    q[0] = make_float4(a.v[0], a.v[1], a.v[2], a.v[3]);
+    q[1] = make_float4(a.v[4], a.v[5], a.v[6], a.v[7]);
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+}  // namespace moe

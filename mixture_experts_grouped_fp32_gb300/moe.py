@@ -11,6 +11,7 @@ import ctypes
 import os
 import threading
 
+import numpy as np
 import torch
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -20,6 +21,7 @@ _P = ctypes.c_void_p
 _I = ctypes.c_int
 _SZ = ctypes.c_size_t
 _F = ctypes.c_float
+_D = ctypes.c_double
 _SIGS = {
     "moe_version": ([], _I),
     "moe_forward_launch_count": ([_I, _I, _I], _I),
@@ -80,6 +82,13 @@ _SIGS = {
     "moe_grouped_mm_workspace_size": ([_I, _I, _I, _I, _I], _SZ),
     "moe_grouped_mm": ([_P, _P, _P, _I, _I, _I, _I, _I, _P, _I, _P, _SZ, _P, _P], _I),
     "moe_grouped_mm_wgrad": ([_P, _P, _P, _I, _I, _I, _I, _P, _I, _I, _P, _SZ, _P, _P], _I),
+    "moe_swiglu": ([_P, _P, _I, _I, _P, _P], _I),
+    "moe_swiglu_backward": ([_P, _P, _P, _I, _I, _P, _P, _P, _P], _I),
+    "moe_block_norm": ([_P, _I, _P, _P, _P, _P, _P, _P, _I, _I, _F, _P, _P, _P], _I),
+    "moe_block_norm_backward_workspace_size": ([_I, _I], _SZ),
+    "moe_block_norm_backward": ([_P, _I, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _F, _P, _P, _P, _P, _P, _P, _P, _P,
+                                 _SZ, _P], _I),
+    "moe_adamw_step": ([_P, _I, _I, _I, _I, _D, _D, _D, _D, _D, _I, _P, _P, _P], _I),
 }
 
 WS_FIELDS = ("status", "idx", "w", "counts", "offsets", "src", "dest", "x_perm", "h", "y_perm", "total")
@@ -916,3 +925,184 @@ def grouped_mm_wgrad(a, g, offsets, out=None, out_dtype=torch.float32, accumulat
     _call("moe_grouped_mm_wgrad", _ptr(a), _ptr(g), _ptr(offsets), M, K, N, E, _ptr(out), f32, int(accumulate),
           _ptr(workspace), nbytes, _ptr(status), _stream(stream))
     return out
+
+
+def swiglu(gu, w=None, h=None, stream=None):
+    """h = w * silu(g) * u, bf16 [M, f], from gu = [g | u] bf16 [M, 2f] and a weight per row (fp32 [M],
+    or None for 1)."""
+    M, f = _gu_dims(gu, w)
+    h = _out(h, (M, f), torch.bfloat16, gu.device, stream, "h")
+    _call("moe_swiglu", _ptr(gu), _ptr(w), M, f, _ptr(h), _stream(stream))
+    return h
+
+
+def _gu_dims(gu, w):
+    _dev(gu, torch.bfloat16, "gu")
+    if gu.dim() != 2 or gu.shape[1] % 2:
+        raise ValueError(f"gu must be [M, 2f], got {tuple(gu.shape)}")
+    M, f = gu.shape[0], gu.shape[1] // 2
+    if w is not None:
+        _dev(w, torch.float32, "w")
+        _shaped(w, (M,), "w")
+    return M, f
+
+
+def swiglu_backward(gu, dh, w=None, want_h: bool = False, dgu=None, dw=None, h=None, stream=None):
+    """Gradient of ``swiglu``: (dgu bf16 [M, 2f], dw fp32 [M] or None without w, h bf16 [M, f] or None
+    without ``want_h``), from dh bf16 [M, f]."""
+    M, f = _gu_dims(gu, w)
+    _dev(dh, torch.bfloat16, "dh")
+    _shaped(dh, (M, f), "dh")
+    dgu = _out(dgu, (M, 2 * f), torch.bfloat16, gu.device, stream, "dgu")
+    dw = _out(dw, (M,), torch.float32, gu.device, stream, "dw") if w is not None else None
+    h = _out(h, (M, f), torch.bfloat16, gu.device, stream, "h") if want_h or h is not None else None
+    _call("moe_swiglu_backward", _ptr(gu), _ptr(dh), _ptr(w), M, f, _ptr(dgu), _ptr(dw), _ptr(h), _stream(stream))
+    return dgu, dw, h
+
+
+def _norm_inputs(x, w_pre, h, w_post, gate, token_gate, res_scale):
+    if x.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"x must be bfloat16 or float32, got {x.dtype}")
+    _dev(x, x.dtype, "x")
+    if x.dim() != 2:
+        raise ValueError(f"x must be [T, d], got {tuple(x.shape)}")
+    T, d = x.shape
+    if h is not None:
+        _dev(h, torch.bfloat16, "h")
+        _shaped(h, (T, d), "h")
+    for t, n, size in ((w_pre, "w_pre", d), (w_post, "w_post", d), (gate, "gate", d), (token_gate, "token_gate", T),
+                       (res_scale, "res_scale", d)):
+        if t is not None:
+            _dev(t, torch.float32, n)
+            _shaped(t, (size,), n)
+    return T, d, int(x.dtype == torch.float32)
+
+
+def block_norm(x, w_pre=None, h=None, w_post=None, gate=None, token_gate=None, res_scale=None, eps: float = 1e-6,
+               y=None, n=None, stream=None):
+    """Norms after and before a block, with its gate and the residual scale:
+
+        y = res_scale * x + (gate * token_gate[:, None]) * (w_post * h / rms(h))
+        n = w_pre * y / rms(y)
+
+    x [T, d] bf16 or fp32 (the residual stream), h [T, d] bf16 (the block's output); w_pre, w_post, gate,
+    res_scale fp32 [d], token_gate fp32 [T].  Returns (y, n): y has x's type, n is bf16.  Without ``h``
+    (before the first block) y is x and is returned as None; without ``w_pre`` n is None."""
+    T, d, f32 = _norm_inputs(x, w_pre, h, w_post, gate, token_gate, res_scale)
+    y = _out(y, (T, d), x.dtype, x.device, stream, "y") if h is not None else None
+    n = _out(n, (T, d), torch.bfloat16, x.device, stream, "n") if w_pre is not None else None
+    _call("moe_block_norm", _ptr(x), f32, _ptr(h), _ptr(w_pre), _ptr(w_post), _ptr(gate), _ptr(token_gate),
+          _ptr(res_scale), T, d, eps, _ptr(y), _ptr(n), _stream(stream))
+    return y, n
+
+
+NORM_GRADS = ("x", "h", "w_pre", "w_post", "gate", "token_gate", "res_scale")
+
+
+def block_norm_backward(x, dy=None, dn=None, w_pre=None, h=None, w_post=None, gate=None, token_gate=None,
+                        res_scale=None, eps: float = 1e-6, workspace=None, stream=None):
+    """Gradients of ``block_norm``, as a dict by the inputs' names (None for an input that was not given):
+    x (x's type) and h (bf16) [T, d], the vectors' in fp32.  dy (x's type) and dn (bf16) [T, d]; one of
+    them may be None (zero).  The same inputs as the forward call; y is recomputed."""
+    T, d, f32 = _norm_inputs(x, w_pre, h, w_post, gate, token_gate, res_scale)
+    for t, n, dt in ((dy, "dy", x.dtype), (dn, "dn", torch.bfloat16)):
+        if t is not None:
+            _dev(t, dt, n)
+            _shaped(t, (T, d), n)
+    if workspace is None:
+        workspace = _empty(int(load().moe_block_norm_backward_workspace_size(T, d)), torch.uint8, x.device, stream)
+    g = dict.fromkeys(NORM_GRADS)
+    g["x"] = _empty((T, d), x.dtype, x.device, stream)
+    if h is not None:
+        g["h"] = _empty((T, d), torch.bfloat16, x.device, stream)
+    for n, t in (("w_pre", w_pre if dn is not None else None), ("w_post", w_post), ("gate", gate),
+                 ("token_gate", token_gate), ("res_scale", res_scale)):
+        if t is not None:
+            g[n] = _empty(t.shape, torch.float32, x.device, stream)
+    _call("moe_block_norm_backward", _ptr(x), f32, _ptr(h), _ptr(dy), _ptr(dn), _ptr(w_pre), _ptr(w_post), _ptr(gate),
+          _ptr(token_gate), _ptr(res_scale), T, d, eps, _ptr(g["x"]), _ptr(g["h"]), _ptr(g["w_pre"]),
+          _ptr(g["w_post"]), _ptr(g["gate"]), _ptr(g["token_gate"]), _ptr(g["res_scale"]), _ptr(workspace),
+          workspace.nbytes, _stream(stream))
+    return g
+
+
+# ---------------------------------------------------------------------------------------------
+# AdamW over many tensors.
+# ---------------------------------------------------------------------------------------------
+ADAMW_BLOCK = 256  # elements that share one scale of an 8-bit moment
+_ADAMW_ENTRY = np.dtype([(n, np.uint64) for n in ("param", "grad", "m", "v", "m_scale", "v_scale", "copy", "n")])
+
+
+def adamw_state(param: torch.Tensor, bits: int = 32):
+    """Fresh moments of one parameter: (m, v) fp32, or with ``bits`` = 8 (m, v, m_scale, v_scale) — E4M3
+    codes of m and of the root of v, with one fp32 scale for each 256 elements."""
+    if bits == 32:
+        return torch.zeros_like(param, dtype=torch.float32), torch.zeros_like(param, dtype=torch.float32)
+    if bits != 8:
+        raise ValueError(f"bits must be 8 or 32, got {bits}")
+    blocks = -(-param.numel() // ADAMW_BLOCK)
+    code = lambda: torch.zeros(param.shape, dtype=torch.float8_e4m3fn, device=param.device)
+    scale = lambda: torch.ones(blocks, dtype=torch.float32, device=param.device)
+    return code(), code(), scale(), scale()
+
+
+def _same(ts, like, name, dtype=None, sizes=None):
+    """Addresses of the tensors of one list, checked against the parameters'."""
+    if len(ts) != len(like):
+        raise ValueError(f"{name}: {len(ts)} tensors for {len(like)} parameters")
+    dtype = dtype if dtype is not None else ts[0].dtype
+    for i, t in enumerate(ts):
+        if not (t.is_cuda and t.dtype is dtype and t.is_contiguous()):
+            raise ValueError(f"{name}[{i}] must be a contiguous CUDA {dtype} tensor (got {t.dtype}, cuda={t.is_cuda}, "
+                             f"contiguous={t.is_contiguous()})")
+    got = [t.numel() for t in ts]
+    if sizes is not None and got != sizes:
+        i = next(i for i, (a, b) in enumerate(zip(got, sizes)) if a != b)
+        raise ValueError(f"{name}[{i}] has {got[i]} elements, {sizes[i]} wanted")
+    return [t.data_ptr() for t in ts], got
+
+
+def adamw_step(params, grads, m, v, lr: float, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8,
+               weight_decay: float = 0.01, step: int = 1, m_scales=None, v_scales=None, copies=None, step_tensor=None,
+               factors=None, stream=None):
+    """One AdamW step over lists of tensors, in place (one launch for up to 400 tensors):
+
+        m = beta1 m + (1 - beta1) g;  v = beta2 v + (1 - beta2) g^2
+        p = p (1 - lr weight_decay) - lr / (1 - beta1^t) m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
+
+    params and grads are bf16 or fp32 (each list of one type); m and v fp32, or float8_e4m3fn codes with
+    ``m_scales`` and ``v_scales`` (see ``adamw_state``).  ``copies``: bf16 tensors that receive the new
+    parameters too.  t is ``step``, or the int32 in ``step_tensor`` on the device; ``factors`` (fp32 [2] on
+    the device) multiplies the gradients by its first value and lr by its second."""
+    if len(params) == 0:
+        return
+    pt, gt, st = params[0].dtype, grads[0].dtype if len(grads) else None, m[0].dtype if len(m) else None
+    for t, n in ((pt, "params"), (gt, "grads")):
+        if t not in (torch.bfloat16, torch.float32):
+            raise ValueError(f"{n} must be bfloat16 or float32, got {t}")
+    if st not in (torch.float32, torch.float8_e4m3fn):
+        raise ValueError(f"m and v must be float32 or float8_e4m3fn, got {st}")
+    eight = st is torch.float8_e4m3fn
+    if eight != (m_scales is not None) or eight != (v_scales is not None):
+        raise ValueError("m_scales and v_scales belong to 8-bit moments, and only to them")
+    tab = np.zeros(len(params), _ADAMW_ENTRY)
+    tab["param"], sizes = _same(params, params, "params", pt)
+    tab["n"] = sizes
+    tab["grad"] = _same(grads, params, "grads", gt, sizes)[0]
+    tab["m"] = _same(m, params, "m", st, sizes)[0]
+    tab["v"] = _same(v, params, "v", st, sizes)[0]
+    if eight:
+        blocks = [-(-n // ADAMW_BLOCK) for n in sizes]
+        tab["m_scale"] = _same(m_scales, params, "m_scales", torch.float32, blocks)[0]
+        tab["v_scale"] = _same(v_scales, params, "v_scales", torch.float32, blocks)[0]
+    if copies is not None:
+        tab["copy"] = _same(copies, params, "copies", torch.bfloat16, sizes)[0]
+    if step_tensor is not None:
+        _dev(step_tensor, torch.int32, "step_tensor")
+        _shaped(step_tensor.view(-1), (1,), "step_tensor")
+    if factors is not None:
+        _dev(factors, torch.float32, "factors")
+        _shaped(factors, (2,), "factors")
+    _call("moe_adamw_step", tab.ctypes.data, len(params), int(pt is torch.bfloat16), int(gt is torch.bfloat16),
+          8 if eight else 32, lr, beta1, beta2, eps, weight_decay, step, _ptr(step_tensor), _ptr(factors),
+          _stream(stream))

@@ -110,6 +110,7 @@ class MoeError(RuntimeError):
 
 _lock = threading.Lock()
 _lib = None
+_fns: dict = {}  # the bound entry points of the loaded library, by name
 
 
 def load(path: str = LIB_PATH) -> ctypes.CDLL:
@@ -125,15 +126,23 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
                 fn = getattr(lib, name)
                 fn.argtypes = args
                 fn.restype = res
+                _fns[name] = fn
             _lib = lib
     return _lib
 
 
+def _fn(name: str):
+    fn = _fns.get(name)
+    if fn is None:
+        load()
+        fn = _fns[name]
+    return fn
+
+
 def _call(name: str, *args) -> None:
-    L = load()
-    rc = getattr(L, name)(*args)
+    rc = _fn(name)(*args)
     if rc != 0:
-        raise MoeError(name, rc, L.moe_last_error_string().decode())
+        raise MoeError(name, rc, _fn("moe_last_error_string")().decode())
 
 
 def _ptr(t: torch.Tensor | None):
@@ -141,8 +150,8 @@ def _ptr(t: torch.Tensor | None):
 
 
 def _stream(stream) -> int | None:
-    if stream is None:
-        stream = torch.cuda.current_stream()
+    if stream is None:  # the current stream's handle, without building a Stream object around it
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else stream
 
 
@@ -1046,20 +1055,23 @@ def adamw_state(param: torch.Tensor, bits: int = 32):
     return code(), code(), scale(), scale()
 
 
-def _same(ts, like, name, dtype=None, sizes=None):
-    """Addresses of the tensors of one list, checked against the parameters'."""
-    if len(ts) != len(like):
-        raise ValueError(f"{name}: {len(ts)} tensors for {len(like)} parameters")
-    dtype = dtype if dtype is not None else ts[0].dtype
-    for i, t in enumerate(ts):
-        if not (t.is_cuda and t.dtype is dtype and t.is_contiguous()):
-            raise ValueError(f"{name}[{i}] must be a contiguous CUDA {dtype} tensor (got {t.dtype}, cuda={t.is_cuda}, "
-                             f"contiguous={t.is_contiguous()})")
-    got = [t.numel() for t in ts]
+_dtype_of, _is_cuda = torch.Tensor.dtype.__get__, torch.Tensor.is_cuda.__get__
+
+
+def _addresses(ts, name, dtype, sizes=None, count=None):
+    """Addresses and sizes of the tensors of one list, which must be contiguous CUDA tensors of one type
+    (mapped over the list in C: a step may hold hundreds of tensors)."""
+    if count is not None and len(ts) != count:
+        raise ValueError(f"{name}: {len(ts)} tensors for {count} parameters")
+    if set(map(_dtype_of, ts)) != {dtype} or not all(map(_is_cuda, ts)) or \
+            not all(map(torch.Tensor.is_contiguous, ts)):
+        for i, t in enumerate(ts):
+            _dev(t, dtype, f"{name}[{i}]")
+    got = list(map(torch.Tensor.numel, ts))
     if sizes is not None and got != sizes:
         i = next(i for i, (a, b) in enumerate(zip(got, sizes)) if a != b)
         raise ValueError(f"{name}[{i}] has {got[i]} elements, {sizes[i]} wanted")
-    return [t.data_ptr() for t in ts], got
+    return list(map(torch.Tensor.data_ptr, ts)), got
 
 
 def adamw_step(params, grads, m, v, lr: float, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8,
@@ -1085,24 +1097,25 @@ def adamw_step(params, grads, m, v, lr: float, beta1: float = 0.9, beta2: float 
     eight = st is torch.float8_e4m3fn
     if eight != (m_scales is not None) or eight != (v_scales is not None):
         raise ValueError("m_scales and v_scales belong to 8-bit moments, and only to them")
-    tab = np.zeros(len(params), _ADAMW_ENTRY)
-    tab["param"], sizes = _same(params, params, "params", pt)
+    n = len(params)
+    tab = np.zeros(n, _ADAMW_ENTRY)
+    tab["param"], sizes = _addresses(params, "params", pt)
     tab["n"] = sizes
-    tab["grad"] = _same(grads, params, "grads", gt, sizes)[0]
-    tab["m"] = _same(m, params, "m", st, sizes)[0]
-    tab["v"] = _same(v, params, "v", st, sizes)[0]
+    lists = [("grad", grads, "grads", gt, sizes), ("m", m, "m", st, sizes), ("v", v, "v", st, sizes)]
     if eight:
-        blocks = [-(-n // ADAMW_BLOCK) for n in sizes]
-        tab["m_scale"] = _same(m_scales, params, "m_scales", torch.float32, blocks)[0]
-        tab["v_scale"] = _same(v_scales, params, "v_scales", torch.float32, blocks)[0]
+        blocks = [-(-k // ADAMW_BLOCK) for k in sizes]
+        lists += [("m_scale", m_scales, "m_scales", torch.float32, blocks),
+                  ("v_scale", v_scales, "v_scales", torch.float32, blocks)]
     if copies is not None:
-        tab["copy"] = _same(copies, params, "copies", torch.bfloat16, sizes)[0]
+        lists.append(("copy", copies, "copies", torch.bfloat16, sizes))
+    for field, ts, name, dtype, want in lists:
+        tab[field] = _addresses(ts, name, dtype, want, n)[0]
     if step_tensor is not None:
         _dev(step_tensor, torch.int32, "step_tensor")
         _shaped(step_tensor.view(-1), (1,), "step_tensor")
     if factors is not None:
         _dev(factors, torch.float32, "factors")
         _shaped(factors, (2,), "factors")
-    _call("moe_adamw_step", tab.ctypes.data, len(params), int(pt is torch.bfloat16), int(gt is torch.bfloat16),
+    _call("moe_adamw_step", tab.ctypes.data, n, int(pt is torch.bfloat16), int(gt is torch.bfloat16),
           8 if eight else 32, lr, beta1, beta2, eps, weight_decay, step, _ptr(step_tensor), _ptr(factors),
           _stream(stream))

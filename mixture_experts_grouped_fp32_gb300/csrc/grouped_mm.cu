@@ -63,8 +63,22 @@ constexpr int GROUP_R = 8;  // row tiles that run together
 constexpr int MAX_E = 256;
 constexpr int MAX_SPLIT = 16;
 constexpr uint16_t BOTH_CTAS = 0x3;
-// Warps: 0 copies, 1 tensor memory and MMAs, 2-5 epilogue, 6 zeroes segment ends (weight gradient).
-constexpr int kFixWarp = 6;
+// Warps: 0 copies, 1 tensor memory and MMAs, then the epilogue's groups of eight, then (weight gradient)
+// one that zeroes segment ends.
+constexpr int kEpiWarps = 8;
+// bf16 outputs: one epilogue group for each accumulator, so that short items (a few blocks of
+// reduction) do not wait for one group to read, convert and store tile after tile.  fp32 outputs: one
+// group, which keeps the tile's running sums in registers across both accumulators.
+template <typename OUT>
+constexpr int epi_groups() { return sizeof(OUT) == 4 ? 1 : 2; }
+template <typename OUT>
+constexpr int fix_warp() { return 2 + kEpiWarps * epi_groups<OUT>(); }
+template <int MODE, typename OUT>
+constexpr int num_threads() { return 32 * (fix_warp<OUT>() + (MODE == kMmWgrad ? 1 : 0)); }
+// fp32 outputs: blocks of 64 summed in tensor memory before the partial sum moves to registers.
+constexpr int CHUNK = 8;
+template <typename OUT>
+constexpr int chunk_blocks() { return sizeof(OUT) == 4 ? CHUNK : 1 << 20; }
 constexpr int SMEM_BYTES = 232448;
 
 struct Ctl {
@@ -90,45 +104,68 @@ __device__ __forceinline__ int row_tiles(int cnt, int K) {
 
 struct Item {
     int e, f0;          // expert, first feature of the pair's tile
-    int r0, rows;       // first output row (of the segment, or of the expert's [K, N]) and how many
+    int r0, rows;       // first output row (of the segment, or of the expert's [K, N]) and how many (> 0)
     int ntok;           // UMMA N: rows rounded up to 32
     int red0, red1;     // reduction range in blocks of 64
     int red_rows;       // weight gradient: rows of the segment
     int slice;
 };
 
+// A role's position in the items of its CTA pair, which it visits in ascending order: the expert is
+// found by walking on from the last one, and what depends on the expert alone is kept.
 template <int MODE>
-__device__ __forceinline__ Item decode_item(const Ctl& c, int K, int E, int f_tiles, int ksplit, int i) {
-    int lo = 0, hi = E;  // item_start[lo] <= i < item_start[lo + 1]
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (c.item_start[mid] <= i) lo = mid; else hi = mid;
+struct Cursor {
+    const Ctl& c;
+    int K, E, f_tiles, ksplit;
+    int e = -1, start = 0, next = 0;  // expert, its first item, the next expert's
+    int cnt = 0, total = 0, rt = 1, per = 32, nkb = 0;
+
+    __device__ __forceinline__ Cursor(const Ctl& ctl, int k, int experts, int ft, int ks)
+        : c(ctl), K(k), E(experts), f_tiles(ft), ksplit(ks) {}
+
+    __device__ __forceinline__ Item at(int i) {
+        if (i >= next) {
+            do {
+                ++e;
+                next = c.item_start[e + 1];
+            } while (i >= next);
+            start = c.item_start[e];
+            cnt = c.seg[e + 1] - c.seg[e];
+            total = MODE == kMmWgrad ? K : cnt;
+            rt = row_tiles<MODE>(cnt, K);
+            per = (((total + rt - 1) / rt) + 31) & ~31;  // equal tiles; the last one may be shorter
+            nkb = ((MODE == kMmWgrad ? cnt : K) + BK - 1) / BK;
+        }
+        Item it;
+        it.e = e;
+        unsigned j = static_cast<unsigned>(i - start);
+        it.slice = 0;
+        if (ksplit > 1) {
+            it.slice = static_cast<int>(j % static_cast<unsigned>(ksplit));
+            j /= static_cast<unsigned>(ksplit);
+        }
+        unsigned g = 0, gr = static_cast<unsigned>(rt);
+        if (rt > GROUP_R) {
+            const unsigned per_group = static_cast<unsigned>(GROUP_R * f_tiles);
+            g = j / per_group;
+            j -= g * per_group;
+            gr = min(static_cast<unsigned>(GROUP_R), gr - g * GROUP_R);
+        }
+        const unsigned ft = j / gr;
+        it.f0 = static_cast<int>(ft) * TILE_F;
+        it.r0 = static_cast<int>(g * GROUP_R + (j - ft * gr)) * per;
+        it.rows = min(per, total - it.r0);
+        it.ntok = (it.rows + 31) & ~31;
+        it.red_rows = cnt;
+        it.red0 = 0;
+        it.red1 = nkb;
+        if (ksplit > 1) {
+            it.red0 = static_cast<int>(static_cast<long long>(nkb) * it.slice / ksplit);
+            it.red1 = static_cast<int>(static_cast<long long>(nkb) * (it.slice + 1) / ksplit);
+        }
+        return it;
     }
-    Item it;
-    it.e = lo;
-    const int cnt = c.seg[lo + 1] - c.seg[lo];
-    const int total = MODE == kMmWgrad ? K : cnt;
-    const int rt = row_tiles<MODE>(cnt, K);
-    int j = i - c.item_start[lo];
-    it.slice = j % ksplit;
-    j /= ksplit;
-    const int per_group = GROUP_R * f_tiles;
-    const int g = j / per_group;
-    j -= g * per_group;
-    const int gr = min(GROUP_R, rt - g * GROUP_R);
-    const int ft = j / gr;
-    const int r = g * GROUP_R + (j - ft * gr);
-    it.f0 = ft * TILE_F;
-    const int per = (((total + rt - 1) / rt) + 31) & ~31;  // equal tiles; the last one may be shorter
-    it.r0 = r * per;
-    it.rows = min(per, total - it.r0);  // may be <= 0 after the rounding to 32
-    it.ntok = (max(it.rows, 1) + 31) & ~31;
-    it.red_rows = cnt;
-    const int nkb = ((MODE == kMmWgrad ? cnt : K) + BK - 1) / BK;
-    it.red0 = static_cast<int>(static_cast<long long>(nkb) * it.slice / ksplit);
-    it.red1 = it.rows > 0 ? static_cast<int>(static_cast<long long>(nkb) * (it.slice + 1) / ksplit) : it.red0;
-    return it;
-}
+};
 
 __device__ __forceinline__ void raise_abort(Ctl& c, int32_t* status) {
     *reinterpret_cast<volatile int*>(&c.abort_flag) = 1;
@@ -145,7 +182,7 @@ __device__ __forceinline__ __nv_bfloat16 cvt_out<__nv_bfloat16>(float v) { retur
 // tmF: the feature operand (weights [E, K, N] / [E, N, K], or G [M, N] as one matrix); tmR, tmR32: the
 // row operand A [M, K] (boxes of 128 and of 32 rows; weight gradient: boxes of 64 rows).
 template <int MODE, typename OUT>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MODE == kMmWgrad ? 224 : 192, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(num_threads<MODE, OUT>(), 1)
 grouped_mm_kernel(const __grid_constant__ CUtensorMap tmF, const __grid_constant__ CUtensorMap tmR,
                   const __grid_constant__ CUtensorMap tmR32, const int32_t* __restrict__ offsets, int M, int K, int N,
                   int E, int ksplit, int accumulate, OUT* __restrict__ out, int32_t* __restrict__ status) {
@@ -171,7 +208,7 @@ grouped_mm_kernel(const __grid_constant__ CUtensorMap tmF, const __grid_constant
         }
         for (int a = 0; a < NUM_ACC; ++a) {
             ptx::mbar_init(&c.tfull[a], 1);
-            ptx::mbar_init(&c.tempty[a], 8);
+            ptx::mbar_init(&c.tempty[a], 2 * kEpiWarps);
         }
         ptx::mbar_init(&c.drain, 1);
         c.abort_flag = 0;
@@ -234,6 +271,7 @@ grouped_mm_kernel(const __grid_constant__ CUtensorMap tmF, const __grid_constant
     const int total = c.total_items;
     uint32_t fill_parity[STAGES];
     int filled_mask = 0;
+    Cursor<MODE> cur(c, K, E, f_tiles, ksplit);
 
     if (warp == 0 && lane == 0) {
         // ------------------------------ copies (both CTAs) ------------------------------
@@ -243,7 +281,7 @@ grouped_mm_kernel(const __grid_constant__ CUtensorMap tmF, const __grid_constant
         uint32_t phase = 0;
         bool aborted = false;
         for (int i = pair_id; i < total && !aborted; i += num_pairs) {
-            const Item it = decode_item<MODE>(c, K, E, f_tiles, ksplit, i);
+            const Item it = cur.at(i);
             const int half = it.ntok >> 1;
             const int f = it.f0 + 128 * rank;           // this CTA's features
             const int seg0 = c.seg[it.e];
@@ -308,55 +346,60 @@ grouped_mm_kernel(const __grid_constant__ CUtensorMap tmF, const __grid_constant
         uint32_t phase = 0, acc = 0, acc_phase = 0;
         bool aborted = false;
         for (int i = pair_id; i < total && !aborted; i += num_pairs) {
-            const Item it = decode_item<MODE>(c, K, E, f_tiles, ksplit, i);
+            const Item it = cur.at(i);
             if (it.red0 >= it.red1) continue;  // nothing to reduce: the epilogue stores zeros
             const uint32_t idesc = ptx::idesc_bf16_f32(TILE_F, static_cast<uint32_t>(it.ntok),
                                                        /*a_mn=*/MODE == kMmTransB ? 0 : 1, /*b_mn=*/WGRAD ? 1 : 0);
-            if (!ptx::mbar_wait(&c.tempty[acc], acc_phase ^ 1u, abort_flag)) {
-                raise_abort(c, status);
-                break;
-            }
-            ptx::tc_fence_after();
-            const uint32_t d_tmem = tmem_base + acc * ACC_COLS;
-            for (int kb = it.red0; kb < it.red1; ++kb) {
-                if (!ptx::mbar_wait(&c.full[stage], phase, abort_flag)) {
+            for (int c0 = it.red0; c0 < it.red1 && !aborted; c0 += chunk_blocks<OUT>()) {
+                if (!ptx::mbar_wait(&c.tempty[acc], acc_phase ^ 1u, abort_flag)) {
                     raise_abort(c, status);
                     aborted = true;
                     break;
                 }
                 ptx::tc_fence_after();
-                const uint32_t sf = ptx::smem_u32(tiles + stage * STAGE_BYTES);
-                // MN-major: 64-wide boxes 8 KB apart, 16 deep = 2 KB.  K-major: 16 deep = 32 bytes.
-                const uint64_t f_desc = ptx::smem_desc_sw128(sf, MODE == kMmTransB ? 16 : BOX_BYTES, 1024);
-                const uint64_t r_desc = ptx::smem_desc_sw128(sf + F_BYTES, WGRAD ? BOX_BYTES : 16, 1024);
-                constexpr uint64_t f_step = (MODE == kMmTransB ? 32 : 2048) >> 4;
-                constexpr uint64_t r_step = (WGRAD ? 2048 : 32) >> 4;
-                const int steps = WGRAD ? min(BK / UMMA_K, (it.red_rows - kb * BK + UMMA_K - 1) / UMMA_K) : BK / UMMA_K;
+                const uint32_t d_tmem = tmem_base + acc * ACC_COLS;
+                const int c1 = min(it.red1, c0 + chunk_blocks<OUT>());
+                for (int kb = c0; kb < c1; ++kb) {
+                    if (!ptx::mbar_wait(&c.full[stage], phase, abort_flag)) {
+                        raise_abort(c, status);
+                        aborted = true;
+                        break;
+                    }
+                    ptx::tc_fence_after();
+                    const uint32_t sf = ptx::smem_u32(tiles + stage * STAGE_BYTES);
+                    // MN-major: 64-wide boxes 8 KB apart, 16 deep = 2 KB.  K-major: 16 deep = 32 bytes.
+                    const uint64_t f_desc = ptx::smem_desc_sw128(sf, MODE == kMmTransB ? 16 : BOX_BYTES, 1024);
+                    const uint64_t r_desc = ptx::smem_desc_sw128(sf + F_BYTES, WGRAD ? BOX_BYTES : 16, 1024);
+                    constexpr uint64_t f_step = (MODE == kMmTransB ? 32 : 2048) >> 4;
+                    constexpr uint64_t r_step = (WGRAD ? 2048 : 32) >> 4;
+                    const int steps =
+                        WGRAD ? min(BK / UMMA_K, (it.red_rows - kb * BK + UMMA_K - 1) / UMMA_K) : BK / UMMA_K;
 #pragma unroll
-                for (int kk = 0; kk < BK / UMMA_K; ++kk)
-                    if (kk < steps)
-                        ptx::mma_bf16_ss_pair(d_tmem, f_desc + kk * f_step, r_desc + kk * r_step, idesc,
-                                              (kb != it.red0 || kk != 0) ? 1u : 0u);
-                ptx::mma_commit_pair(&c.empty[stage], BOTH_CTAS);
-                if (++stage == STAGES) {
-                    stage = 0;
-                    phase ^= 1u;
+                    for (int kk = 0; kk < BK / UMMA_K; ++kk)
+                        if (kk < steps)
+                            ptx::mma_bf16_ss_pair(d_tmem, f_desc + kk * f_step, r_desc + kk * r_step, idesc,
+                                                  (kb != c0 || kk != 0) ? 1u : 0u);
+                    ptx::mma_commit_pair(&c.empty[stage], BOTH_CTAS);
+                    if (++stage == STAGES) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+                if (aborted) break;
+                ptx::mma_commit_pair(&c.tfull[acc], BOTH_CTAS);
+                if (++acc == NUM_ACC) {
+                    acc = 0;
+                    acc_phase ^= 1u;
                 }
             }
-            if (aborted) break;
-            ptx::mma_commit_pair(&c.tfull[acc], BOTH_CTAS);
-            if (++acc == NUM_ACC) {
-                acc = 0;
-                acc_phase ^= 1u;
-            }
         }
-    } else if (WGRAD && warp == kFixWarp) {
+    } else if (WGRAD && warp == fix_warp<OUT>()) {
         // ------------------- zero the rows past a segment's end (both CTAs) -------------------
         int stage = 0;
         uint32_t parity = 0;  // bit s: parity of tail[s]'s next phase
         bool aborted = false;
         for (int i = pair_id; i < total && !aborted; i += num_pairs) {
-            const Item it = decode_item<MODE>(c, K, E, f_tiles, ksplit, i);
+            const Item it = cur.at(i);
             const int n = it.red1 - it.red0;
             if (n > 0 && it.red1 * BK > it.red_rows && (it.red_rows & 15)) {
                 const int st = (stage + n - 1) % STAGES;
@@ -380,65 +423,116 @@ grouped_mm_kernel(const __grid_constant__ CUtensorMap tmF, const __grid_constant
             }
             stage = (stage + n) % STAGES;
         }
-    } else if (warp >= 2 && warp < 6) {
+    } else if (warp >= 2 && warp < fix_warp<OUT>()) {
         // ------------------------------ epilogue (both CTAs) ------------------------------
-        const int quarter = warp & 3;  // this warp's tensor-memory lanes: 32 quarter .. + 31
+        const int quarter = warp & 3;            // this warp's tensor-memory lanes: 32 quarter .. + 31
+        const int col0 = 128 * (((warp - 2) >> 2) & 1);  // and its half of the tile's columns (output rows)
+        const uint32_t group = (warp - 2) / kEpiWarps;   // bf16: the accumulator of this group
         uint32_t acc = 0, acc_phase = 0;
         const size_t slice_elems = WGRAD ? static_cast<size_t>(E) * K * N : static_cast<size_t>(M) * N;
-        for (int i = pair_id; i < total; i += num_pairs) {
-            const Item it = decode_item<MODE>(c, K, E, f_tiles, ksplit, i);
-            const bool any = it.red0 < it.red1;
-            if (any) {
-                if (!ptx::mbar_wait(&c.tfull[acc], acc_phase, abort_flag)) {
-                    raise_abort(c, status);
-                    break;
-                }
-                ptx::tc_fence_after();
+        auto take = [&]() -> bool {  // the next accumulator is final
+            if (!ptx::mbar_wait(&c.tfull[acc], acc_phase, abort_flag)) {
+                raise_abort(c, status);
+                return false;
             }
-            const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + acc * ACC_COLS;
+            ptx::tc_fence_after();
+            return true;
+        };
+        auto give = [&]() {  // and may be overwritten
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive_cluster(ptx::map_to_cta(ptx::smem_u32(&c.tempty[acc]), 0));
+        };
+        auto pass = [&]() {  // on to the next accumulator
+            if (++acc == NUM_ACC) {
+                acc = 0;
+                acc_phase ^= 1u;
+            }
+        };
+        // Stores the warp's 32 output rows from j0 on (a lane holds one column of them), up to `rows`.
+        auto put = [&](OUT* p, const uint32_t (&v)[32], int rows) {
+            if (rows >= 32) {
+#pragma unroll
+                for (int j = 0; j < 32; ++j, p += N) *p = cvt_out<OUT>(__uint_as_float(v[j]));
+            } else {
+#pragma unroll
+                for (int j = 0; j < 32; ++j, p += N)
+                    if (j < rows) *p = cvt_out<OUT>(__uint_as_float(v[j]));
+            }
+        };
+        bool aborted = false;
+        for (int i = pair_id; i < total && !aborted; i += num_pairs) {
+            const Item it = cur.at(i);
             const int n = it.f0 + 128 * rank + 32 * quarter + lane;
             const size_t row0 = WGRAD ? static_cast<size_t>(it.e) * K + it.r0 : static_cast<size_t>(c.seg[it.e]) + it.r0;
-            OUT* dst = out + it.slice * slice_elems + row0 * N + n;
-#pragma unroll 1
-            for (int j0 = 0; j0 < it.rows; j0 += 32, dst += static_cast<size_t>(32) * N) {
-                uint32_t v[32];
-                if (any) {
-                    ptx::tmem_ld_32x32b_x32(taddr + j0, v);
-                    ptx::tmem_ld_wait();
-                } else {
+            OUT* dst = out + it.slice * slice_elems + (row0 + col0) * N + n;
+            const uint32_t lane_addr = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + col0;
+            if constexpr (sizeof(OUT) == 4) {
+                // The chunks' partial sums are added in registers, rounded to nearest: in tensor memory
+                // every addition truncates, a bias that grows with the number of additions.
+                uint32_t sum[4][32];
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) v[j] = 0u;
-                }
-                const int nr = it.rows - j0;
-                if (n < N) {
-                    if constexpr (WGRAD && sizeof(OUT) == 4) {
-                        if (accumulate) {
-                            float old[32];
+                for (int q = 0; q < 4; ++q)
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) sum[q][j] = 0u;
+                for (int c0 = it.red0; c0 < it.red1; c0 += CHUNK) {
+                    if (!take()) {
+                        aborted = true;
+                        break;
+                    }
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        if (col0 + 32 * q < it.rows) {
+                            uint32_t v[32];
+                            ptx::tmem_ld_32x32b_x32(lane_addr + acc * ACC_COLS + 32 * q, v);
+                            ptx::tmem_ld_wait();
 #pragma unroll
                             for (int j = 0; j < 32; ++j)
-                                old[j] = j < nr ? static_cast<float>(dst[static_cast<size_t>(j) * N]) : 0.0f;
-#pragma unroll
-                            for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) + old[j]);
+                                sum[q][j] = __float_as_uint(__uint_as_float(sum[q][j]) + __uint_as_float(v[j]));
                         }
                     }
-                    if (nr >= 32) {
+                    give();
+                    pass();
+                }
+                if (aborted) break;
 #pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            dst[static_cast<size_t>(j) * N] = cvt_out<OUT>(__uint_as_float(v[j]));
-                    } else {
+                for (int q = 0; q < 4; ++q) {
+                    const int nr = it.rows - col0 - 32 * q;
+                    if (nr > 0 && n < N) {
+                        float* p = dst + static_cast<size_t>(32 * q) * N;
+                        if (WGRAD && accumulate) {
+                            float old[32];
 #pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            if (j < nr) dst[static_cast<size_t>(j) * N] = cvt_out<OUT>(__uint_as_float(v[j]));
+                            for (int j = 0; j < 32; ++j) old[j] = j < nr ? p[static_cast<size_t>(j) * N] : 0.0f;
+#pragma unroll
+                            for (int j = 0; j < 32; ++j)
+                                sum[q][j] = __float_as_uint(__uint_as_float(sum[q][j]) + old[j]);
+                        }
+                        put(p, sum[q], nr);
                     }
                 }
-            }
-            if (any) {
-                ptx::tc_fence_before();
-                __syncwarp();
-                if (lane == 0) ptx::mbar_arrive_cluster(ptx::map_to_cta(ptx::smem_u32(&c.tempty[acc]), 0));
-                if (++acc == NUM_ACC) {
-                    acc = 0;
-                    acc_phase ^= 1u;
+            } else {
+                const bool any = it.red0 < it.red1;
+                if (epi_groups<OUT>() > 1 && acc != group) {  // the other group's
+                    if (any) pass();
+                    continue;
+                }
+                if (any && !take()) break;
+#pragma unroll 1
+                for (int j0 = 0; j0 < 128 && col0 + j0 < it.rows; j0 += 32) {
+                    uint32_t v[32];
+                    if (any) {
+                        ptx::tmem_ld_32x32b_x32(lane_addr + acc * ACC_COLS + j0, v);
+                        ptx::tmem_ld_wait();
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) v[j] = 0u;
+                    }
+                    if (n < N) put(dst + static_cast<size_t>(j0) * N, v, it.rows - col0 - j0);
+                }
+                if (any) {
+                    give();
+                    pass();
                 }
             }
         }
@@ -530,7 +624,7 @@ cudaError_t launch_mode(const GroupedMmArgs& a, OUT* out, int ksplit, int accumu
         *why = "cuTensorMapEncodeTiled failed (driver entry point missing or bad operand)";
         return cudaErrorInvalidValue;
     }
-    return launch_k(kPdlTrain, grouped_mm_kernel<MODE, OUT>, dim3(num_sms & ~1), dim3(MODE == kMmWgrad ? 224 : 192),
+    return launch_k(kPdlTrain, grouped_mm_kernel<MODE, OUT>, dim3(num_sms & ~1), dim3(num_threads<MODE, OUT>()),
                     SMEM_BYTES, s, mF, mR, mR32, a.offsets, a.M, a.K, a.N, a.E, ksplit, accumulate, out, a.status);
 }
 

@@ -3,10 +3,11 @@
 //   m = b1 m + (1 - b1) g'          v = b2 v + (1 - b2) g'^2
 //   p = p (1 - lr wd) - (lr / (1 - b1^t)) m / (sqrt(v) / sqrt(1 - b2^t) + eps)
 //
-// in fp32, every operation rounded by itself (no contraction into fused multiply-adds), so that the
-// result does not depend on how a compiler pairs operations — with 8-bit moments a last-bit difference
-// could otherwise move a code.  The parameter is rounded once, when it is bf16; a bf16 copy of an fp32
-// parameter can be written along.
+// in fp32.  In the moments every operation is rounded by itself (no contraction into fused multiply-adds),
+// so that they do not depend on how a compiler pairs operations: with 8-bit moments a last-bit difference
+// could move a code.  The step's quotient is a fast division (2 units in the last place of a term that
+// is far smaller than the parameter).  The parameter is rounded once, when it is bf16; a bf16 copy of an
+// fp32 parameter can be written along.
 //
 // 8-bit moments: blocks of 256 elements of a tensor share one fp32 scale.  The first moment is kept as
 // E4M3 codes of m / scale, scale = max|m| / 448; of the second moment the root r = sqrt(v) is kept the
@@ -17,8 +18,8 @@
 //
 // Bound by memory: 22 to 30 bytes per element (32-bit moments, fp32 parameter) or 10 to 16 (8-bit).  A
 // warp handles one block of 256 elements, eight per lane in 16-byte words where the tensor's pieces are
-// aligned for it, else element by element; chunks of 2048 elements are dealt to the thread blocks over
-// all tensors.  The table of tensors travels in the kernel's parameters (up to 32 KB): nothing is copied
+// aligned for it, else element by element; chunks of 8192 elements are dealt to the thread blocks over
+// all tensors (the search for a chunk's tensor then costs little per element).  The table of tensors travels in the kernel's parameters (up to 32 KB): nothing is copied
 // to the device before the launch and no memory is held.
 #include <cuda_fp8.h>
 
@@ -28,7 +29,8 @@ namespace moe {
 namespace {
 
 constexpr int kBlock = 256;               // elements per scale
-constexpr int kChunk = 8 * kBlock;        // elements per thread block and step
+constexpr int kWarpBlocks = 4;            // blocks of 256 that a warp takes from a chunk
+constexpr int kChunk = 8 * kWarpBlocks * kBlock;  // elements that a thread block takes at a time
 constexpr int kSmallTable = 48, kLargeTable = 400;
 
 struct Entry {
@@ -66,11 +68,25 @@ __device__ __forceinline__ float load1(const __nv_bfloat16* p, long long i) { re
 __device__ __forceinline__ void store1(float* p, long long i, float v) { p[i] = v; }
 __device__ __forceinline__ void store1(__nv_bfloat16* p, long long i, float v) { p[i] = __float2bfloat16_rn(v); }
 
-__device__ __forceinline__ float from_e4m3(uint8_t c) {
-    __half_raw h = __nv_cvt_fp8_to_halfraw(c, __NV_E4M3);
-    return __half2float(*reinterpret_cast<__half*>(&h));
+// Eight codes and their values (E4M3 -> fp16 is exact), two at a time.
+__device__ __forceinline__ void from_e4m3(uint2 c, float (&v)[8]) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const uint32_t w = j < 2 ? c.x : c.y;
+        const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w >> (16 * (j & 1))), __NV_E4M3);
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+        v[2 * j] = f.x;
+        v[2 * j + 1] = f.y;
+    }
 }
-__device__ __forceinline__ uint8_t to_e4m3(float v) { return __nv_cvt_float_to_fp8(v, __NV_SATFINITE, __NV_E4M3); }
+__device__ __forceinline__ uint2 to_e4m3(const float (&v)[8]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        w[j] = __nv_cvt_float2_to_fp8x2(make_float2(v[2 * j], v[2 * j + 1]), __NV_SATFINITE, __NV_E4M3);
+    return make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
+}
+__device__ __forceinline__ uint8_t byte_of(uint2 c, int j) { return (j < 4 ? c.x : c.y) >> (8 * (j & 3)) & 255u; }
 
 // Largest magnitude of the warp's values as fp32 bits: as unsigned integers NaN > infinity > numbers.
 __device__ __forceinline__ float warp_absmax(const float (&v)[8]) {
@@ -104,18 +120,25 @@ __device__ __forceinline__ void step_block(const Entry& t, long long block, cons
         uint8_t* mp = static_cast<uint8_t*>(t.m);
         uint8_t* vp = static_cast<uint8_t*>(t.v);
         const float ms = t.ms[block], vs = t.vs[block];
-        uint8_t mc[8], vc[8];
+        uint2 mc, vc;
         if constexpr (VEC) {
-            *reinterpret_cast<uint2*>(mc) = __ldcs(reinterpret_cast<const uint2*>(mp) + i8);
-            *reinterpret_cast<uint2*>(vc) = __ldcs(reinterpret_cast<const uint2*>(vp) + i8);
+            mc = __ldcs(reinterpret_cast<const uint2*>(mp) + i8);
+            vc = __ldcs(reinterpret_cast<const uint2*>(vp) + i8);
         } else {
+            mc = vc = make_uint2(0, 0);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) mc[j] = in(j) ? mp[at(j)] : 0, vc[j] = in(j) ? vp[at(j)] : 0;
+            for (int j = 0; j < 8; ++j)
+                if (in(j)) {
+                    (j < 4 ? mc.x : mc.y) |= static_cast<uint32_t>(mp[at(j)]) << (8 * (j & 3));
+                    (j < 4 ? vc.x : vc.y) |= static_cast<uint32_t>(vp[at(j)]) << (8 * (j & 3));
+                }
         }
+        from_e4m3(mc, m);
+        from_e4m3(vc, r);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            m[j] = mul(from_e4m3(mc[j]), ms);
-            const float root = mul(from_e4m3(vc[j]), vs);
+            m[j] = mul(m[j], ms);
+            const float root = mul(r[j], vs);
             r[j] = mul(root, root);
         }
     } else {
@@ -137,7 +160,7 @@ __device__ __forceinline__ void step_block(const Entry& t, long long block, cons
         m[j] = add(mul(m[j], h.b1), mul(gj, h.c1));
         v[j] = add(mul(r[j], h.b2), mul(mul(gj, h.c2), gj));
         r[j] = __fsqrt_rn(v[j]);
-        const float up = __fdiv_rn(mul(m[j], h.step), add(mul(r[j], h.inv_root), h.eps));
+        const float up = __fdividef(mul(m[j], h.step), add(mul(r[j], h.inv_root), h.eps));
         p[j] = __fsub_rn(mul(p[j], h.decay), up);
     }
     __nv_bfloat16* copy = static_cast<__nv_bfloat16*>(t.copy);
@@ -161,23 +184,24 @@ __device__ __forceinline__ void step_block(const Entry& t, long long block, cons
         const bool msome = !(mmax < 0x1p-100f), rsome = !(rmax < 0x1p-100f);
         const float ms = msome ? mul(mmax, 1.0f / 448.0f) : 1.0f, rs = rsome ? mul(rmax, 1.0f / 448.0f) : 1.0f;
         const float mi = msome ? __frcp_rn(ms) : 0.0f, ri = rsome ? __frcp_rn(rs) : 0.0f;
-        uint8_t mc[8], vc[8];
+        float qm[8], qr[8];
+        const float least = rsome ? 0x1p-9f : 0.0f;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            mc[j] = to_e4m3(mul(m[j], mi));
-            float q = mul(r[j], ri);
-            if (r[j] > 0.0f && rsome && q < 0x1p-9f) q = 0x1p-9f;
-            vc[j] = to_e4m3(q);
+            qm[j] = mul(m[j], mi);
+            const float q = mul(r[j], ri);
+            qr[j] = (r[j] > 0.0f && q < least) ? least : q;
         }
+        const uint2 mc = to_e4m3(qm), vc = to_e4m3(qr);
         uint8_t* mp = static_cast<uint8_t*>(t.m);
         uint8_t* vp = static_cast<uint8_t*>(t.v);
         if constexpr (VEC) {
-            reinterpret_cast<uint2*>(mp)[i8] = *reinterpret_cast<uint2*>(mc);
-            reinterpret_cast<uint2*>(vp)[i8] = *reinterpret_cast<uint2*>(vc);
+            reinterpret_cast<uint2*>(mp)[i8] = mc;
+            reinterpret_cast<uint2*>(vp)[i8] = vc;
         } else {
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-                if (in(j)) mp[at(j)] = mc[j], vp[at(j)] = vc[j];
+                if (in(j)) mp[at(j)] = byte_of(mc, j), vp[at(j)] = byte_of(vc, j);
         }
         if (lane == 0) t.ms[block] = ms, t.vs[block] = rs;
     } else {
@@ -231,12 +255,16 @@ adamw_kernel(const __grid_constant__ Table<CAP> tab, const __grid_constant__ Hyp
             if (tab.e[mid].first <= c) lo = mid; else hi = mid;
         }
         const Entry& t = tab.e[lo];
-        const long long block = static_cast<long long>(c - t.first) * (kChunk / kBlock) + warp;
-        if (block * kBlock >= t.n) continue;
-        if (t.vec && (block + 1) * kBlock <= t.n)
-            step_block<P, G, EIGHT, true>(t, block, h, factor);
-        else
-            step_block<P, G, EIGHT, false>(t, block, h, factor);
+        const long long first = static_cast<long long>(c - t.first) * (kChunk / kBlock) + warp;
+#pragma unroll 1
+        for (int k = 0; k < kWarpBlocks; ++k) {
+            const long long block = first + 8 * k;
+            if (block * kBlock >= t.n) break;
+            if (t.vec && (block + 1) * kBlock <= t.n)
+                step_block<P, G, EIGHT, true>(t, block, h, factor);
+            else
+                step_block<P, G, EIGHT, false>(t, block, h, factor);
+        }
     }
 }
 

@@ -15,10 +15,17 @@
 // h, n, dn, dh bf16.  Without h: y = x.  Without w_pre: no n.  y is not kept for the backward pass: it
 // is recomputed, in fp32, from x and h, which must be read anyway.
 //
-// One pass over memory each way: a row lives in the registers of one thread block (VPT vectors of eight
-// per thread).  The backward pass keeps the column sums A, dres and dw_pre of all rows that a block
-// visits in registers, writes them once per block, and a second kernel adds the blocks in a fixed order:
-// no atomics, the same result on every run.
+// One pass over memory each way; bound by it.  A thread block works through its rows (persistent, every
+// gridDim-th row) with the next rows on their way into shared memory (cp.async): a thread copies just
+// the vectors that it will use, so the ring of rows needs no barrier.  The row sums need one barrier per
+// row: the sum over h of row k + 1, which that row starts with, is taken in the same reduction as the
+// last sum of row k (forward: one reduction per row, backward: two).  Rows too wide for two of them in
+// shared memory (d > 8192) take the plain kernels, which hold one row in registers.
+//
+// The backward pass keeps the column sums A, dres and dw_pre of all rows that a block visits in
+// registers, writes them once per block, and a second kernel adds the blocks in a fixed order: no
+// atomics, the same result on every run.
+#include "tcgen05.cuh"
 #include "train_util.cuh"
 
 namespace moe {
@@ -41,10 +48,348 @@ __device__ __forceinline__ void block_sum(float (&v)[N], float (*red)[N], int wa
     for (int k = 0; k < N; ++k) v[k] = warp_sum(lane < warps ? red[lane][k] : 0.0f);
 }
 
+// The same with both barrier-free cases: one warp, and the caller's buffers alternating between calls.
+template <int N>
+__device__ __forceinline__ void team_sum(float (&v)[N], float (*red)[N], int warps) {
+    if (warps == 1) {
+#pragma unroll
+        for (int k = 0; k < N; ++k) v[k] = warp_sum(v[k]);
+    } else {
+        block_sum<N>(v, red, warps);
+    }
+}
+
+// 16-byte words of eight values of X.
+template <typename X>
+constexpr int words() { return sizeof(X) == 4 ? 2 : 1; }
+
+// A thread's part of the ring of rows in shared memory: word w of stage s at (s * words + w) * threads.
+struct Ring {
+    uint4* base;  // this thread's first word
+    int per_stage, threads;
+    __device__ __forceinline__ uint4* at(int s, int w) const { return base + (s * per_stage + w) * threads; }
+};
+__device__ __forceinline__ void fetch8(const Ring& r, int s, int w, const __nv_bfloat16* p, size_t i) {
+    ptx::cp_async_16(ptx::smem_u32(r.at(s, w)), reinterpret_cast<const uint4*>(p) + i, 16);
+}
+__device__ __forceinline__ void fetch8(const Ring& r, int s, int w, const float* p, size_t i) {
+    ptx::cp_async_16_l1(ptx::smem_u32(r.at(s, w)), reinterpret_cast<const uint4*>(p) + 2 * i);
+    ptx::cp_async_16_l1(ptx::smem_u32(r.at(s, w + 1)), reinterpret_cast<const uint4*>(p) + 2 * i + 1);
+}
+template <typename X>
+__device__ __forceinline__ Vec8 ring8(const Ring& r, int s, int w) {
+    const uint4 a = *r.at(s, w);
+    if constexpr (sizeof(X) == 2) {
+        return unpack8(a);
+    } else {
+        const uint4 b = *r.at(s, w + 1);
+        return Vec8{{__uint_as_float(a.x), __uint_as_float(a.y), __uint_as_float(a.z), __uint_as_float(a.w),
+                     __uint_as_float(b.x), __uint_as_float(b.y), __uint_as_float(b.z), __uint_as_float(b.w)}};
+    }
+}
+// All but the newest `pending` rows have landed (pending = stages - 2).
+__device__ __forceinline__ void wait_rows(int pending) {
+    if (pending == 2) ptx::cp_async_wait<2>();
+    else if (pending == 1) ptx::cp_async_wait<1>();
+    else ptx::cp_async_wait<0>();
+}
+
 __device__ __forceinline__ Vec8 ones() { return Vec8{{1, 1, 1, 1, 1, 1, 1, 1}}; }
 
-// Threads of a block by its vectors per thread (row_shape).
-constexpr int max_threads(int vpt) { return vpt == 1 ? 256 : vpt == 8 ? 1024 : 512; }
+template <typename X, int VPT>
+__global__ void __launch_bounds__(VPT == 1 ? 256 : 512, VPT == 1 ? 4 : 1)
+norm_rows_kernel(const X* __restrict__ x, const __nv_bfloat16* __restrict__ h, const float* __restrict__ w_pre,
+                 const float* __restrict__ w_post, const float* __restrict__ gate, const float* __restrict__ tgate,
+                 const float* __restrict__ res, int T, int d, float eps, int stages, X* __restrict__ y,
+                 __nv_bfloat16* __restrict__ n) {
+    extern __shared__ uint4 ring_smem[];
+    __shared__ float red[2][kMaxWarps][2];
+    constexpr int XW = words<X>();
+    const int tid = threadIdx.x, nt = blockDim.x, d8 = d / 8, warps = nt >> 5;
+    const float inv_d = 1.0f / static_cast<float>(d);
+    const int per_vec = XW + (h ? 1 : 0);
+    const Ring ring{ring_smem + tid, VPT * per_vec, nt};
+    const int rows = (T - static_cast<int>(blockIdx.x) + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x);
+    pdl_wait();
+    pdl_trigger();
+    auto row_of = [&](int k) { return static_cast<size_t>(blockIdx.x) + static_cast<size_t>(k) * gridDim.x; };
+    auto fetch = [&](int k, int s) {
+        if (k < rows) {
+            const size_t base = row_of(k) * d8;
+#pragma unroll
+            for (int v = 0; v < VPT; ++v) {
+                const int c = tid + v * nt;
+                if (c < d8) {
+                    fetch8(ring, s, v * per_vec, x, base + c);
+                    if (h) fetch8(ring, s, v * per_vec + XW, h, base + c);
+                }
+            }
+        }
+        ptx::cp_async_commit();
+    };
+    for (int k = 0; k < stages - 1; ++k) fetch(k, k);
+    Vec8 wn[VPT], wg[VPT], rs[VPT];  // w_pre, gate w_post, res
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) {
+        const int c = tid + v * nt;
+        wn[v] = wg[v] = rs[v] = ones();
+        if (c < d8) {
+            if (w_pre) wn[v] = load8_cached(w_pre, c);
+            if (h) wg[v] = load8_cached(w_post, c);
+            if (gate) {
+                const Vec8 g = load8_cached(gate, c);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) wg[v].v[j] *= g.v[j];
+            }
+            if (res) rs[v] = load8_cached(res, c);
+        }
+    }
+    auto sum_h = [&](int s) {
+        float a = 0.0f;
+#pragma unroll
+        for (int v = 0; v < VPT; ++v)
+            if (tid + v * nt < d8) {
+                const Vec8 hv = ring8<__nv_bfloat16>(ring, s, v * per_vec + XW);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) a += hv.v[j] * hv.v[j];
+            }
+        return a;
+    };
+    float sums[2] = {0.0f, 0.0f};  // of y^2 in this row, of h^2 in the next
+    if (h) {
+        wait_rows(stages - 2);
+        sums[1] = sum_h(0);
+        team_sum<2>(sums, red[1], warps);
+    }
+    int s = 0;
+    for (int k = 0; k < rows; ++k) {
+        const int free_stage = s == 0 ? stages - 1 : s - 1, next = s + 1 == stages ? 0 : s + 1;
+        fetch(k + stages - 1, free_stage);
+        wait_rows(stages - 2);
+        const size_t t = row_of(k), base = t * d8;
+        const float scale = h ? rsqrtf(sums[1] * inv_d + eps) * (tgate ? __ldg(tgate + t) : 1.0f) : 0.0f;
+        Vec8 yv[VPT];
+        sums[0] = sums[1] = 0.0f;
+#pragma unroll
+        for (int v = 0; v < VPT; ++v) {
+            const int c = tid + v * nt;
+            if (c < d8) {
+                yv[v] = ring8<X>(ring, s, v * per_vec);
+                if (h) {
+                    const Vec8 hv = ring8<__nv_bfloat16>(ring, s, v * per_vec + XW);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        yv[v].v[j] = rs[v].v[j] * yv[v].v[j] + wg[v].v[j] * (hv.v[j] * scale);
+                    if (y) store8(y, base + c, yv[v]);
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j) sums[0] += yv[v].v[j] * yv[v].v[j];
+            }
+        }
+        if (h && k + 1 < rows) sums[1] = sum_h(next);
+        team_sum<2>(sums, red[k & 1], warps);
+        if (n) {
+            const float ry = rsqrtf(sums[0] * inv_d + eps);
+#pragma unroll
+            for (int v = 0; v < VPT; ++v) {
+                const int c = tid + v * nt;
+                if (c < d8) {
+                    Vec8 o;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) o.v[j] = wn[v].v[j] * (yv[v].v[j] * ry);
+                    store8(n, base + c, o);
+                }
+            }
+        }
+        s = next;
+    }
+    ptx::cp_async_wait_all();
+}
+
+// Column sums of a block go to partial[blockIdx][3][d]: A, dres, dw_pre.
+template <typename X, int VPT>
+__global__ void __launch_bounds__(512, 1)
+norm_rows_backward_kernel(const X* __restrict__ x, const __nv_bfloat16* __restrict__ h, const X* __restrict__ dy,
+                          const __nv_bfloat16* __restrict__ dn, const float* __restrict__ w_pre,
+                          const float* __restrict__ w_post, const float* __restrict__ gate,
+                          const float* __restrict__ tgate, const float* __restrict__ res, int T, int d, float eps,
+                          int stages, X* __restrict__ dx, __nv_bfloat16* __restrict__ dh, float* __restrict__ dtgate,
+                          float* __restrict__ partial) {
+    extern __shared__ uint4 ring_smem[];
+    __shared__ float red1[2][kMaxWarps][2], red2[2][kMaxWarps][2];
+    constexpr int XW = words<X>();
+    using B = __nv_bfloat16;
+    const int tid = threadIdx.x, nt = blockDim.x, d8 = d / 8, warps = nt >> 5;
+    const float inv_d = 1.0f / static_cast<float>(d);
+    // Words of a vector: x, then dy, h, dn as given.
+    const int o_dy = XW, o_h = o_dy + (dy ? XW : 0), o_dn = o_h + (h ? 1 : 0), per_vec = o_dn + (dn ? 1 : 0);
+    const Ring ring{ring_smem + tid, VPT * per_vec, nt};
+    const int rows = (T - static_cast<int>(blockIdx.x) + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x);
+    pdl_wait();
+    pdl_trigger();
+    auto row_of = [&](int k) { return static_cast<size_t>(blockIdx.x) + static_cast<size_t>(k) * gridDim.x; };
+    auto fetch = [&](int k, int s) {
+        if (k < rows) {
+            const size_t base = row_of(k) * d8;
+#pragma unroll
+            for (int v = 0; v < VPT; ++v) {
+                const int c = tid + v * nt;
+                if (c < d8) {
+                    fetch8(ring, s, v * per_vec, x, base + c);
+                    if (dy) fetch8(ring, s, v * per_vec + o_dy, dy, base + c);
+                    if (h) fetch8(ring, s, v * per_vec + o_h, h, base + c);
+                    if (dn) fetch8(ring, s, v * per_vec + o_dn, dn, base + c);
+                }
+            }
+        }
+        ptx::cp_async_commit();
+    };
+    for (int k = 0; k < stages - 1; ++k) fetch(k, k);
+    // One vector per thread: the weights stay in registers.  Two: they are read again (L1) where used,
+    // the column sums take the registers.
+    Vec8 kn[VPT], kg[VPT], kr[VPT];
+    auto load_weights = [&](int c, Vec8& n_, Vec8& g_, Vec8& r_) {
+        n_ = w_pre ? load8_cached(w_pre, c) : ones();
+        g_ = h ? load8_cached(w_post, c) : ones();
+        if (gate) {
+            const Vec8 g = load8_cached(gate, c);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) g_.v[j] *= g.v[j];
+        }
+        r_ = res ? load8_cached(res, c) : ones();
+    };
+    if (VPT == 1 && tid < d8) load_weights(tid, kn[0], kg[0], kr[0]);
+    Vec8 sA[VPT], sR[VPT], sP[VPT];
+#pragma unroll
+    for (int v = 0; v < VPT; ++v)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sA[v].v[j] = sR[v].v[j] = sP[v].v[j] = 0.0f;
+    auto sum_h = [&](int s) {
+        float a = 0.0f;
+#pragma unroll
+        for (int v = 0; v < VPT; ++v)
+            if (tid + v * nt < d8) {
+                const Vec8 hv = ring8<B>(ring, s, v * per_vec + o_h);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) a += hv.v[j] * hv.v[j];
+            }
+        return a;
+    };
+    float s2[2] = {0.0f, 0.0f};  // S of this row, sum of h^2 in the next
+    if (h) {
+        wait_rows(stages - 2);
+        s2[1] = sum_h(0);
+        team_sum<2>(s2, red2[1], warps);
+    }
+    int s = 0;
+    for (int k = 0; k < rows; ++k) {
+        const int free_stage = s == 0 ? stages - 1 : s - 1, next = s + 1 == stages ? 0 : s + 1;
+        fetch(k + stages - 1, free_stage);
+        wait_rows(stages - 2);
+        const size_t t = row_of(k), base = t * d8;
+        const float tg = tgate ? __ldg(tgate + t) : 1.0f;
+        const float rh = h ? rsqrtf(s2[1] * inv_d + eps) : 0.0f;
+        const float hs = rh * tg;
+        float ry = 0.0f, mean = 0.0f;
+        if (dn) {
+            float s1[2] = {0.0f, 0.0f};  // sum of y^2, sum of dn w_pre y
+#pragma unroll
+            for (int v = 0; v < VPT; ++v) {
+                const int c = tid + v * nt;
+                if (c < d8) {
+                    Vec8 wn, wg, rs;
+                    if (VPT == 1) wn = kn[0], wg = kg[0], rs = kr[0];
+                    else load_weights(c, wn, wg, rs);
+                    const Vec8 xv = ring8<X>(ring, s, v * per_vec), nv = ring8<B>(ring, s, v * per_vec + o_dn);
+                    Vec8 hv{};
+                    if (h) hv = ring8<B>(ring, s, v * per_vec + o_h);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const float a = h ? rs.v[j] * xv.v[j] + wg.v[j] * (hv.v[j] * hs) : xv.v[j];
+                        s1[0] += a * a;
+                        s1[1] += nv.v[j] * wn.v[j] * a;
+                    }
+                }
+            }
+            team_sum<2>(s1, red1[k & 1], warps);
+            ry = rsqrtf(s1[0] * inv_d + eps);
+            mean = s1[1] * ry * inv_d;
+        }
+        Vec8 q[VPT];
+        s2[0] = s2[1] = 0.0f;
+#pragma unroll
+        for (int v = 0; v < VPT; ++v) {
+            const int c = tid + v * nt;
+            if (c < d8) {
+                Vec8 wn, wg, rs;
+                if (VPT == 1) wn = kn[0], wg = kg[0], rs = kr[0];
+                else load_weights(c, wn, wg, rs);
+                const Vec8 xv = ring8<X>(ring, s, v * per_vec);
+                Vec8 D{}, hv{}, o;
+                if (dy) D = ring8<X>(ring, s, v * per_vec + o_dy);
+                if (h) hv = ring8<B>(ring, s, v * per_vec + o_h);
+                if (dn) {
+                    const Vec8 nv = ring8<B>(ring, s, v * per_vec + o_dn);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const float a = h ? rs.v[j] * xv.v[j] + wg.v[j] * (hv.v[j] * hs) : xv.v[j];
+                        const float yh = a * ry;
+                        sP[v].v[j] += nv.v[j] * yh;
+                        D.v[j] += ry * (nv.v[j] * wn.v[j] - yh * mean);
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    o.v[j] = rs.v[j] * D.v[j];
+                    sR[v].v[j] += D.v[j] * xv.v[j];
+                }
+                store8(dx, base + c, o);
+                if (h) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        sA[v].v[j] += D.v[j] * (hv.v[j] * hs);
+                        q[v].v[j] = D.v[j] * wg.v[j];
+                        s2[0] += q[v].v[j] * hv.v[j];
+                    }
+                }
+            }
+        }
+        if (h) {
+            if (k + 1 < rows) s2[1] = sum_h(next);
+            team_sum<2>(s2, red2[k & 1], warps);
+            const float qmean = s2[0] * rh * inv_d;  // mean of q hh
+            if (dtgate && tid == 0) dtgate[t] = s2[0] * rh;
+#pragma unroll
+            for (int v = 0; v < VPT; ++v) {
+                const int c = tid + v * nt;
+                if (c < d8) {
+                    const Vec8 hv = ring8<B>(ring, s, v * per_vec + o_h);
+                    Vec8 o;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) o.v[j] = hs * (q[v].v[j] - hv.v[j] * rh * qmean);
+                    store8(dh, base + c, o);
+                }
+            }
+        }
+        s = next;
+    }
+    ptx::cp_async_wait_all();
+    float* p = partial + static_cast<size_t>(blockIdx.x) * 3 * d;
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) {
+        const int c = tid + v * nt;
+        if (c < d8) {
+            store8(p, c, sA[v]);
+            store8(p + d, c, sR[v]);
+            store8(p + 2 * static_cast<size_t>(d), c, sP[v]);
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------------------------
+// Wide rows (d > 8192): one row at a time in registers (or the compiler's spills of them).
+// ---------------------------------------------------------------------------------------------
+constexpr int max_threads(int vpt) { return vpt == 8 ? 1024 : 512; }
 
 template <typename X, int VPT>
 __global__ void __launch_bounds__(max_threads(VPT))
@@ -121,7 +466,6 @@ block_norm_kernel(const X* __restrict__ x, const __nv_bfloat16* __restrict__ h,
     }
 }
 
-// Column sums of a block go to partial[blockIdx][3][d]: A, dres, dw_pre.
 template <typename X, int VPT>
 __global__ void __launch_bounds__(max_threads(VPT))
 block_norm_backward_kernel(const X* __restrict__ x, const __nv_bfloat16* __restrict__ h,
@@ -293,53 +637,109 @@ block_norm_join_kernel(const float* __restrict__ partial, int blocks, int d, con
     }
 }
 
-// Vectors of eight per thread, and threads (a multiple of 32, at most max_threads).
-void row_shape(int d, int* vpt, int* threads) {
-    const int d8 = d / 8;
-    *vpt = d8 <= 256 ? 1 : d8 <= 1024 ? 2 : d8 <= 2048 ? 4 : 8;
-    *threads = ((d8 + *vpt - 1) / *vpt + 31) / 32 * 32;
+// How a pass is launched: vectors of eight per thread, threads (a multiple of 32), blocks per SM and rows
+// in the ring; stages = 0: the plain kernels.
+struct Shape {
+    int vpt, threads, per_sm, stages;
+    size_t smem;
+};
+Shape shape_of(const BlockNormArgs& a, bool bwd) {
+    const int d8 = a.d / 8;
+    Shape s{};
+    if (a.d > 8192) {
+        s.vpt = d8 <= 2048 ? 4 : 8;
+        s.threads = ((d8 + s.vpt - 1) / s.vpt + 31) / 32 * 32;
+        s.per_sm = bwd ? 2 : 16;
+        return s;
+    }
+    // Forward: up to 256 threads of one vector or 512 of two, 1024 threads per SM.  Backward: one vector
+    // up to 512 threads, with up to 128 registers a thread 512 threads per SM.
+    s.vpt = d8 <= (bwd ? 512 : 256) ? 1 : 2;
+    s.threads = ((d8 + s.vpt - 1) / s.vpt + 31) / 32 * 32;
+    s.per_sm = bwd ? (s.threads <= 128 ? 4 : s.threads <= 256 ? 2 : 1)
+                   : (s.vpt == 2 ? (s.threads <= 256 ? 2 : 1) : s.threads <= 64 ? 16 : 1024 / s.threads);
+    const int xw = a.x_fp32 ? 2 : 1;
+    const int words = bwd ? xw * (a.dy ? 2 : 1) + (a.h ? 1 : 0) + (a.dn ? 1 : 0) : xw + (a.h ? 1 : 0);
+    const size_t row = static_cast<size_t>(words) * s.vpt * s.threads * 16;
+    const size_t fit = 200 * 1024 / (row * s.per_sm);
+    s.stages = fit >= 4 ? 4 : fit >= 3 ? 3 : 2;
+    s.smem = row * s.stages;
+    return s;
+}
+
+template <typename... KArgs>
+cudaError_t allow_smem(void (*kernel)(KArgs...), bool* done) {
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (dev < 64 && done[dev]) return cudaSuccess;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024);
+    if (e == cudaSuccess && dev < 64) done[dev] = true;
+    return e;
 }
 
 template <typename X, int VPT>
-cudaError_t forward(const BlockNormArgs& a, int threads, int num_sms, cudaStream_t s) {
-    const int most = num_sms * 16;
-    return launch_k(kPdlTrain, block_norm_kernel<X, VPT>, dim3(a.T < most ? a.T : most), dim3(threads), 0, s,
+cudaError_t forward_rows(const BlockNormArgs& a, const Shape& s, int grid, cudaStream_t st) {
+    static bool done[64] = {};
+    const cudaError_t e = allow_smem(norm_rows_kernel<X, VPT>, done);
+    if (e != cudaSuccess) return e;
+    return launch_k(kPdlTrain, norm_rows_kernel<X, VPT>, dim3(grid), dim3(s.threads), s.smem, st,
+                    static_cast<const X*>(a.x), a.h, a.w_pre, a.w_post, a.gate, a.tgate, a.res, a.T, a.d, a.eps,
+                    s.stages, static_cast<X*>(a.y), a.n);
+}
+template <typename X, int VPT>
+cudaError_t forward_wide(const BlockNormArgs& a, const Shape& s, int grid, cudaStream_t st) {
+    return launch_k(kPdlTrain, block_norm_kernel<X, VPT>, dim3(grid), dim3(s.threads), 0, st,
                     static_cast<const X*>(a.x), a.h, a.w_pre, a.w_post, a.gate, a.tgate, a.res, a.T, a.d, a.eps,
                     static_cast<X*>(a.y), a.n);
 }
 template <typename X, int VPT>
-cudaError_t backward(const BlockNormArgs& a, int threads, cudaStream_t s) {
-    cudaError_t e = launch_k(kPdlTrain, block_norm_backward_kernel<X, VPT>, dim3(block_norm_blocks(a.T)), dim3(threads),
-                             0, s, static_cast<const X*>(a.x), a.h, static_cast<const X*>(a.dy), a.dn, a.w_pre,
-                             a.w_post, a.gate, a.tgate, a.res, a.T, a.d, a.eps, static_cast<X*>(a.dx), a.dh, a.dtgate,
-                             a.partial);
+cudaError_t backward_rows(const BlockNormArgs& a, const Shape& s, int grid, cudaStream_t st) {
+    static bool done[64] = {};
+    const cudaError_t e = allow_smem(norm_rows_backward_kernel<X, VPT>, done);
+    if (e != cudaSuccess) return e;
+    return launch_k(kPdlTrain, norm_rows_backward_kernel<X, VPT>, dim3(grid), dim3(s.threads), s.smem, st,
+                    static_cast<const X*>(a.x), a.h, static_cast<const X*>(a.dy), a.dn, a.w_pre, a.w_post, a.gate,
+                    a.tgate, a.res, a.T, a.d, a.eps, s.stages, static_cast<X*>(a.dx), a.dh, a.dtgate, a.partial);
+}
+template <typename X, int VPT>
+cudaError_t backward_wide(const BlockNormArgs& a, const Shape& s, int grid, cudaStream_t st) {
+    return launch_k(kPdlTrain, block_norm_backward_kernel<X, VPT>, dim3(grid), dim3(s.threads), 0, st,
+                    static_cast<const X*>(a.x), a.h, static_cast<const X*>(a.dy), a.dn, a.w_pre, a.w_post, a.gate,
+                    a.tgate, a.res, a.T, a.d, a.eps, static_cast<X*>(a.dx), a.dh, a.dtgate, a.partial);
+}
+
+template <typename X>
+cudaError_t launch_x(const BlockNormArgs& a, bool bwd, int num_sms, cudaStream_t st) {
+    const Shape s = shape_of(a, bwd);
+    const int most = bwd ? block_norm_blocks(a.T, a.d) : num_sms * s.per_sm, grid = a.T < most ? a.T : most;
+    if (!bwd) {
+        if (s.vpt == 1) return forward_rows<X, 1>(a, s, grid, st);
+        if (s.vpt == 2) return forward_rows<X, 2>(a, s, grid, st);
+        return s.vpt == 4 ? forward_wide<X, 4>(a, s, grid, st) : forward_wide<X, 8>(a, s, grid, st);
+    }
+    const cudaError_t e = s.vpt == 1   ? backward_rows<X, 1>(a, s, grid, st)
+                          : s.vpt == 2 ? backward_rows<X, 2>(a, s, grid, st)
+                          : s.vpt == 4 ? backward_wide<X, 4>(a, s, grid, st)
+                                       : backward_wide<X, 8>(a, s, grid, st);
     if (e != cudaSuccess || !(a.dw_pre || a.dw_post || a.dgate || a.dres)) return e;
-    return launch_k(kPdlTrain, block_norm_join_kernel, dim3((3 * a.d + 31) / 32), dim3(512), 0, s,
-                    static_cast<const float*>(a.partial), block_norm_blocks(a.T), a.d, a.w_post, a.gate, a.dw_pre,
-                    a.dw_post, a.dgate, a.dres);
+    return launch_k(kPdlTrain, block_norm_join_kernel, dim3((3 * a.d + 31) / 32), dim3(512), 0, st,
+                    static_cast<const float*>(a.partial), grid, a.d, a.w_post, a.gate, a.dw_pre, a.dw_post, a.dgate,
+                    a.dres);
 }
 
 }  // namespace
 
-// Blocks of the backward pass: two for each of the 152 SMs, or one per row.
-int block_norm_blocks(int T) { return T < 304 ? T : 304; }
+// Blocks of the backward pass on GB300's 152 SMs (the workspace depends on the shape alone).
+int block_norm_blocks(int T, int d) {
+    BlockNormArgs a{};
+    a.d = d;
+    const int most = 152 * shape_of(a, true).per_sm;
+    return T < most ? T : most;
+}
 
 cudaError_t launch_block_norm(const BlockNormArgs& a, bool backward_pass, int num_sms, cudaStream_t s) {
-    int vpt, threads;
-    row_shape(a.d, &vpt, &threads);
-#define MOE_NORM_CASE(V)                                                                            \
-    if (vpt == V) {                                                                                 \
-        if (backward_pass)                                                                          \
-            return a.x_fp32 ? backward<float, V>(a, threads, s) : backward<__nv_bfloat16, V>(a, threads, s); \
-        return a.x_fp32 ? forward<float, V>(a, threads, num_sms, s)                                 \
-                        : forward<__nv_bfloat16, V>(a, threads, num_sms, s);                        \
-    }
-    MOE_NORM_CASE(1)
-    MOE_NORM_CASE(2)
-    MOE_NORM_CASE(4)
-    MOE_NORM_CASE(8)
-#undef MOE_NORM_CASE
-    return cudaErrorInvalidValue;
+    return a.x_fp32 ? launch_x<float>(a, backward_pass, num_sms, s)
+                    : launch_x<__nv_bfloat16>(a, backward_pass, num_sms, s);
 }
 
 }  // namespace moe

@@ -243,9 +243,9 @@ struct BlockNormArgs {
     void* dx;
     __nv_bfloat16* dh;
     float *dw_pre, *dw_post, *dgate, *dtgate, *dres;
-    float* partial;     // [block_norm_blocks(T), 3, d]
+    float* partial;     // [block_norm_blocks(T, d), 3, d]
 };
-int block_norm_blocks(int T);
+int block_norm_blocks(int T, int d);
 cudaError_t launch_block_norm(const BlockNormArgs& a, bool backward_pass, int num_sms, cudaStream_t s);
 
 // AdamW (adamw.cu).  corr1 = 1 - beta1^t, corr2 = sqrt(1 - beta2^t).

@@ -61,6 +61,10 @@ __device__ __forceinline__ void cp_async_16(uint32_t dst_smem, const void* src, 
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst_smem), "l"(src), "r"(src_bytes)
                  : "memory");
 }
+// The same through L1 (for 16-byte pieces that do not cover whole 32-byte sectors by themselves).
+__device__ __forceinline__ void cp_async_16_l1(uint32_t dst_smem, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(dst_smem), "l"(src) : "memory");
+}
 // The same with an L2 cache-eviction policy for the source line (policy from createpolicy).
 __device__ __forceinline__ void cp_async_16_hint(uint32_t dst_smem, const void* src, uint32_t src_bytes,
                                                  uint64_t policy) {

@@ -167,7 +167,7 @@ int moe_block_norm(const void* x, int x_fp32, const void* h, const float* w_pre,
 
 size_t moe_block_norm_backward_workspace_size(int T, int d) {
     if (check_rows("moe_block_norm_backward_workspace_size", T, "T", d, "d") != MOE_OK) return 0;
-    return sizeof(float) * 3 * static_cast<size_t>(d) * block_norm_blocks(T);
+    return sizeof(float) * 3 * static_cast<size_t>(d) * block_norm_blocks(T, d);
 }
 
 int moe_block_norm_backward(const void* x, int x_fp32, const void* h, const void* dy, const void* dn,

@@ -29,7 +29,17 @@ __device__ __forceinline__ uint4 pack8(const Vec8& a) {
 __device__ __forceinline__ Vec8 load8(const __nv_bfloat16* p, size_t i) {
     return unpack8(__ldcs(reinterpret_cast<const uint4*>(p) + i));
 }
+// Eight fp32 values are one 32-byte word where the array is aligned for it (a branch that is the same for
+// all threads): two 16-byte words touch every 32-byte sector twice.
 __device__ __forceinline__ Vec8 load8(const float* p, size_t i) {
+    if ((reinterpret_cast<uintptr_t>(p) & 31u) == 0) {
+        Vec8 r;
+        asm volatile("ld.global.L1::no_allocate.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=f"(r.v[0]), "=f"(r.v[1]), "=f"(r.v[2]), "=f"(r.v[3]), "=f"(r.v[4]), "=f"(r.v[5]),
+                       "=f"(r.v[6]), "=f"(r.v[7])
+                     : "l"(p + 8 * i));
+        return r;
+    }
     const float4 a = __ldcs(reinterpret_cast<const float4*>(p) + 2 * i);
     const float4 b = __ldcs(reinterpret_cast<const float4*>(p) + 2 * i + 1);
     return Vec8{{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}};
@@ -44,6 +54,12 @@ __device__ __forceinline__ void store8(__nv_bfloat16* p, size_t i, const Vec8& a
     reinterpret_cast<uint4*>(p)[i] = pack8(a);
 }
 __device__ __forceinline__ void store8(float* p, size_t i, const Vec8& a) {
+    if ((reinterpret_cast<uintptr_t>(p) & 31u) == 0) {
+        asm volatile("st.global.v8.f32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};" ::"f"(a.v[0]), "f"(a.v[1]),
+                     "f"(a.v[2]), "f"(a.v[3]), "f"(a.v[4]), "f"(a.v[5]), "f"(a.v[6]), "f"(a.v[7]), "l"(p + 8 * i)
+                     : "memory");
+        return;
+    }
     float4* q = reinterpret_cast<float4*>(p) + 2 * i;
     q[0] = make_float4(a.v[0], a.v[1], a.v[2], a.v[3]);
     q[1] = make_float4(a.v[4], a.v[5], a.v[6], a.v[7]);

@@ -18,8 +18,10 @@
 //
 // Bound by memory: 22 to 30 bytes per element (32-bit moments, fp32 parameter) or 10 to 16 (8-bit).  A
 // warp handles one block of 256 elements, eight per lane in 16-byte words where the tensor's pieces are
-// aligned for it, else element by element; chunks of 8192 elements are dealt to the thread blocks over
-// all tensors (the search for a chunk's tensor then costs little per element).  The table of tensors travels in the kernel's parameters (up to 32 KB): nothing is copied
+// aligned for it, else element by element; chunks of 2048 elements over all tensors are dealt to the thread
+// blocks in turn (neighbouring chunks run at the same time: contiguous runs of chunks measured 7 % slower,
+// 420 against 390 us for 75 M elements with 32-bit moments); a thread block walks on in the table from its
+// last chunk's tensor.  The table of tensors travels in the kernel's parameters (up to 32 KB): nothing is copied
 // to the device before the launch and no memory is held.
 #include <cuda_fp8.h>
 
@@ -29,8 +31,9 @@ namespace moe {
 namespace {
 
 constexpr int kBlock = 256;               // elements per scale
-constexpr int kWarpBlocks = 4;            // blocks of 256 that a warp takes from a chunk
-constexpr int kChunk = 8 * kWarpBlocks * kBlock;  // elements that a thread block takes at a time
+constexpr int kChunk = 8 * kBlock;        // elements of a thread block's step, one block per warp
+constexpr unsigned kPerSm = 5;            // resident thread blocks per SM (48 registers a thread)
+constexpr unsigned kGridPerSm = 80;       // launched ones: later ones even out what the first leave
 constexpr int kSmallTable = 48, kLargeTable = 400;
 
 struct Entry {
@@ -222,7 +225,7 @@ __device__ __forceinline__ void step_block(const Entry& t, long long block, cons
 }
 
 template <typename P, typename G, bool EIGHT, int CAP>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, kPerSm)
 adamw_kernel(const __grid_constant__ Table<CAP> tab, const __grid_constant__ Hyper given) {
     __shared__ Hyper sh;
     pdl_wait();
@@ -248,23 +251,24 @@ adamw_kernel(const __grid_constant__ Table<CAP> tab, const __grid_constant__ Hyp
         if (given.factors) factor = given.factors[0];
     }
     const int warp = threadIdx.x >> 5;
+    int i = 0;
+    for (int hi = tab.count; hi - i > 1;) {  // the first chunk's tensor: e[i].first <= chunk < e[hi].first
+        const int mid = (i + hi) >> 1;
+        if (tab.e[mid].first <= blockIdx.x) i = mid; else hi = mid;
+    }
+    unsigned next = i + 1 < tab.count ? tab.e[i + 1].first : tab.chunks;
     for (unsigned c = blockIdx.x; c < tab.chunks; c += gridDim.x) {
-        int lo = 0, hi = tab.count;  // e[lo].first <= c < e[hi].first
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (tab.e[mid].first <= c) lo = mid; else hi = mid;
+        while (c >= next) {
+            ++i;
+            next = i + 1 < tab.count ? tab.e[i + 1].first : tab.chunks;
         }
-        const Entry& t = tab.e[lo];
-        const long long first = static_cast<long long>(c - t.first) * (kChunk / kBlock) + warp;
-#pragma unroll 1
-        for (int k = 0; k < kWarpBlocks; ++k) {
-            const long long block = first + 8 * k;
-            if (block * kBlock >= t.n) break;
-            if (t.vec && (block + 1) * kBlock <= t.n)
-                step_block<P, G, EIGHT, true>(t, block, h, factor);
-            else
-                step_block<P, G, EIGHT, false>(t, block, h, factor);
-        }
+        const Entry& t = tab.e[i];
+        const long long block = static_cast<long long>(c - t.first) * (kChunk / kBlock) + warp;
+        if (block * kBlock >= t.n) continue;
+        if (t.vec && (block + 1) * kBlock <= t.n)
+            step_block<P, G, EIGHT, true>(t, block, h, factor);
+        else
+            step_block<P, G, EIGHT, false>(t, block, h, factor);
     }
 }
 
@@ -288,7 +292,7 @@ cudaError_t launch_table(const moe_adamw_tensor* ts, int count, const Hyper& h, 
     if (chunks >= (1ull << 31)) return cudaErrorInvalidValue;
     tab.count = k;
     tab.chunks = static_cast<unsigned>(chunks);
-    const unsigned most = num_sms * 16u;
+    const unsigned most = num_sms * kGridPerSm;
     return launch_k(kPdlTrain, adamw_kernel<P, G, EIGHT, CAP>, dim3(tab.chunks < most ? tab.chunks : most), dim3(256),
                     0, s, tab, h);
 }

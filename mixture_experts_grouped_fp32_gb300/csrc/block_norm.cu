@@ -48,15 +48,26 @@ __device__ __forceinline__ void block_sum(float (&v)[N], float (*red)[N], int wa
     for (int k = 0; k < N; ++k) v[k] = warp_sum(lane < warps ? red[lane][k] : 0.0f);
 }
 
-// The same with both barrier-free cases: one warp, and the caller's buffers alternating between calls.
-template <int N>
-__device__ __forceinline__ void team_sum(float (&v)[N], float (*red)[N], int warps) {
-    if (warps == 1) {
+// Two sums over the block (at most 16 warps), in every thread: a half-warp takes each after the first
+// exchange, so both cost the shuffles of one.  One barrier (none for a single warp); the caller's buffers
+// alternate between calls.
+__device__ __forceinline__ void pair_sum(float (&v)[2], float (*red)[16], int warps) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const bool up = lane & 16;
+    float a = up ? v[1] : v[0];
+    a += __shfl_xor_sync(0xffffffffu, up ? v[0] : v[1], 16);
 #pragma unroll
-        for (int k = 0; k < N; ++k) v[k] = warp_sum(v[k]);
-    } else {
-        block_sum<N>(v, red, warps);
+    for (int o = 8; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
+    if (warps > 1) {
+        if ((lane & 15) == 0) red[lane >> 4][warp] = a;
+        __syncthreads();
+        a = (lane & 15) < warps ? red[lane >> 4][lane & 15] : 0.0f;
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
     }
+    const float b = __shfl_xor_sync(0xffffffffu, a, 16);
+    v[0] = up ? b : a;
+    v[1] = up ? a : b;
 }
 
 // 16-byte words of eight values of X.
@@ -103,7 +114,7 @@ norm_rows_kernel(const X* __restrict__ x, const __nv_bfloat16* __restrict__ h, c
                  const float* __restrict__ res, int T, int d, float eps, int stages, X* __restrict__ y,
                  __nv_bfloat16* __restrict__ n) {
     extern __shared__ uint4 ring_smem[];
-    __shared__ float red[2][kMaxWarps][2];
+    __shared__ float red[2][2][16];
     constexpr int XW = words<X>();
     const int tid = threadIdx.x, nt = blockDim.x, d8 = d / 8, warps = nt >> 5;
     const float inv_d = 1.0f / static_cast<float>(d);
@@ -156,18 +167,20 @@ norm_rows_kernel(const X* __restrict__ x, const __nv_bfloat16* __restrict__ h, c
         return a;
     };
     float sums[2] = {0.0f, 0.0f};  // of y^2 in this row, of h^2 in the next
+    float tg = tgate ? __ldg(tgate + blockIdx.x) : 1.0f;
     if (h) {
         wait_rows(stages - 2);
         sums[1] = sum_h(0);
-        team_sum<2>(sums, red[1], warps);
+        pair_sum(sums, red[1], warps);
     }
+    else wait_rows(stages - 2);
     int s = 0;
     for (int k = 0; k < rows; ++k) {
         const int free_stage = s == 0 ? stages - 1 : s - 1, next = s + 1 == stages ? 0 : s + 1;
         fetch(k + stages - 1, free_stage);
-        wait_rows(stages - 2);
         const size_t t = row_of(k), base = t * d8;
-        const float scale = h ? rsqrtf(sums[1] * inv_d + eps) * (tgate ? __ldg(tgate + t) : 1.0f) : 0.0f;
+        const float scale = h ? rsqrtf(sums[1] * inv_d + eps) * tg : 0.0f;
+        if (tgate && k + 1 < rows) tg = __ldg(tgate + row_of(k + 1));  // early: a whole row ahead of its use
         Vec8 yv[VPT];
         sums[0] = sums[1] = 0.0f;
 #pragma unroll
@@ -186,8 +199,9 @@ norm_rows_kernel(const X* __restrict__ x, const __nv_bfloat16* __restrict__ h, c
                 for (int j = 0; j < 8; ++j) sums[0] += yv[v].v[j] * yv[v].v[j];
             }
         }
+        wait_rows(stages - 2);  // the next row
         if (h && k + 1 < rows) sums[1] = sum_h(next);
-        team_sum<2>(sums, red[k & 1], warps);
+        pair_sum(sums, red[k & 1], warps);
         if (n) {
             const float ry = rsqrtf(sums[0] * inv_d + eps);
 #pragma unroll
@@ -216,7 +230,7 @@ norm_rows_backward_kernel(const X* __restrict__ x, const __nv_bfloat16* __restri
                           int stages, X* __restrict__ dx, __nv_bfloat16* __restrict__ dh, float* __restrict__ dtgate,
                           float* __restrict__ partial) {
     extern __shared__ uint4 ring_smem[];
-    __shared__ float red1[2][kMaxWarps][2], red2[2][kMaxWarps][2];
+    __shared__ float red1[2][2][16], red2[2][2][16];
     constexpr int XW = words<X>();
     using B = __nv_bfloat16;
     const int tid = threadIdx.x, nt = blockDim.x, d8 = d / 8, warps = nt >> 5;
@@ -276,18 +290,20 @@ norm_rows_backward_kernel(const X* __restrict__ x, const __nv_bfloat16* __restri
         return a;
     };
     float s2[2] = {0.0f, 0.0f};  // S of this row, sum of h^2 in the next
+    float tg_next = tgate ? __ldg(tgate + blockIdx.x) : 1.0f;
     if (h) {
         wait_rows(stages - 2);
         s2[1] = sum_h(0);
-        team_sum<2>(s2, red2[1], warps);
+        pair_sum(s2, red2[1], warps);
     }
+    else wait_rows(stages - 2);
     int s = 0;
     for (int k = 0; k < rows; ++k) {
         const int free_stage = s == 0 ? stages - 1 : s - 1, next = s + 1 == stages ? 0 : s + 1;
         fetch(k + stages - 1, free_stage);
-        wait_rows(stages - 2);
         const size_t t = row_of(k), base = t * d8;
-        const float tg = tgate ? __ldg(tgate + t) : 1.0f;
+        const float tg = tg_next;
+        if (tgate && k + 1 < rows) tg_next = __ldg(tgate + row_of(k + 1));  // early: a whole row ahead of its use
         const float rh = h ? rsqrtf(s2[1] * inv_d + eps) : 0.0f;
         const float hs = rh * tg;
         float ry = 0.0f, mean = 0.0f;
@@ -311,7 +327,7 @@ norm_rows_backward_kernel(const X* __restrict__ x, const __nv_bfloat16* __restri
                     }
                 }
             }
-            team_sum<2>(s1, red1[k & 1], warps);
+            pair_sum(s1, red1[k & 1], warps);
             ry = rsqrtf(s1[0] * inv_d + eps);
             mean = s1[1] * ry * inv_d;
         }
@@ -354,9 +370,10 @@ norm_rows_backward_kernel(const X* __restrict__ x, const __nv_bfloat16* __restri
                 }
             }
         }
+        wait_rows(stages - 2);  // the next row
         if (h) {
             if (k + 1 < rows) s2[1] = sum_h(next);
-            team_sum<2>(s2, red2[k & 1], warps);
+            pair_sum(s2, red2[k & 1], warps);
             const float qmean = s2[0] * rh * inv_d;  // mean of q hh
             if (dtgate && tid == 0) dtgate[t] = s2[0] * rh;
 #pragma unroll

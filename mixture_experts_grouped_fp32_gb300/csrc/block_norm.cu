@@ -48,10 +48,10 @@ __device__ __forceinline__ void block_sum(float (&v)[N], float (*red)[N], int wa
     for (int k = 0; k < N; ++k) v[k] = warp_sum(lane < warps ? red[lane][k] : 0.0f);
 }
 
-// Two sums over the block (at most 16 warps), in every thread: a half-warp takes each after the first
+// Two sums over the block, in every thread: a half-warp takes each after the first
 // exchange, so both cost the shuffles of one.  One barrier (none for a single warp); the caller's buffers
 // alternate between calls.
-__device__ __forceinline__ void pair_sum(float (&v)[2], float (*red)[16], int warps) {
+__device__ __forceinline__ void pair_sum(float (&v)[2], float (*red)[kMaxWarps], int warps) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const bool up = lane & 16;
     float a = up ? v[1] : v[0];
@@ -62,6 +62,7 @@ __device__ __forceinline__ void pair_sum(float (&v)[2], float (*red)[16], int wa
         if ((lane & 15) == 0) red[lane >> 4][warp] = a;
         __syncthreads();
         a = (lane & 15) < warps ? red[lane >> 4][lane & 15] : 0.0f;
+        if ((lane & 15) + 16 < warps) a += red[lane >> 4][(lane & 15) + 16];
 #pragma unroll
         for (int o = 8; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
     }
@@ -98,6 +99,19 @@ __device__ __forceinline__ Vec8 ring8(const Ring& r, int s, int w) {
                      __uint_as_float(b.x), __uint_as_float(b.y), __uint_as_float(b.z), __uint_as_float(b.w)}};
     }
 }
+// tgate of a block's rows, read by a warp 32 rows at a time (a load per row would be waited for in each).
+struct TokenGate {
+    const float* p;
+    int rows;
+    float mine = 1.0f;
+    template <typename RowOf>
+    __device__ __forceinline__ float at(int k, const RowOf& row_of) {
+        if (!p) return 1.0f;
+        const int lane = threadIdx.x & 31;
+        if ((k & 31) == 0) mine = k + lane < rows ? __ldg(p + row_of(k + lane)) : 0.0f;
+        return __shfl_sync(0xffffffffu, mine, k & 31);
+    }
+};
 // All but the newest `pending` rows have landed (pending = stages - 2).
 __device__ __forceinline__ void wait_rows(int pending) {
     if (pending == 2) ptx::cp_async_wait<2>();
@@ -114,7 +128,7 @@ norm_rows_kernel(const X* __restrict__ x, const __nv_bfloat16* __restrict__ h, c
                  const float* __restrict__ res, int T, int d, float eps, int stages, X* __restrict__ y,
                  __nv_bfloat16* __restrict__ n) {
     extern __shared__ uint4 ring_smem[];
-    __shared__ float red[2][2][16];
+    __shared__ float red[2][2][kMaxWarps];
     constexpr int XW = words<X>();
     const int tid = threadIdx.x, nt = blockDim.x, d8 = d / 8, warps = nt >> 5;
     const float inv_d = 1.0f / static_cast<float>(d);
@@ -167,7 +181,7 @@ norm_rows_kernel(const X* __restrict__ x, const __nv_bfloat16* __restrict__ h, c
         return a;
     };
     float sums[2] = {0.0f, 0.0f};  // of y^2 in this row, of h^2 in the next
-    float tg = tgate ? __ldg(tgate + blockIdx.x) : 1.0f;
+    TokenGate token{tgate, rows};
     if (h) {
         wait_rows(stages - 2);
         sums[1] = sum_h(0);
@@ -179,8 +193,7 @@ norm_rows_kernel(const X* __restrict__ x, const __nv_bfloat16* __restrict__ h, c
         const int free_stage = s == 0 ? stages - 1 : s - 1, next = s + 1 == stages ? 0 : s + 1;
         fetch(k + stages - 1, free_stage);
         const size_t t = row_of(k), base = t * d8;
-        const float scale = h ? rsqrtf(sums[1] * inv_d + eps) * tg : 0.0f;
-        if (tgate && k + 1 < rows) tg = __ldg(tgate + row_of(k + 1));  // early: a whole row ahead of its use
+        const float scale = h ? rsqrtf(sums[1] * inv_d + eps) * token.at(k, row_of) : 0.0f;
         Vec8 yv[VPT];
         sums[0] = sums[1] = 0.0f;
 #pragma unroll
@@ -230,7 +243,7 @@ norm_rows_backward_kernel(const X* __restrict__ x, const __nv_bfloat16* __restri
                           int stages, X* __restrict__ dx, __nv_bfloat16* __restrict__ dh, float* __restrict__ dtgate,
                           float* __restrict__ partial) {
     extern __shared__ uint4 ring_smem[];
-    __shared__ float red1[2][2][16], red2[2][2][16];
+    __shared__ float red1[2][2][kMaxWarps], red2[2][2][kMaxWarps];
     constexpr int XW = words<X>();
     using B = __nv_bfloat16;
     const int tid = threadIdx.x, nt = blockDim.x, d8 = d / 8, warps = nt >> 5;
@@ -259,8 +272,8 @@ norm_rows_backward_kernel(const X* __restrict__ x, const __nv_bfloat16* __restri
         ptx::cp_async_commit();
     };
     for (int k = 0; k < stages - 1; ++k) fetch(k, k);
-    // One vector per thread: the weights stay in registers.  Two: they are read again (L1) where used,
-    // the column sums take the registers.
+    // One vector per thread: the weights stay in registers.  Two: they are read again where used (the
+    // column sums take the registers); the ring leaves half of the SM's memory to L1 for them.
     Vec8 kn[VPT], kg[VPT], kr[VPT];
     auto load_weights = [&](int c, Vec8& n_, Vec8& g_, Vec8& r_) {
         n_ = w_pre ? load8_cached(w_pre, c) : ones();
@@ -290,7 +303,7 @@ norm_rows_backward_kernel(const X* __restrict__ x, const __nv_bfloat16* __restri
         return a;
     };
     float s2[2] = {0.0f, 0.0f};  // S of this row, sum of h^2 in the next
-    float tg_next = tgate ? __ldg(tgate + blockIdx.x) : 1.0f;
+    TokenGate token{tgate, rows};
     if (h) {
         wait_rows(stages - 2);
         s2[1] = sum_h(0);
@@ -302,8 +315,7 @@ norm_rows_backward_kernel(const X* __restrict__ x, const __nv_bfloat16* __restri
         const int free_stage = s == 0 ? stages - 1 : s - 1, next = s + 1 == stages ? 0 : s + 1;
         fetch(k + stages - 1, free_stage);
         const size_t t = row_of(k), base = t * d8;
-        const float tg = tg_next;
-        if (tgate && k + 1 < rows) tg_next = __ldg(tgate + row_of(k + 1));  // early: a whole row ahead of its use
+        const float tg = token.at(k, row_of);
         const float rh = h ? rsqrtf(s2[1] * inv_d + eps) : 0.0f;
         const float hs = rh * tg;
         float ry = 0.0f, mean = 0.0f;
@@ -678,7 +690,7 @@ Shape shape_of(const BlockNormArgs& a, bool bwd) {
     const int xw = a.x_fp32 ? 2 : 1;
     const int words = bwd ? xw * (a.dy ? 2 : 1) + (a.h ? 1 : 0) + (a.dn ? 1 : 0) : xw + (a.h ? 1 : 0);
     const size_t row = static_cast<size_t>(words) * s.vpt * s.threads * 16;
-    const size_t fit = 200 * 1024 / (row * s.per_sm);
+    const size_t fit = (bwd && s.vpt == 2 ? 112 : 200) * 1024 / (row * s.per_sm);
     s.stages = fit >= 4 ? 4 : fit >= 3 ? 3 : 2;
     s.smem = row * s.stages;
     return s;

@@ -172,13 +172,6 @@ __device__ __forceinline__ void raise_abort(Ctl& c, int32_t* status) {
     flag_status(status, MOE_STATUS_WAIT_TIMEOUT);
 }
 
-template <typename T>
-__device__ __forceinline__ T cvt_out(float v);
-template <>
-__device__ __forceinline__ float cvt_out<float>(float v) { return v; }
-template <>
-__device__ __forceinline__ __nv_bfloat16 cvt_out<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
-
 // tmF: the feature operand (weights [E, K, N] / [E, N, K], or G [M, N] as one matrix); tmR, tmR32: the
 // row operand A [M, K] (boxes of 128 and of 32 rows; weight gradient: boxes of 64 rows).
 template <int MODE, typename OUT>
@@ -201,7 +194,7 @@ grouped_mm_kernel(const __grid_constant__ CUtensorMap tmF, const __grid_constant
 
     if (tid == 0) {
         for (int s = 0; s < STAGES; ++s) {
-            // Weight gradient: one arrival of each CTA (its producer's, or its zeroing warp's).
+            // Weight gradient: two arrivals, of the leader's producer or of each CTA's zeroing warp.
             ptx::mbar_init(&c.full[s], WGRAD ? 2 : 1);
             ptx::mbar_init(&c.empty[s], 1);
             ptx::mbar_init(&c.tail[s], 1);
@@ -308,8 +301,10 @@ grouped_mm_kernel(const __grid_constant__ CUtensorMap tmF, const __grid_constant
                         ptx::tma_load_2d(sr, &tmR, &c.tail[stage], r, row, pol_r);
                         ptx::tma_load_2d(sr + BOX_BYTES, &tmR, &c.tail[stage], r + 64, row, pol_r);
                     } else {
-                        if (leader) ptx::mbar_arrive_expect_tx(&c.full[stage], 2u * cta_bytes);
-                        else ptx::mbar_arrive_cluster(full_leader);
+                        if (leader) {  // both arrivals: a remote one for each block costs more (14 %)
+                            ptx::mbar_arrive(&c.full[stage]);
+                            ptx::mbar_arrive_expect_tx(&c.full[stage], 2u * cta_bytes);
+                        }
                         ptx::tma_load_2d_pair(sf, &tmF, full_leader, f, row, pol_f);
                         ptx::tma_load_2d_pair(sf + BOX_BYTES, &tmF, full_leader, f + 64, row, pol_f);
                         ptx::tma_load_2d_pair(sr, &tmR, full_leader, r, row, pol_r);
@@ -441,7 +436,10 @@ grouped_mm_kernel(const __grid_constant__ CUtensorMap tmF, const __grid_constant
         auto give = [&]() {  // and may be overwritten
             ptx::tc_fence_before();
             __syncwarp();
-            if (lane == 0) ptx::mbar_arrive_cluster(ptx::map_to_cta(ptx::smem_u32(&c.tempty[acc]), 0));
+            // Relaxed: what came before on this thread are reads of tensor memory, complete since wait::ld
+            // (a releasing arrival would wait for the thread's stores to global memory too: 8 % of the
+            // weight gradients' time).
+            if (lane == 0) ptx::mbar_arrive_cluster_relaxed(ptx::map_to_cta(ptx::smem_u32(&c.tempty[acc]), 0));
         };
         auto pass = [&]() {  // on to the next accumulator
             if (++acc == NUM_ACC) {
@@ -449,15 +447,15 @@ grouped_mm_kernel(const __grid_constant__ CUtensorMap tmF, const __grid_constant
                 acc_phase ^= 1u;
             }
         };
-        // Stores the warp's 32 output rows from j0 on (a lane holds one column of them), up to `rows`.
-        auto put = [&](OUT* p, const uint32_t (&v)[32], int rows) {
+        // fp32: stores 32 output rows of which a lane holds one column, up to `rows` of them.
+        auto put = [&](float* p, const uint32_t (&v)[32], int rows) {
             if (rows >= 32) {
 #pragma unroll
-                for (int j = 0; j < 32; ++j, p += N) *p = cvt_out<OUT>(__uint_as_float(v[j]));
+                for (int j = 0; j < 32; ++j, p += N) *p = __uint_as_float(v[j]);
             } else {
 #pragma unroll
                 for (int j = 0; j < 32; ++j, p += N)
-                    if (j < rows) *p = cvt_out<OUT>(__uint_as_float(v[j]));
+                    if (j < rows) *p = __uint_as_float(v[j]);
             }
         };
         bool aborted = false;
@@ -518,6 +516,9 @@ grouped_mm_kernel(const __grid_constant__ CUtensorMap tmF, const __grid_constant
                     continue;
                 }
                 if (any && !take()) break;
+                // Neighbouring lanes exchange halves of their pairs of rows: an even lane then holds columns n
+                // and n + 1 of the first row, an odd lane n - 1 and n of the second, one 4-byte store each.
+                const uint32_t sel = lane & 1 ? 0x3276u : 0x5410u;
 #pragma unroll 1
                 for (int j0 = 0; j0 < 128 && col0 + j0 < it.rows; j0 += 32) {
                     uint32_t v[32];
@@ -528,7 +529,14 @@ grouped_mm_kernel(const __grid_constant__ CUtensorMap tmF, const __grid_constant
 #pragma unroll
                         for (int j = 0; j < 32; ++j) v[j] = 0u;
                     }
-                    if (n < N) put(dst + static_cast<size_t>(j0) * N, v, it.rows - col0 - j0);
+                    OUT* p = dst + static_cast<size_t>(j0) * N - (lane & 1) + static_cast<size_t>(lane & 1) * N;
+                    const int nr = it.rows - col0 - j0 - (lane & 1);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j, p += 2 * static_cast<size_t>(N)) {
+                        const uint32_t own = pack_bf16x2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
+                        const uint32_t other = __shfl_xor_sync(0xffffffffu, own, 1);
+                        if (2 * j < nr && n < N) *reinterpret_cast<uint32_t*>(p) = __byte_perm(own, other, sel);
+                    }
                 }
                 if (any) {
                     give();

@@ -221,6 +221,10 @@ cudaError_t launch_grouped_mm(int mode, const GroupedMmArgs& a, int num_sms, cud
 // 128-byte swizzle.
 bool make_tensor_map_bf16_3d(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows, uint64_t d2,
                              uint32_t box_rows);
+// bf16 tensor [d3, rows, cols] with a box of `blocks` neighbouring [box_rows, 64 cols] boxes, one after
+// another in shared memory; cols a multiple of 64.
+bool make_tensor_map_bf16_blocks(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows, uint64_t d3,
+                                 uint32_t box_rows, uint32_t blocks);
 
 // SwiGLU with a weight per row, and its gradient (swiglu.cu).  f a multiple of 8.
 cudaError_t launch_swiglu(const __nv_bfloat16* gu, const float* w, int M, int f, __nv_bfloat16* h, int num_sms,

@@ -21,7 +21,10 @@
 //   F (16 KB)  128 features.  kMmTransB: K-major, one box of 128 rows x 64 K.  Otherwise MN-major: two
 //              boxes of 64 features x 64 deep, 8 KB apart.
 //   R (16 KB)  this CTA's half of the tile's rows, at most 128.  Weight gradient: MN-major, two boxes
-//              as for F.  Otherwise K-major: one 128-row box, or as many 32-row boxes as needed.
+//              as for F.  Otherwise K-major: one box of 32, 64 or 128 rows.
+// Each operand is one copy per stage (a view of the matrix as blocks of 64 columns makes two boxes one
+// copy; a column count that is no multiple of 64 takes two): the copies' issue counts, four 32-row
+// boxes instead of one of 128 rows cost 15 % of an 8192 x 4096 x 28672 product.
 // Six stages; two 256-column accumulators, so that one tile's epilogue overlaps the next tile's
 // products.
 //
@@ -53,8 +56,6 @@ constexpr int BOX_BYTES = 64 * BK * 2;           // 8 KB
 constexpr int F_BYTES = 128 * BK * 2;            // 16 KB
 constexpr int R_BYTES = 128 * BK * 2;            // 16 KB
 constexpr int STAGE_BYTES = F_BYTES + R_BYTES;   // 32 KB per CTA
-constexpr int ROW_BOX = 32;
-constexpr int ROW_BOX_BYTES = ROW_BOX * BK * 2;  // 4 KB
 constexpr int STAGES = 6;
 constexpr int ACC_COLS = 256;
 constexpr int NUM_ACC = 2;
@@ -172,13 +173,18 @@ __device__ __forceinline__ void raise_abort(Ctl& c, int32_t* status) {
     flag_status(status, MOE_STATUS_WAIT_TIMEOUT);
 }
 
-// tmF: the feature operand (weights [E, K, N] / [E, N, K], or G [M, N] as one matrix); tmR, tmR32: the
-// row operand A [M, K] (boxes of 128 and of 32 rows; weight gradient: boxes of 64 rows).
+// Tensor maps.  f: the feature operand (weights [E, K, N] / [E, N, K], or G [M, N] as one matrix); r: the
+// row operand A [M, K], for the products by rows with boxes of 128, 64 and 32 rows.  f_blocks / r_blocks:
+// the map's box is both 64-column boxes of the operand.
+struct Maps {
+    CUtensorMap f, r, r64, r32;
+    int f_blocks, r_blocks;
+};
+
 template <int MODE, typename OUT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(num_threads<MODE, OUT>(), 1)
-grouped_mm_kernel(const __grid_constant__ CUtensorMap tmF, const __grid_constant__ CUtensorMap tmR,
-                  const __grid_constant__ CUtensorMap tmR32, const int32_t* __restrict__ offsets, int M, int K, int N,
-                  int E, int ksplit, int accumulate, OUT* __restrict__ out, int32_t* __restrict__ status) {
+grouped_mm_kernel(const __grid_constant__ Maps maps, const int32_t* __restrict__ offsets, int M, int K, int N, int E,
+                  int ksplit, int accumulate, OUT* __restrict__ out, int32_t* __restrict__ status) {
     constexpr bool WGRAD = MODE == kMmWgrad;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = ptx::smem_u32(smem_raw);
@@ -209,9 +215,12 @@ grouped_mm_kernel(const __grid_constant__ CUtensorMap tmF, const __grid_constant
         ptx::fence_proxy_async_smem();
     }
     if (warp == 0 && lane == 0) {
-        ptx::prefetch_tensormap(&tmF);
-        ptx::prefetch_tensormap(&tmR);
-        if (!WGRAD) ptx::prefetch_tensormap(&tmR32);
+        ptx::prefetch_tensormap(&maps.f);
+        ptx::prefetch_tensormap(&maps.r);
+        if (!WGRAD) {
+            ptx::prefetch_tensormap(&maps.r64);
+            ptx::prefetch_tensormap(&maps.r32);
+        }
     }
     if (warp == 1) {
         ptx::tmem_alloc_pair(&c.tmem_base, TMEM_COLS);
@@ -278,9 +287,11 @@ grouped_mm_kernel(const __grid_constant__ CUtensorMap tmF, const __grid_constant
             const int half = it.ntok >> 1;
             const int f = it.f0 + 128 * rank;           // this CTA's features
             const int seg0 = c.seg[it.e];
-            const int rb = (half + ROW_BOX - 1) / ROW_BOX;
-            const uint32_t row_bytes = half == 128 ? R_BYTES : rb * ROW_BOX_BYTES;
-            const uint32_t cta_bytes = F_BYTES + (WGRAD ? R_BYTES : row_bytes);
+            // The smallest row box that holds this CTA's rows (columns, for the weight gradient).
+            const CUtensorMap* mr = WGRAD || half > 64 ? &maps.r : half > 32 ? &maps.r64 : &maps.r32;
+            const uint32_t row_bytes = WGRAD || half > 64 ? R_BYTES : half > 32 ? R_BYTES / 2 : R_BYTES / 4;
+            const uint32_t cta_bytes = F_BYTES + row_bytes;
+            const int r = it.r0 + rank * half;  // this CTA's first output row
             for (int kb = it.red0; kb < it.red1; ++kb) {
                 if (!ptx::mbar_wait(&c.empty[stage], phase ^ 1u, abort_flag)) {
                     raise_abort(c, status);
@@ -292,39 +303,49 @@ grouped_mm_kernel(const __grid_constant__ CUtensorMap tmF, const __grid_constant
                 const uint32_t full_leader = ptx::map_to_cta(ptx::smem_u32(&c.full[stage]), 0);
                 if (WGRAD) {
                     const int row = seg0 + kb * BK;
-                    const int r = it.r0 + rank * half;  // this CTA's output rows = columns of A
                     if ((kb + 1) * BK > it.red_rows && (it.red_rows & 15)) {
                         // The segment's last block, with rows to be zeroed: its copies complete here.
                         ptx::mbar_arrive_expect_tx(&c.tail[stage], cta_bytes);
-                        ptx::tma_load_2d(sf, &tmF, &c.tail[stage], f, row, pol_f);
-                        ptx::tma_load_2d(sf + BOX_BYTES, &tmF, &c.tail[stage], f + 64, row, pol_f);
-                        ptx::tma_load_2d(sr, &tmR, &c.tail[stage], r, row, pol_r);
-                        ptx::tma_load_2d(sr + BOX_BYTES, &tmR, &c.tail[stage], r + 64, row, pol_r);
+                        if (maps.f_blocks) {
+                            ptx::tma_load_4d(sf, &maps.f, &c.tail[stage], 0, row, f >> 6, 0, pol_f);
+                        } else {
+                            ptx::tma_load_2d(sf, &maps.f, &c.tail[stage], f, row, pol_f);
+                            ptx::tma_load_2d(sf + BOX_BYTES, &maps.f, &c.tail[stage], f + 64, row, pol_f);
+                        }
+                        if (maps.r_blocks) {
+                            ptx::tma_load_4d(sr, &maps.r, &c.tail[stage], 0, row, r >> 6, 0, pol_r);
+                        } else {
+                            ptx::tma_load_2d(sr, &maps.r, &c.tail[stage], r, row, pol_r);
+                            ptx::tma_load_2d(sr + BOX_BYTES, &maps.r, &c.tail[stage], r + 64, row, pol_r);
+                        }
                     } else {
                         if (leader) {  // both arrivals: a remote one for each block costs more (14 %)
                             ptx::mbar_arrive(&c.full[stage]);
                             ptx::mbar_arrive_expect_tx(&c.full[stage], 2u * cta_bytes);
                         }
-                        ptx::tma_load_2d_pair(sf, &tmF, full_leader, f, row, pol_f);
-                        ptx::tma_load_2d_pair(sf + BOX_BYTES, &tmF, full_leader, f + 64, row, pol_f);
-                        ptx::tma_load_2d_pair(sr, &tmR, full_leader, r, row, pol_r);
-                        ptx::tma_load_2d_pair(sr + BOX_BYTES, &tmR, full_leader, r + 64, row, pol_r);
+                        if (maps.f_blocks) {
+                            ptx::tma_load_4d_pair(sf, &maps.f, full_leader, 0, row, f >> 6, 0, pol_f);
+                        } else {
+                            ptx::tma_load_2d_pair(sf, &maps.f, full_leader, f, row, pol_f);
+                            ptx::tma_load_2d_pair(sf + BOX_BYTES, &maps.f, full_leader, f + 64, row, pol_f);
+                        }
+                        if (maps.r_blocks) {
+                            ptx::tma_load_4d_pair(sr, &maps.r, full_leader, 0, row, r >> 6, 0, pol_r);
+                        } else {
+                            ptx::tma_load_2d_pair(sr, &maps.r, full_leader, r, row, pol_r);
+                            ptx::tma_load_2d_pair(sr + BOX_BYTES, &maps.r, full_leader, r + 64, row, pol_r);
+                        }
                     }
                 } else {
                     if (leader) ptx::mbar_arrive_expect_tx(&c.full[stage], 2u * cta_bytes);
-                    const int row = seg0 + it.r0 + rank * half;
-                    if (half == 128) {
-                        ptx::tma_load_2d_pair(sr, &tmR, full_leader, kb * BK, row, pol_r);
-                    } else {
-                        for (int q = 0; q < rb; ++q)
-                            ptx::tma_load_2d_pair(sr + q * ROW_BOX_BYTES, &tmR32, full_leader, kb * BK,
-                                                  row + q * ROW_BOX, pol_r);
-                    }
+                    ptx::tma_load_2d_pair(sr, mr, full_leader, kb * BK, seg0 + r, pol_r);
                     if (MODE == kMmTransB) {
-                        ptx::tma_load_3d_pair(sf, &tmF, full_leader, kb * BK, f, it.e, pol_f);
+                        ptx::tma_load_3d_pair(sf, &maps.f, full_leader, kb * BK, f, it.e, pol_f);
+                    } else if (maps.f_blocks) {
+                        ptx::tma_load_4d_pair(sf, &maps.f, full_leader, 0, kb * BK, f >> 6, it.e, pol_f);
                     } else {
-                        ptx::tma_load_3d_pair(sf, &tmF, full_leader, f, kb * BK, it.e, pol_f);
-                        ptx::tma_load_3d_pair(sf + BOX_BYTES, &tmF, full_leader, f + 64, kb * BK, it.e, pol_f);
+                        ptx::tma_load_3d_pair(sf, &maps.f, full_leader, f, kb * BK, it.e, pol_f);
+                        ptx::tma_load_3d_pair(sf + BOX_BYTES, &maps.f, full_leader, f + 64, kb * BK, it.e, pol_f);
                     }
                 }
                 fill_parity[stage] = phase;
@@ -619,21 +640,30 @@ cudaError_t launch_mode(const GroupedMmArgs& a, OUT* out, int ksplit, int accumu
         }
         attr_set[dev] = true;
     }
-    CUtensorMap mF, mR, mR32;
+    Maps m{};
     bool ok;
-    if (MODE == kMmWgrad)
-        ok = make_tensor_map_bf16(&mF, a.B, a.N, a.M, BK) && make_tensor_map_bf16(&mR, a.A, a.K, a.M, BK);
-    else
-        ok = make_tensor_map_bf16(&mR, a.A, a.K, a.M, 128) && make_tensor_map_bf16(&mR32, a.A, a.K, a.M, ROW_BOX) &&
-             (MODE == kMmTransB ? make_tensor_map_bf16_3d(&mF, a.B, a.K, a.N, a.E, 128)
-                                : make_tensor_map_bf16_3d(&mF, a.B, a.N, a.K, a.E, BK));
-    if (MODE == kMmWgrad) mR32 = mR;
+    if (MODE == kMmWgrad) {
+        m.f_blocks = make_tensor_map_bf16_blocks(&m.f, a.B, a.N, a.M, 1, BK, 2);
+        // A's tiles are 256 columns, each CTA's half 128: multiples of 64 when K has whole tiles.
+        m.r_blocks = a.K % TILE_R == 0 && make_tensor_map_bf16_blocks(&m.r, a.A, a.K, a.M, 1, BK, 2);
+        ok = (m.f_blocks || make_tensor_map_bf16(&m.f, a.B, a.N, a.M, BK)) &&
+             (m.r_blocks || make_tensor_map_bf16(&m.r, a.A, a.K, a.M, BK));
+    } else {
+        ok = make_tensor_map_bf16(&m.r, a.A, a.K, a.M, 128) && make_tensor_map_bf16(&m.r64, a.A, a.K, a.M, 64) &&
+             make_tensor_map_bf16(&m.r32, a.A, a.K, a.M, 32);
+        if (MODE == kMmTransB) {
+            ok = ok && make_tensor_map_bf16_3d(&m.f, a.B, a.K, a.N, a.E, 128);
+        } else {
+            m.f_blocks = make_tensor_map_bf16_blocks(&m.f, a.B, a.N, a.K, a.E, BK, 2);
+            ok = ok && (m.f_blocks || make_tensor_map_bf16_3d(&m.f, a.B, a.N, a.K, a.E, BK));
+        }
+    }
     if (!ok) {
         *why = "cuTensorMapEncodeTiled failed (driver entry point missing or bad operand)";
         return cudaErrorInvalidValue;
     }
     return launch_k(kPdlTrain, grouped_mm_kernel<MODE, OUT>, dim3(num_sms & ~1), dim3(num_threads<MODE, OUT>()),
-                    SMEM_BYTES, s, mF, mR, mR32, a.offsets, a.M, a.K, a.N, a.E, ksplit, accumulate, out, a.status);
+                    SMEM_BYTES, s, m, a.offsets, a.M, a.K, a.N, a.E, ksplit, accumulate, out, a.status);
 }
 
 template <int MODE>

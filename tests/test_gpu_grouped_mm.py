@@ -69,7 +69,8 @@ def moe():
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("way", ["fwd", "dgrad", "wgrad"])
-@pytest.mark.parametrize("K,N", [(64, 256), (8, 8), (72, 264), (328, 520), (128, 16)])
+@pytest.mark.parametrize("K,N", [(64, 256), (8, 8), (72, 264), (328, 520), (128, 16), (256, 320),
+                                 (512, 64)])
 @pytest.mark.parametrize("counts", list(COUNTS))
 def test_products(moe, counts, K, N, way, dtype):
     a, b, offs = _inputs(COUNTS[counts], K, N, way)

@@ -48,27 +48,29 @@ __device__ __forceinline__ void block_sum(float (&v)[N], float (*red)[N], int wa
     for (int k = 0; k < N; ++k) v[k] = warp_sum(lane < warps ? red[lane][k] : 0.0f);
 }
 
-// Two sums over the block, in every thread: a half-warp takes each after the first
-// exchange, so both cost the shuffles of one.  One barrier (none for a single warp); the caller's buffers
-// alternate between calls.
-__device__ __forceinline__ void pair_sum(float (&v)[2], float (*red)[kMaxWarps], int warps) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const bool up = lane & 16;
-    float a = up ? v[1] : v[0];
-    a += __shfl_xor_sync(0xffffffffu, up ? v[0] : v[1], 16);
+// Two sums over a warp, in every lane: a half-warp takes each after the first exchange, so both cost
+// little more than the shuffles of one.
+__device__ __forceinline__ float2 warp_pair_sum(float2 v) {
+    const bool up = threadIdx.x & 16;
+    float a = up ? v.y : v.x;
+    a += __shfl_xor_sync(0xffffffffu, up ? v.x : v.y, 16);
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
-    if (warps > 1) {
-        if ((lane & 15) == 0) red[lane >> 4][warp] = a;
-        __syncthreads();
-        a = (lane & 15) < warps ? red[lane >> 4][lane & 15] : 0.0f;
-        if ((lane & 15) + 16 < warps) a += red[lane >> 4][(lane & 15) + 16];
-#pragma unroll
-        for (int o = 8; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
-    }
     const float b = __shfl_xor_sync(0xffffffffu, a, 16);
-    v[0] = up ? b : a;
-    v[1] = up ? a : b;
+    return up ? make_float2(b, a) : make_float2(a, b);
+}
+// Two sums over the block, in every thread, with one barrier (none for a single warp); the caller's
+// buffers alternate between calls.
+__device__ __forceinline__ void pair_sum(float (&v)[2], float2* red, int warps) {
+    float2 s = warp_pair_sum(make_float2(v[0], v[1]));
+    if (warps > 1) {
+        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+        if (lane == 0) red[warp] = s;
+        __syncthreads();
+        s = warp_pair_sum(lane < warps ? red[lane] : make_float2(0.0f, 0.0f));
+    }
+    v[0] = s.x;
+    v[1] = s.y;
 }
 
 // 16-byte words of eight values of X.
@@ -121,18 +123,19 @@ __device__ __forceinline__ void wait_rows(int pending) {
 
 __device__ __forceinline__ Vec8 ones() { return Vec8{{1, 1, 1, 1, 1, 1, 1, 1}}; }
 
-template <typename X, int VPT>
+// H: with h (the block's output, its norm and gates);  N: with n (the next norm).
+template <typename X, int VPT, bool H, bool N>
 __global__ void __launch_bounds__(VPT == 1 ? 256 : 512, VPT == 1 ? 4 : 1)
 norm_rows_kernel(const X* __restrict__ x, const __nv_bfloat16* __restrict__ h, const float* __restrict__ w_pre,
                  const float* __restrict__ w_post, const float* __restrict__ gate, const float* __restrict__ tgate,
                  const float* __restrict__ res, int T, int d, float eps, int stages, X* __restrict__ y,
                  __nv_bfloat16* __restrict__ n) {
     extern __shared__ uint4 ring_smem[];
-    __shared__ float red[2][2][kMaxWarps];
+    __shared__ float2 red[2][kMaxWarps];
     constexpr int XW = words<X>();
     const int tid = threadIdx.x, nt = blockDim.x, d8 = d / 8, warps = nt >> 5;
     const float inv_d = 1.0f / static_cast<float>(d);
-    const int per_vec = XW + (h ? 1 : 0);
+    const int per_vec = XW + (H ? 1 : 0);
     const Ring ring{ring_smem + tid, VPT * per_vec, nt};
     const int rows = (T - static_cast<int>(blockIdx.x) + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x);
     pdl_wait();
@@ -146,7 +149,7 @@ norm_rows_kernel(const X* __restrict__ x, const __nv_bfloat16* __restrict__ h, c
                 const int c = tid + v * nt;
                 if (c < d8) {
                     fetch8(ring, s, v * per_vec, x, base + c);
-                    if (h) fetch8(ring, s, v * per_vec + XW, h, base + c);
+                    if (H) fetch8(ring, s, v * per_vec + XW, h, base + c);
                 }
             }
         }
@@ -159,8 +162,8 @@ norm_rows_kernel(const X* __restrict__ x, const __nv_bfloat16* __restrict__ h, c
         const int c = tid + v * nt;
         wn[v] = wg[v] = rs[v] = ones();
         if (c < d8) {
-            if (w_pre) wn[v] = load8_cached(w_pre, c);
-            if (h) wg[v] = load8_cached(w_post, c);
+            if (N) wn[v] = load8_cached(w_pre, c);
+            if (H) wg[v] = load8_cached(w_post, c);
             if (gate) {
                 const Vec8 g = load8_cached(gate, c);
 #pragma unroll
@@ -182,7 +185,7 @@ norm_rows_kernel(const X* __restrict__ x, const __nv_bfloat16* __restrict__ h, c
     };
     float sums[2] = {0.0f, 0.0f};  // of y^2 in this row, of h^2 in the next
     TokenGate token{tgate, rows};
-    if (h) {
+    if (H) {
         wait_rows(stages - 2);
         sums[1] = sum_h(0);
         pair_sum(sums, red[1], warps);
@@ -193,7 +196,7 @@ norm_rows_kernel(const X* __restrict__ x, const __nv_bfloat16* __restrict__ h, c
         const int free_stage = s == 0 ? stages - 1 : s - 1, next = s + 1 == stages ? 0 : s + 1;
         fetch(k + stages - 1, free_stage);
         const size_t t = row_of(k), base = t * d8;
-        const float scale = h ? rsqrtf(sums[1] * inv_d + eps) * token.at(k, row_of) : 0.0f;
+        const float scale = H ? rsqrtf(sums[1] * inv_d + eps) * token.at(k, row_of) : 0.0f;
         Vec8 yv[VPT];
         sums[0] = sums[1] = 0.0f;
 #pragma unroll
@@ -201,7 +204,7 @@ norm_rows_kernel(const X* __restrict__ x, const __nv_bfloat16* __restrict__ h, c
             const int c = tid + v * nt;
             if (c < d8) {
                 yv[v] = ring8<X>(ring, s, v * per_vec);
-                if (h) {
+                if (H) {
                     const Vec8 hv = ring8<__nv_bfloat16>(ring, s, v * per_vec + XW);
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
@@ -213,9 +216,9 @@ norm_rows_kernel(const X* __restrict__ x, const __nv_bfloat16* __restrict__ h, c
             }
         }
         wait_rows(stages - 2);  // the next row
-        if (h && k + 1 < rows) sums[1] = sum_h(next);
+        if (H && k + 1 < rows) sums[1] = sum_h(next);
         pair_sum(sums, red[k & 1], warps);
-        if (n) {
+        if (N) {
             const float ry = rsqrtf(sums[0] * inv_d + eps);
 #pragma unroll
             for (int v = 0; v < VPT; ++v) {
@@ -234,7 +237,7 @@ norm_rows_kernel(const X* __restrict__ x, const __nv_bfloat16* __restrict__ h, c
 }
 
 // Column sums of a block go to partial[blockIdx][3][d]: A, dres, dw_pre.
-template <typename X, int VPT>
+template <typename X, int VPT, bool H, bool N>
 __global__ void __launch_bounds__(512, 1)
 norm_rows_backward_kernel(const X* __restrict__ x, const __nv_bfloat16* __restrict__ h, const X* __restrict__ dy,
                           const __nv_bfloat16* __restrict__ dn, const float* __restrict__ w_pre,
@@ -243,13 +246,13 @@ norm_rows_backward_kernel(const X* __restrict__ x, const __nv_bfloat16* __restri
                           int stages, X* __restrict__ dx, __nv_bfloat16* __restrict__ dh, float* __restrict__ dtgate,
                           float* __restrict__ partial) {
     extern __shared__ uint4 ring_smem[];
-    __shared__ float red1[2][2][kMaxWarps], red2[2][2][kMaxWarps];
+    __shared__ float2 red1[2][kMaxWarps], red2[2][kMaxWarps];
     constexpr int XW = words<X>();
     using B = __nv_bfloat16;
     const int tid = threadIdx.x, nt = blockDim.x, d8 = d / 8, warps = nt >> 5;
     const float inv_d = 1.0f / static_cast<float>(d);
     // Words of a vector: x, then dy, h, dn as given.
-    const int o_dy = XW, o_h = o_dy + (dy ? XW : 0), o_dn = o_h + (h ? 1 : 0), per_vec = o_dn + (dn ? 1 : 0);
+    const int o_dy = XW, o_h = o_dy + (dy ? XW : 0), o_dn = o_h + (H ? 1 : 0), per_vec = o_dn + (N ? 1 : 0);
     const Ring ring{ring_smem + tid, VPT * per_vec, nt};
     const int rows = (T - static_cast<int>(blockIdx.x) + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x);
     pdl_wait();
@@ -264,8 +267,8 @@ norm_rows_backward_kernel(const X* __restrict__ x, const __nv_bfloat16* __restri
                 if (c < d8) {
                     fetch8(ring, s, v * per_vec, x, base + c);
                     if (dy) fetch8(ring, s, v * per_vec + o_dy, dy, base + c);
-                    if (h) fetch8(ring, s, v * per_vec + o_h, h, base + c);
-                    if (dn) fetch8(ring, s, v * per_vec + o_dn, dn, base + c);
+                    if (H) fetch8(ring, s, v * per_vec + o_h, h, base + c);
+                    if (N) fetch8(ring, s, v * per_vec + o_dn, dn, base + c);
                 }
             }
         }
@@ -276,8 +279,8 @@ norm_rows_backward_kernel(const X* __restrict__ x, const __nv_bfloat16* __restri
     // column sums take the registers); the ring leaves half of the SM's memory to L1 for them.
     Vec8 kn[VPT], kg[VPT], kr[VPT];
     auto load_weights = [&](int c, Vec8& n_, Vec8& g_, Vec8& r_) {
-        n_ = w_pre ? load8_cached(w_pre, c) : ones();
-        g_ = h ? load8_cached(w_post, c) : ones();
+        n_ = N ? load8_cached(w_pre, c) : ones();
+        g_ = H ? load8_cached(w_post, c) : ones();
         if (gate) {
             const Vec8 g = load8_cached(gate, c);
 #pragma unroll
@@ -304,7 +307,7 @@ norm_rows_backward_kernel(const X* __restrict__ x, const __nv_bfloat16* __restri
     };
     float s2[2] = {0.0f, 0.0f};  // S of this row, sum of h^2 in the next
     TokenGate token{tgate, rows};
-    if (h) {
+    if (H) {
         wait_rows(stages - 2);
         s2[1] = sum_h(0);
         pair_sum(s2, red2[1], warps);
@@ -316,10 +319,10 @@ norm_rows_backward_kernel(const X* __restrict__ x, const __nv_bfloat16* __restri
         fetch(k + stages - 1, free_stage);
         const size_t t = row_of(k), base = t * d8;
         const float tg = token.at(k, row_of);
-        const float rh = h ? rsqrtf(s2[1] * inv_d + eps) : 0.0f;
+        const float rh = H ? rsqrtf(s2[1] * inv_d + eps) : 0.0f;
         const float hs = rh * tg;
         float ry = 0.0f, mean = 0.0f;
-        if (dn) {
+        if (N) {
             float s1[2] = {0.0f, 0.0f};  // sum of y^2, sum of dn w_pre y
 #pragma unroll
             for (int v = 0; v < VPT; ++v) {
@@ -330,10 +333,10 @@ norm_rows_backward_kernel(const X* __restrict__ x, const __nv_bfloat16* __restri
                     else load_weights(c, wn, wg, rs);
                     const Vec8 xv = ring8<X>(ring, s, v * per_vec), nv = ring8<B>(ring, s, v * per_vec + o_dn);
                     Vec8 hv{};
-                    if (h) hv = ring8<B>(ring, s, v * per_vec + o_h);
+                    if (H) hv = ring8<B>(ring, s, v * per_vec + o_h);
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
-                        const float a = h ? rs.v[j] * xv.v[j] + wg.v[j] * (hv.v[j] * hs) : xv.v[j];
+                        const float a = H ? rs.v[j] * xv.v[j] + wg.v[j] * (hv.v[j] * hs) : xv.v[j];
                         s1[0] += a * a;
                         s1[1] += nv.v[j] * wn.v[j] * a;
                     }
@@ -355,12 +358,12 @@ norm_rows_backward_kernel(const X* __restrict__ x, const __nv_bfloat16* __restri
                 const Vec8 xv = ring8<X>(ring, s, v * per_vec);
                 Vec8 D{}, hv{}, o;
                 if (dy) D = ring8<X>(ring, s, v * per_vec + o_dy);
-                if (h) hv = ring8<B>(ring, s, v * per_vec + o_h);
-                if (dn) {
+                if (H) hv = ring8<B>(ring, s, v * per_vec + o_h);
+                if (N) {
                     const Vec8 nv = ring8<B>(ring, s, v * per_vec + o_dn);
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
-                        const float a = h ? rs.v[j] * xv.v[j] + wg.v[j] * (hv.v[j] * hs) : xv.v[j];
+                        const float a = H ? rs.v[j] * xv.v[j] + wg.v[j] * (hv.v[j] * hs) : xv.v[j];
                         const float yh = a * ry;
                         sP[v].v[j] += nv.v[j] * yh;
                         D.v[j] += ry * (nv.v[j] * wn.v[j] - yh * mean);
@@ -372,7 +375,7 @@ norm_rows_backward_kernel(const X* __restrict__ x, const __nv_bfloat16* __restri
                     sR[v].v[j] += D.v[j] * xv.v[j];
                 }
                 store8(dx, base + c, o);
-                if (h) {
+                if (H) {
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
                         sA[v].v[j] += D.v[j] * (hv.v[j] * hs);
@@ -383,7 +386,7 @@ norm_rows_backward_kernel(const X* __restrict__ x, const __nv_bfloat16* __restri
             }
         }
         wait_rows(stages - 2);  // the next row
-        if (h) {
+        if (H) {
             if (k + 1 < rows) s2[1] = sum_h(next);
             pair_sum(s2, red2[k & 1], warps);
             const float qmean = s2[0] * rh * inv_d;  // mean of q hh
@@ -706,14 +709,19 @@ cudaError_t allow_smem(void (*kernel)(KArgs...), bool* done) {
     return e;
 }
 
-template <typename X, int VPT>
-cudaError_t forward_rows(const BlockNormArgs& a, const Shape& s, int grid, cudaStream_t st) {
+template <typename X, int VPT, bool H, bool N>
+cudaError_t forward_as(const BlockNormArgs& a, const Shape& s, int grid, cudaStream_t st) {
     static bool done[64] = {};
-    const cudaError_t e = allow_smem(norm_rows_kernel<X, VPT>, done);
+    const cudaError_t e = allow_smem(norm_rows_kernel<X, VPT, H, N>, done);
     if (e != cudaSuccess) return e;
-    return launch_k(kPdlTrain, norm_rows_kernel<X, VPT>, dim3(grid), dim3(s.threads), s.smem, st,
+    return launch_k(kPdlTrain, norm_rows_kernel<X, VPT, H, N>, dim3(grid), dim3(s.threads), s.smem, st,
                     static_cast<const X*>(a.x), a.h, a.w_pre, a.w_post, a.gate, a.tgate, a.res, a.T, a.d, a.eps,
                     s.stages, static_cast<X*>(a.y), a.n);
+}
+template <typename X, int VPT>
+cudaError_t forward_rows(const BlockNormArgs& a, const Shape& s, int grid, cudaStream_t st) {
+    if (!a.h) return forward_as<X, VPT, false, true>(a, s, grid, st);
+    return a.n ? forward_as<X, VPT, true, true>(a, s, grid, st) : forward_as<X, VPT, true, false>(a, s, grid, st);
 }
 template <typename X, int VPT>
 cudaError_t forward_wide(const BlockNormArgs& a, const Shape& s, int grid, cudaStream_t st) {
@@ -721,14 +729,20 @@ cudaError_t forward_wide(const BlockNormArgs& a, const Shape& s, int grid, cudaS
                     static_cast<const X*>(a.x), a.h, a.w_pre, a.w_post, a.gate, a.tgate, a.res, a.T, a.d, a.eps,
                     static_cast<X*>(a.y), a.n);
 }
-template <typename X, int VPT>
-cudaError_t backward_rows(const BlockNormArgs& a, const Shape& s, int grid, cudaStream_t st) {
+template <typename X, int VPT, bool H, bool N>
+cudaError_t backward_as(const BlockNormArgs& a, const Shape& s, int grid, cudaStream_t st) {
     static bool done[64] = {};
-    const cudaError_t e = allow_smem(norm_rows_backward_kernel<X, VPT>, done);
+    const cudaError_t e = allow_smem(norm_rows_backward_kernel<X, VPT, H, N>, done);
     if (e != cudaSuccess) return e;
-    return launch_k(kPdlTrain, norm_rows_backward_kernel<X, VPT>, dim3(grid), dim3(s.threads), s.smem, st,
+    return launch_k(kPdlTrain, norm_rows_backward_kernel<X, VPT, H, N>, dim3(grid), dim3(s.threads), s.smem, st,
                     static_cast<const X*>(a.x), a.h, static_cast<const X*>(a.dy), a.dn, a.w_pre, a.w_post, a.gate,
                     a.tgate, a.res, a.T, a.d, a.eps, s.stages, static_cast<X*>(a.dx), a.dh, a.dtgate, a.partial);
+}
+template <typename X, int VPT>
+cudaError_t backward_rows(const BlockNormArgs& a, const Shape& s, int grid, cudaStream_t st) {
+    if (a.h)
+        return a.dn ? backward_as<X, VPT, true, true>(a, s, grid, st) : backward_as<X, VPT, true, false>(a, s, grid, st);
+    return a.dn ? backward_as<X, VPT, false, true>(a, s, grid, st) : backward_as<X, VPT, false, false>(a, s, grid, st);
 }
 template <typename X, int VPT>
 cudaError_t backward_wide(const BlockNormArgs& a, const Shape& s, int grid, cudaStream_t st) {

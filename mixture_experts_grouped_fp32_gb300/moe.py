@@ -8,6 +8,7 @@ library has not been built, the first call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -151,7 +152,7 @@ def _ptr(t: torch.Tensor | None):
 
 def _stream(stream) -> int | None:
     if stream is None:  # the current stream's handle, without building a Stream object around it
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else stream
 
 
@@ -865,18 +866,31 @@ def _empty(shape, dtype, device, stream):
 
 
 def _shaped(t: torch.Tensor, shape: tuple, name: str) -> None:
-    if tuple(t.shape) != shape:
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+
+
+def _arg(t: torch.Tensor, dtype, shape: tuple, name: str) -> int:
+    """The address of an operand of this type and shape (these checks and no more on the usual path: a
+    small call is bound by them)."""
+    if t.dtype is not dtype or t.shape != shape or not t.is_cuda or not t.is_contiguous():
+        _dev(t, dtype, name)
+        _shaped(t, shape, name)
+    return t.data_ptr()
+
+
+def _opt(t, dtype, shape, name):
+    return None if t is None else _arg(t, dtype, shape, name)
 
 
 def _out(out, shape, dtype, device, stream, name="out"):
     if out is None:
         return _empty(shape, dtype, device, stream)
-    _dev(out, dtype, name)
-    _shaped(out, tuple(shape), name)
+    _arg(out, dtype, tuple(shape), name)
     return out
 
 
+@functools.lru_cache(maxsize=4096)
 def grouped_mm_workspace_size(mode: int, M: int, K: int, N: int, E: int) -> int:
     """Bytes of workspace of a grouped product (mode 0: plain, 1: transpose_b, 2: weight gradient)."""
     return int(load().moe_grouped_mm_workspace_size(mode, M, K, N, E))
@@ -900,19 +914,17 @@ def grouped_mm(a, b, offsets, transpose_b: bool = False, out=None, out_dtype=tor
     """Products grouped by expert: out[r] = a[r] @ b[e] for the rows r of segment e of ``offsets`` [E+1]
     int32, with b [E, K, N]; or a[r] @ b[e].T with ``transpose_b`` and b [E, N, K].  a [M, K] and b are
     bf16; out [M, N] is bf16 or fp32.  Rows outside the segments are left as they are."""
-    _dev(a, torch.bfloat16, "a")
-    _dev(b, torch.bfloat16, "b")
-    _dev(offsets, torch.int32, "offsets")
     if a.dim() != 2 or b.dim() != 3:
         raise ValueError("a must be [M, K] and b [E, K, N] (or [E, N, K] with transpose_b)")
     M, K = a.shape
     E, N = b.shape[0], b.shape[1 if transpose_b else 2]
-    _shaped(b, (E, N, K) if transpose_b else (E, K, N), "b")
-    _shaped(offsets, (E + 1,), "offsets")
+    pa = _arg(a, torch.bfloat16, (M, K), "a")
+    pb = _arg(b, torch.bfloat16, (E, N, K) if transpose_b else (E, K, N), "b")
+    po = _arg(offsets, torch.int32, (E + 1,), "offsets")
     out, f32, workspace, nbytes = _mm_args(1 if transpose_b else 0, M, K, N, E, out, out_dtype, (M, N), workspace,
                                            a.device, stream)
-    _call("moe_grouped_mm", _ptr(a), _ptr(b), _ptr(offsets), M, K, N, E, int(transpose_b), _ptr(out), f32,
-          _ptr(workspace), nbytes, _ptr(status), _stream(stream))
+    _call("moe_grouped_mm", pa, pb, po, M, K, N, E, int(transpose_b), out.data_ptr(), f32, _ptr(workspace), nbytes,
+          _ptr(status), _stream(stream))
     return out
 
 
@@ -920,71 +932,60 @@ def grouped_mm_wgrad(a, g, offsets, out=None, out_dtype=torch.float32, accumulat
                      status=None, stream=None):
     """Weight gradient of a grouped product: out[e] = a[rows of e].T @ g[rows of e], [E, K, N] fp32 or
     bf16, zero for an empty segment; with ``accumulate`` (fp32 ``out`` given) it is added to out."""
-    _dev(a, torch.bfloat16, "a")
-    _dev(g, torch.bfloat16, "g")
-    _dev(offsets, torch.int32, "offsets")
     if a.dim() != 2 or g.dim() != 2 or offsets.dim() != 1:
         raise ValueError("a must be [M, K], g [M, N] and offsets [E + 1]")
     M, K = a.shape
     N, E = g.shape[1], offsets.shape[0] - 1
-    _shaped(g, (M, N), "g")
+    pa, pg = _arg(a, torch.bfloat16, (M, K), "a"), _arg(g, torch.bfloat16, (M, N), "g")
+    po = _arg(offsets, torch.int32, (E + 1,), "offsets")
     if accumulate and out is None:
         raise ValueError("accumulate adds to out: give out")
     out, f32, workspace, nbytes = _mm_args(2, M, K, N, E, out, out_dtype, (E, K, N), workspace, a.device, stream)
-    _call("moe_grouped_mm_wgrad", _ptr(a), _ptr(g), _ptr(offsets), M, K, N, E, _ptr(out), f32, int(accumulate),
-          _ptr(workspace), nbytes, _ptr(status), _stream(stream))
+    _call("moe_grouped_mm_wgrad", pa, pg, po, M, K, N, E, out.data_ptr(), f32, int(accumulate), _ptr(workspace), nbytes,
+          _ptr(status), _stream(stream))
     return out
 
 
 def swiglu(gu, w=None, h=None, stream=None):
     """h = w * silu(g) * u, bf16 [M, f], from gu = [g | u] bf16 [M, 2f] and a weight per row (fp32 [M],
     or None for 1)."""
-    M, f = _gu_dims(gu, w)
+    M, f, pg, pw = _gu_dims(gu, w)
     h = _out(h, (M, f), torch.bfloat16, gu.device, stream, "h")
-    _call("moe_swiglu", _ptr(gu), _ptr(w), M, f, _ptr(h), _stream(stream))
+    _call("moe_swiglu", pg, pw, M, f, h.data_ptr(), _stream(stream))
     return h
 
 
 def _gu_dims(gu, w):
-    _dev(gu, torch.bfloat16, "gu")
     if gu.dim() != 2 or gu.shape[1] % 2:
         raise ValueError(f"gu must be [M, 2f], got {tuple(gu.shape)}")
-    M, f = gu.shape[0], gu.shape[1] // 2
-    if w is not None:
-        _dev(w, torch.float32, "w")
-        _shaped(w, (M,), "w")
-    return M, f
+    M, f2 = gu.shape
+    return M, f2 // 2, _arg(gu, torch.bfloat16, (M, f2), "gu"), _opt(w, torch.float32, (M,), "w")
 
 
 def swiglu_backward(gu, dh, w=None, want_h: bool = False, dgu=None, dw=None, h=None, stream=None):
     """Gradient of ``swiglu``: (dgu bf16 [M, 2f], dw fp32 [M] or None without w, h bf16 [M, f] or None
     without ``want_h``), from dh bf16 [M, f]."""
-    M, f = _gu_dims(gu, w)
-    _dev(dh, torch.bfloat16, "dh")
-    _shaped(dh, (M, f), "dh")
+    M, f, pg, pw = _gu_dims(gu, w)
+    pd = _arg(dh, torch.bfloat16, (M, f), "dh")
     dgu = _out(dgu, (M, 2 * f), torch.bfloat16, gu.device, stream, "dgu")
     dw = _out(dw, (M,), torch.float32, gu.device, stream, "dw") if w is not None else None
     h = _out(h, (M, f), torch.bfloat16, gu.device, stream, "h") if want_h or h is not None else None
-    _call("moe_swiglu_backward", _ptr(gu), _ptr(dh), _ptr(w), M, f, _ptr(dgu), _ptr(dw), _ptr(h), _stream(stream))
+    _call("moe_swiglu_backward", pg, pd, pw, M, f, dgu.data_ptr(), _ptr(dw), _ptr(h), _stream(stream))
     return dgu, dw, h
 
 
 def _norm_inputs(x, w_pre, h, w_post, gate, token_gate, res_scale):
-    if x.dtype not in (torch.bfloat16, torch.float32):
-        raise ValueError(f"x must be bfloat16 or float32, got {x.dtype}")
-    _dev(x, x.dtype, "x")
+    """T, d, whether x is fp32, and the addresses of x, h, w_pre, w_post, gate, token_gate, res_scale."""
+    dt = x.dtype
+    if dt is not torch.bfloat16 and dt is not torch.float32:
+        raise ValueError(f"x must be bfloat16 or float32, got {dt}")
     if x.dim() != 2:
         raise ValueError(f"x must be [T, d], got {tuple(x.shape)}")
     T, d = x.shape
-    if h is not None:
-        _dev(h, torch.bfloat16, "h")
-        _shaped(h, (T, d), "h")
-    for t, n, size in ((w_pre, "w_pre", d), (w_post, "w_post", d), (gate, "gate", d), (token_gate, "token_gate", T),
-                       (res_scale, "res_scale", d)):
-        if t is not None:
-            _dev(t, torch.float32, n)
-            _shaped(t, (size,), n)
-    return T, d, int(x.dtype == torch.float32)
+    f, vec = torch.float32, (d,)
+    return (T, d, int(dt is f), _arg(x, dt, (T, d), "x"), _opt(h, torch.bfloat16, (T, d), "h"),
+            _opt(w_pre, f, vec, "w_pre"), _opt(w_post, f, vec, "w_post"), _opt(gate, f, vec, "gate"),
+            _opt(token_gate, f, (T,), "token_gate"), _opt(res_scale, f, vec, "res_scale"))
 
 
 def block_norm(x, w_pre=None, h=None, w_post=None, gate=None, token_gate=None, res_scale=None, eps: float = 1e-6,
@@ -997,11 +998,10 @@ def block_norm(x, w_pre=None, h=None, w_post=None, gate=None, token_gate=None, r
     x [T, d] bf16 or fp32 (the residual stream), h [T, d] bf16 (the block's output); w_pre, w_post, gate,
     res_scale fp32 [d], token_gate fp32 [T].  Returns (y, n): y has x's type, n is bf16.  Without ``h``
     (before the first block) y is x and is returned as None; without ``w_pre`` n is None."""
-    T, d, f32 = _norm_inputs(x, w_pre, h, w_post, gate, token_gate, res_scale)
+    T, d, f32, px, ph, *vectors = _norm_inputs(x, w_pre, h, w_post, gate, token_gate, res_scale)
     y = _out(y, (T, d), x.dtype, x.device, stream, "y") if h is not None else None
     n = _out(n, (T, d), torch.bfloat16, x.device, stream, "n") if w_pre is not None else None
-    _call("moe_block_norm", _ptr(x), f32, _ptr(h), _ptr(w_pre), _ptr(w_post), _ptr(gate), _ptr(token_gate),
-          _ptr(res_scale), T, d, eps, _ptr(y), _ptr(n), _stream(stream))
+    _call("moe_block_norm", px, f32, ph, *vectors, T, d, eps, _ptr(y), _ptr(n), _stream(stream))
     return y, n
 
 
@@ -1013,13 +1013,10 @@ def block_norm_backward(x, dy=None, dn=None, w_pre=None, h=None, w_post=None, ga
     """Gradients of ``block_norm``, as a dict by the inputs' names (None for an input that was not given):
     x (x's type) and h (bf16) [T, d], the vectors' in fp32.  dy (x's type) and dn (bf16) [T, d]; one of
     them may be None (zero).  The same inputs as the forward call; y is recomputed."""
-    T, d, f32 = _norm_inputs(x, w_pre, h, w_post, gate, token_gate, res_scale)
-    for t, n, dt in ((dy, "dy", x.dtype), (dn, "dn", torch.bfloat16)):
-        if t is not None:
-            _dev(t, dt, n)
-            _shaped(t, (T, d), n)
+    T, d, f32, px, ph, *vectors = _norm_inputs(x, w_pre, h, w_post, gate, token_gate, res_scale)
+    pdy, pdn = _opt(dy, x.dtype, (T, d), "dy"), _opt(dn, torch.bfloat16, (T, d), "dn")
     if workspace is None:
-        workspace = _empty(int(load().moe_block_norm_backward_workspace_size(T, d)), torch.uint8, x.device, stream)
+        workspace = _empty((_norm_workspace(T, d),), torch.uint8, x.device, stream)
     g = dict.fromkeys(NORM_GRADS)
     g["x"] = _empty((T, d), x.dtype, x.device, stream)
     if h is not None:
@@ -1028,11 +1025,15 @@ def block_norm_backward(x, dy=None, dn=None, w_pre=None, h=None, w_post=None, ga
                  ("token_gate", token_gate), ("res_scale", res_scale)):
         if t is not None:
             g[n] = _empty(t.shape, torch.float32, x.device, stream)
-    _call("moe_block_norm_backward", _ptr(x), f32, _ptr(h), _ptr(dy), _ptr(dn), _ptr(w_pre), _ptr(w_post), _ptr(gate),
-          _ptr(token_gate), _ptr(res_scale), T, d, eps, _ptr(g["x"]), _ptr(g["h"]), _ptr(g["w_pre"]),
-          _ptr(g["w_post"]), _ptr(g["gate"]), _ptr(g["token_gate"]), _ptr(g["res_scale"]), _ptr(workspace),
-          workspace.nbytes, _stream(stream))
+    _call("moe_block_norm_backward", px, f32, ph, pdy, pdn, *vectors, T, d, eps, g["x"].data_ptr(), _ptr(g["h"]),
+          _ptr(g["w_pre"]), _ptr(g["w_post"]), _ptr(g["gate"]), _ptr(g["token_gate"]), _ptr(g["res_scale"]),
+          workspace.data_ptr(), workspace.nbytes, _stream(stream))
     return g
+
+
+@functools.lru_cache(maxsize=4096)
+def _norm_workspace(T: int, d: int) -> int:
+    return int(load().moe_block_norm_backward_workspace_size(T, d))
 
 
 # ---------------------------------------------------------------------------------------------

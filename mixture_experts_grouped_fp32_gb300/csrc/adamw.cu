@@ -5,8 +5,8 @@
 //
 // in fp32.  In the moments every operation is rounded by itself (no contraction into fused multiply-adds),
 // so that they do not depend on how a compiler pairs operations: with 8-bit moments a last-bit difference
-// could move a code.  The step's quotient is a fast division (2 units in the last place of a term that
-// is far smaller than the parameter).  The parameter is rounded once, when it is bf16; a bf16 copy of an
+// could move a code.  The step itself uses fused operations and a fast division (2 units in the last
+// place of a term that is far smaller than the parameter).  The parameter is rounded once, when it is bf16; a bf16 copy of an
 // fp32 parameter can be written along.
 //
 // 8-bit moments: blocks of 256 elements of a tensor share one fp32 scale.  The first moment is kept as
@@ -139,10 +139,11 @@ __device__ __forceinline__ void step_block(const Entry& t, long long block, cons
         from_e4m3(mc, m);
         from_e4m3(vc, r);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            m[j] = mul(m[j], ms);
-            const float root = mul(r[j], vs);
-            r[j] = mul(root, root);
+        for (int j = 0; j < 8; j += 2) {
+            const float2 mj = mul2(make_float2(m[j], m[j + 1]), ms), root = mul2(make_float2(r[j], r[j + 1]), vs);
+            const float2 vj = mul2(root, root);
+            m[j] = mj.x, m[j + 1] = mj.y;
+            r[j] = vj.x, r[j + 1] = vj.y;
         }
     } else {
         const float* mp = static_cast<const float*>(t.m);
@@ -158,13 +159,20 @@ __device__ __forceinline__ void step_block(const Entry& t, long long block, cons
     }
     float v[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const float gj = mul(g[j], factor);
-        m[j] = add(mul(m[j], h.b1), mul(gj, h.c1));
-        v[j] = add(mul(r[j], h.b2), mul(mul(gj, h.c2), gj));
-        r[j] = __fsqrt_rn(v[j]);
-        const float up = __fdividef(mul(m[j], h.step), add(mul(r[j], h.inv_root), h.eps));
-        p[j] = __fsub_rn(mul(p[j], h.decay), up);
+    for (int j = 0; j < 8; j += 2) {
+        // The moments one by one: packed multiplications and additions are contracted.
+#pragma unroll
+        for (int k = j; k < j + 2; ++k) {
+            const float gk = mul(g[k], factor);
+            m[k] = add(mul(m[k], h.b1), mul(gk, h.c1));
+            v[k] = add(mul(r[k], h.b2), mul(mul(gk, h.c2), gk));
+            r[k] = __fsqrt_rn(v[k]);
+        }
+        const float2 num = mul2(make_float2(m[j], m[j + 1]), h.step);
+        const float2 den = fma2(make_float2(r[j], r[j + 1]), h.inv_root, make_float2(h.eps, h.eps));
+        const float2 up = make_float2(__fdividef(num.x, den.x), __fdividef(num.y, den.y));
+        const float2 pj = fma2(make_float2(p[j], p[j + 1]), h.decay, make_float2(-up.x, -up.y));
+        p[j] = pj.x, p[j + 1] = pj.y;
     }
     __nv_bfloat16* copy = static_cast<__nv_bfloat16*>(t.copy);
     if constexpr (VEC) {

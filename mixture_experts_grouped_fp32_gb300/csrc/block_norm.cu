@@ -167,21 +167,21 @@ norm_rows_kernel(const X* __restrict__ x, const __nv_bfloat16* __restrict__ h, c
             if (gate) {
                 const Vec8 g = load8_cached(gate, c);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) wg[v].v[j] *= g.v[j];
+                for (int j = 0; j < 4; ++j) wg[v].set(j, mul2(wg[v].pair(j), g.pair(j)));
             }
             if (res) rs[v] = load8_cached(res, c);
         }
     }
     auto sum_h = [&](int s) {
-        float a = 0.0f;
+        float2 a = make_float2(0.0f, 0.0f);
 #pragma unroll
         for (int v = 0; v < VPT; ++v)
             if (tid + v * nt < d8) {
                 const Vec8 hv = ring8<__nv_bfloat16>(ring, s, v * per_vec + XW);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) a += hv.v[j] * hv.v[j];
+                for (int j = 0; j < 4; ++j) a = fma2(hv.pair(j), hv.pair(j), a);
             }
-        return a;
+        return a.x + a.y;
     };
     float sums[2] = {0.0f, 0.0f};  // of y^2 in this row, of h^2 in the next
     TokenGate token{tgate, rows};
@@ -198,7 +198,7 @@ norm_rows_kernel(const X* __restrict__ x, const __nv_bfloat16* __restrict__ h, c
         const size_t t = row_of(k), base = t * d8;
         const float scale = H ? rsqrtf(sums[1] * inv_d + eps) * token.at(k, row_of) : 0.0f;
         Vec8 yv[VPT];
-        sums[0] = sums[1] = 0.0f;
+        float2 yy = make_float2(0.0f, 0.0f);
 #pragma unroll
         for (int v = 0; v < VPT; ++v) {
             const int c = tid + v * nt;
@@ -207,16 +207,17 @@ norm_rows_kernel(const X* __restrict__ x, const __nv_bfloat16* __restrict__ h, c
                 if (H) {
                     const Vec8 hv = ring8<__nv_bfloat16>(ring, s, v * per_vec + XW);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        yv[v].v[j] = rs[v].v[j] * yv[v].v[j] + wg[v].v[j] * (hv.v[j] * scale);
+                    for (int j = 0; j < 4; ++j)
+                        yv[v].set(j, fma2(rs[v].pair(j), yv[v].pair(j), mul2(wg[v].pair(j), mul2(hv.pair(j), scale))));
                     if (y) store8(y, base + c, yv[v]);
                 }
 #pragma unroll
-                for (int j = 0; j < 8; ++j) sums[0] += yv[v].v[j] * yv[v].v[j];
+                for (int j = 0; j < 4; ++j) yy = fma2(yv[v].pair(j), yv[v].pair(j), yy);
             }
         }
         wait_rows(stages - 2);  // the next row
-        if (H && k + 1 < rows) sums[1] = sum_h(next);
+        sums[0] = yy.x + yy.y;
+        sums[1] = H && k + 1 < rows ? sum_h(next) : 0.0f;
         pair_sum(sums, red[k & 1], warps);
         if (N) {
             const float ry = rsqrtf(sums[0] * inv_d + eps);
@@ -226,7 +227,7 @@ norm_rows_kernel(const X* __restrict__ x, const __nv_bfloat16* __restrict__ h, c
                 if (c < d8) {
                     Vec8 o;
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) o.v[j] = wn[v].v[j] * (yv[v].v[j] * ry);
+                    for (int j = 0; j < 4; ++j) o.set(j, mul2(wn[v].pair(j), mul2(yv[v].pair(j), ry)));
                     store8(n, base + c, o);
                 }
             }
@@ -284,7 +285,7 @@ norm_rows_backward_kernel(const X* __restrict__ x, const __nv_bfloat16* __restri
         if (gate) {
             const Vec8 g = load8_cached(gate, c);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) g_.v[j] *= g.v[j];
+            for (int j = 0; j < 4; ++j) g_.set(j, mul2(g_.pair(j), g.pair(j)));
         }
         r_ = res ? load8_cached(res, c) : ones();
     };
@@ -295,15 +296,19 @@ norm_rows_backward_kernel(const X* __restrict__ x, const __nv_bfloat16* __restri
 #pragma unroll
         for (int j = 0; j < 8; ++j) sA[v].v[j] = sR[v].v[j] = sP[v].v[j] = 0.0f;
     auto sum_h = [&](int s) {
-        float a = 0.0f;
+        float2 a = make_float2(0.0f, 0.0f);
 #pragma unroll
         for (int v = 0; v < VPT; ++v)
             if (tid + v * nt < d8) {
                 const Vec8 hv = ring8<B>(ring, s, v * per_vec + o_h);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) a += hv.v[j] * hv.v[j];
+                for (int j = 0; j < 4; ++j) a = fma2(hv.pair(j), hv.pair(j), a);
             }
-        return a;
+        return a.x + a.y;
+    };
+    // Pair j of the row's y (res x + gate w_post h tgate / rms(h)).
+    auto stream = [&](const Vec8& xv, const Vec8& hv, const Vec8& wg, const Vec8& rs, float hs, int j) {
+        return H ? fma2(rs.pair(j), xv.pair(j), mul2(wg.pair(j), mul2(hv.pair(j), hs))) : xv.pair(j);
     };
     float s2[2] = {0.0f, 0.0f};  // S of this row, sum of h^2 in the next
     TokenGate token{tgate, rows};
@@ -323,7 +328,7 @@ norm_rows_backward_kernel(const X* __restrict__ x, const __nv_bfloat16* __restri
         const float hs = rh * tg;
         float ry = 0.0f, mean = 0.0f;
         if (N) {
-            float s1[2] = {0.0f, 0.0f};  // sum of y^2, sum of dn w_pre y
+            float2 yy = make_float2(0.0f, 0.0f), ey = yy;  // sums of y^2 and of dn w_pre y
 #pragma unroll
             for (int v = 0; v < VPT; ++v) {
                 const int c = tid + v * nt;
@@ -335,19 +340,20 @@ norm_rows_backward_kernel(const X* __restrict__ x, const __nv_bfloat16* __restri
                     Vec8 hv{};
                     if (H) hv = ring8<B>(ring, s, v * per_vec + o_h);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const float a = H ? rs.v[j] * xv.v[j] + wg.v[j] * (hv.v[j] * hs) : xv.v[j];
-                        s1[0] += a * a;
-                        s1[1] += nv.v[j] * wn.v[j] * a;
+                    for (int j = 0; j < 4; ++j) {
+                        const float2 a = stream(xv, hv, wg, rs, hs, j);
+                        yy = fma2(a, a, yy);
+                        ey = fma2(mul2(nv.pair(j), wn.pair(j)), a, ey);
                     }
                 }
             }
+            float s1[2] = {yy.x + yy.y, ey.x + ey.y};
             pair_sum(s1, red1[k & 1], warps);
             ry = rsqrtf(s1[0] * inv_d + eps);
             mean = s1[1] * ry * inv_d;
         }
         Vec8 q[VPT];
-        s2[0] = s2[1] = 0.0f;
+        float2 qh = make_float2(0.0f, 0.0f);
 #pragma unroll
         for (int v = 0; v < VPT; ++v) {
             const int c = tid + v * nt;
@@ -362,32 +368,32 @@ norm_rows_backward_kernel(const X* __restrict__ x, const __nv_bfloat16* __restri
                 if (N) {
                     const Vec8 nv = ring8<B>(ring, s, v * per_vec + o_dn);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const float a = H ? rs.v[j] * xv.v[j] + wg.v[j] * (hv.v[j] * hs) : xv.v[j];
-                        const float yh = a * ry;
-                        sP[v].v[j] += nv.v[j] * yh;
-                        D.v[j] += ry * (nv.v[j] * wn.v[j] - yh * mean);
+                    for (int j = 0; j < 4; ++j) {
+                        const float2 yh = mul2(stream(xv, hv, wg, rs, hs, j), ry);
+                        sP[v].set(j, fma2(nv.pair(j), yh, sP[v].pair(j)));
+                        D.set(j, fma2(fma2(yh, -mean, mul2(nv.pair(j), wn.pair(j))), ry, D.pair(j)));
                     }
                 }
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    o.v[j] = rs.v[j] * D.v[j];
-                    sR[v].v[j] += D.v[j] * xv.v[j];
+                for (int j = 0; j < 4; ++j) {
+                    o.set(j, mul2(rs.pair(j), D.pair(j)));
+                    sR[v].set(j, fma2(D.pair(j), xv.pair(j), sR[v].pair(j)));
                 }
                 store8(dx, base + c, o);
                 if (H) {
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        sA[v].v[j] += D.v[j] * (hv.v[j] * hs);
-                        q[v].v[j] = D.v[j] * wg.v[j];
-                        s2[0] += q[v].v[j] * hv.v[j];
+                    for (int j = 0; j < 4; ++j) {
+                        sA[v].set(j, fma2(D.pair(j), mul2(hv.pair(j), hs), sA[v].pair(j)));
+                        q[v].set(j, mul2(D.pair(j), wg.pair(j)));
+                        qh = fma2(q[v].pair(j), hv.pair(j), qh);
                     }
                 }
             }
         }
         wait_rows(stages - 2);  // the next row
         if (H) {
-            if (k + 1 < rows) s2[1] = sum_h(next);
+            s2[0] = qh.x + qh.y;
+            s2[1] = k + 1 < rows ? sum_h(next) : 0.0f;
             pair_sum(s2, red2[k & 1], warps);
             const float qmean = s2[0] * rh * inv_d;  // mean of q hh
             if (dtgate && tid == 0) dtgate[t] = s2[0] * rh;
@@ -398,7 +404,7 @@ norm_rows_backward_kernel(const X* __restrict__ x, const __nv_bfloat16* __restri
                     const Vec8 hv = ring8<B>(ring, s, v * per_vec + o_h);
                     Vec8 o;
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) o.v[j] = hs * (q[v].v[j] - hv.v[j] * rh * qmean);
+                    for (int j = 0; j < 4; ++j) o.set(j, mul2(fma2(hv.pair(j), -rh * qmean, q[v].pair(j)), hs));
                     store8(dh, base + c, o);
                 }
             }

@@ -8,7 +8,18 @@ namespace moe {
 // Eight consecutive values, loaded and stored as 16-byte words (bf16: one, fp32: two).
 struct Vec8 {
     float v[8];
+    __device__ __forceinline__ float2 pair(int j) const { return make_float2(v[2 * j], v[2 * j + 1]); }
+    __device__ __forceinline__ void set(int j, float2 a) {
+        v[2 * j] = a.x;
+        v[2 * j + 1] = a.y;
+    }
 };
+// Two fp32 operations in one instruction, each rounded as the single one.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ float2 mul2(float2 a, float b) { return __fmul2_rn(a, make_float2(b, b)); }
+__device__ __forceinline__ float2 add2(float2 a, float2 b) { return __fadd2_rn(a, b); }
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
+__device__ __forceinline__ float2 fma2(float2 a, float b, float2 c) { return __ffma2_rn(a, make_float2(b, b), c); }
 __device__ __forceinline__ void unpack_bf16x2(uint32_t u, float& lo, float& hi) {
     lo = __uint_as_float(u << 16);
     hi = __uint_as_float(u & 0xffff0000u);

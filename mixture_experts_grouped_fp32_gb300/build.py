@@ -5,6 +5,10 @@
 The CUDA runtime is linked statically, and the driver's tensor-map encoder is reached through
 ``cudaGetDriverEntryPointByVersion``, so the library loads on a machine without a GPU driver
 (its entry points then return MOE_ERR_CUDA).
+
+Beside it, ``_moe_fast.so``: the binding's usual calls without Python's share of their cost (g++ against
+torch's headers).  Its functions only forward to ``libmoe.so``; where it cannot be built the binding
+works without it.
 """
 from __future__ import annotations
 
@@ -14,12 +18,14 @@ import glob
 import os
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libmoe.so")
+FAST = os.path.join(HERE, "_moe_fast.so")
 
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -38,11 +44,38 @@ def _compile(src: str, verbose: bool) -> tuple[str, str]:
     return obj, res.stderr
 
 
+def _build_fast() -> str:
+    """Compiles the fast binding; returns why not if it cannot be."""
+    import torch
+    t = os.path.dirname(torch.__file__)
+    tmp = FAST + ".tmp"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I" + os.path.join(t, "include"),
+           "-I" + os.path.join(t, "include", "torch", "csrc", "api", "include"),
+           "-I" + sysconfig.get_paths()["include"], "-I" + os.path.join(os.path.dirname(os.path.dirname(NVCC)), "include"),
+           os.path.join(CSRC, "binding.cpp"), "-o", tmp, "-L" + os.path.join(t, "lib"), "-ltorch_python", "-ltorch_cpu",
+           "-lc10", "-lc10_cuda", "-ldl"]
+    try:
+        res = subprocess.run(cmd, capture_output=True, text=True)
+    except OSError as e:
+        return str(e)
+    if res.returncode != 0:
+        return res.stderr
+    os.replace(tmp, FAST)
+    return ""
+
+
 def build(verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     srcs = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
-    with cf.ThreadPoolExecutor(max_workers=len(srcs)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=len(srcs) + 1) as ex:
+        fast = ex.submit(_build_fast)
         results = list(ex.map(lambda s: _compile(s, verbose), srcs))
+        why = fast.result()
+    if why:
+        if os.path.exists(FAST):
+            os.remove(FAST)  # an older one could expect another library
+        sys.stderr.write(f"_moe_fast.so was not built (the binding works without it):\n{why[-2000:]}\n")
     if verbose:
         for _, log in results:
             sys.stderr.write(log)

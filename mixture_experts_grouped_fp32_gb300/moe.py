@@ -112,11 +112,12 @@ class MoeError(RuntimeError):
 _lock = threading.Lock()
 _lib = None
 _fns: dict = {}  # the bound entry points of the loaded library, by name
+_fast = None  # the usual calls in C++ (_moe_fast.so), where it was built
 
 
 def load(path: str = LIB_PATH) -> ctypes.CDLL:
     """Load ``libmoe.so`` (once).  Raises if it has not been built."""
-    global _lib
+    global _lib, _fast
     with _lock:
         if _lib is None:
             if not os.path.exists(path):
@@ -128,6 +129,10 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
                 fn.argtypes = args
                 fn.restype = res
                 _fns[name] = fn
+            if os.path.exists(os.path.join(_HERE, "_moe_fast.so")):
+                from . import _moe_fast
+                _moe_fast.init(path)
+                _fast = _moe_fast
             _lib = lib
     return _lib
 
@@ -144,6 +149,13 @@ def _call(name: str, *args) -> None:
     rc = _fn(name)(*args)
     if rc != 0:
         raise MoeError(name, rc, _fn("moe_last_error_string")().decode())
+
+
+def _done(name: str, result):
+    """The result of a call through ``_fast`` (an int is the C call's error code)."""
+    if type(result) is int and result != 0:
+        raise MoeError(name, result, _fn("moe_last_error_string")().decode())
+    return result
 
 
 def _ptr(t: torch.Tensor | None):
@@ -896,10 +908,13 @@ def grouped_mm_workspace_size(mode: int, M: int, K: int, N: int, E: int) -> int:
     return int(load().moe_grouped_mm_workspace_size(mode, M, K, N, E))
 
 
+_MM_OUT = (torch.bfloat16, torch.float32)
+
+
 def _mm_args(mode, M, K, N, E, out, out_dtype, shape, workspace, device, stream):
     if out is not None:
         out_dtype = out.dtype
-    if out_dtype not in (torch.bfloat16, torch.float32):
+    if out_dtype not in _MM_OUT:
         raise ValueError(f"out must be bfloat16 or float32, got {out_dtype}")
     out = _out(out, shape, out_dtype, device, stream)
     if workspace is None:
@@ -914,6 +929,10 @@ def grouped_mm(a, b, offsets, transpose_b: bool = False, out=None, out_dtype=tor
     """Products grouped by expert: out[r] = a[r] @ b[e] for the rows r of segment e of ``offsets`` [E+1]
     int32, with b [E, K, N]; or a[r] @ b[e].T with ``transpose_b`` and b [E, N, K].  a [M, K] and b are
     bf16; out [M, N] is bf16 or fp32.  Rows outside the segments are left as they are."""
+    if _fast is not None and out is None and workspace is None and stream is None and out_dtype in _MM_OUT:
+        r = _fast.grouped_mm(a, b, offsets, transpose_b, out_dtype is torch.float32, status)
+        if r is not None:
+            return _done("moe_grouped_mm", r)
     if a.dim() != 2 or b.dim() != 3:
         raise ValueError("a must be [M, K] and b [E, K, N] (or [E, N, K] with transpose_b)")
     M, K = a.shape
@@ -932,6 +951,12 @@ def grouped_mm_wgrad(a, g, offsets, out=None, out_dtype=torch.float32, accumulat
                      status=None, stream=None):
     """Weight gradient of a grouped product: out[e] = a[rows of e].T @ g[rows of e], [E, K, N] fp32 or
     bf16, zero for an empty segment; with ``accumulate`` (fp32 ``out`` given) it is added to out."""
+    if _fast is not None and workspace is None and stream is None:
+        dtype = out_dtype if out is None else out.dtype
+        if dtype in _MM_OUT:
+            r = _fast.grouped_mm_wgrad(a, g, offsets, out, dtype is torch.float32, accumulate, status)
+            if r is not None:
+                return _done("moe_grouped_mm_wgrad", r)
     if a.dim() != 2 or g.dim() != 2 or offsets.dim() != 1:
         raise ValueError("a must be [M, K], g [M, N] and offsets [E + 1]")
     M, K = a.shape
@@ -949,6 +974,10 @@ def grouped_mm_wgrad(a, g, offsets, out=None, out_dtype=torch.float32, accumulat
 def swiglu(gu, w=None, h=None, stream=None):
     """h = w * silu(g) * u, bf16 [M, f], from gu = [g | u] bf16 [M, 2f] and a weight per row (fp32 [M],
     or None for 1)."""
+    if _fast is not None and h is None and stream is None:
+        r = _fast.swiglu(gu, w)
+        if r is not None:
+            return _done("moe_swiglu", r)
     M, f, pg, pw = _gu_dims(gu, w)
     h = _out(h, (M, f), torch.bfloat16, gu.device, stream, "h")
     _call("moe_swiglu", pg, pw, M, f, h.data_ptr(), _stream(stream))
@@ -965,6 +994,10 @@ def _gu_dims(gu, w):
 def swiglu_backward(gu, dh, w=None, want_h: bool = False, dgu=None, dw=None, h=None, stream=None):
     """Gradient of ``swiglu``: (dgu bf16 [M, 2f], dw fp32 [M] or None without w, h bf16 [M, f] or None
     without ``want_h``), from dh bf16 [M, f]."""
+    if _fast is not None and dgu is None and dw is None and h is None and stream is None:
+        r = _fast.swiglu_backward(gu, dh, w, want_h)
+        if r is not None:
+            return _done("moe_swiglu_backward", r)
     M, f, pg, pw = _gu_dims(gu, w)
     pd = _arg(dh, torch.bfloat16, (M, f), "dh")
     dgu = _out(dgu, (M, 2 * f), torch.bfloat16, gu.device, stream, "dgu")
@@ -998,6 +1031,10 @@ def block_norm(x, w_pre=None, h=None, w_post=None, gate=None, token_gate=None, r
     x [T, d] bf16 or fp32 (the residual stream), h [T, d] bf16 (the block's output); w_pre, w_post, gate,
     res_scale fp32 [d], token_gate fp32 [T].  Returns (y, n): y has x's type, n is bf16.  Without ``h``
     (before the first block) y is x and is returned as None; without ``w_pre`` n is None."""
+    if _fast is not None and y is None and n is None and stream is None:
+        r = _fast.block_norm(x, w_pre, h, w_post, gate, token_gate, res_scale, eps)
+        if r is not None:
+            return _done("moe_block_norm", r)
     T, d, f32, px, ph, *vectors = _norm_inputs(x, w_pre, h, w_post, gate, token_gate, res_scale)
     y = _out(y, (T, d), x.dtype, x.device, stream, "y") if h is not None else None
     n = _out(n, (T, d), torch.bfloat16, x.device, stream, "n") if w_pre is not None else None
@@ -1013,6 +1050,10 @@ def block_norm_backward(x, dy=None, dn=None, w_pre=None, h=None, w_post=None, ga
     """Gradients of ``block_norm``, as a dict by the inputs' names (None for an input that was not given):
     x (x's type) and h (bf16) [T, d], the vectors' in fp32.  dy (x's type) and dn (bf16) [T, d]; one of
     them may be None (zero).  The same inputs as the forward call; y is recomputed."""
+    if _fast is not None and workspace is None and stream is None:
+        r = _fast.block_norm_backward(x, dy, dn, w_pre, h, w_post, gate, token_gate, res_scale, eps)
+        if r is not None:
+            return dict(zip(NORM_GRADS, _done("moe_block_norm_backward", r)))
     T, d, f32, px, ph, *vectors = _norm_inputs(x, w_pre, h, w_post, gate, token_gate, res_scale)
     pdy, pdn = _opt(dy, x.dtype, (T, d), "dy"), _opt(dn, torch.bfloat16, (T, d), "dn")
     if workspace is None:
@@ -1089,6 +1130,11 @@ def adamw_step(params, grads, m, v, lr: float, beta1: float = 0.9, beta2: float 
     the device) multiplies the gradients by its first value and lr by its second."""
     if len(params) == 0:
         return
+    if _fast is not None and step_tensor is None and factors is None and stream is None:
+        r = _fast.adamw_step(params, grads, m, v, m_scales, v_scales, copies, lr, beta1, beta2, eps, weight_decay, step)
+        if r is not None:
+            _done("moe_adamw_step", r)
+            return
     pt, gt, st = params[0].dtype, grads[0].dtype if len(grads) else None, m[0].dtype if len(m) else None
     for t, n in ((pt, "params"), (gt, "grads")):
         if t not in (torch.bfloat16, torch.float32):

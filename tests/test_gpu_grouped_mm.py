@@ -61,10 +61,17 @@ def _run(moe, a, b, offs, way, **kw):
     return moe.grouped_mm(a, b, offs, transpose_b=way == "dgrad", **kw)
 
 
-@pytest.fixture(scope="module")
-def moe():
+@pytest.fixture(scope="module", params=["fast", "ctypes"])
+def moe(request):
+    """The binding with its C++ calls, and with ctypes alone."""
     from mixture_experts_grouped_fp32_gb300 import moe as m
-    return m
+    m.load()
+    fast = m._fast
+    if request.param == "fast" and fast is None:
+        pytest.skip("_moe_fast.so was not built here")
+    m._fast = fast if request.param == "fast" else None
+    yield m
+    m._fast = fast
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])

@@ -15,10 +15,17 @@ BF16, F32, D = torch.bfloat16, torch.float32, torch.float64
 FP32_SLACK = 2.0 ** -18
 
 
-@pytest.fixture(scope="module")
-def moe():
+@pytest.fixture(scope="module", params=["fast", "ctypes"])
+def moe(request):
+    """The binding with its C++ calls, and with ctypes alone."""
     from mixture_experts_grouped_fp32_gb300 import moe as m
-    return m
+    m.load()
+    fast = m._fast
+    if request.param == "fast" and fast is None:
+        pytest.skip("_moe_fast.so was not built here")
+    m._fast = fast if request.param == "fast" else None
+    yield m
+    m._fast = fast
 
 
 def check(got, ref, mag, what):

@@ -65,7 +65,7 @@ constexpr int MAX_E = 256;
 constexpr int MAX_SPLIT = 16;
 constexpr uint16_t BOTH_CTAS = 0x3;
 // Warps: 0 copies, 1 tensor memory and MMAs, then the epilogue's groups of eight, then (weight gradient)
-// one that zeroes segment ends.
+// one that zeroes segment ends and one that stores the gradients of empty segments.
 constexpr int kEpiWarps = 8;
 // bf16 outputs: one epilogue group for each accumulator, so that short items (a few blocks of
 // reduction) do not wait for one group to read, convert and store tile after tile.  fp32 outputs: one
@@ -75,7 +75,7 @@ constexpr int epi_groups() { return sizeof(OUT) == 4 ? 1 : 2; }
 template <typename OUT>
 constexpr int fix_warp() { return 2 + kEpiWarps * epi_groups<OUT>(); }
 template <int MODE, typename OUT>
-constexpr int num_threads() { return 32 * (fix_warp<OUT>() + (MODE == kMmWgrad ? 1 : 0)); }
+constexpr int num_threads() { return 32 * (fix_warp<OUT>() + (MODE == kMmWgrad ? 2 : 0)); }
 // fp32 outputs: blocks of 64 summed in tensor memory before the partial sum moves to registers.
 constexpr int CHUNK = 8;
 template <typename OUT>
@@ -482,6 +482,7 @@ grouped_mm_kernel(const __grid_constant__ Maps maps, const int32_t* __restrict__
         bool aborted = false;
         for (int i = pair_id; i < total && !aborted; i += num_pairs) {
             const Item it = cur.at(i);
+            if (it.red0 >= it.red1) continue;  // nothing to add up
             const int n = it.f0 + 128 * rank + 32 * quarter + lane;
             const size_t row0 = WGRAD ? static_cast<size_t>(it.e) * K + it.r0 : static_cast<size_t>(c.seg[it.e]) + it.r0;
             OUT* dst = out + it.slice * slice_elems + (row0 + col0) * N + n;
@@ -531,25 +532,22 @@ grouped_mm_kernel(const __grid_constant__ Maps maps, const int32_t* __restrict__
                     }
                 }
             } else {
-                const bool any = it.red0 < it.red1;
                 if (epi_groups<OUT>() > 1 && acc != group) {  // the other group's
-                    if (any) pass();
+                    pass();
                     continue;
                 }
-                if (any && !take()) break;
+                if (!take()) {
+                    aborted = true;
+                    break;
+                }
                 // Neighbouring lanes exchange halves of their pairs of rows: an even lane then holds columns n
                 // and n + 1 of the first row, an odd lane n - 1 and n of the second, one 4-byte store each.
                 const uint32_t sel = lane & 1 ? 0x3276u : 0x5410u;
 #pragma unroll 1
                 for (int j0 = 0; j0 < 128 && col0 + j0 < it.rows; j0 += 32) {
                     uint32_t v[32];
-                    if (any) {
-                        ptx::tmem_ld_32x32b_x32(lane_addr + acc * ACC_COLS + j0, v);
-                        ptx::tmem_ld_wait();
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) v[j] = 0u;
-                    }
+                    ptx::tmem_ld_32x32b_x32(lane_addr + acc * ACC_COLS + j0, v);
+                    ptx::tmem_ld_wait();
                     OUT* p = dst + static_cast<size_t>(j0) * N - (lane & 1) + static_cast<size_t>(lane & 1) * N;
                     const int nr = it.rows - col0 - j0 - (lane & 1);
 #pragma unroll
@@ -559,10 +557,37 @@ grouped_mm_kernel(const __grid_constant__ Maps maps, const int32_t* __restrict__
                         if (2 * j < nr && n < N) *reinterpret_cast<uint32_t*>(p) = __byte_perm(own, other, sel);
                     }
                 }
-                if (any) {
-                    give();
-                    pass();
-                }
+                give();
+                pass();
+            }
+        }
+    } else if (WGRAD && warp == fix_warp<OUT>() + 1) {
+        // ------- zeros where there is nothing to add up (empty segments, slices past a short one) -------
+        // A warp of its own: in the epilogue's loop this cost the other items registers (6 % of the gradients
+        // of 256 experts).  An empty expert's tiles share its [K, N] as one run of memory, in equal parts: by
+        // tiles, rows that do not start at whole 32-byte sectors took twice the time.
+        const size_t slice_elems = static_cast<size_t>(E) * K * N;
+        auto fill = [&](uint4* p, long long from, long long to, int stride) {
+            long long w = from;
+            for (; w + 7 * stride < to; w += 8 * stride)
+#pragma unroll
+                for (int k = 0; k < 8; ++k) p[w + k * stride] = make_uint4(0, 0, 0, 0);
+            for (; w < to; w += stride) p[w] = make_uint4(0, 0, 0, 0);
+        };
+        for (int i = pair_id; i < total; i += num_pairs) {
+            const Item it = cur.at(i);
+            if (it.red0 < it.red1) continue;
+            OUT* z = out + it.slice * slice_elems + static_cast<size_t>(it.e) * K * N;
+            if (it.red_rows == 0) {
+                const long long words = static_cast<long long>(K) * N * sizeof(OUT) / 16;
+                const int tiles = (cur.next - cur.start) / ksplit, t = (i - cur.start) / ksplit;
+                fill(reinterpret_cast<uint4*>(z), words * t / tiles + 32 * rank + lane, words * (t + 1) / tiles, 64);
+            } else {
+                constexpr int per_word = 16 / sizeof(OUT), lanes = 128 / per_word, step = 32 / lanes;
+                const int col = it.f0 + 128 * rank + (lane % lanes) * per_word, r = lane / lanes;
+                if (col < N)
+                    for (int j = r; j < it.rows; j += step)
+                        *reinterpret_cast<uint4*>(z + static_cast<size_t>(it.r0 + j) * N + col) = make_uint4(0, 0, 0, 0);
             }
         }
     }

@@ -174,6 +174,28 @@ def test_split_reduction(moe, way, M, K, N, E):
         _check(acc, 2 * ref, 2 * mag, n + 2, way)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("K,N", [(264, 520), (904, 72), (256, 256)])
+def test_wgrad_of_mostly_empty_segments(moe, K, N, dtype):
+    counts = [0] * 20 + [3] + [0] * 7 + [70] + [0] * 30
+    a, g, offs = _inputs(counts, K, N, "wgrad")
+    out = torch.full((len(counts), K, N), 9.0, dtype=dtype, device="cuda")
+    _run(moe, a, g, offs, "wgrad", out=out)
+    ref, mag = _reference(a, g, offs, "wgrad")
+    _check(out, ref, mag, 70, "mostly empty")
+
+
+def test_wgrad_split_with_short_segments(moe):
+    """Slices of a split reduction that lie past a short segment's rows are zero."""
+    counts = [3, 4300]
+    assert moe.grouped_mm_workspace_size(2, sum(counts), 72, 136, 2) > 0
+    a, g, offs = _inputs(counts, 72, 136, "wgrad")
+    a = (a.float() / 64).bfloat16()
+    ref, mag = _reference(a, g, offs, "wgrad")
+    for dtype in (torch.float32, torch.bfloat16):
+        _check(_run(moe, a, g, offs, "wgrad", out_dtype=dtype), ref, mag, 4300, "split, short segments")
+
+
 def test_bad_offsets_write_nothing_and_set_the_status(moe):
     a, b, _ = _inputs([10], 64, 64, "fwd")
     for offs in ([0, 11], [5, 3], [-1, 10]):

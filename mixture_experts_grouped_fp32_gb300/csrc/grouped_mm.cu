@@ -717,8 +717,11 @@ cudaError_t launch_any(const GroupedMmArgs& a, int num_sms, cudaStream_t s, cons
 
 // The reduction is split when its tiles would leave most CTA pairs idle (serving a few tokens, or the
 // weight gradient of few experts over many rows).  Tiles are bounded above from the shape alone (the
-// row counts are on the device).  Among the slice counts that leave each slice at least 16 blocks of 64
-// and add at most a quarter to the bytes moved, the one with the fullest last round is taken.
+// row counts are on the device).  A slice keeps at least 16 blocks of 64, and the slices add at most a
+// quarter to the bytes moved.  As many slices as one round of CTA pairs holds; more only if that leaves
+// over a quarter of the pairs idle and the fuller rounds win a sixth (two rows of 14336 against 4096
+// columns, 32 tiles: 45.9 us in 2 slices, one round 84 % full; 48.9 in 7, three rounds 98 % full; 73.7
+// unsplit).
 int grouped_mm_ksplit(int mode, int M, int K, int N, int E, int num_sms) {
     const long long pairs = num_sms / 2;
     const long long f_tiles = (N + TILE_F - 1) / TILE_F;
@@ -737,18 +740,16 @@ int grouped_mm_ksplit(int mode, int M, int K, int N, int E, int num_sms) {
         bytes = 2ll * M * K + 2ll * active * K * N;
     }
     if (tiles * 4 > pairs * 3 || tiles == 0) return 1;
-    int best = 1;
-    double best_eff = 0.0;
-    for (int s = 1; s <= MAX_SPLIT; ++s) {
-        if (s > 1 && (blocks / s < 16 || 8ll * s * out_elems * 4 > bytes)) break;
-        const long long rounds = (tiles * s + pairs - 1) / pairs;
-        const double eff = static_cast<double>(tiles * s) / static_cast<double>(rounds * pairs);
-        if (eff > best_eff * 1.02) {
-            best_eff = eff;
-            best = s;
-        }
-    }
-    return best;
+    auto allowed = [&](long long n) { return n <= MAX_SPLIT && blocks / n >= 16 && 32ll * n * out_elems <= bytes; };
+    auto full = [&](long long n) {
+        return static_cast<double>(tiles * n) / static_cast<double>((tiles * n + pairs - 1) / pairs * pairs);
+    };
+    long long best = pairs / tiles > 1 ? pairs / tiles : 1;
+    while (best > 1 && !allowed(best)) --best;
+    if (full(best) < 0.75)
+        for (long long n = best + 1; allowed(n); ++n)
+            if (full(n) > full(best) * 1.17) best = n;
+    return static_cast<int>(best);
 }
 
 cudaError_t launch_grouped_mm(int mode, const GroupedMmArgs& a, int num_sms, cudaStream_t s, const char** why) {

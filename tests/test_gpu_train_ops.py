@@ -211,6 +211,27 @@ def test_block_norm_zero_rows_and_missing_gradients(moe):
     assert g["x"].shape == (0, 264) and all((g[k] == 0).all() for k in ("w_pre", "w_post", "gate", "res_scale"))
 
 
+@pytest.mark.parametrize("xt", [BF16, F32])
+def test_block_norm_of_tensors_aligned_to_16_bytes(moe, xt):
+    """Pieces of larger buffers that start at 16 bytes past a multiple of 32: the same results."""
+    v, dy, dn = norm_inputs(9, 264, xt, True, True, True, seed=2)
+
+    def moved(t):
+        skip = 16 // t.element_size()
+        buf = torch.zeros(t.numel() + skip, dtype=t.dtype, device="cuda")
+        buf[skip:].copy_(t.reshape(-1))
+        return buf[skip:].view(t.shape)
+    at = {k: t.cuda() for k, t in v.items()}
+    off = {k: t.cuda() if k == "token_gate" else moved(t) for k, t in v.items()}
+    for a, b in zip(moe.block_norm(**at), moe.block_norm(**off)):
+        assert torch.equal(a, b)
+    ga = moe.block_norm_backward(dy=dy.cuda(), dn=dn.cuda(), **at)
+    gb = moe.block_norm_backward(dy=moved(dy), dn=moved(dn), **off)
+    assert all(torch.equal(ga[k], gb[k]) for k in ga)
+    y = moved(torch.zeros(9, 264, dtype=xt))
+    assert torch.equal(moe.block_norm(**at, y=y)[0], moe.block_norm(**at)[0])
+
+
 def test_block_norm_difference(moe):
     """Directional derivatives against central differences of the kernel's forward pass (fp32 stream)."""
     v, dy, _ = norm_inputs(6, 256, F32, True, False, True, seed=4)
@@ -256,11 +277,11 @@ def blocks(t):
     return torch.nn.functional.pad(t, (0, -t.numel() % 256)).view(-1, 256)
 
 
-@pytest.mark.parametrize("shift", [0, 1, 3])
+@pytest.mark.parametrize("shift", [0, 1, 3, 4])
 @pytest.mark.parametrize("pt,gt", [(F32, F32), (F32, BF16), (BF16, F32), (BF16, BF16)])
 def test_adamw32(moe, pt, gt, shift):
     g = torch.Generator().manual_seed(1)
-    # shift: pieces that start one or three elements off the alignment of 16 bytes
+    # shift: pieces that start off the alignment of 16 bytes (1, 3), or off that of 32 (4)
     make = lambda n, dt, f: f(torch.randn(n + shift, generator=g)).to(dt)
     ps = [make(n, pt, lambda t: t) for n in SIZES]
     gs = [make(n, gt, lambda t: 0.1 * t) for n in SIZES]
@@ -282,7 +303,7 @@ def test_adamw32(moe, pt, gt, shift):
             assert torch.equal(t[:shift].cpu(), before[:shift])  # the neighbours stay
 
 
-@pytest.mark.parametrize("shift", [0, 1])
+@pytest.mark.parametrize("shift", [0, 1, 8])
 @pytest.mark.parametrize("pt,gt", [(F32, BF16), (BF16, F32)])
 def test_adamw8(moe, pt, gt, shift):
     """8-bit moments: values from codes, a 64-bit step, and codes of the result — equal to the documented

@@ -562,7 +562,8 @@ typedef struct {
 /* One AdamW step over `count` tensors (a host array, read during the call).  With g' = c g:
  *   m = beta1 m + (1 - beta1) g';   v = beta2 v + (1 - beta2) g'^2;
  *   p = p (1 - lr weight_decay) - lr / (1 - beta1^t) * m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
- * in fp32, each operation rounded by itself.  state_bits 32: m and v fp32.  state_bits 8: blocks of 256
+ * in fp32 (the moments' operations each rounded by itself, so that they are the same everywhere).
+ * state_bits 32: m and v fp32.  state_bits 8: blocks of 256
  * elements; m = code * m_scale, m_scale = max|m| / 448; sqrt(v) = code * v_scale likewise, where a root
  * that is not zero has at least the code of 2^-9; a block whose maximum is below 2^-100 has codes 0 and
  * scale 1 (so zeroed codes and any finite scales are a fresh state); a block with a NaN or an infinity

@@ -22,6 +22,10 @@
 // last sum of row k (forward: one reduction per row, backward: two).  Rows too wide for two of them in
 // shared memory (d > 8192) take the plain kernels, which hold one row in registers.
 //
+// Measured: 4096 x 7168 with an fp32 stream 62 us (5.6 TB/s; 54 under ncu), gradient of 4096 x 4096 52 us
+// (3.8 TB/s: 16 warps per SM, whose instruction latency shows; an earlier form that loaded tgate in the row
+// that uses it took 78).
+//
 // The backward pass keeps the column sums A, dres and dw_pre of all rows that a block visits in
 // registers, writes them once per block, and a second kernel adds the blocks in a fixed order: no
 // atomics, the same result on every run.

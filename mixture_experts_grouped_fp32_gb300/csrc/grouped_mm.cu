@@ -380,7 +380,9 @@ grouped_mm_kernel(const __grid_constant__ Maps maps, const int32_t* __restrict__
                 const uint32_t d_tmem = tmem_base + acc * ACC_COLS;
                 const int c1 = min(it.red1, c0 + chunk_blocks<OUT>());
                 for (int kb = c0; kb < c1; ++kb) {
-                    if (!ptx::mbar_wait(&c.full[stage], phase, abort_flag)) {
+                    // (Weight gradient: the other CTA's zeroing warp arrives after its own writes.)
+                    if (!(WGRAD ? ptx::mbar_wait_cluster(&c.full[stage], phase, abort_flag)
+                                : ptx::mbar_wait(&c.full[stage], phase, abort_flag))) {
                         raise_abort(c, status);
                         aborted = true;
                         break;

@@ -721,41 +721,47 @@ cudaError_t launch_any(const GroupedMmArgs& a, int num_sms, cudaStream_t s, cons
 
 }  // namespace
 
-// The reduction is split when its tiles would leave most CTA pairs idle (serving a few tokens, or the
-// weight gradient of few experts over many rows).  Tiles are bounded above from the shape alone (the
-// row counts are on the device).  A slice keeps at least 16 blocks of 64, and the slices add at most a
-// quarter to the bytes moved.  As many slices as one round of CTA pairs holds; more only if that leaves
-// over a quarter of the pairs idle and the fuller rounds win a sixth (two rows of 14336 against 4096
-// columns, 32 tiles: 45.9 us in 2 slices, one round 84 % full; 48.9 in 7, three rounds 98 % full; 73.7
-// unsplit).
+// The reduction is split when its tiles would leave CTA pairs idle (serving a few tokens, few experts, the
+// weight gradient of few experts over many rows).  The row counts are on the device, so the tiles
+// are estimated from the shape, and the longest segment is taken as three times the average.  The slice count
+// is the one with the least modelled time: rounds of CTA pairs x blocks per slice x 0.34 us (a block's
+// products, or its share of the memory rate), not less than the bytes take; 1.5 us for each round's fill and
+// drain; for slices the join's launch (3 us) and their way to the L2 and back.  Two rows of 14336 against
+// 4096 columns (32 tiles): 45.9 us in 2 slices, 48.9 in 7, 73.7 unsplit; 1551 rows of 13136 against 344
+// columns (14 tiles): 43 us in 2 slices, 30 in 5; 7 experts' gradients of 112 x 80 from 7597 rows: 27 us
+// unsplit, 14 in 10.
 int grouped_mm_ksplit(int mode, int M, int K, int N, int E, int num_sms) {
     const long long pairs = num_sms / 2;
     const long long f_tiles = (N + TILE_F - 1) / TILE_F;
     const long long active = M < E ? M : E;
-    long long tiles, blocks, out_elems, bytes;
+    long long tiles, blocks;
+    double out_elems, bytes;
     if (mode == kMmWgrad) {
         tiles = E * f_tiles * ((K + TILE_R - 1) / TILE_R);
-        blocks = M / E / BK;
-        out_elems = static_cast<long long>(E) * K * N;
-        bytes = 2ll * M * (K + N) + 4 * out_elems;
+        blocks = M / BK;
+        if (blocks > 3 * blocks / E) blocks = 3 * blocks / E;
+        out_elems = static_cast<double>(E) * K * N;
+        bytes = 2.0 * M * (static_cast<double>(K) + N) + 4 * out_elems;
     } else {
-        const long long long_tiles = M / TILE_R;
-        tiles = f_tiles * (active > long_tiles ? active : long_tiles);
+        // Segments shorter than a tile take one each, longer ones half a tile more than their rows.
+        tiles = f_tiles * (M < TILE_R * active ? active + M / (2 * TILE_R) : M / TILE_R + (active + 1) / 2);
         blocks = K / BK;
-        out_elems = static_cast<long long>(M) * N;
-        bytes = 2ll * M * K + 2ll * active * K * N;
+        out_elems = static_cast<double>(M) * N;
+        bytes = 2.0 * M * K + 2.0 * active * K * N;
     }
-    if (tiles * 4 > pairs * 3 || tiles == 0) return 1;
-    auto allowed = [&](long long n) { return n <= MAX_SPLIT && blocks / n >= 16 && 32ll * n * out_elems <= bytes; };
-    auto full = [&](long long n) {
-        return static_cast<double>(tiles * n) / static_cast<double>((tiles * n + pairs - 1) / pairs * pairs);
-    };
-    long long best = pairs / tiles > 1 ? pairs / tiles : 1;
-    while (best > 1 && !allowed(best)) --best;
-    if (full(best) < 0.75)
-        for (long long n = best + 1; allowed(n); ++n)
-            if (full(n) > full(best) * 1.17) best = n;
-    return static_cast<int>(best);
+    if (tiles == 0 || tiles > pairs) return 1;
+    int best = 1;
+    double best_us = 0.0;
+    for (int n = 1; n <= MAX_SPLIT && (n == 1 || blocks / n >= 4); ++n) {
+        const double rounds = static_cast<double>((tiles * n + pairs - 1) / pairs);
+        const double work = rounds * static_cast<double>((blocks + n - 1) / n) * 0.34, memory = bytes / 6.5e6;
+        const double us = (work > memory ? work : memory) + 1.5 * rounds + (n > 1 ? 3.0 + n * out_elems * 8 / 8e6 : 0.0);
+        if (n == 1 || us < 0.97 * best_us) {
+            best = n;
+            best_us = us;
+        }
+    }
+    return best;
 }
 
 cudaError_t launch_grouped_mm(int mode, const GroupedMmArgs& a, int num_sms, cudaStream_t s, const char** why) {

@@ -71,19 +71,19 @@ constexpr uint16_t BOTH_CTAS = 0x3;
 // Warps: 0 copies, 1 tensor memory and MMAs, then the epilogue's groups of eight, then (weight gradient)
 // one that zeroes segment ends and one that stores the gradients of empty segments.
 constexpr int kEpiWarps = 8;
-// bf16 outputs: one epilogue group for each accumulator, so that short items (a few blocks of
-// reduction) do not wait for one group to read, convert and store tile after tile.  fp32 outputs: one
-// group, which keeps the tile's running sums in registers across both accumulators.
-template <typename OUT>
-constexpr int epi_groups() { return sizeof(OUT) == 4 ? 1 : 2; }
-template <typename OUT>
-constexpr int fix_warp() { return 2 + kEpiWarps * epi_groups<OUT>(); }
-template <int MODE, typename OUT>
-constexpr int num_threads() { return 32 * (fix_warp<OUT>() + (MODE == kMmWgrad ? 2 : 0)); }
-// fp32 outputs: blocks of 64 summed in tensor memory before the partial sum moves to registers.
+// CHUNKED: fp32 outputs of reductions over more than CHUNK blocks of 64, whose partial sums move from tensor
+// memory to registers after every CHUNK of them: one epilogue group keeps the tile's sums across both
+// accumulators.  Otherwise one group for each accumulator, so that short items (a few blocks of reduction)
+// do not wait for one group to read, convert and store tile after tile.
 constexpr int CHUNK = 8;
-template <typename OUT>
-constexpr int chunk_blocks() { return sizeof(OUT) == 4 ? CHUNK : 1 << 20; }
+template <bool CHUNKED>
+constexpr int chunk_blocks() { return CHUNKED ? CHUNK : 1 << 20; }
+template <bool CHUNKED>
+constexpr int epi_groups() { return CHUNKED ? 1 : 2; }
+template <bool CHUNKED>
+constexpr int fix_warp() { return 2 + kEpiWarps * epi_groups<CHUNKED>(); }
+template <int MODE, bool CHUNKED>
+constexpr int num_threads() { return 32 * (fix_warp<CHUNKED>() + (MODE == kMmWgrad ? 2 : 0)); }
 constexpr int SMEM_BYTES = 232448;
 
 struct Ctl {
@@ -185,8 +185,8 @@ struct Maps {
     int f_blocks, r_blocks;
 };
 
-template <int MODE, typename OUT>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(num_threads<MODE, OUT>(), 1)
+template <int MODE, typename OUT, bool CHUNKED>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(num_threads<MODE, CHUNKED>(), 1)
 grouped_mm_kernel(const __grid_constant__ Maps maps, const int32_t* __restrict__ offsets, int M, int K, int N, int E,
                   int ksplit, int accumulate, OUT* __restrict__ out, int32_t* __restrict__ status) {
     constexpr bool WGRAD = MODE == kMmWgrad;
@@ -370,7 +370,7 @@ grouped_mm_kernel(const __grid_constant__ Maps maps, const int32_t* __restrict__
             if (it.red0 >= it.red1) continue;  // nothing to reduce: the epilogue stores zeros
             const uint32_t idesc = ptx::idesc_bf16_f32(TILE_F, static_cast<uint32_t>(it.ntok),
                                                        /*a_mn=*/MODE == kMmTransB ? 0 : 1, /*b_mn=*/WGRAD ? 1 : 0);
-            for (int c0 = it.red0; c0 < it.red1 && !aborted; c0 += chunk_blocks<OUT>()) {
+            for (int c0 = it.red0; c0 < it.red1 && !aborted; c0 += chunk_blocks<CHUNKED>()) {
                 if (!ptx::mbar_wait(&c.tempty[acc], acc_phase ^ 1u, abort_flag)) {
                     raise_abort(c, status);
                     aborted = true;
@@ -378,7 +378,7 @@ grouped_mm_kernel(const __grid_constant__ Maps maps, const int32_t* __restrict__
                 }
                 ptx::tc_fence_after();
                 const uint32_t d_tmem = tmem_base + acc * ACC_COLS;
-                const int c1 = min(it.red1, c0 + chunk_blocks<OUT>());
+                const int c1 = min(it.red1, c0 + chunk_blocks<CHUNKED>());
                 for (int kb = c0; kb < c1; ++kb) {
                     // (Weight gradient: the other CTA's zeroing warp arrives after its own writes.)
                     if (!(WGRAD ? ptx::mbar_wait_cluster(&c.full[stage], phase, abort_flag)
@@ -415,7 +415,7 @@ grouped_mm_kernel(const __grid_constant__ Maps maps, const int32_t* __restrict__
                 }
             }
         }
-    } else if (WGRAD && warp == fix_warp<OUT>()) {
+    } else if (WGRAD && warp == fix_warp<CHUNKED>()) {
         // ------------------- zero the rows past a segment's end (both CTAs) -------------------
         int stage = 0;
         uint32_t parity = 0;  // bit s: parity of tail[s]'s next phase
@@ -445,7 +445,7 @@ grouped_mm_kernel(const __grid_constant__ Maps maps, const int32_t* __restrict__
             }
             stage = (stage + n) % STAGES;
         }
-    } else if (warp >= 2 && warp < fix_warp<OUT>()) {
+    } else if (warp >= 2 && warp < fix_warp<CHUNKED>()) {
         // ------------------------------ epilogue (both CTAs) ------------------------------
         const int quarter = warp & 3;            // this warp's tensor-memory lanes: 32 quarter .. + 31
         const int col0 = 128 * (((warp - 2) >> 2) & 1);  // and its half of the tile's columns (output rows)
@@ -485,6 +485,13 @@ grouped_mm_kernel(const __grid_constant__ Maps maps, const int32_t* __restrict__
                     if (j < rows) *p = __uint_as_float(v[j]);
             }
         };
+        auto add_old = [&](const float* p, uint32_t (&v)[32], int rows) {
+            float old[32];
+#pragma unroll
+            for (int j = 0; j < 32; ++j) old[j] = j < rows ? p[static_cast<size_t>(j) * N] : 0.0f;
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) + old[j]);
+        };
         bool aborted = false;
         for (int i = pair_id; i < total && !aborted; i += num_pairs) {
             const Item it = cur.at(i);
@@ -493,7 +500,7 @@ grouped_mm_kernel(const __grid_constant__ Maps maps, const int32_t* __restrict__
             const size_t row0 = WGRAD ? static_cast<size_t>(it.e) * K + it.r0 : static_cast<size_t>(c.seg[it.e]) + it.r0;
             OUT* dst = out + it.slice * slice_elems + (row0 + col0) * N + n;
             const uint32_t lane_addr = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + col0;
-            if constexpr (sizeof(OUT) == 4) {
+            if constexpr (CHUNKED) {
                 // The chunks' partial sums are added in registers, rounded to nearest: in tensor memory
                 // every addition truncates, a bias that grows with the number of additions.
                 uint32_t sum[4][32];
@@ -526,19 +533,12 @@ grouped_mm_kernel(const __grid_constant__ Maps maps, const int32_t* __restrict__
                     const int nr = it.rows - col0 - 32 * q;
                     if (nr > 0 && n < N) {
                         float* p = dst + static_cast<size_t>(32 * q) * N;
-                        if (WGRAD && accumulate) {
-                            float old[32];
-#pragma unroll
-                            for (int j = 0; j < 32; ++j) old[j] = j < nr ? p[static_cast<size_t>(j) * N] : 0.0f;
-#pragma unroll
-                            for (int j = 0; j < 32; ++j)
-                                sum[q][j] = __float_as_uint(__uint_as_float(sum[q][j]) + old[j]);
-                        }
+                        if (WGRAD && accumulate) add_old(p, sum[q], nr);
                         put(p, sum[q], nr);
                     }
                 }
             } else {
-                if (epi_groups<OUT>() > 1 && acc != group) {  // the other group's
+                if (epi_groups<CHUNKED>() > 1 && acc != group) {  // the other group's
                     pass();
                     continue;
                 }
@@ -546,28 +546,37 @@ grouped_mm_kernel(const __grid_constant__ Maps maps, const int32_t* __restrict__
                     aborted = true;
                     break;
                 }
-                // Neighbouring lanes exchange halves of their pairs of rows: an even lane then holds columns n
-                // and n + 1 of the first row, an odd lane n - 1 and n of the second, one 4-byte store each.
+                // bf16: neighbouring lanes exchange halves of their pairs of rows: an even lane then holds columns
+                // n and n + 1 of the first row, an odd lane n - 1 and n of the second, one 4-byte store each.
                 const uint32_t sel = lane & 1 ? 0x3276u : 0x5410u;
 #pragma unroll 1
                 for (int j0 = 0; j0 < 128 && col0 + j0 < it.rows; j0 += 32) {
                     uint32_t v[32];
                     ptx::tmem_ld_32x32b_x32(lane_addr + acc * ACC_COLS + j0, v);
                     ptx::tmem_ld_wait();
-                    OUT* p = dst + static_cast<size_t>(j0) * N - (lane & 1) + static_cast<size_t>(lane & 1) * N;
-                    const int nr = it.rows - col0 - j0 - (lane & 1);
+                    if constexpr (sizeof(OUT) == 4) {
+                        if (n < N) {
+                            float* p = dst + static_cast<size_t>(j0) * N;
+                            const int nr = it.rows - col0 - j0;
+                            if (WGRAD && accumulate) add_old(p, v, nr);
+                            put(p, v, nr);
+                        }
+                    } else {
+                        OUT* p = dst + static_cast<size_t>(j0) * N - (lane & 1) + static_cast<size_t>(lane & 1) * N;
+                        const int nr = it.rows - col0 - j0 - (lane & 1);
 #pragma unroll
-                    for (int j = 0; j < 16; ++j, p += 2 * static_cast<size_t>(N)) {
-                        const uint32_t own = pack_bf16x2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
-                        const uint32_t other = __shfl_xor_sync(0xffffffffu, own, 1);
-                        if (2 * j < nr && n < N) *reinterpret_cast<uint32_t*>(p) = __byte_perm(own, other, sel);
+                        for (int j = 0; j < 16; ++j, p += 2 * static_cast<size_t>(N)) {
+                            const uint32_t own = pack_bf16x2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
+                            const uint32_t other = __shfl_xor_sync(0xffffffffu, own, 1);
+                            if (2 * j < nr && n < N) *reinterpret_cast<uint32_t*>(p) = __byte_perm(own, other, sel);
+                        }
                     }
                 }
                 give();
                 pass();
             }
         }
-    } else if (WGRAD && warp == fix_warp<OUT>() + 1) {
+    } else if (WGRAD && warp == fix_warp<CHUNKED>() + 1) {
         // ------- zeros where there is nothing to add up (empty segments, slices past a short one) -------
         // A warp of its own: in the epilogue's loop this cost the other items registers (6 % of the gradients
         // of 256 experts).  An empty expert's tiles share its [K, N] as one run of memory, in equal parts: by
@@ -656,14 +665,14 @@ grouped_mm_join_kernel(const float4* __restrict__ partial, const int32_t* __rest
     }
 }
 
-template <int MODE, typename OUT>
-cudaError_t launch_mode(const GroupedMmArgs& a, OUT* out, int ksplit, int accumulate, int num_sms, cudaStream_t s,
+template <int MODE, typename OUT, bool CHUNKED>
+cudaError_t launch_as(const GroupedMmArgs& a, OUT* out, int ksplit, int accumulate, int num_sms, cudaStream_t s,
                         const char** why) {
     static bool attr_set[64] = {};
     int dev = 0;
     cudaGetDevice(&dev);
     if (dev < 64 && !attr_set[dev]) {
-        cudaError_t e = cudaFuncSetAttribute(grouped_mm_kernel<MODE, OUT>,
+        cudaError_t e = cudaFuncSetAttribute(grouped_mm_kernel<MODE, OUT, CHUNKED>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
         if (e != cudaSuccess) {
             *why = "cudaFuncSetAttribute(max dynamic shared memory) failed";
@@ -693,14 +702,28 @@ cudaError_t launch_mode(const GroupedMmArgs& a, OUT* out, int ksplit, int accumu
         *why = "cuTensorMapEncodeTiled failed (driver entry point missing or bad operand)";
         return cudaErrorInvalidValue;
     }
-    return launch_k(kPdlTrain, grouped_mm_kernel<MODE, OUT>, dim3(num_sms & ~1), dim3(num_threads<MODE, OUT>()),
+    return launch_k(kPdlTrain, grouped_mm_kernel<MODE, OUT, CHUNKED>, dim3(num_sms & ~1), dim3(num_threads<MODE, CHUNKED>()),
                     SMEM_BYTES, s, m, a.offsets, a.M, a.K, a.N, a.E, ksplit, accumulate, out, a.status);
+}
+
+template <int MODE>
+cudaError_t launch_mode(const GroupedMmArgs& a, float* out, int ksplit, int accumulate, int num_sms, cudaStream_t s,
+                        const char** why) {
+    // Blocks of the longest reduction, at most.
+    const int blocks = ((MODE == kMmWgrad ? a.M : a.K) + BK - 1) / BK;
+    return (blocks + ksplit - 1) / ksplit > CHUNK ? launch_as<MODE, float, true>(a, out, ksplit, accumulate, num_sms, s, why)
+                                                  : launch_as<MODE, float, false>(a, out, ksplit, accumulate, num_sms, s, why);
+}
+template <int MODE>
+cudaError_t launch_mode(const GroupedMmArgs& a, __nv_bfloat16* out, int ksplit, int accumulate, int num_sms,
+                        cudaStream_t s, const char** why) {
+    return launch_as<MODE, __nv_bfloat16, false>(a, out, ksplit, accumulate, num_sms, s, why);
 }
 
 template <int MODE>
 cudaError_t launch_any(const GroupedMmArgs& a, int num_sms, cudaStream_t s, const char** why) {
     if (a.ksplit > 1) {
-        cudaError_t e = launch_mode<MODE, float>(a, a.partial, a.ksplit, 0, num_sms, s, why);
+        cudaError_t e = launch_mode<MODE>(a, a.partial, a.ksplit, 0, num_sms, s, why);
         if (e != cudaSuccess) return e;
         const size_t n4 = (MODE == kMmWgrad ? static_cast<size_t>(a.E) * a.K : static_cast<size_t>(a.M)) * a.N / 4;
         const size_t want = (n4 + 255) / 256, most = static_cast<size_t>(num_sms) * 8;
@@ -715,8 +738,8 @@ cudaError_t launch_any(const GroupedMmArgs& a, int num_sms, cudaStream_t s, cons
                         a.N, a.E, n4, a.ksplit, by_row, acc, static_cast<__nv_bfloat16*>(a.out));
     }
     const int acc = a.accumulate ? 1 : 0;
-    return a.out_f32 ? launch_mode<MODE, float>(a, static_cast<float*>(a.out), 1, acc, num_sms, s, why)
-                     : launch_mode<MODE, __nv_bfloat16>(a, static_cast<__nv_bfloat16*>(a.out), 1, acc, num_sms, s, why);
+    return a.out_f32 ? launch_mode<MODE>(a, static_cast<float*>(a.out), 1, acc, num_sms, s, why)
+                     : launch_mode<MODE>(a, static_cast<__nv_bfloat16*>(a.out), 1, acc, num_sms, s, why);
 }
 
 }  // namespace

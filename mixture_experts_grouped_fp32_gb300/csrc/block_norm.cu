@@ -248,8 +248,8 @@ norm_rows_backward_kernel(const X* __restrict__ x, const __nv_bfloat16* __restri
                           const __nv_bfloat16* __restrict__ dn, const float* __restrict__ w_pre,
                           const float* __restrict__ w_post, const float* __restrict__ gate,
                           const float* __restrict__ tgate, const float* __restrict__ res, int T, int d, float eps,
-                          int stages, X* __restrict__ dx, __nv_bfloat16* __restrict__ dh, float* __restrict__ dtgate,
-                          float* __restrict__ partial) {
+                          int stages, int kept, X* __restrict__ dx, __nv_bfloat16* __restrict__ dh,
+                          float* __restrict__ dtgate, float* __restrict__ partial) {
     extern __shared__ uint4 ring_smem[];
     __shared__ float2 red1[2][kMaxWarps], red2[2][kMaxWarps];
     constexpr int XW = words<X>();
@@ -281,7 +281,8 @@ norm_rows_backward_kernel(const X* __restrict__ x, const __nv_bfloat16* __restri
     };
     for (int k = 0; k < stages - 1; ++k) fetch(k, k);
     // One vector per thread: the weights stay in registers.  Two: they are read again where used (the
-    // column sums take the registers); the ring leaves half of the SM's memory to L1 for them.
+    // column sums take the registers), from shared memory behind the ring where they fit (`kept`; each thread
+    // keeps its own), else from global memory, for which the ring leaves half of the SM's memory to L1.
     Vec8 kn[VPT], kg[VPT], kr[VPT];
     auto load_weights = [&](int c, Vec8& n_, Vec8& g_, Vec8& r_) {
         n_ = N ? load8_cached(w_pre, c) : ones();
@@ -294,6 +295,40 @@ norm_rows_backward_kernel(const X* __restrict__ x, const __nv_bfloat16* __restri
         r_ = res ? load8_cached(res, c) : ones();
     };
     if (VPT == 1 && tid < d8) load_weights(tid, kn[0], kg[0], kr[0]);
+    // Word w of 6 of vector v: w_pre, gate w_post, res, two words each.
+    uint4* const keep = ring_smem + stages * VPT * per_vec * nt + tid;
+    auto keep_at = [&](int v, int w) { return reinterpret_cast<float4*>(keep + (v * 6 + w) * nt); };
+    if (VPT > 1 && kept) {
+#pragma unroll
+        for (int v = 0; v < VPT; ++v) {
+            const int c = tid + v * nt;
+            if (c < d8) {
+                Vec8 a, b, r;
+                load_weights(c, a, b, r);
+                const Vec8* all[3] = {&a, &b, &r};
+#pragma unroll
+                for (int w = 0; w < 6; ++w) {
+                    const float* p = all[w / 2]->v + 4 * (w & 1);
+                    *keep_at(v, w) = make_float4(p[0], p[1], p[2], p[3]);
+                }
+            }
+        }
+    }
+    auto weights = [&](int v, int c, Vec8& n_, Vec8& g_, Vec8& r_) {
+        if (VPT == 1) {
+            n_ = kn[0], g_ = kg[0], r_ = kr[0];
+        } else if (kept) {
+            auto get = [&](int w, Vec8& o) {
+                const float4 a = *keep_at(v, w), b = *keep_at(v, w + 1);
+                o = Vec8{{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}};
+            };
+            get(0, n_);
+            get(2, g_);
+            get(4, r_);
+        } else {
+            load_weights(c, n_, g_, r_);
+        }
+    };
     Vec8 sA[VPT], sR[VPT], sP[VPT];
 #pragma unroll
     for (int v = 0; v < VPT; ++v)
@@ -338,8 +373,7 @@ norm_rows_backward_kernel(const X* __restrict__ x, const __nv_bfloat16* __restri
                 const int c = tid + v * nt;
                 if (c < d8) {
                     Vec8 wn, wg, rs;
-                    if (VPT == 1) wn = kn[0], wg = kg[0], rs = kr[0];
-                    else load_weights(c, wn, wg, rs);
+                    weights(v, c, wn, wg, rs);
                     const Vec8 xv = ring8<X>(ring, s, v * per_vec), nv = ring8<B>(ring, s, v * per_vec + o_dn);
                     Vec8 hv{};
                     if (H) hv = ring8<B>(ring, s, v * per_vec + o_h);
@@ -363,8 +397,7 @@ norm_rows_backward_kernel(const X* __restrict__ x, const __nv_bfloat16* __restri
             const int c = tid + v * nt;
             if (c < d8) {
                 Vec8 wn, wg, rs;
-                if (VPT == 1) wn = kn[0], wg = kg[0], rs = kr[0];
-                else load_weights(c, wn, wg, rs);
+                weights(v, c, wn, wg, rs);
                 const Vec8 xv = ring8<X>(ring, s, v * per_vec);
                 Vec8 D{}, hv{}, o;
                 if (dy) D = ring8<X>(ring, s, v * per_vec + o_dy);
@@ -683,8 +716,11 @@ block_norm_join_kernel(const float* __restrict__ partial, int blocks, int d, con
 // in the ring; stages = 0: the plain kernels.
 struct Shape {
     int vpt, threads, per_sm, stages;
+    int kept;  // backward, two vectors per thread: the weights fit behind the ring
     size_t smem;
 };
+constexpr size_t kMostSmem = 225 * 1024;  // dynamic shared memory of a block, at most
+
 Shape shape_of(const BlockNormArgs& a, bool bwd) {
     const int d8 = a.d / 8;
     Shape s{};
@@ -706,6 +742,12 @@ Shape shape_of(const BlockNormArgs& a, bool bwd) {
     const size_t fit = (bwd && s.vpt == 2 ? 112 : 200) * 1024 / (row * s.per_sm);
     s.stages = fit >= 4 ? 4 : fit >= 3 ? 3 : 2;
     s.smem = row * s.stages;
+    const size_t weights = static_cast<size_t>(6) * s.vpt * s.threads * 16;
+    if (bwd && s.vpt == 2 && 2 * row + weights <= kMostSmem) {
+        s.kept = 1;
+        s.stages = 3 * row + weights <= kMostSmem ? 3 : 2;
+        s.smem = s.stages * row + weights;
+    }
     return s;
 }
 
@@ -714,7 +756,7 @@ cudaError_t allow_smem(void (*kernel)(KArgs...), bool* done) {
     int dev = 0;
     cudaGetDevice(&dev);
     if (dev < 64 && done[dev]) return cudaSuccess;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024);
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostSmem);
     if (e == cudaSuccess && dev < 64) done[dev] = true;
     return e;
 }
@@ -746,7 +788,8 @@ cudaError_t backward_as(const BlockNormArgs& a, const Shape& s, int grid, cudaSt
     if (e != cudaSuccess) return e;
     return launch_k(kPdlTrain, norm_rows_backward_kernel<X, VPT, H, N>, dim3(grid), dim3(s.threads), s.smem, st,
                     static_cast<const X*>(a.x), a.h, static_cast<const X*>(a.dy), a.dn, a.w_pre, a.w_post, a.gate,
-                    a.tgate, a.res, a.T, a.d, a.eps, s.stages, static_cast<X*>(a.dx), a.dh, a.dtgate, a.partial);
+                    a.tgate, a.res, a.T, a.d, a.eps, s.stages, s.kept, static_cast<X*>(a.dx), a.dh, a.dtgate,
+                    a.partial);
 }
 template <typename X, int VPT>
 cudaError_t backward_rows(const BlockNormArgs& a, const Shape& s, int grid, cudaStream_t st) {

@@ -127,8 +127,8 @@ def norm_inputs(T, d, xt, post, pre, gates, seed=0):
     return v, r(T, d).to(xt), r(T, d).to(BF16)
 
 
-NORM_SHAPES = [(1, 8), (1, 4096), (2, 264), (5, 2048), (7, 2056), (33, 512), (3, 7168), (2, 8200), (2, 16384),
-               (1, 20480), (1, 65536), (700, 72)]
+NORM_SHAPES = [(1, 8), (1, 4096), (2, 264), (5, 2048), (7, 2056), (33, 512), (3, 7168), (5, 5120), (460, 4104),
+               (2, 8192), (2, 8200), (2, 16384), (1, 20480), (1, 65536), (700, 72)]
 
 
 @pytest.mark.parametrize("post,pre,gates", [(True, True, True), (True, True, False), (True, False, True),

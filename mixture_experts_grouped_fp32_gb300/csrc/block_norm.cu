@@ -22,7 +22,7 @@
 // last sum of row k (forward: one reduction per row, backward: two).  Rows too wide for two of them in
 // shared memory (d > 8192) take the plain kernels, which hold one row in registers.
 //
-// Measured: 4096 x 7168 with an fp32 stream 62 us (5.6 TB/s; 54 under ncu), gradient of 4096 x 4096 52 us
+// Measured: 4096 x 7168 with an fp32 stream 60 us (5.8 TB/s; 54 under ncu), gradient of 4096 x 4096 52 us
 // (3.8 TB/s: 16 warps per SM, whose instruction latency shows; an earlier form that loaded tgate in the row
 // that uses it took 78).
 //
@@ -739,7 +739,9 @@ Shape shape_of(const BlockNormArgs& a, bool bwd) {
     const int xw = a.x_fp32 ? 2 : 1;
     const int words = bwd ? xw * (a.dy ? 2 : 1) + (a.h ? 1 : 0) + (a.dn ? 1 : 0) : xw + (a.h ? 1 : 0);
     const size_t row = static_cast<size_t>(words) * s.vpt * s.threads * 16;
-    const size_t fit = (bwd && s.vpt == 2 ? 112 : 200) * 1024 / (row * s.per_sm);
+    // Up to four rows in 150 KB per SM (200 KB, a row more for the widest: 62 against 60 us for 4096 x 7168 with
+    // an fp32 stream; 100 KB: 67).
+    const size_t fit = (bwd && s.vpt == 2 ? 112 : 150) * 1024 / (row * s.per_sm);
     s.stages = fit >= 4 ? 4 : fit >= 3 ? 3 : 2;
     s.smem = row * s.stages;
     const size_t weights = static_cast<size_t>(6) * s.vpt * s.threads * 16;

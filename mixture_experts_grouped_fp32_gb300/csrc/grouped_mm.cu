@@ -230,6 +230,8 @@ grouped_mm_kernel(const __grid_constant__ Maps maps, const int32_t* __restrict__
         ptx::tmem_alloc_pair(&c.tmem_base, TMEM_COLS);
         ptx::tmem_relinquish_pair();
     }
+    __syncwarp();
+    ptx::cluster_arrive();  // this CTA's barriers exist; the wait is after the offsets, whose latency covers it
     pdl_wait();
     pdl_trigger();
     if (warp == 2) {
@@ -270,7 +272,7 @@ grouped_mm_kernel(const __grid_constant__ Maps maps, const int32_t* __restrict__
     }
     ptx::tc_fence_before();
     __syncthreads();
-    ptx::cluster_sync();  // both CTAs' barriers exist before any cross-CTA arrive or copy
+    ptx::cluster_wait();  // both CTAs' barriers exist before any cross-CTA arrive or copy
     ptx::tc_fence_after();
 
     const uint32_t tmem_base = c.tmem_base;

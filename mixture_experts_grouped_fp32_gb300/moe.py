@@ -130,9 +130,12 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
                 fn.restype = res
                 _fns[name] = fn
             if os.path.exists(os.path.join(_HERE, "_moe_fast.so")):
-                from . import _moe_fast
-                _moe_fast.init(path)
-                _fast = _moe_fast
+                try:
+                    from . import _moe_fast
+                    _moe_fast.init(path)
+                    _fast = _moe_fast
+                except (ImportError, OSError):  # built against another torch: ctypes does the same
+                    _fast = None
             _lib = lib
     return _lib
 

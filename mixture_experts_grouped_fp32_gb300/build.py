@@ -53,7 +53,7 @@ def _build_fast() -> str:
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I" + os.path.join(t, "include"),
            "-I" + os.path.join(t, "include", "torch", "csrc", "api", "include"),
            "-I" + sysconfig.get_paths()["include"], "-I" + os.path.join(os.path.dirname(os.path.dirname(NVCC)), "include"),
-           os.path.join(CSRC, "binding.cpp"), "-o", tmp, "-L" + os.path.join(t, "lib"), "-ltorch_python", "-ltorch_cpu",
+           os.path.join(CSRC, "binding.cpp"), "-o", tmp, "-L" + os.path.join(t, "lib"), "-ltorch_python", "-ltorch_cpu", "-ltorch_cuda",
            "-lc10", "-lc10_cuda", "-ldl"]
     try:
         res = subprocess.run(cmd, capture_output=True, text=True)

@@ -8,7 +8,7 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAStream.h>
 #include <dlfcn.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -61,7 +61,7 @@ struct Args {
 };
 
 at::Tensor make(at::IntArrayRef shape, ScalarType type, const at::Tensor& like) {
-    return at::empty(shape, like.options().dtype(type));
+    return at::Tensor(at::detail::empty_cuda(shape, type, like.device(), std::nullopt));
 }
 void* ptr(const at::Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; }
 PyObject* wrap(const at::Tensor& t) {

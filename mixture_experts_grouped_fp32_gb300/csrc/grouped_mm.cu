@@ -41,7 +41,8 @@
 //
 // Measured: 8192 rows, 4096 -> 28672 over 8 experts 1.19 to 1.27 ms (1.5 to 1.6 PFLOP/s; tensor pipe 82 %
 // active at the power limit); two rows of 14336 -> 4096 45 us (5.2 TB/s); gradients of 256 experts,
-// 2048 x 7168 from 16384 rows, 1.41 to 1.46 ms (5.5 TB/s of mostly writes).
+// 2048 x 7168 from 16384 rows, 1.41 to 1.46 ms (5.5 TB/s of mostly writes); 32 experts' fp32 gradients of
+// that size added to what was there 0.69 ms (5.9 TB/s).
 //
 // Synchronisation across the pair is that of the layer's SM-pair kernel: full[s] lives in CTA 0 and
 // counts both CTAs' copies, empty[s] and tfull[a] are arrived on in both CTAs by CTA 0's multicast
@@ -487,12 +488,14 @@ grouped_mm_kernel(const __grid_constant__ Maps maps, const int32_t* __restrict__
                     if (j < rows) *p = __uint_as_float(v[j]);
             }
         };
-        auto add_old = [&](const float* p, uint32_t (&v)[32], int rows) {
-            float old[32];
+        // Adds to what is there, in the L2: each element is added to once in a launch, so that the result is
+        // that of a load, an addition rounded to nearest and a store (where values under 2^-126 count as zero),
+        // without waiting for the load (32 experts' 2048 x 7168 from 16384 rows: 1044 us with loads, 800 so, 691
+        // with the lines fetched ahead; pairs of columns per addition took the same time).
+        auto add = [&](float* p, const uint32_t (&v)[32], int rows) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j) old[j] = j < rows ? p[static_cast<size_t>(j) * N] : 0.0f;
-#pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) + old[j]);
+            for (int j = 0; j < 32; ++j, p += N)
+                if (j < rows) ptx::red_add_f32(p, __uint_as_float(v[j]));
         };
         bool aborted = false;
         for (int i = pair_id; i < total && !aborted; i += num_pairs) {
@@ -502,6 +505,14 @@ grouped_mm_kernel(const __grid_constant__ Maps maps, const int32_t* __restrict__
             const size_t row0 = WGRAD ? static_cast<size_t>(it.e) * K + it.r0 : static_cast<size_t>(c.seg[it.e]) + it.r0;
             OUT* dst = out + it.slice * slice_elems + (row0 + col0) * N + n;
             const uint32_t lane_addr = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + col0;
+            if (WGRAD && accumulate && i != pair_id) {
+                // What will be added to, into the L2 while the products run (a pair's first item is short of
+                // time itself: 10.5 against 11.1 us for 3 experts' 464 x 2688).
+                const int n0 = n - lane;
+                if (n0 < N)
+                    for (int j = lane; j < 128 && col0 + j < it.rows; j += 32)
+                        ptx::prefetch_l2(dst + static_cast<size_t>(j) * N - lane);
+            }
             if constexpr (CHUNKED) {
                 // The chunks' partial sums are added in registers, rounded to nearest: in tensor memory
                 // every addition truncates, a bias that grows with the number of additions.
@@ -535,8 +546,8 @@ grouped_mm_kernel(const __grid_constant__ Maps maps, const int32_t* __restrict__
                     const int nr = it.rows - col0 - 32 * q;
                     if (nr > 0 && n < N) {
                         float* p = dst + static_cast<size_t>(32 * q) * N;
-                        if (WGRAD && accumulate) add_old(p, sum[q], nr);
-                        put(p, sum[q], nr);
+                        if (WGRAD && accumulate) add(p, sum[q], nr);
+                        else put(p, sum[q], nr);
                     }
                 }
             } else {
@@ -560,8 +571,8 @@ grouped_mm_kernel(const __grid_constant__ Maps maps, const int32_t* __restrict__
                         if (n < N) {
                             float* p = dst + static_cast<size_t>(j0) * N;
                             const int nr = it.rows - col0 - j0;
-                            if (WGRAD && accumulate) add_old(p, v, nr);
-                            put(p, v, nr);
+                            if (WGRAD && accumulate) add(p, v, nr);
+                            else put(p, v, nr);
                         }
                     } else {
                         OUT* p = dst + static_cast<size_t>(j0) * N - (lane & 1) + static_cast<size_t>(lane & 1) * N;

@@ -132,6 +132,12 @@ __device__ __forceinline__ bool mbar_wait_ns(uint64_t* bar, uint32_t parity, uin
     return true;
 }
 
+// *p += v in the L2, nothing returned.
+__device__ __forceinline__ void red_add_f32(float* p, float v) {
+    asm volatile("red.relaxed.gpu.global.add.f32 [%0], %1;" ::"l"(p), "f"(v) : "memory");
+}
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
 // ---------------------------------------------------------------------------------------------
 // TMA (cp.async.bulk.tensor), 2-D tiled, completion counted on an mbarrier
 // ---------------------------------------------------------------------------------------------

@@ -146,6 +146,24 @@ def test_wgrad_accumulates(moe):
     _check(out, want, 2 * mag + 3 * start.double().abs(), 40, "accumulate")
 
 
+@pytest.mark.parametrize("counts,K,N", [([3, 0, 40, 17] * 24, 264, 1032), ([600, 1, 0, 555] * 5, 520, 1288)])
+def test_wgrad_adds_once(moe, counts, K, N):
+    """The sum is that of the gradient and what was there, rounded once, over several tiles per SM pair; empty
+    segments' stay as they are, infinities and NaN too."""
+    a, g, offs = _inputs(counts, K, N, "wgrad")
+    start = torch.randn(len(counts), K, N, generator=torch.Generator().manual_seed(9))
+    start[1, 0, :2] = torch.tensor([float("inf"), float("nan")])
+    start[2, K - 1, N - 1] = float("-inf")
+    start = start.cuda()
+    want = start + _run(moe, a, g, offs, "wgrad")
+    for _ in range(2):
+        out = start.clone()
+        _run(moe, a, g, offs, "wgrad", out=out, accumulate=True)
+        assert torch.equal(out.nan_to_num(7.5), want.nan_to_num(7.5)) and torch.equal(out.isnan(), want.isnan())
+        assert torch.equal(out[torch.tensor(counts) == 0].nan_to_num(7.5),
+                           start[torch.tensor(counts) == 0].nan_to_num(7.5))
+
+
 @pytest.mark.parametrize("way,M,K,N,E", [("fwd", 3, 8192, 256, 2), ("dgrad", 70, 4104, 264, 1), ("wgrad", 4099, 72, 136, 1)])
 def test_split_reduction(moe, way, M, K, N, E):
     """A long reduction over few tiles is split into slices; the result is the same on every run, and

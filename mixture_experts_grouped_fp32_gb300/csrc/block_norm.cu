@@ -29,6 +29,8 @@
 // The backward pass keeps the column sums A, dres and dw_pre of all rows that a block visits in
 // registers, writes them once per block, and a second kernel adds the blocks in a fixed order: no
 // atomics, the same result on every run.
+#include <algorithm>
+
 #include "tcgen05.cuh"
 #include "train_util.cuh"
 
@@ -63,14 +65,16 @@ __device__ __forceinline__ float2 warp_pair_sum(float2 v) {
     const float b = __shfl_xor_sync(0xffffffffu, a, 16);
     return up ? make_float2(b, a) : make_float2(a, b);
 }
-// Two sums over the block, in every thread, with one barrier (none for a single warp); the caller's
-// buffers alternate between calls.
-__device__ __forceinline__ void pair_sum(float (&v)[2], float2* red, int warps) {
+// Two sums over the threads of a row (threadIdx.x), in each of them, with one barrier (none for a single
+// warp); the caller's buffers alternate between calls.  `barrier`: 0 if the block has no other threads, else
+// one of the row's own.
+__device__ __forceinline__ void pair_sum(float (&v)[2], float2* red, int warps, int barrier = 0) {
     float2 s = warp_pair_sum(make_float2(v[0], v[1]));
     if (warps > 1) {
         const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
         if (lane == 0) red[warp] = s;
-        __syncthreads();
+        if (barrier == 0) __syncthreads();
+        else asm volatile("bar.sync %0, %1;" ::"r"(barrier), "r"(warps * 32) : "memory");
         s = warp_pair_sum(lane < warps ? red[lane] : make_float2(0.0f, 0.0f));
     }
     v[0] = s.x;
@@ -241,8 +245,11 @@ norm_rows_kernel(const X* __restrict__ x, const __nv_bfloat16* __restrict__ h, c
     ptx::cp_async_wait_all();
 }
 
-// Column sums of a block go to partial[blockIdx][3][d]: A, dres, dw_pre.
-template <typename X, int VPT, bool H, bool N>
+// Column sums of a block go to partial[blockIdx][3][d]: A, dres, dw_pre.  SIDE (narrow rows): the block works
+// on blockDim.y of them side by side, each with its threads, ring and barrier, and adds up their column sums at
+// the end: the SM's 512 threads are used whatever the width, and fewer blocks' sums remain to be joined (16384
+// rows of 256 values 15 us, of 512 29, 4096 of 1024 18; as four blocks per SM 28, 42 and 20).
+template <typename X, int VPT, bool H, bool N, bool SIDE>
 __global__ void __launch_bounds__(512, 1)
 norm_rows_backward_kernel(const X* __restrict__ x, const __nv_bfloat16* __restrict__ h, const X* __restrict__ dy,
                           const __nv_bfloat16* __restrict__ dn, const float* __restrict__ w_pre,
@@ -255,14 +262,17 @@ norm_rows_backward_kernel(const X* __restrict__ x, const __nv_bfloat16* __restri
     constexpr int XW = words<X>();
     using B = __nv_bfloat16;
     const int tid = threadIdx.x, nt = blockDim.x, d8 = d / 8, warps = nt >> 5;
+    const int group = SIDE ? threadIdx.y : 0, groups = SIDE ? blockDim.y : 1;
+    const int warp0 = group * warps, barrier = SIDE ? 1 + group : 0;
     const float inv_d = 1.0f / static_cast<float>(d);
     // Words of a vector: x, then dy, h, dn as given.
     const int o_dy = XW, o_h = o_dy + (dy ? XW : 0), o_dn = o_h + (H ? 1 : 0), per_vec = o_dn + (N ? 1 : 0);
-    const Ring ring{ring_smem + tid, VPT * per_vec, nt};
-    const int rows = (T - static_cast<int>(blockIdx.x) + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x);
+    const Ring ring{ring_smem + group * (stages * VPT * per_vec * nt) + tid, VPT * per_vec, nt};
+    const int first = static_cast<int>(blockIdx.x) * groups + group, step = static_cast<int>(gridDim.x) * groups;
+    const int rows = first < T ? (T - first - 1) / step + 1 : 0;
     pdl_wait();
     pdl_trigger();
-    auto row_of = [&](int k) { return static_cast<size_t>(blockIdx.x) + static_cast<size_t>(k) * gridDim.x; };
+    auto row_of = [&](int k) { return static_cast<size_t>(first) + static_cast<size_t>(k) * step; };
     auto fetch = [&](int k, int s) {
         if (k < rows) {
             const size_t base = row_of(k) * d8;
@@ -354,7 +364,7 @@ norm_rows_backward_kernel(const X* __restrict__ x, const __nv_bfloat16* __restri
     if (H) {
         wait_rows(stages - 2);
         s2[1] = sum_h(0);
-        pair_sum(s2, red2[1], warps);
+        pair_sum(s2, red2[1] + warp0, warps, barrier);
     }
     else wait_rows(stages - 2);
     int s = 0;
@@ -386,7 +396,7 @@ norm_rows_backward_kernel(const X* __restrict__ x, const __nv_bfloat16* __restri
                 }
             }
             float s1[2] = {yy.x + yy.y, ey.x + ey.y};
-            pair_sum(s1, red1[k & 1], warps);
+            pair_sum(s1, red1[k & 1] + warp0, warps, barrier);
             ry = rsqrtf(s1[0] * inv_d + eps);
             mean = s1[1] * ry * inv_d;
         }
@@ -431,7 +441,7 @@ norm_rows_backward_kernel(const X* __restrict__ x, const __nv_bfloat16* __restri
         if (H) {
             s2[0] = qh.x + qh.y;
             s2[1] = k + 1 < rows ? sum_h(next) : 0.0f;
-            pair_sum(s2, red2[k & 1], warps);
+            pair_sum(s2, red2[k & 1] + warp0, warps, barrier);
             const float qmean = s2[0] * rh * inv_d;  // mean of q hh
             if (dtgate && tid == 0) dtgate[t] = s2[0] * rh;
 #pragma unroll
@@ -450,6 +460,27 @@ norm_rows_backward_kernel(const X* __restrict__ x, const __nv_bfloat16* __restri
     }
     ptx::cp_async_wait_all();
     float* p = partial + static_cast<size_t>(blockIdx.x) * 3 * d;
+    if constexpr (SIDE) {
+        __syncthreads();  // the rings are done with
+        float* all = reinterpret_cast<float*>(ring_smem);
+        auto put = [&](int which, const Vec8& a) {  // (store8 is for global memory)
+            float4* q = reinterpret_cast<float4*>(all + (group * 3 + which) * d) + 2 * tid;
+            q[0] = make_float4(a.v[0], a.v[1], a.v[2], a.v[3]);
+            q[1] = make_float4(a.v[4], a.v[5], a.v[6], a.v[7]);
+        };
+        if (tid < d8) {
+            put(0, sA[0]);
+            put(1, sR[0]);
+            put(2, sP[0]);
+        }
+        __syncthreads();
+        for (int c = group * nt + tid; c < 3 * d; c += groups * nt) {
+            float a = all[c];
+            for (int g = 1; g < groups; ++g) a += all[g * 3 * d + c];
+            p[c] = a;
+        }
+        return;
+    }
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
         const int c = tid + v * nt;
@@ -716,14 +747,17 @@ block_norm_join_kernel(const float* __restrict__ partial, int blocks, int d, con
 // in the ring; stages = 0: the plain kernels.
 struct Shape {
     int vpt, threads, per_sm, stages;
+    int groups;  // rows that a block works on side by side
     int kept;  // backward, two vectors per thread: the weights fit behind the ring
     size_t smem;
 };
+constexpr int kSms = 152;                 // of a GB300
 constexpr size_t kMostSmem = 225 * 1024;  // dynamic shared memory of a block, at most
 
 Shape shape_of(const BlockNormArgs& a, bool bwd) {
     const int d8 = a.d / 8;
     Shape s{};
+    s.groups = 1;
     if (a.d > 8192) {
         s.vpt = d8 <= 2048 ? 4 : 8;
         s.threads = ((d8 + s.vpt - 1) / s.vpt + 31) / 32 * 32;
@@ -731,19 +765,22 @@ Shape shape_of(const BlockNormArgs& a, bool bwd) {
         return s;
     }
     // Forward: up to 256 threads of one vector or 512 of two, 1024 threads per SM.  Backward: one vector
-    // up to 512 threads, with up to 128 registers a thread 512 threads per SM.
+    // up to 512 threads, with up to 128 registers a thread 512 threads per SM; rows of up to 1024 values side by
+    // side in one block, no more of them than leave each of the 152 SMs rows (of 2048 values, two blocks: 30.0
+    // against 30.8 us for 4096 rows).
     s.vpt = d8 <= (bwd ? 512 : 256) ? 1 : 2;
     s.threads = ((d8 + s.vpt - 1) / s.vpt + 31) / 32 * 32;
-    s.per_sm = bwd ? (s.threads <= 128 ? 4 : s.threads <= 256 ? 2 : 1)
+    if (bwd && s.threads <= 128) s.groups = std::max(1, std::min(512 / s.threads, (a.T - 1) / kSms + 1));
+    s.per_sm = bwd ? (s.threads > 128 && s.threads <= 256 ? 2 : 1)
                    : (s.vpt == 2 ? (s.threads <= 256 ? 2 : 1) : s.threads <= 64 ? 16 : 1024 / s.threads);
     const int xw = a.x_fp32 ? 2 : 1;
     const int words = bwd ? xw * (a.dy ? 2 : 1) + (a.h ? 1 : 0) + (a.dn ? 1 : 0) : xw + (a.h ? 1 : 0);
     const size_t row = static_cast<size_t>(words) * s.vpt * s.threads * 16;
     // Up to four rows in 150 KB per SM (200 KB, a row more for the widest: 62 against 60 us for 4096 x 7168 with
     // an fp32 stream; 100 KB: 67).
-    const size_t fit = (bwd && s.vpt == 2 ? 112 : 150) * 1024 / (row * s.per_sm);
+    const size_t fit = (bwd && s.vpt == 2 ? 112 : 150) * 1024 / (row * s.per_sm * s.groups);
     s.stages = fit >= 4 ? 4 : fit >= 3 ? 3 : 2;
-    s.smem = row * s.stages;
+    s.smem = std::max(row * s.stages, s.groups > 1 ? sizeof(float) * 3 * a.d : 0) * s.groups;
     const size_t weights = static_cast<size_t>(6) * s.vpt * s.threads * 16;
     if (bwd && s.vpt == 2 && 2 * row + weights <= kMostSmem) {
         s.kept = 1;
@@ -783,15 +820,21 @@ cudaError_t forward_wide(const BlockNormArgs& a, const Shape& s, int grid, cudaS
                     static_cast<const X*>(a.x), a.h, a.w_pre, a.w_post, a.gate, a.tgate, a.res, a.T, a.d, a.eps,
                     static_cast<X*>(a.y), a.n);
 }
+template <typename X, int VPT, bool H, bool N, bool SIDE>
+cudaError_t backward_with(const BlockNormArgs& a, const Shape& s, int grid, cudaStream_t st) {
+    static bool done[64] = {};
+    const cudaError_t e = allow_smem(norm_rows_backward_kernel<X, VPT, H, N, SIDE>, done);
+    if (e != cudaSuccess) return e;
+    return launch_k(kPdlTrain, norm_rows_backward_kernel<X, VPT, H, N, SIDE>, dim3(grid), dim3(s.threads, s.groups),
+                    s.smem, st, static_cast<const X*>(a.x), a.h, static_cast<const X*>(a.dy), a.dn, a.w_pre, a.w_post,
+                    a.gate, a.tgate, a.res, a.T, a.d, a.eps, s.stages, s.kept, static_cast<X*>(a.dx), a.dh, a.dtgate,
+                    a.partial);
+}
 template <typename X, int VPT, bool H, bool N>
 cudaError_t backward_as(const BlockNormArgs& a, const Shape& s, int grid, cudaStream_t st) {
-    static bool done[64] = {};
-    const cudaError_t e = allow_smem(norm_rows_backward_kernel<X, VPT, H, N>, done);
-    if (e != cudaSuccess) return e;
-    return launch_k(kPdlTrain, norm_rows_backward_kernel<X, VPT, H, N>, dim3(grid), dim3(s.threads), s.smem, st,
-                    static_cast<const X*>(a.x), a.h, static_cast<const X*>(a.dy), a.dn, a.w_pre, a.w_post, a.gate,
-                    a.tgate, a.res, a.T, a.d, a.eps, s.stages, s.kept, static_cast<X*>(a.dx), a.dh, a.dtgate,
-                    a.partial);
+    if constexpr (VPT == 1)
+        if (s.groups > 1) return backward_with<X, VPT, H, N, true>(a, s, grid, st);
+    return backward_with<X, VPT, H, N, false>(a, s, grid, st);
 }
 template <typename X, int VPT>
 cudaError_t backward_rows(const BlockNormArgs& a, const Shape& s, int grid, cudaStream_t st) {
@@ -809,7 +852,7 @@ cudaError_t backward_wide(const BlockNormArgs& a, const Shape& s, int grid, cuda
 template <typename X>
 cudaError_t launch_x(const BlockNormArgs& a, bool bwd, int num_sms, cudaStream_t st) {
     const Shape s = shape_of(a, bwd);
-    const int most = bwd ? block_norm_blocks(a.T, a.d) : num_sms * s.per_sm, grid = a.T < most ? a.T : most;
+    const int grid = bwd ? block_norm_blocks(a.T, a.d) : std::min(a.T, num_sms * s.per_sm);
     if (!bwd) {
         if (s.vpt == 1) return forward_rows<X, 1>(a, s, grid, st);
         if (s.vpt == 2) return forward_rows<X, 2>(a, s, grid, st);
@@ -830,9 +873,9 @@ cudaError_t launch_x(const BlockNormArgs& a, bool bwd, int num_sms, cudaStream_t
 // Blocks of the backward pass on GB300's 152 SMs (the workspace depends on the shape alone).
 int block_norm_blocks(int T, int d) {
     BlockNormArgs a{};
-    a.d = d;
-    const int most = 152 * shape_of(a, true).per_sm;
-    return T < most ? T : most;
+    a.T = T, a.d = d;
+    const Shape s = shape_of(a, true);
+    return T == 0 ? 0 : std::min((T - 1) / s.groups + 1, kSms * s.per_sm);
 }
 
 cudaError_t launch_block_norm(const BlockNormArgs& a, bool backward_pass, int num_sms, cudaStream_t s) {

@@ -128,7 +128,8 @@ def norm_inputs(T, d, xt, post, pre, gates, seed=0):
 
 
 NORM_SHAPES = [(1, 8), (1, 4096), (2, 264), (5, 2048), (7, 2056), (33, 512), (3, 7168), (5, 5120), (460, 4104),
-               (2, 8192), (2, 8200), (2, 16384), (1, 20480), (1, 65536), (700, 72)]
+               (2, 8192), (2, 8200), (2, 16384), (1, 20480), (1, 65536), (700, 72),
+               (153, 8), (2500, 264), (1000, 640), (611, 1000)]
 
 
 @pytest.mark.parametrize("post,pre,gates", [(True, True, True), (True, True, False), (True, False, True),

@@ -117,8 +117,9 @@ struct Item {
     int slice;
 };
 
-// A role's position in the items of its CTA pair, which it visits in ascending order: the expert is
-// found by walking on from the last one, and what depends on the expert alone is kept.
+// A role's position in the items of its CTA pair, which it visits in ascending order: the expert is the last
+// one, the next one or found by bisection of those after (walking over empty experts: 8 tokens in 256 experts
+// 19.8 against 14.7 us), and what depends on the expert alone is kept.
 template <int MODE>
 struct Cursor {
     const Ctl& c;
@@ -131,10 +132,17 @@ struct Cursor {
 
     __device__ __forceinline__ Item at(int i) {
         if (i >= next) {
-            do {
-                ++e;
+            next = c.item_start[++e + 1];
+            if (i >= next) {  // further on (i < item_start[E])
+                int lo = e + 1, hi = E - 1;
+                while (lo < hi) {
+                    const int mid = (lo + hi) >> 1;
+                    if (c.item_start[mid + 1] > i) hi = mid;
+                    else lo = mid + 1;
+                }
+                e = lo;
                 next = c.item_start[e + 1];
-            } while (i >= next);
+            }
             start = c.item_start[e];
             cnt = c.seg[e + 1] - c.seg[e];
             total = MODE == kMmWgrad ? K : cnt;

@@ -102,6 +102,19 @@ def test_many_experts(moe, way):
     _check(got, ref, mag, max(counts) if way == "wgrad" else 136, way)
 
 
+@pytest.mark.parametrize("way", ["fwd", "dgrad", "wgrad"])
+@pytest.mark.parametrize("active", [(0,), (255,), (0, 255), (254, 255), (1, 2, 3, 100, 101, 250), tuple(range(7, 256, 31))])
+def test_few_of_many_experts(moe, way, active):
+    """Tokens in a few of 256 experts, next to each other and far apart, with several tiles each."""
+    counts = [0] * 256
+    for k, e in enumerate(active):
+        counts[e] = 1 + 5 * k if k % 3 else 270
+    a, b, offs = _inputs(counts, 72, 1288 if way != "wgrad" else 136, way)
+    got = _run(moe, a, b, offs, way, out_dtype=torch.float32)
+    ref, mag = _reference(a, b, offs, way)
+    _check(got, ref, mag, max(counts) if way == "wgrad" else 72, way)
+
+
 @pytest.mark.parametrize("way", ["fwd", "dgrad"])
 def test_rows_outside_the_segments_stay(moe, way):
     a, b, offs = _inputs([5, 0, 40], 64, 136, way, lead=3, trail=70)

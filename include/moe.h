@@ -497,7 +497,8 @@ MOE_API int moe_forward_grouped_fp8b(const void* x, const float* logits, const f
  * (transpose_b = 1) or 2 (wgrad); with it a reduction whose tiles cannot fill the GPU is split into
  * slices that are added in a fixed order (one launch more, same result on every run).  0 bytes means
  * the shape is never split; NULL never splits.  status: device int32 or NULL (MOE_STATUS_BAD_OFFSETS:
- * nothing is written; MOE_STATUS_WAIT_TIMEOUT). */
+ * out is left as it was; MOE_STATUS_WAIT_TIMEOUT: out is left as it was where the reduction is split,
+ * else incomplete). */
 MOE_API size_t moe_grouped_mm_workspace_size(int mode, int M, int K, int N, int E);
 MOE_API int moe_grouped_mm(const void* a, const void* b, const int32_t* offsets, int M, int K, int N, int E,
                            int transpose_b, void* out, int out_fp32, void* workspace, size_t workspace_bytes,

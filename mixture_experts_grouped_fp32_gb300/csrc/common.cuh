@@ -212,8 +212,10 @@ struct GroupedMmArgs {
     bool accumulate;  // mode 2, fp32: out += instead of out =
     int ksplit;       // slices of the reduction; > 1 needs `partial`
     float* partial;   // [ksplit, out elements] fp32
+    int32_t* done;    // with a split: [kGroupedMmDone], a word for each CTA whose slices are there
     int32_t* status;
 };
+constexpr int kGroupedMmDone = 256;
 // Slices of the reduction that a call of this shape uses (1 = no split).
 int grouped_mm_ksplit(int mode, int M, int K, int N, int E, int num_sms);
 cudaError_t launch_grouped_mm(int mode, const GroupedMmArgs& a, int num_sms, cudaStream_t s, const char** why);

@@ -68,6 +68,7 @@ constexpr int TMEM_COLS = NUM_ACC * ACC_COLS;
 constexpr int GROUP_R = 8;  // row tiles that run together
 constexpr int MAX_E = 256;
 constexpr int MAX_SPLIT = 16;
+constexpr int kMaxCtas = kGroupedMmDone;  // of a launch; and threads of the join, one for each of them at least
 constexpr uint16_t BOTH_CTAS = 0x3;
 // Warps: 0 copies, 1 tensor memory and MMAs, then the epilogue's groups of eight, then (weight gradient)
 // one that zeroes segment ends and one that stores the gradients of empty segments.
@@ -96,6 +97,7 @@ struct Ctl {
     uint64_t drain;
     uint32_t tmem_base;
     int abort_flag;
+    int bad_offsets;
     int total_items;
     int seg[MAX_E + 1];
     int item_start[MAX_E + 1];
@@ -197,7 +199,8 @@ struct Maps {
 template <int MODE, typename OUT, bool CHUNKED>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(num_threads<MODE, CHUNKED>(), 1)
 grouped_mm_kernel(const __grid_constant__ Maps maps, const int32_t* __restrict__ offsets, int M, int K, int N, int E,
-                  int ksplit, int accumulate, OUT* __restrict__ out, int32_t* __restrict__ status) {
+                  int ksplit, int accumulate, OUT* __restrict__ out, int32_t* __restrict__ done,
+                  int32_t* __restrict__ status) {
     constexpr bool WGRAD = MODE == kMmWgrad;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = ptx::smem_u32(smem_raw);
@@ -276,6 +279,7 @@ grouped_mm_kernel(const __grid_constant__ Maps maps, const int32_t* __restrict__
         if (lane == 31) {
             c.item_start[E] = incl;
             c.total_items = incl;
+            c.bad_offsets = !ok;
         }
         if (!ok && lane == 0 && leader) flag_status(status, MOE_STATUS_BAD_OFFSETS);
     }
@@ -631,6 +635,8 @@ grouped_mm_kernel(const __grid_constant__ Maps maps, const int32_t* __restrict__
     // ------------------------------ teardown ------------------------------
     ptx::tc_fence_before();
     __syncthreads();
+    // A split reduction's slices are there (each CTA writes its word on every launch).
+    if (done && tid == 0) done[blockIdx.x] = !c.bad_offsets && !c.abort_flag;
     if (warp == 0 && lane == 0 && c.abort_flag) {
         if (leader) {
             for (int s = 0; s < STAGES; ++s)
@@ -652,27 +658,38 @@ grouped_mm_kernel(const __grid_constant__ Maps maps, const int32_t* __restrict__
 }
 
 // Joins the slices of a split reduction: out = sum over s of partial[s], in slice order.  Rows outside
-// [offsets[0], offsets[E]) are not touched (modes with row output); a bad segmentation touches nothing.
+// [offsets[0], offsets[E]) are not touched (modes with row output).  Unless each of the product's `ctas` CTAs
+// has left its word in `done` (a bad segmentation or an expired wait in one: its slices are not there), nothing is
+// written; the first slices are loaded while the words are on their way.
 template <typename OUT>
-__global__ void __launch_bounds__(256)
-grouped_mm_join_kernel(const float4* __restrict__ partial, const int32_t* __restrict__ offsets, int M, int N, int E,
-                       size_t n4, int ksplit, int by_row, int accumulate, OUT* __restrict__ out) {
+__global__ void __launch_bounds__(kMaxCtas)
+grouped_mm_join_kernel(const float4* __restrict__ partial, const int32_t* __restrict__ done, int ctas,
+                       const int32_t* __restrict__ offsets, int M, int N, int E, size_t n4, int ksplit, int by_row,
+                       int accumulate, OUT* __restrict__ out) {
     pdl_wait();
     pdl_trigger();
+    const int good = static_cast<int>(threadIdx.x) < ctas ? __ldcg(done + threadIdx.x) : 1;
     size_t lo = 0, hi = n4;
     if (by_row) {
         const int r0 = __ldg(offsets), r1 = __ldg(offsets + E);
-        if (r0 < 0 || r1 > M || r0 > r1) return;
-        lo = static_cast<size_t>(r0) * N / 4;
-        hi = static_cast<size_t>(r1) * N / 4;
+        const bool inside = r0 >= 0 && r1 <= M && r0 <= r1;
+        lo = inside ? static_cast<size_t>(r0) * N / 4 : 0;
+        hi = inside ? static_cast<size_t>(r1) * N / 4 : 0;
     }
-    for (size_t i = lo + static_cast<size_t>(blockIdx.x) * 256 + threadIdx.x; i < hi;
-         i += static_cast<size_t>(gridDim.x) * 256) {
+    auto sum = [&](size_t i) {
         float4 a = __ldcg(partial + i);
         for (int s = 1; s < ksplit; ++s) {
             const float4 b = __ldcg(partial + s * n4 + i);
             a.x += b.x; a.y += b.y; a.z += b.z; a.w += b.w;
         }
+        return a;
+    };
+    const size_t step = static_cast<size_t>(gridDim.x) * kMaxCtas;
+    size_t i = lo + static_cast<size_t>(blockIdx.x) * kMaxCtas + threadIdx.x;
+    float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (i < hi) a = sum(i);
+    if (!__syncthreads_and(good)) return;
+    while (i < hi) {
         if constexpr (sizeof(OUT) == 4) {
             float4* o = reinterpret_cast<float4*>(out) + i;
             if (accumulate) {
@@ -683,8 +700,12 @@ grouped_mm_join_kernel(const float4* __restrict__ partial, const int32_t* __rest
         } else {
             reinterpret_cast<uint2*>(out)[i] = make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w));
         }
+        i += step;
+        if (i < hi) a = sum(i);
     }
 }
+
+int ctas_of(int num_sms) { return (num_sms < kMaxCtas ? num_sms : kMaxCtas) & ~1; }
 
 template <int MODE, typename OUT, bool CHUNKED>
 cudaError_t launch_as(const GroupedMmArgs& a, OUT* out, int ksplit, int accumulate, int num_sms, cudaStream_t s,
@@ -723,8 +744,9 @@ cudaError_t launch_as(const GroupedMmArgs& a, OUT* out, int ksplit, int accumula
         *why = "cuTensorMapEncodeTiled failed (driver entry point missing or bad operand)";
         return cudaErrorInvalidValue;
     }
-    return launch_k(kPdlTrain, grouped_mm_kernel<MODE, OUT, CHUNKED>, dim3(num_sms & ~1), dim3(num_threads<MODE, CHUNKED>()),
-                    SMEM_BYTES, s, m, a.offsets, a.M, a.K, a.N, a.E, ksplit, accumulate, out, a.status);
+    return launch_k(kPdlTrain, grouped_mm_kernel<MODE, OUT, CHUNKED>, dim3(ctas_of(num_sms)), dim3(num_threads<MODE, CHUNKED>()),
+                    SMEM_BYTES, s, m, a.offsets, a.M, a.K, a.N, a.E, ksplit, accumulate, out, ksplit > 1 ? a.done : nullptr,
+                    a.status);
 }
 
 template <int MODE>
@@ -747,16 +769,16 @@ cudaError_t launch_any(const GroupedMmArgs& a, int num_sms, cudaStream_t s, cons
         cudaError_t e = launch_mode<MODE>(a, a.partial, a.ksplit, 0, num_sms, s, why);
         if (e != cudaSuccess) return e;
         const size_t n4 = (MODE == kMmWgrad ? static_cast<size_t>(a.E) * a.K : static_cast<size_t>(a.M)) * a.N / 4;
-        const size_t want = (n4 + 255) / 256, most = static_cast<size_t>(num_sms) * 8;
+        const size_t want = (n4 + kMaxCtas - 1) / kMaxCtas, most = static_cast<size_t>(num_sms) * 8;
         const dim3 grid(static_cast<unsigned>(want < most ? want : most));
         const int by_row = MODE != kMmWgrad, acc = a.accumulate ? 1 : 0;
         *why = "slice join";
         const float4* p = reinterpret_cast<const float4*>(a.partial);
         if (a.out_f32)
-            return launch_k(kPdlTrain, grouped_mm_join_kernel<float>, grid, dim3(256), 0, s, p, a.offsets, a.M, a.N,
-                            a.E, n4, a.ksplit, by_row, acc, static_cast<float*>(a.out));
-        return launch_k(kPdlTrain, grouped_mm_join_kernel<__nv_bfloat16>, grid, dim3(256), 0, s, p, a.offsets, a.M,
-                        a.N, a.E, n4, a.ksplit, by_row, acc, static_cast<__nv_bfloat16*>(a.out));
+            return launch_k(kPdlTrain, grouped_mm_join_kernel<float>, grid, dim3(kMaxCtas), 0, s, p, a.done,
+                            ctas_of(num_sms), a.offsets, a.M, a.N, a.E, n4, a.ksplit, by_row, acc, static_cast<float*>(a.out));
+        return launch_k(kPdlTrain, grouped_mm_join_kernel<__nv_bfloat16>, grid, dim3(kMaxCtas), 0, s, p, a.done,
+                        ctas_of(num_sms), a.offsets, a.M, a.N, a.E, n4, a.ksplit, by_row, acc, static_cast<__nv_bfloat16*>(a.out));
     }
     const int acc = a.accumulate ? 1 : 0;
     return a.out_f32 ? launch_mode<MODE>(a, static_cast<float*>(a.out), 1, acc, num_sms, s, why)

@@ -20,11 +20,16 @@ int check_grouped(const char* name, int mode, int M, int K, int N, int E) {
     return MOE_OK;
 }
 
-size_t grouped_workspace(int mode, int M, int K, int N, int E) {
+// Floats of the slices of a split reduction (a multiple of 8); 0 if the shape is not split.
+size_t grouped_slices(int mode, int M, int K, int N, int E) {
     const int ks = grouped_mm_ksplit(mode, M, K, N, E, kPlanSms);
-    if (ks <= 1) return 0;
     const size_t rows = mode == kMmWgrad ? static_cast<size_t>(E) * K : static_cast<size_t>(M);
-    return sizeof(float) * ks * rows * N;
+    return ks > 1 ? ks * rows * N : 0;
+}
+// The slices, then the words that say that they are there.
+size_t grouped_workspace(int mode, int M, int K, int N, int E) {
+    const size_t slices = grouped_slices(mode, M, K, N, E);
+    return slices ? sizeof(float) * slices + sizeof(int32_t) * kGroupedMmDone : 0;
 }
 
 int grouped_entry(const char* name, int mode, const void* a, const void* b, const int32_t* offsets, int M, int K,
@@ -47,10 +52,11 @@ int grouped_entry(const char* name, int mode, const void* a, const void* b, cons
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (M == 0)  // the weight gradient of no rows
         return launched(cudaMemsetAsync(out, 0, static_cast<size_t>(E) * K * N * (out_fp32 ? 4 : 2), s), name);
-    GroupedMmArgs g{a, b, offsets, M, K, N, E, out, out_fp32 != 0, accumulate != 0, 1, nullptr, status};
+    GroupedMmArgs g{a, b, offsets, M, K, N, E, out, out_fp32 != 0, accumulate != 0, 1, nullptr, nullptr, status};
     if (workspace && need) {
         g.ksplit = grouped_mm_ksplit(mode, M, K, N, E, kPlanSms);
         g.partial = static_cast<float*>(workspace);
+        g.done = reinterpret_cast<int32_t*>(g.partial + grouped_slices(mode, M, K, N, E));
     }
     const char* why = "launch";
     const cudaError_t e = launch_grouped_mm(mode, g, sms, s, &why);

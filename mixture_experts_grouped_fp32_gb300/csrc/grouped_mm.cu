@@ -73,13 +73,19 @@ constexpr uint16_t BOTH_CTAS = 0x3;
 // Warps: 0 copies, 1 tensor memory and MMAs, then the epilogue's groups of eight, then (weight gradient)
 // one that zeroes segment ends and one that stores the gradients of empty segments.
 constexpr int kEpiWarps = 8;
-// CHUNKED: fp32 outputs of reductions over more than CHUNK blocks of 64, whose partial sums move from tensor
-// memory to registers after every CHUNK of them: one epilogue group keeps the tile's sums across both
-// accumulators.  Otherwise one group for each accumulator, so that short items (a few blocks of reduction)
-// do not wait for one group to read, convert and store tile after tile.
-constexpr int CHUNK = 8;
-template <bool CHUNKED>
-constexpr int chunk_blocks() { return CHUNKED ? CHUNK : 1 << 20; }
+// CHUNKED: long reductions, whose partial sums move from tensor memory to registers after every chunk_blocks
+// blocks of 64, because an addition in tensor memory truncates: one epilogue group keeps the tile's sums across
+// both accumulators.  Otherwise one group for each accumulator, so that short items (a few blocks of reduction)
+// do not wait for one group to read, convert and store tile after tile; the whole reduction then runs in
+// tensor memory.
+//   fp32 outputs: chunks of 8 blocks, for reductions of more than one chunk.
+//   bf16 outputs: unbroken up to UNBROKEN blocks (262144 rows; K ends at 65536), whose 4 truncations a block, of
+//   2^-23 each, come to 2^-9 at the very most, half of a rounding to bf16.  Measured: of 8192 x 28672 outputs summed
+//   over 4096 random products 0.23 % are the neighbour of what an fp32 sum is rounded to, and all are as far
+//   from the sum in 64 bits.  Beyond, chunks of 64 blocks.
+template <typename OUT>
+constexpr int chunk_blocks() { return sizeof(OUT) == 4 ? 8 : 64; }
+constexpr int UNBROKEN = 4096;
 template <bool CHUNKED>
 constexpr int epi_groups() { return CHUNKED ? 1 : 2; }
 template <bool CHUNKED>
@@ -385,7 +391,8 @@ grouped_mm_kernel(const __grid_constant__ Maps maps, const int32_t* __restrict__
             if (it.red0 >= it.red1) continue;  // nothing to reduce: the epilogue stores zeros
             const uint32_t idesc = ptx::idesc_bf16_f32(TILE_F, static_cast<uint32_t>(it.ntok),
                                                        /*a_mn=*/MODE == kMmTransB ? 0 : 1, /*b_mn=*/WGRAD ? 1 : 0);
-            for (int c0 = it.red0; c0 < it.red1 && !aborted; c0 += chunk_blocks<CHUNKED>()) {
+            const int depth = CHUNKED ? chunk_blocks<OUT>() : it.red1 - it.red0;
+            for (int c0 = it.red0; c0 < it.red1 && !aborted; c0 += depth) {
                 if (!ptx::mbar_wait(&c.tempty[acc], acc_phase ^ 1u, abort_flag)) {
                     raise_abort(c, status);
                     aborted = true;
@@ -393,7 +400,7 @@ grouped_mm_kernel(const __grid_constant__ Maps maps, const int32_t* __restrict__
                 }
                 ptx::tc_fence_after();
                 const uint32_t d_tmem = tmem_base + acc * ACC_COLS;
-                const int c1 = min(it.red1, c0 + chunk_blocks<CHUNKED>());
+                const int c1 = min(it.red1, c0 + depth);
                 for (int kb = c0; kb < c1; ++kb) {
                     // (Weight gradient: the other CTA's zeroing warp arrives after its own writes.)
                     if (!(WGRAD ? ptx::mbar_wait_cluster(&c.full[stage], phase, abort_flag)
@@ -489,25 +496,42 @@ grouped_mm_kernel(const __grid_constant__ Maps maps, const int32_t* __restrict__
                 acc_phase ^= 1u;
             }
         };
-        // fp32: stores 32 output rows of which a lane holds one column, up to `rows` of them.
-        auto put = [&](float* p, const uint32_t (&v)[32], int rows) {
-            if (rows >= 32) {
+        // Stores 32 output rows of which a lane holds one column (column n, p its first row), up to `rows` of them.
+        // bf16: neighbouring lanes exchange halves of their pairs of rows: an even lane then holds columns n and
+        // n + 1 of the first row, an odd lane n - 1 and n of the second, one 4-byte store each.
+        const uint32_t sel = lane & 1 ? 0x3276u : 0x5410u;
+        auto put = [&](OUT* p, const uint32_t (&v)[32], int rows, bool mine) {
+            if constexpr (sizeof(OUT) == 4) {
+                if (!mine) return;
+                if (rows >= 32) {
 #pragma unroll
-                for (int j = 0; j < 32; ++j, p += N) *p = __uint_as_float(v[j]);
+                    for (int j = 0; j < 32; ++j, p += N) *p = __uint_as_float(v[j]);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j, p += N)
+                        if (j < rows) *p = __uint_as_float(v[j]);
+                }
             } else {
+                p += static_cast<ptrdiff_t>(lane & 1) * (N - 1);
+                const int nr = rows - (lane & 1);
 #pragma unroll
-                for (int j = 0; j < 32; ++j, p += N)
-                    if (j < rows) *p = __uint_as_float(v[j]);
+                for (int j = 0; j < 16; ++j, p += 2 * static_cast<size_t>(N)) {
+                    const uint32_t own = pack_bf16x2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
+                    const uint32_t other = __shfl_xor_sync(0xffffffffu, own, 1);
+                    if (2 * j < nr && mine) *reinterpret_cast<uint32_t*>(p) = __byte_perm(own, other, sel);
+                }
             }
         };
         // Adds to what is there, in the L2: each element is added to once in a launch, so that the result is
         // that of a load, an addition rounded to nearest and a store (where values under 2^-126 count as zero),
         // without waiting for the load (32 experts' 2048 x 7168 from 16384 rows: 1044 us with loads, 800 so, 691
         // with the lines fetched ahead; pairs of columns per addition took the same time).
-        auto add = [&](float* p, const uint32_t (&v)[32], int rows) {
+        auto add = [&](OUT* p, const uint32_t (&v)[32], int rows, bool mine) {
+            if constexpr (sizeof(OUT) == 4) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j, p += N)
-                if (j < rows) ptx::red_add_f32(p, __uint_as_float(v[j]));
+                for (int j = 0; j < 32; ++j, p += N)
+                    if (j < rows && mine) ptx::red_add_f32(p, __uint_as_float(v[j]));
+            }
         };
         bool aborted = false;
         for (int i = pair_id; i < total && !aborted; i += num_pairs) {
@@ -526,14 +550,13 @@ grouped_mm_kernel(const __grid_constant__ Maps maps, const int32_t* __restrict__
                         ptx::prefetch_l2(dst + static_cast<size_t>(j) * N - lane);
             }
             if constexpr (CHUNKED) {
-                // The chunks' partial sums are added in registers, rounded to nearest: in tensor memory
-                // every addition truncates, a bias that grows with the number of additions.
+                // The chunks' partial sums are added in registers, rounded to nearest.
                 uint32_t sum[4][32];
 #pragma unroll
                 for (int q = 0; q < 4; ++q)
 #pragma unroll
                     for (int j = 0; j < 32; ++j) sum[q][j] = 0u;
-                for (int c0 = it.red0; c0 < it.red1; c0 += CHUNK) {
+                for (int c0 = it.red0; c0 < it.red1; c0 += chunk_blocks<OUT>()) {
                     if (!take()) {
                         aborted = true;
                         break;
@@ -556,10 +579,10 @@ grouped_mm_kernel(const __grid_constant__ Maps maps, const int32_t* __restrict__
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                     const int nr = it.rows - col0 - 32 * q;
-                    if (nr > 0 && n < N) {
-                        float* p = dst + static_cast<size_t>(32 * q) * N;
-                        if (WGRAD && accumulate) add(p, sum[q], nr);
-                        else put(p, sum[q], nr);
+                    if (nr > 0) {
+                        OUT* p = dst + static_cast<size_t>(32 * q) * N;
+                        if (WGRAD && accumulate) add(p, sum[q], nr, n < N);
+                        else put(p, sum[q], nr, n < N);
                     }
                 }
             } else {
@@ -571,31 +594,14 @@ grouped_mm_kernel(const __grid_constant__ Maps maps, const int32_t* __restrict__
                     aborted = true;
                     break;
                 }
-                // bf16: neighbouring lanes exchange halves of their pairs of rows: an even lane then holds columns
-                // n and n + 1 of the first row, an odd lane n - 1 and n of the second, one 4-byte store each.
-                const uint32_t sel = lane & 1 ? 0x3276u : 0x5410u;
 #pragma unroll 1
                 for (int j0 = 0; j0 < 128 && col0 + j0 < it.rows; j0 += 32) {
                     uint32_t v[32];
                     ptx::tmem_ld_32x32b_x32(lane_addr + acc * ACC_COLS + j0, v);
                     ptx::tmem_ld_wait();
-                    if constexpr (sizeof(OUT) == 4) {
-                        if (n < N) {
-                            float* p = dst + static_cast<size_t>(j0) * N;
-                            const int nr = it.rows - col0 - j0;
-                            if (WGRAD && accumulate) add(p, v, nr);
-                            else put(p, v, nr);
-                        }
-                    } else {
-                        OUT* p = dst + static_cast<size_t>(j0) * N - (lane & 1) + static_cast<size_t>(lane & 1) * N;
-                        const int nr = it.rows - col0 - j0 - (lane & 1);
-#pragma unroll
-                        for (int j = 0; j < 16; ++j, p += 2 * static_cast<size_t>(N)) {
-                            const uint32_t own = pack_bf16x2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
-                            const uint32_t other = __shfl_xor_sync(0xffffffffu, own, 1);
-                            if (2 * j < nr && n < N) *reinterpret_cast<uint32_t*>(p) = __byte_perm(own, other, sel);
-                        }
-                    }
+                    OUT* p = dst + static_cast<size_t>(j0) * N;
+                    if (WGRAD && accumulate) add(p, v, it.rows - col0 - j0, n < N);
+                    else put(p, v, it.rows - col0 - j0, n < N);
                 }
                 give();
                 pass();
@@ -754,12 +760,16 @@ cudaError_t launch_mode(const GroupedMmArgs& a, float* out, int ksplit, int accu
                         const char** why) {
     // Blocks of the longest reduction, at most.
     const int blocks = ((MODE == kMmWgrad ? a.M : a.K) + BK - 1) / BK;
-    return (blocks + ksplit - 1) / ksplit > CHUNK ? launch_as<MODE, float, true>(a, out, ksplit, accumulate, num_sms, s, why)
+    return (blocks + ksplit - 1) / ksplit > chunk_blocks<float>() ? launch_as<MODE, float, true>(a, out, ksplit, accumulate, num_sms, s, why)
                                                   : launch_as<MODE, float, false>(a, out, ksplit, accumulate, num_sms, s, why);
 }
 template <int MODE>
 cudaError_t launch_mode(const GroupedMmArgs& a, __nv_bfloat16* out, int ksplit, int accumulate, int num_sms,
                         cudaStream_t s, const char** why) {
+    // A segment's rows are on the device: the rule goes by all of them (300000 rows, 2048 x 1408: 64 segments 1200 us
+    // unbroken and 1228 in chunks, 256 segments 1355 and 1403; 256 of 512 x 512 150 and 155).
+    if constexpr (MODE == kMmWgrad)
+        if ((a.M + BK - 1) / BK > UNBROKEN) return launch_as<MODE, __nv_bfloat16, true>(a, out, ksplit, accumulate, num_sms, s, why);
     return launch_as<MODE, __nv_bfloat16, false>(a, out, ksplit, accumulate, num_sms, s, why);
 }
 

@@ -1,0 +1,75 @@
+"""Grouped products over long reductions, against 64 bits.
+
+Tolerances: the products of bf16 values are exact in fp32.  Within a chunk of 64-row (or 64-column) blocks each of four
+additions a block truncates, by 2^-23 of a partial sum at most; the chunks' sums are added rounded to nearest,
+2^-24 each; a bf16 output is rounded once more, by at most 2^-8 of its value.  A chunk is 64 blocks for a bf16
+output of more than 262144 rows, all of them for one of fewer."""
+import numpy as np
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+BF16, F32, D = torch.bfloat16, torch.float32, torch.float64
+
+
+@pytest.fixture(scope="module")
+def moe():
+    from mixture_experts_grouped_fp32_gb300 import moe as m
+    yield m
+    torch.cuda.empty_cache()
+
+
+def wgrad64(a, g, lo, hi, step=1 << 22):
+    """Gradient of one segment in 64 bits, and the sum of its terms' magnitudes."""
+    ref = torch.zeros(a.shape[1], g.shape[1], dtype=D, device="cuda")
+    mag = torch.zeros_like(ref)
+    for r in range(lo, hi, step):
+        x, y = a[r:min(hi, r + step)].to(D), g[r:min(hi, r + step)].to(D)
+        ref += x.T @ y
+        mag += x.abs().T @ y.abs()
+    return ref, mag
+
+
+def check_bf16(got, ref, mag, rows, chunk_rows, what):
+    chunks = -(-rows // chunk_rows)
+    sums = min(rows, chunk_rows) / 16 * 2.0 ** -23 + chunks * 2.0 ** -24
+    off = (got.to(D) - ref).abs()
+    bound = sums * mag + 2.0 ** -8 * ref.abs() + 1e-30
+    assert (off <= bound).all(), f"{what}: worst {float((off / bound).max())} of the bound"
+
+
+@pytest.mark.parametrize("rows", [262144 - 3000, 262144 + 40, 300000])
+def test_bf16_gradients_of_long_segments(moe, rows):
+    """Positive terms, whose truncations all go one way; segments of all lengths beside the long one."""
+    counts = [0, 5, rows - 2600, 700, 0, 1, 64, 1830]
+    M, K, N = sum(counts), 264, 520
+    offs = np.concatenate([[0], np.cumsum(counts)])
+    gen = torch.Generator("cuda").manual_seed(rows)
+    a = (torch.rand(M, K, generator=gen, device="cuda") + 0.5).to(BF16)
+    g = (torch.rand(M, N, generator=gen, device="cuda") + 0.5).to(BF16)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    # (Without a workspace, so that the reduction is not split.)
+    out = torch.full((len(counts), K, N), 7.0, dtype=BF16, device="cuda")
+    L = moe.load()
+    o = torch.tensor(offs, dtype=torch.int32, device="cuda")
+    assert L.moe_grouped_mm_wgrad(a.data_ptr(), g.data_ptr(), o.data_ptr(), M, K, N, len(counts), out.data_ptr(), 0, 0, None,
+                                  0, status.data_ptr(), torch.cuda.current_stream().cuda_stream) == 0
+    assert moe.get_device_error(status) == 0
+    for e, n in enumerate(counts):
+        ref, mag = wgrad64(a, g, int(offs[e]), int(offs[e + 1]))
+        check_bf16(out[e], ref, mag, n, 4096 if M > 262144 else 262144, f"segment of {n} rows")
+
+
+def test_bf16_gradient_of_a_segment_of_seventy_million_rows(moe):
+    long = (1 << 26) + (1 << 22)
+    counts = [1000] * 40 + [long] + [1000] * 59  # 100 tiles: more than there are SM pairs, so never split
+    M = sum(counts)
+    assert moe.grouped_mm_workspace_size(2, M, 8, 8, len(counts)) == 0
+    gen = torch.Generator("cuda").manual_seed(1)
+    a, g = (torch.rand(M, 8, generator=gen, device="cuda").add_(0.5).to(BF16) for _ in range(2))
+    offs = np.concatenate([[0], np.cumsum(counts)])
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = moe.grouped_mm_wgrad(a, g, torch.tensor(offs, dtype=torch.int32, device="cuda"), out_dtype=BF16, status=status)
+    assert moe.get_device_error(status) == 0
+    for e, n in enumerate(counts):
+        check_bf16(out[e], *wgrad64(a, g, int(offs[e]), int(offs[e + 1])), n, 4096, f"segment {e} of {n} rows")

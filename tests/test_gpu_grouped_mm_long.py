@@ -73,3 +73,29 @@ def test_bf16_gradient_of_a_segment_of_seventy_million_rows(moe):
     assert moe.get_device_error(status) == 0
     for e, n in enumerate(counts):
         check_bf16(out[e], *wgrad64(a, g, int(offs[e]), int(offs[e + 1])), n, 4096, f"segment {e} of {n} rows")
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_gradient_of_a_segment_that_takes_seconds(moe, dtype):
+    """No wait inside the kernel runs out while one segment is worked on, however long it is."""
+    counts = [1000] * 40 + [750_000_005] + [1000] * 59
+    M = sum(counts)
+    a, g = (torch.empty(M, 8, dtype=BF16, device="cuda") for _ in range(2))
+    gen = torch.Generator("cuda").manual_seed(2)
+    for t in (a, g):
+        t.uniform_(0.5, 1.5, generator=gen)
+    offs = np.concatenate([[0], np.cumsum(counts)])
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    start, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    start.record()
+    out = moe.grouped_mm_wgrad(a, g, torch.tensor(offs, dtype=torch.int32, device="cuda"), out_dtype=dtype, status=status)
+    end.record()
+    assert moe.get_device_error(status) == 0
+    print(f"{start.elapsed_time(end):.0f} ms")
+    for e in (0, 39, 40, 41, 76, 99):
+        n = counts[e]
+        ref, mag = wgrad64(a, g, int(offs[e]), int(offs[e + 1]))
+        if dtype == BF16:
+            check_bf16(out[e], ref, mag, n, 4096, f"segment {e}")
+        else:  # chunks of 512 rows: 32 truncations each, then the chunks' sums
+            assert ((out[e].to(D) - ref).abs() <= (32 * 2.0 ** -23 + -(-n // 512) * 2.0 ** -24) * mag).all(), e

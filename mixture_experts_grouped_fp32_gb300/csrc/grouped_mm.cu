@@ -155,7 +155,8 @@ struct Cursor {
             cnt = c.seg[e + 1] - c.seg[e];
             total = MODE == kMmWgrad ? K : cnt;
             rt = row_tiles<MODE>(cnt, K);
-            per = (((total + rt - 1) / rt) + 31) & ~31;  // equal tiles; the last one may be shorter
+            // Equal tiles; the last one may be shorter.  (total + rt passes 2^31.)
+            per = ((static_cast<int>((static_cast<unsigned>(total) + rt - 1u) / rt)) + 31) & ~31;
             nkb = ((MODE == kMmWgrad ? cnt : K) + BK - 1) / BK;
         }
         Item it;

@@ -99,3 +99,36 @@ def test_gradient_of_a_segment_that_takes_seconds(moe, dtype):
             check_bf16(out[e], ref, mag, n, 4096, f"segment {e}")
         else:  # chunks of 512 rows: 32 truncations each, then the chunks' sums
             assert ((out[e].to(D) - ref).abs() <= (32 * 2.0 ** -23 + -(-n // 512) * 2.0 ** -24) * mag).all(), e
+
+
+MOST = 2 ** 31 - 1025  # rows that the calls accept
+
+
+@pytest.mark.parametrize("way", ["fwd", "dgrad"])
+def test_as_many_rows_as_the_calls_accept(moe, way):
+    """One segment of (nearly) all rows: its tile counts and positions pass 2^31 in sums."""
+    gen = torch.Generator("cuda").manual_seed(3)
+    a = torch.empty(MOST, 8, dtype=BF16, device="cuda").uniform_(-1, 1, generator=gen)
+    b = torch.empty(2, 8, 8, dtype=BF16, device="cuda").uniform_(-1, 1, generator=gen)
+    offs = torch.tensor([0, 3, MOST], dtype=torch.int32, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = moe.grouped_mm(a, b, offs, transpose_b=way == "dgrad", status=status)
+    assert moe.get_device_error(status) == 0
+    for lo in (0, 1 << 20, 1 << 30, 2139127680 - 500, MOST - 2000):
+        x = a[lo:lo + 2000].to(D)
+        w = (b if way == "fwd" else b.transpose(1, 2)).to(D)
+        e = torch.ones(2000, dtype=torch.long, device="cuda")
+        if lo == 0:
+            e[:3] = 0
+        ref, mag = torch.einsum("rk,rkn->rn", x, w[e]), torch.einsum("rk,rkn->rn", x.abs(), w[e].abs())
+        assert ((out[lo:lo + 2000].to(D) - ref).abs() <= 2.0 ** -8 * ref.abs() + 8 * 2.0 ** -23 * mag).all(), lo
+
+
+def test_gradient_of_as_many_rows_as_the_calls_accept(moe):
+    gen = torch.Generator("cuda").manual_seed(4)
+    a, g = (torch.empty(MOST, 8, dtype=BF16, device="cuda").uniform_(0.5, 1.5, generator=gen) for _ in range(2))
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = moe.grouped_mm_wgrad(a, g, torch.tensor([0, MOST], dtype=torch.int32, device="cuda"), status=status)
+    assert moe.get_device_error(status) == 0
+    ref, mag = wgrad64(a, g, 0, MOST)
+    assert ((out[0].to(D) - ref).abs() <= (32 * 2.0 ** -23 + (MOST // 512 + 1) * 2.0 ** -24) * mag).all()

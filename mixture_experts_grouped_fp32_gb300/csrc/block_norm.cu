@@ -145,7 +145,7 @@ norm_rows_kernel(const X* __restrict__ x, const __nv_bfloat16* __restrict__ h, c
     const float inv_d = 1.0f / static_cast<float>(d);
     const int per_vec = XW + (H ? 1 : 0);
     const Ring ring{ring_smem + tid, VPT * per_vec, nt};
-    const int rows = (T - static_cast<int>(blockIdx.x) + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x);
+    const int rows = (T - static_cast<int>(blockIdx.x) - 1) / static_cast<int>(gridDim.x) + 1;  // gridDim.x <= T
     pdl_wait();
     pdl_trigger();
     auto row_of = [&](int k) { return static_cast<size_t>(blockIdx.x) + static_cast<size_t>(k) * gridDim.x; };

@@ -894,6 +894,13 @@ def _arg(t: torch.Tensor, dtype, shape: tuple, name: str) -> int:
     return t.data_ptr()
 
 
+def _fit(**sizes) -> None:
+    """The C calls take sizes as 32-bit integers, and ctypes passes larger ones on modulo 2^32."""
+    for name, v in sizes.items():
+        if not -2 ** 31 <= v < 2 ** 31:
+            raise ValueError(f"{name} = {v} is not below 2^31")
+
+
 def _opt(t, dtype, shape, name):
     return None if t is None else _arg(t, dtype, shape, name)
 
@@ -908,6 +915,7 @@ def _out(out, shape, dtype, device, stream, name="out"):
 @functools.lru_cache(maxsize=4096)
 def grouped_mm_workspace_size(mode: int, M: int, K: int, N: int, E: int) -> int:
     """Bytes of workspace of a grouped product (mode 0: plain, 1: transpose_b, 2: weight gradient)."""
+    _fit(M=M, K=K, N=N, E=E)
     return int(load().moe_grouped_mm_workspace_size(mode, M, K, N, E))
 
 
@@ -940,6 +948,7 @@ def grouped_mm(a, b, offsets, transpose_b: bool = False, out=None, out_dtype=tor
         raise ValueError("a must be [M, K] and b [E, K, N] (or [E, N, K] with transpose_b)")
     M, K = a.shape
     E, N = b.shape[0], b.shape[1 if transpose_b else 2]
+    _fit(M=M, K=K, N=N, E=E)
     pa = _arg(a, torch.bfloat16, (M, K), "a")
     pb = _arg(b, torch.bfloat16, (E, N, K) if transpose_b else (E, K, N), "b")
     po = _arg(offsets, torch.int32, (E + 1,), "offsets")
@@ -964,6 +973,7 @@ def grouped_mm_wgrad(a, g, offsets, out=None, out_dtype=torch.float32, accumulat
         raise ValueError("a must be [M, K], g [M, N] and offsets [E + 1]")
     M, K = a.shape
     N, E = g.shape[1], offsets.shape[0] - 1
+    _fit(M=M, K=K, N=N, E=E)
     pa, pg = _arg(a, torch.bfloat16, (M, K), "a"), _arg(g, torch.bfloat16, (M, N), "g")
     po = _arg(offsets, torch.int32, (E + 1,), "offsets")
     if accumulate and out is None:
@@ -991,6 +1001,7 @@ def _gu_dims(gu, w):
     if gu.dim() != 2 or gu.shape[1] % 2:
         raise ValueError(f"gu must be [M, 2f], got {tuple(gu.shape)}")
     M, f2 = gu.shape
+    _fit(M=M, f=f2 // 2)
     return M, f2 // 2, _arg(gu, torch.bfloat16, (M, f2), "gu"), _opt(w, torch.float32, (M,), "w")
 
 
@@ -1018,6 +1029,7 @@ def _norm_inputs(x, w_pre, h, w_post, gate, token_gate, res_scale):
     if x.dim() != 2:
         raise ValueError(f"x must be [T, d], got {tuple(x.shape)}")
     T, d = x.shape
+    _fit(T=T, d=d)
     f, vec = torch.float32, (d,)
     return (T, d, int(dt is f), _arg(x, dt, (T, d), "x"), _opt(h, torch.bfloat16, (T, d), "h"),
             _opt(w_pre, f, vec, "w_pre"), _opt(w_post, f, vec, "w_post"), _opt(gate, f, vec, "gate"),
@@ -1148,6 +1160,7 @@ def adamw_step(params, grads, m, v, lr: float, beta1: float = 0.9, beta2: float 
     if eight != (m_scales is not None) or eight != (v_scales is not None):
         raise ValueError("m_scales and v_scales belong to 8-bit moments, and only to them")
     n = len(params)
+    _fit(step=step)
     tab = np.zeros(n, _ADAMW_ENTRY)
     tab["param"], sizes = _addresses(params, "params", pt)
     tab["n"] = sizes

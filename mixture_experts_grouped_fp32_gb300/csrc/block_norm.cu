@@ -31,7 +31,7 @@
 // atomics, the same result on every run.
 #include <algorithm>
 
-#include "tcgen05.cuh"
+#include "train_ptx.cuh"
 #include "train_util.cuh"
 
 namespace moe {

@@ -711,36 +711,6 @@ bool make_tensor_map_bf16(CUtensorMap* m, const void* base, uint64_t cols, uint6
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// 3-D bf16 tensor [d2, rows, cols] (cols contiguous), box = [1, box_rows, 64 cols], 128-byte swizzle.
-bool make_tensor_map_bf16_3d(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows, uint64_t d2,
-                             uint32_t box_rows) {
-    auto enc = get_encode_fn();
-    if (!enc) return false;
-    cuuint64_t dims[3] = {cols, rows, d2};
-    cuuint64_t strides[2] = {cols * 2, cols * rows * 2};
-    cuuint32_t box[3] = {64, box_rows, 1};
-    cuuint32_t estr[3] = {1, 1, 1};
-    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// bf16 tensor [d3, rows, cols] viewed as [d3, cols / 64, rows, 64] (cols a multiple of 64): box = [1,
-// blocks, box_rows, 64], i.e. `blocks` neighbouring 64-column boxes in one copy, one after another in
-// shared memory, 128-byte swizzle.
-bool make_tensor_map_bf16_blocks(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows, uint64_t d3,
-                                 uint32_t box_rows, uint32_t blocks) {
-    auto enc = get_encode_fn();
-    if (!enc || cols % 64) return false;
-    cuuint64_t dims[4] = {64, rows, cols / 64, d3};
-    cuuint64_t strides[3] = {cols * 2, 128, cols * rows * 2};
-    cuuint32_t box[4] = {64, box_rows, blocks, 1};
-    cuuint32_t estr[4] = {1, 1, 1, 1};
-    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, estr,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 // Blocked FP8 weight codes [rows / 64, K / 128, 64, 128] as a 4-D tensor (innermost first: 128 K
 // codes, 64 rows, K block, 64-row group); box = 128 codes x 64 rows x 1 K block x box_rows / 64
 // groups, which lands in shared memory as box_rows K-major rows of 128 bytes, 128-byte swizzled.

@@ -48,7 +48,7 @@
 // counts both CTAs' copies, empty[s] and tfull[a] are arrived on in both CTAs by CTA 0's multicast
 // commits, tempty[a] lives in CTA 0.  Every wait is bounded and reports MOE_STATUS_WAIT_TIMEOUT.
 #include "common.cuh"
-#include "tcgen05.cuh"
+#include "train_ptx.cuh"
 
 namespace moe {
 namespace {

@@ -11,9 +11,9 @@
 #include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAStream.h>
 #include <dlfcn.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
-#include <exception>
 #include <vector>
 
 #include "../../include/moe.h"
@@ -72,15 +72,13 @@ PyObject* code(int rc) { return PyLong_FromLong(rc); }
 moe_stream_t stream() { return c10::cuda::getCurrentCUDAStream().stream(); }
 bool fits(int64_t v) { return v >= 0 && v < (1ll << 31); }
 
-// Runs a function's body; a C++ exception (an allocation that failed, say) becomes a Python one.
+// Runs a function's body; a C++ exception becomes the Python one that torch's own functions raise for it (an
+// allocation that failed: torch.OutOfMemoryError).
 template <typename F>
 PyObject* guarded(F body) {
-    try {
-        return body();
-    } catch (const std::exception& e) {
-        if (!PyErr_Occurred()) PyErr_SetString(PyExc_RuntimeError, e.what());
-        return nullptr;
-    }
+    HANDLE_TH_ERRORS
+    return body();
+    END_HANDLE_TH_ERRORS
 }
 
 // swiglu(gu, w)

@@ -81,6 +81,17 @@ PyObject* guarded(F body) {
     END_HANDLE_TH_ERRORS
 }
 
+// A C call without the interpreter lock, as ctypes makes it: a launch waits where the launch queue is full, perhaps
+// for a host function on the stream that needs the lock.
+template <typename F>
+int unlocked(F call) {
+    struct Lock {
+        PyThreadState* state = PyEval_SaveThread();
+        ~Lock() { PyEval_RestoreThread(state); }
+    } released;
+    return call();
+}
+
 // swiglu(gu, w)
 PyObject* swiglu(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return guarded([&]() -> PyObject* {
@@ -92,7 +103,9 @@ PyObject* swiglu(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const void* pw = c.opt(a[1], F32, {M});
         if (!c.ok) Py_RETURN_NONE;
         at::Tensor h = make({M, f}, BF16, *gu);
-        const int rc = lib.moe_swiglu(pg, static_cast<const float*>(pw), M, f, ptr(h), stream());
+        const int rc = unlocked([&] {
+            return lib.moe_swiglu(pg, static_cast<const float*>(pw), M, f, ptr(h), stream());
+        });
         return rc ? code(rc) : wrap(h);
     });
 }
@@ -111,8 +124,10 @@ PyObject* swiglu_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
         at::Tensor dgu = make({M, 2 * f}, BF16, *gu), dw, h;
         if (a[2] != Py_None) dw = make({M}, F32, *gu);
         if (PyObject_IsTrue(a[3])) h = make({M, f}, BF16, *gu);
-        const int rc = lib.moe_swiglu_backward(pg, pd, static_cast<const float*>(pw), M, f, ptr(dgu),
-                                               static_cast<float*>(ptr(dw)), ptr(h), stream());
+        const int rc = unlocked([&] {
+            return lib.moe_swiglu_backward(pg, pd, static_cast<const float*>(pw), M, f, ptr(dgu),
+                                           static_cast<float*>(ptr(dw)), ptr(h), stream());
+        });
         return rc ? code(rc) : Py_BuildValue("(NNN)", wrap(dgu), wrap(dw), wrap(h));
     });
 }
@@ -152,8 +167,10 @@ PyObject* block_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
         at::Tensor y, out;
         if (v.has_h) y = make({v.T, v.d}, v.type, *v.x);
         if (v.has_pre) out = make({v.T, v.d}, BF16, *v.x);
-        const int rc = lib.moe_block_norm(v.px, v.type == F32, v.h, v.w_pre, v.w_post, v.gate, v.tgate, v.res, v.T,
-                                          v.d, static_cast<float>(eps), ptr(y), ptr(out), stream());
+        const int rc = unlocked([&] {
+            return lib.moe_block_norm(v.px, v.type == F32, v.h, v.w_pre, v.w_post, v.gate, v.tgate, v.res, v.T,
+                                      v.d, static_cast<float>(eps), ptr(y), ptr(out), stream());
+        });
         return rc ? code(rc) : Py_BuildValue("(NN)", wrap(y), wrap(out));
     });
 }
@@ -178,9 +195,11 @@ PyObject* block_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
         for (int k = 0; k < 4; ++k)  // w_post, gate, token_gate, res_scale
             if (a[5 + k] != Py_None) g[3 + k] = make({k == 2 ? v.T : v.d}, F32, *v.x);
         auto f = [&](int k) { return static_cast<float*>(ptr(g[k])); };
-        const int rc = lib.moe_block_norm_backward(v.px, v.type == F32, v.h, dy, dn, v.w_pre, v.w_post, v.gate, v.tgate,
-                                                   v.res, v.T, v.d, static_cast<float>(eps), ptr(g[0]), ptr(g[1]), f(2),
-                                                   f(3), f(4), f(5), f(6), ptr(ws), need, stream());
+        const int rc = unlocked([&] {
+            return lib.moe_block_norm_backward(v.px, v.type == F32, v.h, dy, dn, v.w_pre, v.w_post, v.gate, v.tgate,
+                                               v.res, v.T, v.d, static_cast<float>(eps), ptr(g[0]), ptr(g[1]), f(2),
+                                               f(3), f(4), f(5), f(6), ptr(ws), need, stream());
+        });
         return rc ? code(rc)
                   : Py_BuildValue("(NNNNNNN)", wrap(g[0]), wrap(g[1]), wrap(g[2]), wrap(g[3]), wrap(g[4]), wrap(g[5]),
                                   wrap(g[6]));
@@ -203,8 +222,10 @@ PyObject* grouped_mm(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const size_t need = lib.moe_grouped_mm_workspace_size(trans ? 1 : 0, M, K, N, E);
         at::Tensor ws, out = make({M, N}, f32 ? F32 : BF16, *x);
         if (need) ws = make({static_cast<int64_t>(need)}, ScalarType::Byte, *x);
-        const int rc = lib.moe_grouped_mm(pa, pb, static_cast<const int32_t*>(po), M, K, N, E, trans, ptr(out), f32,
-                                          ptr(ws), need, static_cast<int32_t*>(st), stream());
+        const int rc = unlocked([&] {
+            return lib.moe_grouped_mm(pa, pb, static_cast<const int32_t*>(po), M, K, N, E, trans, ptr(out), f32,
+                                      ptr(ws), need, static_cast<int32_t*>(st), stream());
+        });
         return rc ? code(rc) : wrap(out);
     });
 }
@@ -227,8 +248,10 @@ PyObject* grouped_mm_wgrad(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const size_t need = lib.moe_grouped_mm_workspace_size(2, M, K, N, E);
         at::Tensor ws, out = a[3] == Py_None ? make({E, K, N}, f32 ? F32 : BF16, *x) : *tensor(a[3]);
         if (need) ws = make({static_cast<int64_t>(need)}, ScalarType::Byte, *x);
-        const int rc = lib.moe_grouped_mm_wgrad(pa, pg, static_cast<const int32_t*>(po), M, K, N, E, ptr(out), f32, acc,
-                                                ptr(ws), need, static_cast<int32_t*>(st), stream());
+        const int rc = unlocked([&] {
+            return lib.moe_grouped_mm_wgrad(pa, pg, static_cast<const int32_t*>(po), M, K, N, E, ptr(out), f32, acc,
+                                            ptr(ws), need, static_cast<int32_t*>(st), stream());
+        });
         if (rc) return code(rc);
         if (a[3] == Py_None) return wrap(out);
         Py_INCREF(a[3]);
@@ -288,9 +311,10 @@ PyObject* adamw_step(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const long step = PyLong_AsLong(a[12]);
         if (step == -1 && PyErr_Occurred()) return nullptr;
         if (step < 1 || step > 0x7fffffff) Py_RETURN_NONE;
-        return code(lib.moe_adamw_step(table.data(), static_cast<int>(count), pt == BF16, gt == BF16, eight ? 8 : 32,
-                                       h[0], h[1], h[2], h[3], h[4], static_cast<int>(step), nullptr, nullptr,
-                                       stream()));
+        return code(unlocked([&] {
+            return lib.moe_adamw_step(table.data(), static_cast<int>(count), pt == BF16, gt == BF16, eight ? 8 : 32, h[0],
+                                      h[1], h[2], h[3], h[4], static_cast<int>(step), nullptr, nullptr, stream());
+        }));
     });
 }
 

@@ -33,3 +33,59 @@ def test_a_failed_allocation_is_torchs_error(moe):
     finally:
         torch.cuda.set_per_process_memory_fraction(1.0)
     assert moe.grouped_mm(a[:8], b, offs.clamp_max(8)).shape == (8, 8192)
+
+
+STUB = r"""
+#include <stddef.h>
+#include <time.h>
+#define API __attribute__((visibility("default")))
+API volatile int entered, go;
+/* Waits up to 3 s for another thread of the interpreter to set `go`. */
+API int moe_swiglu() {
+    struct timespec ms = {0, 1000000};
+    entered = 1;
+    for (int i = 0; i < 3000 && !go; ++i) nanosleep(&ms, NULL);
+    return go ? 0 : 99;
+}
+API int moe_swiglu_backward() { return 0; }
+API int moe_block_norm() { return 0; }
+API int moe_block_norm_backward() { return 0; }
+API size_t moe_block_norm_backward_workspace_size() { return 0; }
+API int moe_grouped_mm() { return 0; }
+API int moe_grouped_mm_wgrad() { return 0; }
+API size_t moe_grouped_mm_workspace_size() { return 0; }
+API int moe_adamw_step() { return 0; }
+"""
+
+
+def test_other_threads_run_during_a_call(tmp_path):
+    """A call that waits (here in a library that stands in for the real one) does not hold the interpreter lock."""
+    import ctypes
+    import shutil
+    import subprocess
+    import threading
+    import time
+
+    from mixture_experts_grouped_fp32_gb300 import moe as m
+    m.load()
+    fast = pytest.importorskip("mixture_experts_grouped_fp32_gb300._moe_fast")
+    if not shutil.which("gcc"):
+        pytest.skip("no gcc")
+    src, lib = tmp_path / "stub.c", tmp_path / "libstub.so"
+    src.write_text(STUB)
+    subprocess.run(["gcc", "-shared", "-fPIC", "-o", str(lib), str(src)], check=True)
+    stub = ctypes.CDLL(str(lib))
+    entered, go = (ctypes.c_int.in_dll(stub, n) for n in ("entered", "go"))
+    gu, result = z(4, 16), []
+    fast.init(str(lib))
+    try:
+        caller = threading.Thread(target=lambda: result.append(fast.swiglu(gu, None)))
+        caller.start()
+        end = time.time() + 10
+        while not entered.value and time.time() < end:
+            time.sleep(0.001)
+        go.value = 1
+        caller.join()
+    finally:
+        fast.init(m.LIB_PATH)
+    assert isinstance(result[0], torch.Tensor), "the call held the lock until it gave up"

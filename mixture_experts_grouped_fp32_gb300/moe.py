@@ -113,11 +113,12 @@ _lock = threading.Lock()
 _lib = None
 _fns: dict = {}  # the bound entry points of the loaded library, by name
 _fast = None  # the usual calls in C++ (_moe_fast.so), where it was built
+_several = True  # devices; of one, all CUDA tensors are on it (known once the library is loaded)
 
 
 def load(path: str = LIB_PATH) -> ctypes.CDLL:
     """Load ``libmoe.so`` (once).  Raises if it has not been built."""
-    global _lib, _fast
+    global _lib, _fast, _several
     with _lock:
         if _lib is None:
             if not os.path.exists(path):
@@ -136,6 +137,7 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
                     _fast = _moe_fast
                 except (ImportError, OSError):  # built against another torch: ctypes does the same
                     _fast = None
+            _several = torch.cuda.device_count() > 1
             _lib = lib
     return _lib
 
@@ -891,13 +893,46 @@ def _arg(t: torch.Tensor, dtype, shape: tuple, name: str) -> int:
     if t.dtype is not dtype or t.shape != shape or not t.is_cuda or not t.is_contiguous():
         _dev(t, dtype, name)
         _shaped(t, shape, name)
+    if _several:
+        _here(t, name)
     return t.data_ptr()
+
+
+def _here(t: torch.Tensor, name: str) -> None:
+    """The calls launch on the current device."""
+    if t.get_device() != torch._C._cuda_getDevice():
+        raise ValueError(f"{name} is on device {t.get_device()}, the current one is {torch._C._cuda_getDevice()}")
+
+
+def _word(status) -> int | None:
+    """The address of a status word (which may be a piece of a workspace)."""
+    if status is None:
+        return None
+    if status.dtype is not torch.int32 or not status.is_cuda or status.numel() < 1:
+        raise ValueError(f"status must be a CUDA int32 tensor, got {status.dtype}, cuda={status.is_cuda}")
+    if _several:
+        _here(status, "status")
+    return status.data_ptr()
+
+
+def _scratch(workspace) -> tuple:
+    """The address and bytes of a workspace."""
+    if workspace is None:
+        return None, 0
+    if not workspace.is_cuda or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous CUDA tensor")
+    if _several:
+        _here(workspace, "workspace")
+    return workspace.data_ptr(), workspace.nbytes
+
+
+_INT_MAX = 2 ** 31 - 1
 
 
 def _fit(**sizes) -> None:
     """The C calls take sizes as 32-bit integers, and ctypes passes larger ones on modulo 2^32."""
     for name, v in sizes.items():
-        if not -2 ** 31 <= v < 2 ** 31:
+        if not -2 ** 31 <= v <= _INT_MAX:
             raise ValueError(f"{name} = {v} is not below 2^31")
 
 
@@ -932,7 +967,7 @@ def _mm_args(mode, M, K, N, E, out, out_dtype, shape, workspace, device, stream)
         need = grouped_mm_workspace_size(mode, M, K, N, E)
         if need:
             workspace = _empty(need, torch.uint8, device, stream)
-    return out, int(out_dtype == torch.float32), workspace, 0 if workspace is None else workspace.nbytes
+    return (out, int(out_dtype == torch.float32), *_scratch(workspace), workspace)
 
 
 def grouped_mm(a, b, offsets, transpose_b: bool = False, out=None, out_dtype=torch.bfloat16, workspace=None,
@@ -948,14 +983,15 @@ def grouped_mm(a, b, offsets, transpose_b: bool = False, out=None, out_dtype=tor
         raise ValueError("a must be [M, K] and b [E, K, N] (or [E, N, K] with transpose_b)")
     M, K = a.shape
     E, N = b.shape[0], b.shape[1 if transpose_b else 2]
-    _fit(M=M, K=K, N=N, E=E)
+    if max(M, K, N, E) > _INT_MAX:
+        _fit(M=M, K=K, N=N, E=E)
     pa = _arg(a, torch.bfloat16, (M, K), "a")
     pb = _arg(b, torch.bfloat16, (E, N, K) if transpose_b else (E, K, N), "b")
     po = _arg(offsets, torch.int32, (E + 1,), "offsets")
-    out, f32, workspace, nbytes = _mm_args(1 if transpose_b else 0, M, K, N, E, out, out_dtype, (M, N), workspace,
-                                           a.device, stream)
-    _call("moe_grouped_mm", pa, pb, po, M, K, N, E, int(transpose_b), out.data_ptr(), f32, _ptr(workspace), nbytes,
-          _ptr(status), _stream(stream))
+    out, f32, pws, nbytes, _kept = _mm_args(1 if transpose_b else 0, M, K, N, E, out, out_dtype, (M, N), workspace,
+                                               a.device, stream)
+    _call("moe_grouped_mm", pa, pb, po, M, K, N, E, int(transpose_b), out.data_ptr(), f32, pws, nbytes,
+          _word(status), _stream(stream))
     return out
 
 
@@ -973,14 +1009,15 @@ def grouped_mm_wgrad(a, g, offsets, out=None, out_dtype=torch.float32, accumulat
         raise ValueError("a must be [M, K], g [M, N] and offsets [E + 1]")
     M, K = a.shape
     N, E = g.shape[1], offsets.shape[0] - 1
-    _fit(M=M, K=K, N=N, E=E)
+    if max(M, K, N, E) > _INT_MAX:
+        _fit(M=M, K=K, N=N, E=E)
     pa, pg = _arg(a, torch.bfloat16, (M, K), "a"), _arg(g, torch.bfloat16, (M, N), "g")
     po = _arg(offsets, torch.int32, (E + 1,), "offsets")
     if accumulate and out is None:
         raise ValueError("accumulate adds to out: give out")
-    out, f32, workspace, nbytes = _mm_args(2, M, K, N, E, out, out_dtype, (E, K, N), workspace, a.device, stream)
-    _call("moe_grouped_mm_wgrad", pa, pg, po, M, K, N, E, out.data_ptr(), f32, int(accumulate), _ptr(workspace), nbytes,
-          _ptr(status), _stream(stream))
+    out, f32, pws, nbytes, _kept = _mm_args(2, M, K, N, E, out, out_dtype, (E, K, N), workspace, a.device, stream)
+    _call("moe_grouped_mm_wgrad", pa, pg, po, M, K, N, E, out.data_ptr(), f32, int(accumulate), pws, nbytes,
+          _word(status), _stream(stream))
     return out
 
 
@@ -1001,7 +1038,8 @@ def _gu_dims(gu, w):
     if gu.dim() != 2 or gu.shape[1] % 2:
         raise ValueError(f"gu must be [M, 2f], got {tuple(gu.shape)}")
     M, f2 = gu.shape
-    _fit(M=M, f=f2 // 2)
+    if max(M, f2) > _INT_MAX:
+        _fit(M=M, f=f2 // 2)
     return M, f2 // 2, _arg(gu, torch.bfloat16, (M, f2), "gu"), _opt(w, torch.float32, (M,), "w")
 
 
@@ -1029,7 +1067,8 @@ def _norm_inputs(x, w_pre, h, w_post, gate, token_gate, res_scale):
     if x.dim() != 2:
         raise ValueError(f"x must be [T, d], got {tuple(x.shape)}")
     T, d = x.shape
-    _fit(T=T, d=d)
+    if max(T, d) > _INT_MAX:
+        _fit(T=T, d=d)
     f, vec = torch.float32, (d,)
     return (T, d, int(dt is f), _arg(x, dt, (T, d), "x"), _opt(h, torch.bfloat16, (T, d), "h"),
             _opt(w_pre, f, vec, "w_pre"), _opt(w_post, f, vec, "w_post"), _opt(gate, f, vec, "gate"),
@@ -1083,7 +1122,7 @@ def block_norm_backward(x, dy=None, dn=None, w_pre=None, h=None, w_post=None, ga
             g[n] = _empty(t.shape, torch.float32, x.device, stream)
     _call("moe_block_norm_backward", px, f32, ph, pdy, pdn, *vectors, T, d, eps, g["x"].data_ptr(), _ptr(g["h"]),
           _ptr(g["w_pre"]), _ptr(g["w_post"]), _ptr(g["gate"]), _ptr(g["token_gate"]), _ptr(g["res_scale"]),
-          workspace.data_ptr(), workspace.nbytes, _stream(stream))
+          *_scratch(workspace), _stream(stream))
     return g
 
 
@@ -1124,6 +1163,9 @@ def _addresses(ts, name, dtype, sizes=None, count=None):
             not all(map(torch.Tensor.is_contiguous, ts)):
         for i, t in enumerate(ts):
             _dev(t, dtype, f"{name}[{i}]")
+    if _several:
+        for i, t in enumerate(ts):
+            _here(t, f"{name}[{i}]")
     got = list(map(torch.Tensor.numel, ts))
     if sizes is not None and got != sizes:
         i = next(i for i, (a, b) in enumerate(zip(got, sizes)) if a != b)
@@ -1175,9 +1217,13 @@ def adamw_step(params, grads, m, v, lr: float, beta1: float = 0.9, beta2: float 
         tab[field] = _addresses(ts, name, dtype, want, n)[0]
     if step_tensor is not None:
         _dev(step_tensor, torch.int32, "step_tensor")
+        if _several:
+            _here(step_tensor, "step_tensor")
         _shaped(step_tensor.view(-1), (1,), "step_tensor")
     if factors is not None:
         _dev(factors, torch.float32, "factors")
+        if _several:
+            _here(factors, "factors")
         _shaped(factors, (2,), "factors")
     _call("moe_adamw_step", tab.ctypes.data, n, int(pt is torch.bfloat16), int(gt is torch.bfloat16),
           8 if eight else 32, lr, beta1, beta2, eps, weight_decay, step, _ptr(step_tensor), _ptr(factors),

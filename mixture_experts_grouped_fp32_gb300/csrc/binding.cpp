@@ -100,6 +100,11 @@ int unlocked(F call) {
     return call();
 }
 
+// Tells autograd that a tensor of the caller's has been written to.
+void touch(const at::Tensor& t) {
+    if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+
 // swiglu(gu, w)
 PyObject* swiglu(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return guarded([&]() -> PyObject* {
@@ -262,6 +267,7 @@ PyObject* grouped_mm_wgrad(PyObject*, PyObject* const* a, Py_ssize_t n) {
         });
         if (rc) return code(rc);
         if (a[3] == Py_None) return wrap(out);
+        touch(out);
         Py_INCREF(a[3]);
         return a[3];
     });
@@ -300,6 +306,7 @@ PyObject* adamw_step(PyObject*, PyObject* const* a, Py_ssize_t n) {
                 const int64_t want = l == 4 || l == 5 ? (e.n + 255) / 256 : e.n;
                 void* p = c.plain(*t, types[l]);
                 if (!c.ok || t->numel() != want) Py_RETURN_NONE;
+                if (l == 0 || l == 6) touch(*t);
                 switch (l) {
                     case 0: e.param = p; break;
                     case 1: e.grad = p; break;
@@ -319,10 +326,26 @@ PyObject* adamw_step(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const long step = PyLong_AsLong(a[12]);
         if (step == -1 && PyErr_Occurred()) return nullptr;
         if (step < 1 || step > 0x7fffffff) Py_RETURN_NONE;
-        return code(unlocked([&] {
+        const int rc = unlocked([&] {
             return lib.moe_adamw_step(table.data(), static_cast<int>(count), pt == BF16, gt == BF16, eight ? 8 : 32, h[0],
                                       h[1], h[2], h[3], h[4], static_cast<int>(step), nullptr, nullptr, stream());
-        }));
+        });
+        return code(rc);
+    });
+}
+
+// wrote(tensors, lists of tensors or None ...)
+PyObject* wrote(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded([&]() -> PyObject* {
+        for (Py_ssize_t k = 0; k < n; ++k) {
+            const bool many = PyList_Check(a[k]) || PyTuple_Check(a[k]);
+            const Py_ssize_t count = many ? PySequence_Fast_GET_SIZE(a[k]) : 1;
+            for (Py_ssize_t i = 0; i < count; ++i) {
+                const at::Tensor* t = tensor(many ? PySequence_Fast_GET_ITEM(a[k], i) : a[k]);
+                if (t) touch(*t);
+            }
+        }
+        Py_RETURN_NONE;
     });
 }
 
@@ -352,6 +375,7 @@ PyObject* init(PyObject*, PyObject* const* a, Py_ssize_t n) {
 #define FAST(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(name)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {FAST(init),          FAST(swiglu),     FAST(swiglu_backward),  FAST(block_norm),
                          FAST(block_norm_backward), FAST(grouped_mm), FAST(grouped_mm_wgrad), FAST(adamw_step),
+                         FAST(wrote),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_moe_fast", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

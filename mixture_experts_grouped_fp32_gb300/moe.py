@@ -870,7 +870,11 @@ def forward_grouped_fp8(x, logits, bias, w8_gate_up, s_gate_up, w8_down, s_down,
 
 
 # ---------------------------------------------------------------------------------------------
-# Training: grouped products and their gradients.
+# Training: grouped products and their gradients, SwiGLU, the norms around a block, AdamW.
+#
+# None of these calls takes part in torch's autograd: an operand that requires a gradient gets none through them, and
+# each gradient is a call of its own (``train.py`` runs them in order).  What a call writes in place counts as
+# modified, so that a graph that has saved it refuses its backward pass.
 # ---------------------------------------------------------------------------------------------
 def _empty(shape, dtype, device, stream):
     """torch.empty on the stream that the call runs on, so that the allocator orders its reuse there."""
@@ -940,6 +944,17 @@ def _opt(t, dtype, shape, name):
     return None if t is None else _arg(t, dtype, shape, name)
 
 
+def _wrote(*given) -> None:
+    """Tells autograd that a call has written to tensors of its caller (or to lists of them): a graph that has saved
+    one of them then refuses its backward pass instead of computing with the new values."""
+    if _fast is not None:
+        _fast.wrote(*given)
+        return
+    for t in given:
+        if t is not None:
+            torch.autograd.graph.increment_version(t)
+
+
 def _out(out, shape, dtype, device, stream, name="out"):
     if out is None:
         return _empty(shape, dtype, device, stream)
@@ -974,7 +989,8 @@ def grouped_mm(a, b, offsets, transpose_b: bool = False, out=None, out_dtype=tor
                status=None, stream=None):
     """Products grouped by expert: out[r] = a[r] @ b[e] for the rows r of segment e of ``offsets`` [E+1]
     int32, with b [E, K, N]; or a[r] @ b[e].T with ``transpose_b`` and b [E, N, K].  a [M, K] and b are
-    bf16; out [M, N] is bf16 or fp32.  Rows outside the segments are left as they are."""
+    bf16; out [M, N] is bf16 or fp32.  Rows outside the segments are left as they are.  Not recorded by
+    autograd: the gradients are ``transpose_b`` and ``grouped_mm_wgrad``."""
     if _fast is not None and out is None and workspace is None and stream is None and out_dtype in _MM_OUT:
         r = _fast.grouped_mm(a, b, offsets, transpose_b, out_dtype is torch.float32, status)
         if r is not None:
@@ -988,10 +1004,12 @@ def grouped_mm(a, b, offsets, transpose_b: bool = False, out=None, out_dtype=tor
     pa = _arg(a, torch.bfloat16, (M, K), "a")
     pb = _arg(b, torch.bfloat16, (E, N, K) if transpose_b else (E, K, N), "b")
     po = _arg(offsets, torch.int32, (E + 1,), "offsets")
+    given = out
     out, f32, pws, nbytes, _kept = _mm_args(1 if transpose_b else 0, M, K, N, E, out, out_dtype, (M, N), workspace,
                                                a.device, stream)
     _call("moe_grouped_mm", pa, pb, po, M, K, N, E, int(transpose_b), out.data_ptr(), f32, pws, nbytes,
           _word(status), _stream(stream))
+    _wrote(given)
     return out
 
 
@@ -1015,22 +1033,26 @@ def grouped_mm_wgrad(a, g, offsets, out=None, out_dtype=torch.float32, accumulat
     po = _arg(offsets, torch.int32, (E + 1,), "offsets")
     if accumulate and out is None:
         raise ValueError("accumulate adds to out: give out")
+    given = out
     out, f32, pws, nbytes, _kept = _mm_args(2, M, K, N, E, out, out_dtype, (E, K, N), workspace, a.device, stream)
     _call("moe_grouped_mm_wgrad", pa, pg, po, M, K, N, E, out.data_ptr(), f32, int(accumulate), pws, nbytes,
           _word(status), _stream(stream))
+    _wrote(given)
     return out
 
 
 def swiglu(gu, w=None, h=None, stream=None):
     """h = w * silu(g) * u, bf16 [M, f], from gu = [g | u] bf16 [M, 2f] and a weight per row (fp32 [M],
-    or None for 1)."""
+    or None for 1).  Not recorded by autograd: the gradient is ``swiglu_backward``."""
     if _fast is not None and h is None and stream is None:
         r = _fast.swiglu(gu, w)
         if r is not None:
             return _done("moe_swiglu", r)
     M, f, pg, pw = _gu_dims(gu, w)
+    given = h
     h = _out(h, (M, f), torch.bfloat16, gu.device, stream, "h")
     _call("moe_swiglu", pg, pw, M, f, h.data_ptr(), _stream(stream))
+    _wrote(given)
     return h
 
 
@@ -1052,10 +1074,12 @@ def swiglu_backward(gu, dh, w=None, want_h: bool = False, dgu=None, dw=None, h=N
             return _done("moe_swiglu_backward", r)
     M, f, pg, pw = _gu_dims(gu, w)
     pd = _arg(dh, torch.bfloat16, (M, f), "dh")
+    given = (dgu, dw if w is not None else None, h)
     dgu = _out(dgu, (M, 2 * f), torch.bfloat16, gu.device, stream, "dgu")
     dw = _out(dw, (M,), torch.float32, gu.device, stream, "dw") if w is not None else None
     h = _out(h, (M, f), torch.bfloat16, gu.device, stream, "h") if want_h or h is not None else None
     _call("moe_swiglu_backward", pg, pd, pw, M, f, dgu.data_ptr(), _ptr(dw), _ptr(h), _stream(stream))
+    _wrote(*given)
     return dgu, dw, h
 
 
@@ -1084,15 +1108,18 @@ def block_norm(x, w_pre=None, h=None, w_post=None, gate=None, token_gate=None, r
 
     x [T, d] bf16 or fp32 (the residual stream), h [T, d] bf16 (the block's output); w_pre, w_post, gate,
     res_scale fp32 [d], token_gate fp32 [T].  Returns (y, n): y has x's type, n is bf16.  Without ``h``
-    (before the first block) y is x and is returned as None; without ``w_pre`` n is None."""
+    (before the first block) y is x and is returned as None; without ``w_pre`` n is None.  Not recorded by
+    autograd: the gradient is ``block_norm_backward``."""
     if _fast is not None and y is None and n is None and stream is None:
         r = _fast.block_norm(x, w_pre, h, w_post, gate, token_gate, res_scale, eps)
         if r is not None:
             return _done("moe_block_norm", r)
     T, d, f32, px, ph, *vectors = _norm_inputs(x, w_pre, h, w_post, gate, token_gate, res_scale)
+    given = (y if h is not None else None, n if w_pre is not None else None)
     y = _out(y, (T, d), x.dtype, x.device, stream, "y") if h is not None else None
     n = _out(n, (T, d), torch.bfloat16, x.device, stream, "n") if w_pre is not None else None
     _call("moe_block_norm", px, f32, ph, *vectors, T, d, eps, _ptr(y), _ptr(n), _stream(stream))
+    _wrote(*given)
     return y, n
 
 
@@ -1184,7 +1211,8 @@ def adamw_step(params, grads, m, v, lr: float, beta1: float = 0.9, beta2: float 
     params and grads are bf16 or fp32 (each list of one type); m and v fp32, or float8_e4m3fn codes with
     ``m_scales`` and ``v_scales`` (see ``adamw_state``).  ``copies``: bf16 tensors that receive the new
     parameters too.  t is ``step``, or the int32 in ``step_tensor`` on the device; ``factors`` (fp32 [2] on
-    the device) multiplies the gradients by its first value and lr by its second."""
+    the device) multiplies the gradients by its first value and lr by its second.  Gradients are the ones
+    given (autograd's ``.grad`` is not looked at); parameters and copies count as modified in place."""
     if len(params) == 0:
         return
     if _fast is not None and step_tensor is None and factors is None and stream is None:
@@ -1228,3 +1256,4 @@ def adamw_step(params, grads, m, v, lr: float, beta1: float = 0.9, beta2: float 
     _call("moe_adamw_step", tab.ctypes.data, n, int(pt is torch.bfloat16), int(gt is torch.bfloat16),
           8 if eight else 32, lr, beta1, beta2, eps, weight_decay, step, _ptr(step_tensor), _ptr(factors),
           _stream(stream))
+    _wrote(params, copies)

@@ -89,3 +89,61 @@ def test_other_threads_run_during_a_call(tmp_path):
     finally:
         fast.init(m.LIB_PATH)
     assert isinstance(result[0], torch.Tensor), "the call held the lock until it gave up"
+
+
+def versions(ts):
+    return [t._version for t in ts]
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("device_step", [False, True])
+def test_adamw_raises_the_versions_of_parameters_and_copies(moe, bits, device_step):
+    p = [torch.ones(300, device="cuda"), torch.ones(7, device="cuda")]
+    g, copies = [torch.ones_like(t) for t in p], [t.bfloat16() for t in p]
+    state = list(zip(*(moe.adamw_state(t, bits) for t in p)))
+    written = [*p, *copies]  # (the moments are the optimizer's own: no graph has them)
+    before, grads = versions(written), versions(g)
+    kw = {"step_tensor": torch.ones(1, dtype=torch.int32, device="cuda")} if device_step else {}
+    if bits == 8:
+        kw.update(m_scales=list(state[2]), v_scales=list(state[3]))
+    moe.adamw_step(p, g, list(state[0]), list(state[1]), lr=1e-3, copies=copies, **kw)
+    assert all(a > b for a, b in zip(versions(written), before)) and versions(g) == grads
+
+
+def test_a_graph_that_saved_a_parameter_notices_its_step(moe):
+    p = torch.ones(16, device="cuda", requires_grad=True)
+    loss = (p * p).sum()  # saves p
+    s = moe.adamw_state(p.detach())
+    moe.adamw_step([p], [torch.ones(16, device="cuda")], [s[0]], [s[1]], lr=1e-3)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()
+
+
+def test_outputs_that_are_given_count_as_written(moe):
+    offs = torch.tensor([0, 4], dtype=torch.int32, device="cuda")
+    a, b, gu, x, w = z(4, 8), z(1, 8, 16), z(4, 16), z(4, 8), z(8, dtype=F32)
+    rows = z(4, dtype=F32)
+    calls = {
+        "grouped_mm": lambda o: moe.grouped_mm(a, b, offs, out=o[0]),
+        "grouped_mm_wgrad": lambda o: moe.grouped_mm_wgrad(a, z(4, 16), offs, out=o[0], accumulate=True),
+        "swiglu": lambda o: moe.swiglu(gu, h=o[0]),
+        "swiglu_backward": lambda o: moe.swiglu_backward(gu, a, rows, dgu=o[0], dw=o[1], h=o[2]),
+        "block_norm": lambda o: moe.block_norm(x, w, a, w, y=o[0], n=o[1]),
+    }
+    outs = {"grouped_mm": [z(4, 16)], "grouped_mm_wgrad": [z(1, 8, 16, dtype=F32)], "swiglu": [z(4, 8)],
+            "swiglu_backward": [z(4, 16), z(4, dtype=F32), z(4, 8)], "block_norm": [z(4, 8), z(4, 8)]}
+    for name, call in calls.items():
+        before = versions(outs[name])
+        call(outs[name])
+        assert all(n > o for n, o in zip(versions(outs[name]), before)), name
+    assert versions([a, b, gu, x, w, rows]) == [0] * 6
+
+
+def test_inference_tensors_have_no_versions_to_raise(moe):
+    with torch.inference_mode():
+        p, g, m, v = (torch.ones(16, device="cuda") for _ in range(4))
+        moe.adamw_step([p], [g], [m], [v], lr=1e-3)
+        out = torch.ones(1, 8, 16, device="cuda")
+        moe.grouped_mm_wgrad(z(4, 8), z(4, 16), torch.tensor([0, 4], dtype=torch.int32, device="cuda"), out=out)
+    moe.adamw_step([p], [g], [m], [v], lr=1e-3)
+    assert (p < 1).all() and (out == 0).all()

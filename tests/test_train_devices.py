@@ -40,6 +40,7 @@ def calls(monkeypatch):
     monkeypatch.setattr(moe, "_fast", None)
     monkeypatch.setattr(moe, "_call", lambda name, *a: made.append(name))
     monkeypatch.setattr(moe, "_stream", lambda s: None)
+    monkeypatch.setattr(moe, "_wrote", lambda *ts: None, raising=False)
     monkeypatch.setattr(moe, "grouped_mm_workspace_size", lambda *a: 0)
     monkeypatch.setattr(moe, "_several", True, raising=False)
     monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)

@@ -381,4 +381,9 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_moe_fast", nullptr, -1, methods, 
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__moe_fast() { return PyModule_Create(&module); }
+// torch_version: of the torch whose headers this was compiled against (MOE_TORCH_VERSION, from the build).
+PyMODINIT_FUNC PyInit__moe_fast() {
+    PyObject* m = PyModule_Create(&module);
+    if (m && PyModule_AddStringConstant(m, "torch_version", MOE_TORCH_VERSION) < 0) Py_CLEAR(m);
+    return m;
+}

@@ -133,10 +133,11 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
             if os.path.exists(os.path.join(_HERE, "_moe_fast.so")):
                 try:
                     from . import _moe_fast
-                    _moe_fast.init(path)
-                    _fast = _moe_fast
-                except (ImportError, OSError):  # built against another torch: ctypes does the same
-                    _fast = None
+                    if getattr(_moe_fast, "torch_version", None) == torch.__version__:
+                        _moe_fast.init(path)
+                        _fast = _moe_fast
+                except (ImportError, OSError):
+                    pass  # (and of another torch, whose tensors it would misread): ctypes does the same
             _several = torch.cuda.device_count() > 1
             _lib = lib
     return _lib

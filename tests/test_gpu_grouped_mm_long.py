@@ -131,4 +131,62 @@ def test_gradient_of_as_many_rows_as_the_calls_accept(moe):
     out = moe.grouped_mm_wgrad(a, g, torch.tensor([0, MOST], dtype=torch.int32, device="cuda"), status=status)
     assert moe.get_device_error(status) == 0
     ref, mag = wgrad64(a, g, 0, MOST)
-    assert ((out[0].to(D) - ref).abs() <= (32 * 2.0 ** -23 + (MOST // 512 + 1) * 2.0 ** -24) * mag).all()
+    slices = 16  # of the reduction: their workspace is that many gradients and more
+    assert moe.grouped_mm_workspace_size(2, MOST, 8, 8, 1) > slices * 8 * 8 * 4
+    assert ((out[0].to(D) - ref).abs() <= (32 * 2.0 ** -23 + (MOST // 512 // slices + 1 + slices) * 2.0 ** -24) * mag).all()
+
+
+# fp32 outputs: chunks of 512 of the reduction.  Elementwise as above.  By the 2-norm, for terms of random sign: a
+# chunk's partial sums grow as the root of the 32 additions' number, each loses 2^-23 at most, and the chunks' losses are
+# independent: (2/3) 32^1.5 sqrt(16 / 512) 2^-23 = 21.4 * 2^-23 of the sum's norm, and 2^-24 for each chunk's addition.  Unbroken,
+# n additions would lose (2/3) n of 2^-23: 341 for 8192 terms, about a third of that on average.
+def check_fp32(got, ref, mag, n, what):
+    chunks = -(-n // 512)
+    off = (got.to(D) - ref).abs()
+    assert (off <= (min(n, 512) / 16 * 2.0 ** -23 + chunks * 2.0 ** -24) * mag + 1e-30).all(), what
+    rel = float(torch.linalg.norm(off) / torch.linalg.norm(ref))
+    assert rel <= 21.4 * 2.0 ** -23 + chunks * 2.0 ** -24, f"{what}: off by {rel:.2e} in the 2-norm"
+
+
+def unsplit(moe, way, a, b, offs, shape):
+    """The C call without a workspace: the reduction is not split into slices."""
+    out = torch.full(shape, 9.0, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    E, s = offs.numel() - 1, torch.cuda.current_stream().cuda_stream
+    L = moe.load()
+    if way == "wgrad":
+        rc = L.moe_grouped_mm_wgrad(a.data_ptr(), b.data_ptr(), offs.data_ptr(), a.shape[0], a.shape[1], b.shape[1], E,
+                                    out.data_ptr(), 1, 0, None, 0, status.data_ptr(), s)
+    else:
+        rc = L.moe_grouped_mm(a.data_ptr(), b.data_ptr(), offs.data_ptr(), a.shape[0], a.shape[1], shape[1], E,
+                              int(way == "dgrad"), out.data_ptr(), 1, None, 0, status.data_ptr(), s)
+    assert rc == 0 and moe.get_device_error(status) == 0
+    return out
+
+
+@pytest.mark.parametrize("way", ["fwd", "dgrad"])
+@pytest.mark.parametrize("K", [512, 520, 1024, 1032, 1544, 2888, 8192])  # 1, 2, 2, 3, 4, 6 and 16 chunks
+@pytest.mark.parametrize("counts,N", [([3], 264), ([700, 0, 1, 260, 33, 2000], 1544)])  # 2 items, and 2 for each SM pair
+def test_fp32_products_in_chunks(moe, way, K, counts, N):
+    gen = torch.Generator("cuda").manual_seed(K)
+    r = lambda *s: torch.randn(*s, generator=gen, device="cuda").to(BF16)
+    offs = np.concatenate([[0], np.cumsum(counts)])
+    a, b = r(sum(counts), K), r(len(counts), K, N) if way == "fwd" else r(len(counts), N, K)
+    out = unsplit(moe, way, a, b, torch.tensor(offs, dtype=torch.int32, device="cuda"), (sum(counts), N))
+    for e, n in enumerate(counts):
+        if n:
+            x, w = a[offs[e]:offs[e + 1]].to(D), (b[e] if way == "fwd" else b[e].T).to(D)
+            check_fp32(out[offs[e]:offs[e + 1]], x @ w, x.abs() @ w.abs(), K, f"{way} of {n} rows over {K}")
+
+
+@pytest.mark.parametrize("counts,K,N", [([8192, 0, 520, 1033], 264, 328), ([100, 513, 3000] * 12, 264, 520)])
+def test_fp32_gradients_in_chunks(moe, counts, K, N):
+    gen = torch.Generator("cuda").manual_seed(K)
+    offs = np.concatenate([[0], np.cumsum(counts)])
+    a, g = (torch.randn(sum(counts), w, generator=gen, device="cuda").to(BF16) for w in (K, N))
+    out = unsplit(moe, "wgrad", a, g, torch.tensor(offs, dtype=torch.int32, device="cuda"), (len(counts), K, N))
+    for e, n in enumerate(counts):
+        if n:
+            check_fp32(out[e], *wgrad64(a, g, int(offs[e]), int(offs[e + 1])), n, f"gradient of {n} rows")
+        else:
+            assert (out[e] == 0).all()

@@ -12,6 +12,8 @@ int fail(int code, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
 int ok();
 // The current device must be compute capability 10.3; fills its SM count.
 int check_device(int* num_sms);
+// Failure-detection test hook: 1 with MOE_INJECT_STALL=1 in the environment.
+int inject_stall();
 // A launch's error as a return code.
 int launched(cudaError_t e, const char* what);
 

@@ -212,6 +212,7 @@ struct GroupedMmArgs {
     bool accumulate;  // mode 2, fp32: out += instead of out =
     int ksplit;       // slices of the reduction; > 1 needs `partial`
     float* partial;   // [ksplit, out elements] fp32
+    int inject_stall;  // test hook: make one pipeline wait run out
     int32_t* done;    // with a split: [kGroupedMmDone], a word for each CTA whose slices are there
     int32_t* status;
 };

@@ -206,7 +206,7 @@ struct Maps {
 template <int MODE, typename OUT, bool CHUNKED>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(num_threads<MODE, CHUNKED>(), 1)
 grouped_mm_kernel(const __grid_constant__ Maps maps, const int32_t* __restrict__ offsets, int M, int K, int N, int E,
-                  int ksplit, int accumulate, OUT* __restrict__ out, int32_t* __restrict__ done,
+                  int ksplit, int accumulate, int inject_stall, OUT* __restrict__ out, int32_t* __restrict__ done,
                   int32_t* __restrict__ status) {
     constexpr bool WGRAD = MODE == kMmWgrad;
     extern __shared__ uint8_t smem_raw[];
@@ -307,6 +307,7 @@ grouped_mm_kernel(const __grid_constant__ Maps maps, const int32_t* __restrict__
         const uint64_t pol_f = ptx::policy_evict_normal();
         int stage = 0;
         uint32_t phase = 0;
+        uint32_t extra = inject_stall && blockIdx.x == 0 ? 16u : 0u;  // (test hook: the first stage waits in vain)
         bool aborted = false;
         for (int i = pair_id; i < total && !aborted; i += num_pairs) {
             const Item it = cur.at(i);
@@ -331,7 +332,7 @@ grouped_mm_kernel(const __grid_constant__ Maps maps, const int32_t* __restrict__
                     const int row = seg0 + kb * BK;
                     if ((kb + 1) * BK > it.red_rows && (it.red_rows & 15)) {
                         // The segment's last block, with rows to be zeroed: its copies complete here.
-                        ptx::mbar_arrive_expect_tx(&c.tail[stage], cta_bytes);
+                        ptx::mbar_arrive_expect_tx(&c.tail[stage], cta_bytes + extra);
                         if (maps.f_blocks) {
                             ptx::tma_load_4d(sf, &maps.f, &c.tail[stage], 0, row, f >> 6, 0, pol_f);
                         } else {
@@ -347,7 +348,7 @@ grouped_mm_kernel(const __grid_constant__ Maps maps, const int32_t* __restrict__
                     } else {
                         if (leader) {  // both arrivals: a remote one for each block costs more (14 %)
                             ptx::mbar_arrive(&c.full[stage]);
-                            ptx::mbar_arrive_expect_tx(&c.full[stage], 2u * cta_bytes);
+                            ptx::mbar_arrive_expect_tx(&c.full[stage], 2u * cta_bytes + extra);
                         }
                         if (maps.f_blocks) {
                             ptx::tma_load_4d_pair(sf, &maps.f, full_leader, 0, row, f >> 6, 0, pol_f);
@@ -363,7 +364,7 @@ grouped_mm_kernel(const __grid_constant__ Maps maps, const int32_t* __restrict__
                         }
                     }
                 } else {
-                    if (leader) ptx::mbar_arrive_expect_tx(&c.full[stage], 2u * cta_bytes);
+                    if (leader) ptx::mbar_arrive_expect_tx(&c.full[stage], 2u * cta_bytes + extra);
                     ptx::tma_load_2d_pair(sr, mr, full_leader, kb * BK, seg0 + r, pol_r);
                     if (MODE == kMmTransB) {
                         ptx::tma_load_3d_pair(sf, &maps.f, full_leader, kb * BK, f, it.e, pol_f);
@@ -374,6 +375,7 @@ grouped_mm_kernel(const __grid_constant__ Maps maps, const int32_t* __restrict__
                         ptx::tma_load_3d_pair(sf + BOX_BYTES, &maps.f, full_leader, f + 64, kb * BK, it.e, pol_f);
                     }
                 }
+                extra = 0;
                 fill_parity[stage] = phase;
                 filled_mask |= 1 << stage;
                 if (++stage == STAGES) {
@@ -760,7 +762,7 @@ cudaError_t launch_as(const GroupedMmArgs& a, OUT* out, int ksplit, int accumula
         return cudaErrorInvalidValue;
     }
     return launch_k(kPdlTrain, grouped_mm_kernel<MODE, OUT, CHUNKED>, dim3(ctas_of(num_sms)), dim3(num_threads<MODE, CHUNKED>()),
-                    SMEM_BYTES, s, m, a.offsets, a.M, a.K, a.N, a.E, ksplit, accumulate, out, ksplit > 1 ? a.done : nullptr,
+                    SMEM_BYTES, s, m, a.offsets, a.M, a.K, a.N, a.E, ksplit, accumulate, a.inject_stall, out, ksplit > 1 ? a.done : nullptr,
                     a.status);
 }
 

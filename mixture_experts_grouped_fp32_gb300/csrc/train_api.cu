@@ -52,7 +52,7 @@ int grouped_entry(const char* name, int mode, const void* a, const void* b, cons
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (M == 0)  // the weight gradient of no rows
         return launched(cudaMemsetAsync(out, 0, static_cast<size_t>(E) * K * N * (out_fp32 ? 4 : 2), s), name);
-    GroupedMmArgs g{a, b, offsets, M, K, N, E, out, out_fp32 != 0, accumulate != 0, 1, nullptr, nullptr, status};
+    GroupedMmArgs g{a, b, offsets, M, K, N, E, out, out_fp32 != 0, accumulate != 0, 1, nullptr, inject_stall(), nullptr, status};
     if (workspace && need) {
         g.ksplit = grouped_mm_ksplit(mode, M, K, N, E, kPlanSms);
         g.partial = static_cast<float*>(workspace);

@@ -30,6 +30,7 @@
 // registers, writes them once per block, and a second kernel adds the blocks in a fixed order: no
 // atomics, the same result on every run.
 #include <algorithm>
+#include <atomic>
 
 #include "train_ptx.cuh"
 #include "train_util.cuh"
@@ -791,7 +792,7 @@ Shape shape_of(const BlockNormArgs& a, bool bwd) {
 }
 
 template <typename... KArgs>
-cudaError_t allow_smem(void (*kernel)(KArgs...), bool* done) {
+cudaError_t allow_smem(void (*kernel)(KArgs...), std::atomic<bool>* done) {
     int dev = 0;
     cudaGetDevice(&dev);
     if (dev < 64 && done[dev]) return cudaSuccess;
@@ -802,7 +803,7 @@ cudaError_t allow_smem(void (*kernel)(KArgs...), bool* done) {
 
 template <typename X, int VPT, bool H, bool N>
 cudaError_t forward_as(const BlockNormArgs& a, const Shape& s, int grid, cudaStream_t st) {
-    static bool done[64] = {};
+    static std::atomic<bool> done[64] = {};
     const cudaError_t e = allow_smem(norm_rows_kernel<X, VPT, H, N>, done);
     if (e != cudaSuccess) return e;
     return launch_k(kPdlTrain, norm_rows_kernel<X, VPT, H, N>, dim3(grid), dim3(s.threads), s.smem, st,
@@ -822,7 +823,7 @@ cudaError_t forward_wide(const BlockNormArgs& a, const Shape& s, int grid, cudaS
 }
 template <typename X, int VPT, bool H, bool N, bool SIDE>
 cudaError_t backward_with(const BlockNormArgs& a, const Shape& s, int grid, cudaStream_t st) {
-    static bool done[64] = {};
+    static std::atomic<bool> done[64] = {};
     const cudaError_t e = allow_smem(norm_rows_backward_kernel<X, VPT, H, N, SIDE>, done);
     if (e != cudaSuccess) return e;
     return launch_k(kPdlTrain, norm_rows_backward_kernel<X, VPT, H, N, SIDE>, dim3(grid), dim3(s.threads, s.groups),

@@ -47,6 +47,8 @@
 // Synchronisation across the pair is that of the layer's SM-pair kernel: full[s] lives in CTA 0 and
 // counts both CTAs' copies, empty[s] and tfull[a] are arrived on in both CTAs by CTA 0's multicast
 // commits, tempty[a] lives in CTA 0.  Every wait is bounded and reports MOE_STATUS_WAIT_TIMEOUT.
+#include <atomic>
+
 #include "common.cuh"
 #include "train_ptx.cuh"
 
@@ -727,7 +729,7 @@ int ctas_of(int num_sms) { return (num_sms < kMaxCtas ? num_sms : kMaxCtas) & ~1
 template <int MODE, typename OUT, bool CHUNKED>
 cudaError_t launch_as(const GroupedMmArgs& a, OUT* out, int ksplit, int accumulate, int num_sms, cudaStream_t s,
                         const char** why) {
-    static bool attr_set[64] = {};
+    static std::atomic<bool> attr_set[64] = {};  // (set by whichever thread comes first, or by several)
     int dev = 0;
     cudaGetDevice(&dev);
     if (dev < 64 && !attr_set[dev]) {

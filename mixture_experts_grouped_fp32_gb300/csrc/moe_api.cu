@@ -67,6 +67,10 @@ int check_device(int* num_sms) {
             (e = cudaDeviceGetAttribute(&di.minor, cudaDevAttrComputeCapabilityMinor, dev)) != cudaSuccess ||
             (e = cudaDeviceGetAttribute(&di.sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess)
             return fail(MOE_ERR_CUDA, "cudaDeviceGetAttribute: %s", cudaGetErrorString(e));
+        // The tensor-map encoder is looked up on first use, without a lock: here, behind this one, before any call of
+        // several threads' first ones needs it.
+        CUtensorMap map;
+        make_tensor_map_bf16(&map, nullptr, 64, 1, 1);
         di.init = true;
     }
     if (di.major != 10 || di.minor != 3)

@@ -483,14 +483,17 @@ MOE_API int moe_forward_grouped_fp8b(const void* x, const float* logits, const f
  * ------------------------------------------------------------------------------------------- */
 
 /* Grouped products.  Row segment e is rows offsets[e] .. offsets[e+1]-1 (moe_permute's offsets; a
- * segment may be empty).  bf16 operands, fp32 accumulation, one rounding when out is bf16.
+ * segment may be empty).  bf16 operands, fp32 accumulation, one rounding when out is bf16.  (Additions in
+ * tensor memory truncate, by 2^-23 of a partial sum at most, one for every 16 of the reduction; fp32 outputs, and bf16
+ * gradients of more than 262144 rows, add up chunks of 512 resp. 4096 of it rounded to nearest.)
  *   moe_grouped_mm        out[r] = a[r] . b[e]      b [E,K,N]           (transpose_b = 0)
  *                         out[r] = a[r] . b[e]^T    b [E,N,K]           (transpose_b = 1: the input
  *                         gradient, with a the gradient of the product's output and b its weights)
  *     a [M,K] bf16;  out [M,N] bf16, or fp32 with out_fp32 = 1; rows outside the segments untouched.
  *   moe_grouped_mm_wgrad  out[e] = sum over the rows r of segment e of a[r]^T . g[r], the weight
  *                         gradient; an empty segment's is zero.  accumulate = 1 (fp32 only) adds to
- *                         out instead.
+ *                         out instead (one addition per element, in which values under 2^-126 may count as
+ *                         zero; an empty segment's is left as it is).
  *     a [M,K], g [M,N] bf16;  out [E,K,N] bf16 or fp32.
  * K and N multiples of 8 in [8, 65536], 1 <= E <= 256; a, b, g, out and workspace 16-byte aligned.
  * workspace: moe_grouped_mm_workspace_size(mode, ...) bytes with mode 0 (transpose_b = 0), 1

@@ -16,13 +16,14 @@
 // step's m by eps alone.  A block whose maximum is below 2^-100 is zero with scale 1; one with a NaN or
 // an infinity becomes NaN.  The step itself uses the new moments before their rounding to codes.
 //
-// Bound by memory: 22 to 30 bytes per element (32-bit moments, fp32 parameter) or 10 to 16 (8-bit).
-// Measured: 75 M elements with 32-bit moments 378 us (6.9 TB/s), 310 M with 8-bit moments 795 us (6.3 TB/s,
-// 64 % of the issue slots).  A
+// Bound by memory, in bytes per element: with 32-bit moments 22 or 24 for bf16 parameters and 26 to 30 for fp32
+// ones (gradient in bf16 or fp32, with a bf16 copy 2 more), with 8-bit moments 12 less and 1/16 for the scales.
+// Measured: 93.5 M elements with 32-bit moments (fp32, bf16 gradients and copies: 28 bytes) 378 us (6.9 TB/s), 310 M
+// with 8-bit moments (all fp32: 16 bytes) 795 us (6.2 TB/s, 64 % of the issue slots).  A
 // warp handles one block of 256 elements, eight per lane in 16-byte words where the tensor's pieces are
 // aligned for it, else element by element; chunks of 2048 elements over all tensors are dealt to the thread
 // blocks in turn (neighbouring chunks run at the same time: contiguous runs of chunks measured 7 % slower,
-// 420 against 390 us for 75 M elements with 32-bit moments); a thread block walks on in the table from its
+// 420 against 390 us for 93.5 M elements with 32-bit moments); a thread block walks on in the table from its
 // last chunk's tensor.  The table of tensors travels in the kernel's parameters (up to 32 KB): nothing is copied
 // to the device before the launch and no memory is held.
 #include <cuda_fp8.h>

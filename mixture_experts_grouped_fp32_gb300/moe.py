@@ -1017,7 +1017,8 @@ def grouped_mm(a, b, offsets, transpose_b: bool = False, out=None, out_dtype=tor
 def grouped_mm_wgrad(a, g, offsets, out=None, out_dtype=torch.float32, accumulate: bool = False, workspace=None,
                      status=None, stream=None):
     """Weight gradient of a grouped product: out[e] = a[rows of e].T @ g[rows of e], [E, K, N] fp32 or
-    bf16, zero for an empty segment; with ``accumulate`` (fp32 ``out`` given) it is added to out."""
+    bf16, zero for an empty segment; with ``accumulate`` (fp32 ``out`` given) it is added to out (where values
+    under 2^-126 may count as zero).  Not recorded by autograd."""
     if _fast is not None and workspace is None and stream is None:
         dtype = out_dtype if out is None else out.dtype
         if dtype in _MM_OUT:

@@ -10,7 +10,9 @@ and experts(n) is: route the fp32 logits n @ w_router, sort the assignments by e
 grouped product with w_gate_up, SwiGLU weighted by the routing weights, grouped product with w_down, sum
 of a token's rows (``moe.combine`` with weights 1).  Every backward step is the same kernels' gradient.
 
-The operators take no part in torch's autograd: ``backward`` is written out, as the forward pass is.
+The operators take no part in torch's autograd: ``backward`` is written out, as the forward pass is.  The
+router's product, its gradients and the gradient of its softmax are torch operations in fp32 (with
+``torch.backends.cuda.matmul.allow_tf32`` the products run in TF32, and close choices of experts may differ).
 
 Parameters are fp32 with bf16 copies of the expert weights for the products; ``step`` updates both in
 one launch.  Nothing synchronises with the host and the step number lives on the device, so forward,

@@ -18,8 +18,8 @@
 //
 // Bound by memory, in bytes per element: with 32-bit moments 22 or 24 for bf16 parameters and 26 to 30 for fp32
 // ones (gradient in bf16 or fp32, with a bf16 copy 2 more), with 8-bit moments 12 less and 1/16 for the scales.
-// Measured: 93.5 M elements with 32-bit moments (fp32, bf16 gradients and copies: 28 bytes) 378 us (6.9 TB/s), 310 M
-// with 8-bit moments (all fp32: 16 bytes) 795 us (6.2 TB/s, 64 % of the issue slots).  A
+// Measured: 93.5 M elements with 32-bit moments (fp32, bf16 gradients and copies: 28 bytes) 379 us (6.9 TB/s), 310 M
+// with 8-bit moments (all fp32: 16 bytes) 802 us (6.2 TB/s, 64 % of the issue slots).  A
 // warp handles one block of 256 elements, eight per lane in 16-byte words where the tensor's pieces are
 // aligned for it, else element by element; chunks of 2048 elements over all tensors are dealt to the thread
 // blocks in turn (neighbouring chunks run at the same time: contiguous runs of chunks measured 7 % slower,

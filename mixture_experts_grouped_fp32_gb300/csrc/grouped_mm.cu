@@ -39,10 +39,10 @@
 // group run together and share the feature operand through L2, and groups of 8 keep the rows
 // re-read per feature tile few when a segment is long.
 //
-// Measured: 8192 rows, 4096 -> 28672 over 8 experts 1.19 to 1.28 ms (1.5 to 1.6 PFLOP/s; tensor pipe 82 %
+// Measured: 8192 rows, 4096 -> 28672 over 8 experts 1.19 to 1.29 ms (1.5 to 1.6 PFLOP/s; tensor pipe 82 %
 // active at the power limit); two rows of 14336 -> 4096 45 us (5.2 TB/s); gradients of 256 experts,
-// 2048 x 7168 from 16384 rows, 1.41 to 1.46 ms (5.5 TB/s of mostly writes); 32 experts' fp32 gradients of
-// that size added to what was there 0.69 ms (5.9 TB/s).
+// 2048 x 7168 from 16384 rows, 1.41 to 1.48 ms (5.5 TB/s of mostly writes); 32 experts' gradients of that size from as
+// many rows 0.43 ms in bf16, 0.59 in fp32 (3.7 TB/s), 0.68 added to what was there (6.0 TB/s).
 //
 // Synchronisation across the pair is that of the layer's SM-pair kernel: full[s] lives in CTA 0 and
 // counts both CTAs' copies, empty[s] and tfull[a] are arrived on in both CTAs by CTA 0's multicast

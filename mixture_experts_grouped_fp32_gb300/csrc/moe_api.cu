@@ -214,16 +214,18 @@ bool fuse_route_permute(int T, int E) {
     return route_permute_fusable(T, E);
 }
 
+}  // namespace
+
 // Failure-detection test hook, off unless the environment sets MOE_INJECT_STALL=1: the next
 // grouped-GEMM launches (the stage calls' and the bf16 layer's, on the 1-SM kernel) and grouped products run with one
 // pipeline stage armed for bytes that never arrive, so a bounded wait expires (~1 s), the kernel
 // reports MOE_STATUS_WAIT_TIMEOUT in the status word, releases its tensor memory and returns.
 // Nothing faults, traps or hangs.
-}  // namespace
 int inject_stall() {
     const char* v = std::getenv("MOE_INJECT_STALL");
     return (v && v[0] == '1') ? 1 : 0;
 }
+
 namespace {
 
 // K slices for the down projection of a layer shape.  The down GEMM has d/256 N-tiles per M-tile.

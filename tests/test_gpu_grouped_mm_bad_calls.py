@@ -53,7 +53,7 @@ def test_bad_offsets_leave_the_output(moe, way, split, dtype, bad):
 
 @pytest.mark.parametrize("way", list(MODES))
 def test_a_good_call_after_a_bad_one_in_the_same_workspace(moe, way):
-    """The verdict is the call's own: not one that an earlier call left in the workspace."""
+    """The slices are joined by the call's own words, not by ones that an earlier call left in the workspace."""
     M, K, N, E = SPLIT[way]
     a, b = operands(way, M, K, N, E)
     good, bad = [0, M // 2, M // 2, M], [0, M // 2 + 1, M // 2 - 1, M]

@@ -62,6 +62,7 @@ extern "C" {
 #define MOE_STATUS_BAD_DEST 0x4      /* combine: a dest row outside [0, T*top_k) */
 #define MOE_STATUS_WAIT_TIMEOUT 0x8  /* grouped GEMM: a pipeline wait gave up after ~1 s */
 #define MOE_STATUS_BAD_SRC 0x10      /* gathering gate+up GEMM or FP8 row quantiser: a src index out of range (row zeroed) */
+#define MOE_STATUS_BAD_TOKEN 0x20    /* embedding: an id outside [0,V) (row zeroed, resp. left out) */
 
 typedef void* moe_stream_t; /* a cudaStream_t */
 
@@ -580,6 +581,91 @@ typedef struct {
 MOE_API int moe_adamw_step(const moe_adamw_tensor* tensors, int count, int param_bf16, int grad_bf16, int state_bits,
                            double lr, double beta1, double beta2, double eps, double weight_decay, int step,
                            const int32_t* step_dev, const float* factors, moe_stream_t stream);
+
+/* ---------------------------------------------------------------------------------------------
+ * Around the blocks of a stack that reads tokens: routing by scores, layer norm, dropout, embedding.
+ * Rows of any width from 1 on and tensors aligned to their elements; widths that are multiples of 8 in
+ * 16-byte aligned tensors run faster.  T is any number of rows, 0 included.
+ * ------------------------------------------------------------------------------------------- */
+
+/* Routing by scores.  Per token, over E experts in n_group equal groups (experts g*E/n_group ..):
+ *   s[e] = exp(l[e]) / sum exp(l)  (scoring 0)   or   1 / (1 + exp(-l[e]))  (scoring 1)
+ *   c[e] = s[e] + bias[e]          (bias NULL: 0; it steers the choice only)
+ *   kept groups: the topk_group with the largest sum of their q = max(1, top_k / topk_group) largest c
+ *                (at most E / n_group of them; equal sums: lower group first)
+ *   idx[t,.] = the top_k largest c among the kept groups' experts, falling (equal: lower id first)
+ *   w[t,j]   = scale * s[idx[t,j]] / (renormalize ? sum_j' s[idx[t,j']] : 1)
+ * The choice is the one of these formulas in 64-bit arithmetic: scores that fp32 cannot tell apart are computed
+ * again in fp64.  Without bias and groups the logits themselves are compared (the same order).
+ *   logits [T,E] fp32 or bf16;  bias [E] fp32 or NULL;  idx [T,top_k] int32 out;  w [T,top_k] fp32 out;
+ *   scores [T,E] fp32 out (s; for a balancing loss), or NULL.
+ * An expert with logit -inf has score 0; a token whose chosen scores are all 0 has weights 0 (that of a row of -inf
+ * is such a token).  NaN: a c that is NaN ranks below every number, NaNs by ascending id; a softmax over a NaN or
+ * over +inf is NaN throughout, and weights that it reaches are NaN.
+ * 1 <= E <= 256, 1 <= top_k <= 8, n_group in [1, 32] dividing E, 1 <= topk_group <= n_group, top_k <= topk_group *
+ * E / n_group, scale finite. */
+MOE_API int moe_route_scores(const void* logits, int logits_bf16, const float* bias, int T, int E, int top_k,
+                             int scoring, int n_group, int topk_group, int renormalize, float scale, int32_t* idx,
+                             float* w, float* scores, moe_stream_t stream);
+
+/* Its gradient: dlogits [T,E] (the logits' type) from dw [T,top_k] fp32 and the idx that the forward call chose, and
+ * from the gradient of the scores (dscores fp32: [T,E] with dscores_per_token, else [E], the same for all tokens: a
+ * loss on the mean scores).  Either may be NULL.  The choice itself has no gradient (nor has the bias).  An id
+ * outside [0,E) takes part in nothing; one that a token has twice counts twice. */
+MOE_API int moe_route_scores_backward(const void* logits, int logits_bf16, const int32_t* idx, const float* dw,
+                                      const float* dscores, int dscores_per_token, int T, int E, int top_k, int scoring,
+                                      int renormalize, float scale, void* dlogits, moe_stream_t stream);
+
+/* Dropout: out[i] = residual[i] + (stays(i) ? x[i] / (1 - p) : 0), residual NULL: 0.  p counts in 65536ths (to the
+ * nearest; 1 - p is that of the p used).  stays(i) is a function of (seed, offset, i) alone, i the place in memory
+ * order: bits of Philox4x32 with ten rounds, key = seed (low word first), counter = (i / 8, offset) as 64-bit
+ * numbers; of the four result words' eight 16-bit halves (lower half first) the (i % 8)-th must be at least 65536 p.
+ * So the gradient of x is the same call on the gradient of out, and that of the residual is it itself.  What is
+ * dropped is 0 whatever it was, an infinity or NaN too.
+ *   offset_dev: an int64 on the device that is added to the offset, or NULL (a captured graph then replays with
+ *   other masks).  x bf16 or fp32;  residual and out of one type, bf16 or fp32 (without residual: x's);  out may be
+ *   x or residual, of its type.  p in [0, 1 - 2^-17), n in [0, 2^40]. */
+MOE_API int moe_dropout(const void* x, int x_fp32, const void* residual, int residual_fp32, long long n, double p,
+                        uint64_t seed, int64_t offset, const int64_t* offset_dev, void* out, moe_stream_t stream);
+
+/* Layer norm of a residual stream after a block's output was added to it.  Per row:
+ *   y = x + dropout(h)          as moe_dropout's over [T,d] (h NULL: y is x and is not written)
+ *   n = weight * (y - mean) / std + bias,  mean = mean of y,  std = sqrt(mean of (y - mean)^2 + eps)
+ * of y as it is stored, after its rounding.  x, y [T,d] bf16, or fp32 with x_fp32 = 1;  h, n [T,d] bf16;  weight, bias
+ * [d] fp32 (NULL: 1, 0);  stats [T,2] fp32 out: mean and 1 / std, 8-byte aligned.  1 <= d <= 65536, eps >= 0; p and
+ * what follows it as for moe_dropout (p = 0 without h).  y may be x; other outputs must not overlap the inputs. */
+MOE_API int moe_layer_norm(const void* x, int x_fp32, const void* h, const float* weight, const float* bias, int T,
+                           int d, float eps, double p, uint64_t seed, int64_t offset, const int64_t* offset_dev, void* y,
+                           void* n, float* stats, moe_stream_t stream);
+
+/* Its gradient, from dn [T,d] bf16 and dy [T,d] (the stream's type; NULL = 0), with x the stream that was normed
+ * (moe_layer_norm's y, or its x without h) and its stats:
+ *   dx [T,d] (the stream's type): the whole gradient of the stream before the addition, x's;
+ *   dh [T,d] bf16, or NULL: dropout(dx), with the forward call's p, seed and offset;
+ *   dweight, dbias [d] fp32, or NULL: sums over the rows in a fixed order, written, not added to.
+ * dx may be dy.  workspace: 16-byte aligned, moe_layer_norm_backward_workspace_size(T, d) bytes. */
+MOE_API size_t moe_layer_norm_backward_workspace_size(int T, int d);
+MOE_API int moe_layer_norm_backward(const void* x, int x_fp32, const float* stats, const void* dn, const void* dy,
+                                    const float* weight, int T, int d, double p, uint64_t seed, int64_t offset,
+                                    const int64_t* offset_dev, void* dx, void* dh, float* dweight, float* dbias,
+                                    void* workspace, size_t workspace_bytes, moe_stream_t stream);
+
+/* Embedding: out[t] = scale * table[ids[t]], a row of zeros for an id outside [0,V) (MOE_STATUS_BAD_TOKEN).
+ *   ids [T] int32, or int64 with ids_int64 = 1;  table [V,d] and out [T,d] bf16 or fp32;  status: device int32 or
+ *   NULL.  1 <= V <= 2^31 - 1025, 1 <= d <= 65536, scale finite. */
+MOE_API int moe_embed(const void* ids, int ids_int64, const void* table, int table_fp32, int T, int V, int d,
+                      float scale, void* out, int out_fp32, int32_t* status, moe_stream_t stream);
+
+/* The table's gradient: out[v] = scale * sum over the t with ids[t] = v of dy[t], [V,d] written whole (zero for an id
+ * that no token has); with accumulate = 1 (fp32 only) added to out (one addition per element, in which values under
+ * 2^-126 may count as zero; rows of other ids are left as they are).  The sums are in fp32 and in a fixed order: the
+ * same result on every run.  Ids outside [0,V) are left out (MOE_STATUS_BAD_TOKEN).
+ *   dy [T,d] bf16 or fp32;  out bf16 or fp32;  workspace: 16-byte aligned,
+ *   moe_embed_backward_workspace_size(T, V, d) bytes. */
+MOE_API size_t moe_embed_backward_workspace_size(int T, int V, int d);
+MOE_API int moe_embed_backward(const void* ids, int ids_int64, const void* dy, int dy_fp32, int T, int V, int d,
+                               float scale, void* out, int out_fp32, int accumulate, void* workspace,
+                               size_t workspace_bytes, int32_t* status, moe_stream_t stream);
 
 /* Reads (synchronously: cudaMemcpy) a device status word — a stage call's `status` pointer, or
  * the workspace of moe_forward — into *code (0 = no device-side error).  With

@@ -25,9 +25,15 @@ namespace {
     X(moe_swiglu) X(moe_swiglu_backward) X(moe_block_norm) X(moe_block_norm_backward)                       \
     X(moe_block_norm_backward_workspace_size) X(moe_grouped_mm) X(moe_grouped_mm_wgrad)                     \
     X(moe_grouped_mm_workspace_size) X(moe_adamw_step)
+// Calls that a library may lack: their functions here then leave the work to the Python ones.
+#define MOE_FAST_MORE_CALLS(X)                                                                              \
+    X(moe_route_scores) X(moe_route_scores_backward) X(moe_layer_norm) X(moe_layer_norm_backward)           \
+    X(moe_layer_norm_backward_workspace_size) X(moe_dropout) X(moe_embed) X(moe_embed_backward)             \
+    X(moe_embed_backward_workspace_size)
 struct Lib {
 #define X(name) decltype(&::name) name = nullptr;
     MOE_FAST_CALLS(X)
+    MOE_FAST_MORE_CALLS(X)
 #undef X
 } lib;
 
@@ -334,6 +340,246 @@ PyObject* adamw_step(PyObject*, PyObject* const* a, Py_ssize_t n) {
     });
 }
 
+// A Python integer or number that fits, else false (and no error is left behind: the Python function reports it).
+template <typename V, typename F>
+bool number(F convert, PyObject* o, V* out) {
+    const auto v = convert(o);
+    if (PyErr_Occurred()) {
+        PyErr_Clear();
+        return false;
+    }
+    *out = static_cast<V>(v);
+    return static_cast<decltype(v)>(*out) == v || v != v;
+}
+bool integer(PyObject* o, int* out) { return PyLong_Check(o) && number(PyLong_AsLong, o, out); }
+bool real(PyObject* o, double* out) { return number(PyFloat_AsDouble, o, out); }
+bool real(PyObject* o, float* out) {
+    double v;
+    if (!real(o, &v)) return false;
+    *out = static_cast<float>(v);
+    return true;
+}
+bool one_of(ScalarType t) { return t == BF16 || t == F32; }
+
+// "softmax" 0, "sigmoid" 1, anything else -1.
+int scoring_of(PyObject* o) {
+    if (!PyUnicode_Check(o)) return -1;
+    return PyUnicode_CompareWithASCIIString(o, "softmax") == 0 ? 0 : PyUnicode_CompareWithASCIIString(o, "sigmoid") == 0 ? 1 : -1;
+}
+
+// route_scores(logits, top_k, scoring, bias, n_group, topk_group, renormalize, scale, want_scores) -> (idx, w, scores)
+PyObject* route_scores(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded([&]() -> PyObject* {
+        Args c;
+        const at::Tensor* l = n == 9 && lib.moe_route_scores ? c.need(a[0], 2) : nullptr;
+        if (!l || !one_of(l->scalar_type()) || !fits(l->size(0)) || !fits(l->size(1))) Py_RETURN_NONE;
+        const int64_t T = l->size(0), E = l->size(1);
+        int k, groups, kept;
+        float scale;
+        const int how = scoring_of(a[2]);
+        if (how < 0 || !integer(a[1], &k) || !integer(a[4], &groups) || !integer(a[5], &kept) || !real(a[7], &scale) || k < 1)
+            Py_RETURN_NONE;
+        const void *pl = c.plain(*l, l->scalar_type()), *pb = c.opt(a[3], F32, {E});
+        if (!c.ok) Py_RETURN_NONE;
+        const bool renorm = PyObject_IsTrue(a[6]);
+        at::Tensor idx = make({T, k}, I32, *l), w = make({T, k}, F32, *l), scores;
+        if (PyObject_IsTrue(a[8])) scores = make({T, E}, F32, *l);
+        const int rc = unlocked([&] {
+            return lib.moe_route_scores(pl, l->scalar_type() == BF16, static_cast<const float*>(pb), T, E, k, how, groups,
+                                        kept, renorm, scale, static_cast<int32_t*>(ptr(idx)), static_cast<float*>(ptr(w)),
+                                        static_cast<float*>(ptr(scores)), stream());
+        });
+        return rc ? code(rc) : Py_BuildValue("(NNN)", wrap(idx), wrap(w), wrap(scores));
+    });
+}
+
+// route_scores_backward(logits, idx, dw, dscores, scoring, renormalize, scale)
+PyObject* route_scores_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded([&]() -> PyObject* {
+        Args c;
+        const at::Tensor* l = n == 7 && lib.moe_route_scores_backward ? c.need(a[0], 2) : nullptr;
+        if (!l || !one_of(l->scalar_type()) || !fits(l->size(0)) || !fits(l->size(1))) Py_RETURN_NONE;
+        const int64_t T = l->size(0), E = l->size(1);
+        float scale;
+        const int how = scoring_of(a[4]);
+        if (how < 0 || !real(a[6], &scale)) Py_RETURN_NONE;
+        int64_t k = 1;
+        const void *pl = c.plain(*l, l->scalar_type()), *pi = nullptr, *pw = nullptr;
+        if (a[2] != Py_None) {
+            const at::Tensor* w = c.need(a[2], 2);
+            if (!w || !fits(w->size(1))) Py_RETURN_NONE;
+            k = w->size(1);
+            pw = c.at(a[2], F32, {T, k});
+            pi = c.at(a[1], I32, {T, k});
+        }
+        const at::Tensor* ds = tensor(a[3]);
+        const bool per_token = ds && ds->dim() == 2;
+        const void* ps = per_token ? c.at(a[3], F32, {T, E}) : c.opt(a[3], F32, {E});
+        if (!c.ok) Py_RETURN_NONE;
+        const bool renorm = PyObject_IsTrue(a[5]);
+        at::Tensor out = make({T, E}, l->scalar_type(), *l);
+        const int rc = unlocked([&] {
+            return lib.moe_route_scores_backward(pl, l->scalar_type() == BF16, static_cast<const int32_t*>(pi),
+                                                 static_cast<const float*>(pw), static_cast<const float*>(ps), per_token, T,
+                                                 E, k, how, renorm, scale, ptr(out), stream());
+        });
+        return rc ? code(rc) : wrap(out);
+    });
+}
+
+// p, seed, offset, offset_tensor of the calls with dropout.
+struct Dropping {
+    double p;
+    uint64_t seed;
+    int64_t offset;
+    const int64_t* dev;
+    bool read(Args& c, PyObject* const* a) {
+        if (!real(a[0], &p) || !PyLong_Check(a[1]) || !PyLong_Check(a[2])) return false;
+        if (!number(PyLong_AsUnsignedLongLong, a[1], &seed) || !number(PyLong_AsLongLong, a[2], &offset)) return false;
+        dev = static_cast<const int64_t*>(c.opt(a[3], ScalarType::Long, {1}));
+        return c.ok;
+    }
+};
+
+// dropout(x, p, seed, offset, offset_tensor, residual)
+PyObject* dropout(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded([&]() -> PyObject* {
+        Args c;
+        const at::Tensor* x = n == 6 && lib.moe_dropout ? tensor(a[0]) : nullptr;
+        if (!x || !one_of(x->scalar_type())) Py_RETURN_NONE;
+        const at::Tensor* r = a[5] == Py_None ? x : tensor(a[5]);
+        if (!r || !one_of(r->scalar_type())) Py_RETURN_NONE;
+        Dropping drop;
+        const void *px = c.plain(*x, x->scalar_type()), *pr = c.opt(a[5], r->scalar_type(), x->sizes());
+        if (!c.ok || !drop.read(c, a + 1)) Py_RETURN_NONE;
+        at::Tensor out = make(x->sizes(), r->scalar_type(), *x);
+        const int rc = unlocked([&] {
+            return lib.moe_dropout(px, x->scalar_type() == F32, pr, r->scalar_type() == F32, x->numel(), drop.p, drop.seed,
+                                   drop.offset, drop.dev, ptr(out), stream());
+        });
+        return rc ? code(rc) : wrap(out);
+    });
+}
+
+// layer_norm(x, weight, bias, h, p, seed, offset, offset_tensor, eps) -> (y, n, stats)
+PyObject* layer_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded([&]() -> PyObject* {
+        Args c;
+        const at::Tensor* x = n == 9 && lib.moe_layer_norm ? c.need(a[0], 2) : nullptr;
+        if (!x || !one_of(x->scalar_type()) || !fits(x->size(0)) || !fits(x->size(1))) Py_RETURN_NONE;
+        const int64_t T = x->size(0), d = x->size(1);
+        const ScalarType type = x->scalar_type();
+        const void *px = c.plain(*x, type), *pw = c.opt(a[1], F32, {d}), *pb = c.opt(a[2], F32, {d}),
+                   *ph = c.opt(a[3], BF16, {T, d});
+        Dropping drop;
+        float eps;
+        if (!c.ok || !drop.read(c, a + 4) || !real(a[8], &eps)) Py_RETURN_NONE;
+        at::Tensor y, out = make({T, d}, BF16, *x), stats = make({T, 2}, F32, *x);
+        if (a[3] != Py_None) y = make({T, d}, type, *x);
+        const int rc = unlocked([&] {
+            return lib.moe_layer_norm(px, type == F32, ph, static_cast<const float*>(pw), static_cast<const float*>(pb), T, d,
+                                      eps, drop.p, drop.seed, drop.offset, drop.dev, ptr(y), ptr(out),
+                                      static_cast<float*>(ptr(stats)), stream());
+        });
+        return rc ? code(rc) : Py_BuildValue("(NNN)", wrap(y), wrap(out), wrap(stats));
+    });
+}
+
+// layer_norm_backward(x, stats, dn, dy, weight, bias, want_h, p, seed, offset, offset_tensor)
+//   -> gradients of (x, h, weight, bias)
+PyObject* layer_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded([&]() -> PyObject* {
+        Args c;
+        const at::Tensor* x = n == 11 && lib.moe_layer_norm_backward ? c.need(a[0], 2) : nullptr;
+        if (!x || !one_of(x->scalar_type()) || !fits(x->size(0)) || !fits(x->size(1))) Py_RETURN_NONE;
+        const int64_t T = x->size(0), d = x->size(1);
+        const ScalarType type = x->scalar_type();
+        const void *px = c.plain(*x, type), *ps = c.at(a[1], F32, {T, 2}), *pn = c.at(a[2], BF16, {T, d}),
+                   *py = c.opt(a[3], type, {T, d}), *pw = c.opt(a[4], F32, {d});
+        c.opt(a[5], F32, {d});
+        Dropping drop;
+        if (!c.ok || !drop.read(c, a + 7)) Py_RETURN_NONE;
+        const size_t need = lib.moe_layer_norm_backward_workspace_size(T, d);
+        at::Tensor ws = make({static_cast<int64_t>(need)}, ScalarType::Byte, *x), dx = make({T, d}, type, *x), dh, dw, db;
+        if (PyObject_IsTrue(a[6])) dh = make({T, d}, BF16, *x);
+        if (a[4] != Py_None) dw = make({d}, F32, *x);
+        if (a[5] != Py_None) db = make({d}, F32, *x);
+        const int rc = unlocked([&] {
+            return lib.moe_layer_norm_backward(px, type == F32, static_cast<const float*>(ps), pn, py,
+                                               static_cast<const float*>(pw), T, d, drop.p, drop.seed, drop.offset, drop.dev,
+                                               ptr(dx), ptr(dh), static_cast<float*>(ptr(dw)), static_cast<float*>(ptr(db)),
+                                               ptr(ws), need, stream());
+        });
+        return rc ? code(rc) : Py_BuildValue("(NNNN)", wrap(dx), wrap(dh), wrap(dw), wrap(db));
+    });
+}
+
+// The ids of the embedding calls: contiguous int32 or int64 of any shape.
+const at::Tensor* ids_of(Args& c, PyObject* o, const void** p) {
+    const at::Tensor* t = tensor(o);
+    if (!t || (t->scalar_type() != I32 && t->scalar_type() != ScalarType::Long) || !fits(t->numel())) return nullptr;
+    *p = c.plain(*t, t->scalar_type());
+    return c.ok ? t : nullptr;
+}
+
+// embed(ids, table, scale, whether the result is fp32 or None for the table's type, status)
+PyObject* embed(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded([&]() -> PyObject* {
+        Args c;
+        const at::Tensor* w = n == 5 && lib.moe_embed ? c.need(a[1], 2) : nullptr;
+        const void* pi = nullptr;
+        const at::Tensor* ids = w ? ids_of(c, a[0], &pi) : nullptr;
+        if (!ids || !one_of(w->scalar_type()) || !fits(w->size(0)) || !fits(w->size(1))) Py_RETURN_NONE;
+        if (a[3] != Py_None && !PyBool_Check(a[3])) Py_RETURN_NONE;
+        float scale;
+        const void* pw = c.plain(*w, w->scalar_type());
+        void* st = c.opt(a[4], I32, {1});
+        if (!c.ok || !real(a[2], &scale)) Py_RETURN_NONE;
+        const ScalarType type = a[3] == Py_None ? w->scalar_type() : a[3] == Py_True ? F32 : BF16;
+        at::DimVector shape(ids->sizes());
+        shape.push_back(w->size(1));
+        at::Tensor out = make(shape, type, *w);
+        const int rc = unlocked([&] {
+            return lib.moe_embed(pi, ids->scalar_type() != I32, pw, w->scalar_type() == F32, ids->numel(), w->size(0),
+                                 w->size(1), scale, ptr(out), type == F32, static_cast<int32_t*>(st), stream());
+        });
+        return rc ? code(rc) : wrap(out);
+    });
+}
+
+// embed_backward(ids, dy, V, scale, out or None, fp32, accumulate, status)
+PyObject* embed_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded([&]() -> PyObject* {
+        Args c;
+        const at::Tensor* dy = n == 8 && lib.moe_embed_backward ? tensor(a[1]) : nullptr;
+        const void* pi = nullptr;
+        const at::Tensor* ids = dy ? ids_of(c, a[0], &pi) : nullptr;
+        if (!ids || !one_of(dy->scalar_type()) || dy->dim() != ids->dim() + 1) Py_RETURN_NONE;
+        const int64_t d = dy->size(-1);
+        if (!fits(d) || dy->sizes().slice(0, ids->dim()) != ids->sizes()) Py_RETURN_NONE;
+        int V;
+        float scale;
+        if (!integer(a[2], &V) || V < 1 || !real(a[3], &scale)) Py_RETURN_NONE;
+        const bool f32 = PyObject_IsTrue(a[5]), acc = PyObject_IsTrue(a[6]);
+        const void* py = c.plain(*dy, dy->scalar_type());
+        c.opt(a[4], f32 ? F32 : BF16, {V, d});
+        void* st = c.opt(a[7], I32, {1});
+        if (!c.ok || (acc && a[4] == Py_None)) Py_RETURN_NONE;
+        const size_t need = lib.moe_embed_backward_workspace_size(ids->numel(), V, d);
+        at::Tensor ws, out = a[4] == Py_None ? make({V, d}, f32 ? F32 : BF16, *dy) : *tensor(a[4]);
+        if (need) ws = make({static_cast<int64_t>(need)}, ScalarType::Byte, *dy);
+        const int rc = unlocked([&] {
+            return lib.moe_embed_backward(pi, ids->scalar_type() != I32, py, dy->scalar_type() == F32, ids->numel(), V, d,
+                                          scale, ptr(out), f32, acc, ptr(ws), need, static_cast<int32_t*>(st), stream());
+        });
+        if (rc) return code(rc);
+        if (a[4] == Py_None) return wrap(out);
+        touch(out);
+        Py_INCREF(a[4]);
+        return a[4];
+    });
+}
+
 // wrote(tensors, lists of tensors or None ...)
 PyObject* wrote(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return guarded([&]() -> PyObject* {
@@ -369,6 +615,9 @@ PyObject* init(PyObject*, PyObject* const* a, Py_ssize_t n) {
     }
     MOE_FAST_CALLS(X)
 #undef X
+#define X(name) lib.name = reinterpret_cast<decltype(&::name)>(dlsym(h, #name));
+    MOE_FAST_MORE_CALLS(X)
+#undef X
     Py_RETURN_NONE;
 }
 
@@ -376,6 +625,8 @@ PyObject* init(PyObject*, PyObject* const* a, Py_ssize_t n) {
 PyMethodDef methods[] = {FAST(init),          FAST(swiglu),     FAST(swiglu_backward),  FAST(block_norm),
                          FAST(block_norm_backward), FAST(grouped_mm), FAST(grouped_mm_wgrad), FAST(adamw_step),
                          FAST(wrote),
+                         FAST(route_scores),  FAST(route_scores_backward), FAST(layer_norm), FAST(layer_norm_backward),
+                         FAST(dropout),       FAST(embed),      FAST(embed_backward),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_moe_fast", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -260,6 +260,28 @@ cudaError_t launch_adamw(const moe_adamw_tensor* ts, int count, bool p_bf16, boo
                          double beta1, double beta2, double eps, double wd, double corr1, double corr2,
                          const int32_t* step_dev, const float* factors, int num_sms, cudaStream_t s);
 
+// The operators around the blocks of a stack (layer_norm.cu, embed.cu, route_scores.cu; dropout.cu: stack_ops.cuh).
+struct EmbedArgs {
+    const void* ids;   // [T] int32, or int64 with ids64
+    bool ids64;
+    const void* rows;  // forward: the table [V, d]; gradient: dy [T, d]
+    bool rows_fp32;
+    int T, V, d;
+    float scale;
+    void* out;         // [T, d] resp. [V, d]
+    bool out_fp32, accumulate;
+    int32_t* status;
+};
+cudaError_t launch_embed(const EmbedArgs& a, cudaStream_t s);
+size_t embed_backward_workspace(int T, int d);
+cudaError_t launch_embed_backward(const EmbedArgs& a, void* workspace, cudaStream_t s);
+cudaError_t launch_route_scores(const void* logits, bool bf16, const float* bias, int T, int E, int k, bool sigmoid,
+                                int n_group, int topk_group, bool renorm, float scale, int32_t* idx, float* w,
+                                float* scores, cudaStream_t s);
+cudaError_t launch_route_scores_backward(const void* logits, bool bf16, const int32_t* idx, const float* dw,
+                                         const float* dscores, bool per_token, int T, int E, int k, bool sigmoid,
+                                         bool renorm, float scale, void* dlogits, cudaStream_t s);
+
 // FP8 quantisation (fp8.cu).  Rows: row r of the bf16 [*, C] matrix a (row src[r] when src is
 // given, src values checked against src_rows) -> E4M3 codes q [R, C] and scale [R].  Weights:
 // W [E, K, N] bf16 -> Wq codes, transposed and blocked ([E, N/64, K/128, 64, 128]: code (e, n, k) at

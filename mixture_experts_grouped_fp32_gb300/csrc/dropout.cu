@@ -1,0 +1,76 @@
+// dropout.cu — out = residual + keep(i) x / (1 - p), the mask from a counter-based generator (stack_ops.cuh).
+//
+// Elements are taken in memory order, eight to a thread and step, the random block of an element its index / 8: the
+// gradient is the same call on the gradient of the output.  One pass over memory, bound by it: the generator runs
+// while the loads are under way.
+#include <algorithm>
+
+#include "stack_ops.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kThreads = 256, kPer = 2;  // vectors of a thread
+
+template <typename X, typename R, bool RES, bool ALIGNED>
+__global__ void __launch_bounds__(kThreads)
+dropout_kernel(const X* x, const R* residual, size_t n, DropArgs args, R* out) {
+    pdl_wait();
+    pdl_trigger();
+    const Drop drop(args);
+    const size_t n8 = (n + 7) / 8;
+    const size_t first = static_cast<size_t>(blockIdx.x) * (kThreads * kPer) + threadIdx.x;
+    Raw8<X> xr[kPer];
+    Raw8<R> rr[kPer];
+    int count[kPer];
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+        const size_t i = first + k * kThreads;
+        count[k] = i < n8 ? static_cast<int>(min(static_cast<size_t>(8), n - 8 * i)) : 0;
+        if (count[k] == 8) {
+            fetch_raw<ALIGNED>(xr[k], x + 8 * i, 8);
+            if (RES) fetch_raw<ALIGNED>(rr[k], residual + 8 * i, 8);
+        } else if (count[k] > 0) {
+            fetch_raw<false>(xr[k], x + 8 * i, count[k]);
+            if (RES) fetch_raw<false>(rr[k], residual + 8 * i, count[k]);
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+        const size_t i = first + k * kThreads;
+        if (count[k] == 0) continue;
+        Vec8 v = values(xr[k]);
+        if (drop.on()) drop.apply(v, 8 * i);
+        if (RES) {
+            const Vec8 r = values(rr[k]);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v.v[j] += r.v[j];
+        }
+        if (count[k] == 8) put8<ALIGNED>(out + 8 * i, v, 8);
+        else put8<false>(out + 8 * i, v, count[k]);
+    }
+}
+
+template <typename X, typename R, bool RES>
+cudaError_t launch_as(const void* x, const void* residual, long long n, const DropArgs& a, void* out, cudaStream_t s) {
+    const long long n8 = (n + 7) / 8, blocks = (n8 + kThreads * kPer - 1) / (kThreads * kPer);
+    const auto words = reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(residual) | reinterpret_cast<uintptr_t>(out);
+    const dim3 grid(static_cast<unsigned>(blocks)), block(kThreads);
+    const X* xp = static_cast<const X*>(x);
+    const R* rp = static_cast<const R*>(residual);
+    R* op = static_cast<R*>(out);
+    if (words & 15) return launch_k(kPdlTrain, dropout_kernel<X, R, RES, false>, grid, block, 0, s, xp, rp, n, a, op);
+    return launch_k(kPdlTrain, dropout_kernel<X, R, RES, true>, grid, block, 0, s, xp, rp, n, a, op);
+}
+
+}  // namespace
+
+cudaError_t launch_dropout(const void* x, bool x_fp32, const void* residual, bool res_fp32, long long n,
+                           const DropArgs& a, void* out, cudaStream_t s) {
+    using B = __nv_bfloat16;
+    if (!residual) return x_fp32 ? launch_as<float, float, false>(x, nullptr, n, a, out, s) : launch_as<B, B, false>(x, nullptr, n, a, out, s);
+    if (x_fp32) return res_fp32 ? launch_as<float, float, true>(x, residual, n, a, out, s) : launch_as<float, B, true>(x, residual, n, a, out, s);
+    return res_fp32 ? launch_as<B, float, true>(x, residual, n, a, out, s) : launch_as<B, B, true>(x, residual, n, a, out, s);
+}
+
+}  // namespace moe

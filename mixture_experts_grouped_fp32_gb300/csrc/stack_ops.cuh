@@ -1,0 +1,192 @@
+// stack_ops.cuh — dropout masks as a function of (seed, offset, element), so that none is stored.
+//
+// Philox4x32 with ten rounds (J. K. Salmon, M. A. Moraes, R. O. Dror, D. E. Shaw, "Parallel random numbers: as
+// easy as 1, 2, 3", SC 2011): the counter of elements 8 b .. 8 b + 7 is (b, offset), 64 bits each, the key is the
+// seed; the four words of the result are eight 16-bit numbers, the lower half of a word first.  An element stays if
+// its number is at least `cut` = p 65536 (rounded); those that stay are multiplied by 65536 / (65536 - cut), the
+// inverse of the probability itself, so that the expectation is exact for the p that is used.
+//
+// Sixteen bits an element: a block of ten rounds costs about 80 issue slots, ten for each of eight elements; with 32
+// bits it would be twenty, and a bf16 dropout (4 bytes an element) would wait for the arithmetic, not for the memory.
+#pragma once
+
+#include "train_util.cuh"
+
+namespace moe {
+
+struct DropArgs {
+    uint32_t cut;  // 0: everything stays
+    float up;
+    uint32_t key0, key1;
+    uint64_t offset;
+    const int64_t* offset_dev;  // added to the offset, or null
+};
+
+// p in [0, 1) -> cut and factor; false for another p (or one that rounds to 1).
+inline bool drop_args(double p, uint64_t seed, int64_t offset, const int64_t* offset_dev, DropArgs* a) {
+    if (!(p >= 0.0 && p < 1.0)) return false;
+    const long cut = static_cast<long>(p * 65536.0 + 0.5);
+    if (cut > 65535) return false;
+    a->cut = static_cast<uint32_t>(cut);
+    a->up = static_cast<float>(65536.0 / (65536 - cut));
+    a->key0 = static_cast<uint32_t>(seed);
+    a->key1 = static_cast<uint32_t>(seed >> 32);
+    a->offset = static_cast<uint64_t>(offset);
+    a->offset_dev = offset_dev;
+    return true;
+}
+
+__device__ __forceinline__ uint4 philox(uint32_t k0, uint32_t k1, uint64_t block, uint64_t offset) {
+    uint32_t c0 = static_cast<uint32_t>(block), c1 = static_cast<uint32_t>(block >> 32);
+    uint32_t c2 = static_cast<uint32_t>(offset), c3 = static_cast<uint32_t>(offset >> 32);
+#pragma unroll
+    for (int r = 0; r < 10; ++r) {
+        const uint64_t a = static_cast<uint64_t>(c0) * 0xD2511F53u, b = static_cast<uint64_t>(c2) * 0xCD9E8D57u;
+        c0 = static_cast<uint32_t>(b >> 32) ^ c1 ^ k0;
+        c1 = static_cast<uint32_t>(b);
+        c2 = static_cast<uint32_t>(a >> 32) ^ c3 ^ k1;
+        c3 = static_cast<uint32_t>(a);
+        k0 += 0x9E3779B9u;
+        k1 += 0xBB67AE85u;
+    }
+    return make_uint4(c0, c1, c2, c3);
+}
+
+cudaError_t launch_dropout(const void* x, bool x_fp32, const void* residual, bool res_fp32, long long n,
+                           const DropArgs& a, void* out, cudaStream_t s);
+
+// Layer norm after a residual (layer_norm.cu); x, y, dy, dx fp32 with x_fp32, else bf16.
+struct LayerNormArgs {
+    bool x_fp32;
+    const void* x;  // backward: the stream that was normed
+    const __nv_bfloat16* h;
+    const float *weight, *bias;
+    int T, d;
+    float eps;
+    DropArgs drop;
+    void* y;  // forward
+    __nv_bfloat16* n;
+    float* stats;             // [T, 2]: mean, 1 / standard deviation
+    const __nv_bfloat16* dn;  // backward
+    const void* dy;
+    void* dx;
+    __nv_bfloat16* dh;
+    float *dweight, *dbias;
+    float* partial;           // [layer_norm_blocks(T, d), 2, d]
+};
+int layer_norm_blocks(int T, int d);
+cudaError_t launch_layer_norm(const LayerNormArgs& a, int num_sms, cudaStream_t s);
+cudaError_t launch_layer_norm_backward(const LayerNormArgs& a, cudaStream_t s);
+
+// What a kernel keeps of its arguments.
+struct Drop {
+    uint32_t cut16, key0, key1;  // cut << 16
+    float up;
+    uint64_t offset;
+    __device__ __forceinline__ explicit Drop(const DropArgs& a)
+        : cut16(a.cut << 16), key0(a.key0), key1(a.key1), up(a.up),
+          offset(a.offset + (a.offset_dev && a.cut ? static_cast<uint64_t>(__ldg(a.offset_dev)) : 0)) {}
+    __device__ __forceinline__ bool on() const { return cut16 != 0; }
+    // The eight elements from `first` on (a multiple of 8): zeroed or scaled.  What is dropped is 0 whatever it was,
+    // an infinity or a NaN too.
+    __device__ __forceinline__ void apply(Vec8& v, uint64_t first) const {
+        const uint4 q = philox(key0, key1, first >> 3, offset);
+        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            v.v[2 * j] = (w[j] << 16) >= cut16 ? v.v[2 * j] * up : 0.0f;
+            v.v[2 * j + 1] = w[j] >= cut16 ? v.v[2 * j + 1] * up : 0.0f;
+        }
+    }
+    // The same for any first element: its eight numbers lie in two blocks.
+    __device__ __forceinline__ void apply_any(Vec8& v, uint64_t first) const {
+        const int shift = static_cast<int>(first & 7);
+        if (shift == 0) return apply(v, first);
+        const uint4 a = philox(key0, key1, first >> 3, offset), b = philox(key0, key1, (first >> 3) + 1, offset);
+        const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+        uint32_t m = 0;  // bit i: number i of the two blocks stays
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            m |= ((w[j] << 16) >= cut16 ? 1u : 0u) << (2 * j) | (w[j] >= cut16 ? 1u : 0u) << (2 * j + 1);
+        m >>= shift;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v.v[j] = (m >> j) & 1u ? v.v[j] * up : 0.0f;
+    }
+};
+
+// ---------------------------------------------------------------------------------------------
+// Eight values of a row whose width or alignment may be anything: as they are in memory (raw), so that loads can
+// be under way while the last ones are worked on.  ALIGNED: width a multiple of 8, 16-byte aligned rows; else values
+// one by one, `count` of them (the others are 0).
+// ---------------------------------------------------------------------------------------------
+template <typename X>
+struct Raw8;
+template <>
+struct Raw8<__nv_bfloat16> {
+    uint4 q;
+};
+template <>
+struct Raw8<float> {
+    float4 a, b;
+};
+
+template <bool ALIGNED>
+__device__ __forceinline__ void fetch_raw(Raw8<__nv_bfloat16>& r, const __nv_bfloat16* p, int count) {
+    if constexpr (ALIGNED) {
+        r.q = __ldcs(reinterpret_cast<const uint4*>(p));
+    } else {
+        const unsigned short* u = reinterpret_cast<const unsigned short*>(p);
+        uint32_t h[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) h[j] = j < count ? u[j] : 0u;
+        r.q = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
+    }
+}
+template <bool ALIGNED>
+__device__ __forceinline__ void fetch_raw(Raw8<float>& r, const float* p, int count) {
+    if constexpr (ALIGNED) {
+        const Vec8 v = load8(p, 0);
+        r.a = make_float4(v.v[0], v.v[1], v.v[2], v.v[3]);
+        r.b = make_float4(v.v[4], v.v[5], v.v[6], v.v[7]);
+    } else {
+        float f[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] = j < count ? p[j] : 0.0f;
+        r.a = make_float4(f[0], f[1], f[2], f[3]);
+        r.b = make_float4(f[4], f[5], f[6], f[7]);
+    }
+}
+__device__ __forceinline__ Vec8 values(const Raw8<__nv_bfloat16>& r) { return unpack8(r.q); }
+__device__ __forceinline__ Vec8 values(const Raw8<float>& r) {
+    return Vec8{{r.a.x, r.a.y, r.a.z, r.a.w, r.b.x, r.b.y, r.b.z, r.b.w}};
+}
+// The values as they read after a store.
+__device__ __forceinline__ Vec8 rounded(const Vec8& v, const __nv_bfloat16*) { return unpack8(pack8(v)); }
+__device__ __forceinline__ Vec8 rounded(const Vec8& v, const float*) { return v; }
+
+__device__ __forceinline__ void put(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+__device__ __forceinline__ void put(float* p, float v) { *p = v; }
+template <bool ALIGNED, typename X>
+__device__ __forceinline__ void put8(X* p, const Vec8& v, int count) {
+    if constexpr (ALIGNED) {
+        store8(p, 0, v);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (j < count) put(p + j, v.v[j]);
+    }
+}
+// Eight fp32 values of a vector that every row reads.
+template <bool ALIGNED>
+__device__ __forceinline__ Vec8 cached8(const float* p, int count) {
+    if constexpr (ALIGNED) {
+        return load8_cached(p, 0);
+    } else {
+        Vec8 v;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v.v[j] = j < count ? __ldg(p + j) : 0.0f;
+        return v;
+    }
+}
+
+}  // namespace moe

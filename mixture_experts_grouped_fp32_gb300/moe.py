@@ -23,6 +23,8 @@ _I = ctypes.c_int
 _SZ = ctypes.c_size_t
 _F = ctypes.c_float
 _D = ctypes.c_double
+_I64 = ctypes.c_int64
+_U64 = ctypes.c_uint64
 _SIGS = {
     "moe_version": ([], _I),
     "moe_forward_launch_count": ([_I, _I, _I], _I),
@@ -90,6 +92,15 @@ _SIGS = {
     "moe_block_norm_backward": ([_P, _I, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _F, _P, _P, _P, _P, _P, _P, _P, _P,
                                  _SZ, _P], _I),
     "moe_adamw_step": ([_P, _I, _I, _I, _I, _D, _D, _D, _D, _D, _I, _P, _P, _P], _I),
+    "moe_route_scores": ([_P, _I, _P, _I, _I, _I, _I, _I, _I, _I, _F, _P, _P, _P, _P], _I),
+    "moe_route_scores_backward": ([_P, _I, _P, _P, _P, _I, _I, _I, _I, _I, _I, _F, _P, _P], _I),
+    "moe_layer_norm": ([_P, _I, _P, _P, _P, _I, _I, _F, _D, _U64, _I64, _P, _P, _P, _P, _P], _I),
+    "moe_layer_norm_backward_workspace_size": ([_I, _I], _SZ),
+    "moe_layer_norm_backward": ([_P, _I, _P, _P, _P, _P, _I, _I, _D, _U64, _I64, _P, _P, _P, _P, _P, _P, _SZ, _P], _I),
+    "moe_dropout": ([_P, _I, _P, _I, _I64, _D, _U64, _I64, _P, _P, _P], _I),
+    "moe_embed": ([_P, _I, _P, _I, _I, _I, _I, _F, _P, _I, _P, _P], _I),
+    "moe_embed_backward_workspace_size": ([_I, _I, _I], _SZ),
+    "moe_embed_backward": ([_P, _I, _P, _I, _I, _I, _I, _F, _P, _I, _I, _P, _SZ, _P, _P], _I),
 }
 
 WS_FIELDS = ("status", "idx", "w", "counts", "offsets", "src", "dest", "x_perm", "h", "y_perm", "total")
@@ -101,6 +112,7 @@ STATUS_BAD_OFFSETS = 0x2
 STATUS_BAD_DEST = 0x4
 STATUS_WAIT_TIMEOUT = 0x8
 STATUS_BAD_SRC = 0x10
+STATUS_BAD_TOKEN = 0x20
 
 
 class MoeError(RuntimeError):
@@ -1259,3 +1271,261 @@ def adamw_step(params, grads, m, v, lr: float, beta1: float = 0.9, beta2: float 
           8 if eight else 32, lr, beta1, beta2, eps, weight_decay, step, _ptr(step_tensor), _ptr(factors),
           _stream(stream))
     _wrote(params, copies)
+
+
+# ---------------------------------------------------------------------------------------------
+# Around the blocks of a stack that reads tokens: routing by scores, layer norm, dropout, embedding.  As the training
+# calls above, none of them is recorded by autograd: each gradient is a call of its own.
+# ---------------------------------------------------------------------------------------------
+_SCORING = {"softmax": 0, "sigmoid": 1}
+_FLOATS = (torch.bfloat16, torch.float32)
+
+
+def _float_type(t, name: str):
+    """bfloat16 or float32."""
+    if t not in _FLOATS:
+        raise ValueError(f"{name} must be bfloat16 or float32, got {t}")
+    return t
+
+
+def _logits_args(logits, scoring):
+    """The logits' address, whether they are bf16, T, E and the scoring's number."""
+    if scoring not in _SCORING:
+        raise ValueError(f"scoring must be 'softmax' or 'sigmoid', got {scoring!r}")
+    if logits.dim() != 2:
+        raise ValueError(f"logits must be [T, E], got {tuple(logits.shape)}")
+    dt = _float_type(logits.dtype, "logits")
+    T, E = logits.shape
+    _fit(T=T, E=E)
+    return _arg(logits, dt, (T, E), "logits"), int(dt is torch.bfloat16), T, E, _SCORING[scoring]
+
+
+def route_scores(logits, top_k: int, scoring: str = "softmax", bias=None, n_group: int = 1, topk_group: int = 1,
+                 renormalize: bool = True, scale: float = 1.0, want_scores: bool = False, idx=None, w=None, scores=None,
+                 stream=None):
+    """Routing by scores s (softmax or sigmoid of the logits [T, E], fp32 or bf16): the top_k largest s + bias of the
+    ``topk_group`` best of ``n_group`` groups, with weights scale * s, divided by the chosen scores' sum with
+    ``renormalize``.  Returns (idx int32 [T, top_k], w fp32 [T, top_k], s fp32 [T, E] with ``want_scores``, else None).
+    The choice is the one of 64-bit arithmetic; equal scores go to the lower expert.  Not recorded by autograd: the
+    gradient is ``route_scores_backward``."""
+    if _fast is not None and idx is None and w is None and scores is None and stream is None:
+        r = _fast.route_scores(logits, top_k, scoring, bias, n_group, topk_group, renormalize, scale, want_scores)
+        if r is not None:
+            return _done("moe_route_scores", r)
+    pl, bf16, T, E, how = _logits_args(logits, scoring)
+    _fit(top_k=top_k, n_group=n_group, topk_group=topk_group)
+    if top_k < 1:
+        raise ValueError(f"top_k = {top_k} must be at least 1")
+    pb = _opt(bias, torch.float32, (E,), "bias")
+    given = (idx, w, scores)
+    idx = _out(idx, (T, top_k), torch.int32, logits.device, stream, "idx")
+    w = _out(w, (T, top_k), torch.float32, logits.device, stream, "w")
+    if want_scores or scores is not None:
+        scores = _out(scores, (T, E), torch.float32, logits.device, stream, "scores")
+    _call("moe_route_scores", pl, bf16, pb, T, E, top_k, how, n_group, topk_group, int(bool(renormalize)), scale,
+          idx.data_ptr(), w.data_ptr(), _ptr(scores), _stream(stream))
+    _wrote(*given)
+    return idx, w, scores
+
+
+def route_scores_backward(logits, idx=None, dw=None, dscores=None, scoring: str = "softmax", renormalize: bool = True,
+                          scale: float = 1.0, dlogits=None, stream=None):
+    """Gradient of ``route_scores`` with respect to the logits ([T, E], their type), from the gradients dw fp32
+    [T, top_k] of its weights (with the idx that it returned) and dscores fp32 of its scores, [T, E] or [E] (the same
+    for every token: a loss on the mean scores); either may be None."""
+    if _fast is not None and dlogits is None and stream is None:
+        r = _fast.route_scores_backward(logits, idx, dw, dscores, scoring, renormalize, scale)
+        if r is not None:
+            return _done("moe_route_scores_backward", r)
+    pl, bf16, T, E, how = _logits_args(logits, scoring)
+    if dw is not None and (idx is None or idx.dim() != 2):
+        raise ValueError("dw needs the idx [T, top_k] of its experts")
+    k = idx.shape[1] if dw is not None else 1
+    _fit(top_k=k)
+    pi = _opt(idx if dw is not None else None, torch.int32, (T, k), "idx")
+    pw = _opt(dw, torch.float32, (T, k), "dw")
+    per_token = dscores is not None and dscores.dim() == 2
+    ps = _opt(dscores, torch.float32, (T, E) if per_token else (E,), "dscores")
+    given = dlogits
+    dlogits = _out(dlogits, (T, E), logits.dtype, logits.device, stream, "dlogits")
+    _call("moe_route_scores_backward", pl, bf16, pi, pw, ps, int(per_token), T, E, k, how, int(bool(renormalize)), scale,
+          dlogits.data_ptr(), _stream(stream))
+    _wrote(given)
+    return dlogits
+
+
+def _drop_args(p, seed, offset, offset_tensor):
+    """p, seed, offset and the address of the offset on the device."""
+    if not 0 <= seed < 2 ** 64:
+        raise ValueError(f"seed = {seed} outside [0, 2^64)")
+    if not -2 ** 63 <= offset < 2 ** 63:
+        raise ValueError(f"offset = {offset} does not fit 64 bits")
+    if offset_tensor is None:
+        return p, seed, offset, None
+    return p, seed, offset, _arg(offset_tensor, torch.int64, (1,), "offset_tensor")
+
+
+def dropout(x, p: float, seed: int, offset: int = 0, offset_tensor=None, residual=None, out=None, stream=None):
+    """residual + x with elements zeroed with probability p (in 65536ths) and the others divided by 1 - p.  Which ones is
+    a function of seed, offset (plus the int64 in ``offset_tensor`` [1] on the device: a captured graph then replays
+    with other masks) and the element's place, so the gradient of x is the same call on the gradient of the result.
+    x and residual are bf16 or fp32; the result has residual's type, or x's, and may be written over either with
+    ``out``.  Not recorded by autograd."""
+    if _fast is not None and out is None and stream is None:
+        r = _fast.dropout(x, p, seed, offset, offset_tensor, residual)
+        if r is not None:
+            return _done("moe_dropout", r)
+    dt = _float_type(x.dtype, "x")
+    rt = dt if residual is None else _float_type(residual.dtype, "residual")
+    px, pr = _arg(x, dt, x.shape, "x"), _opt(residual, rt, x.shape, "residual")
+    drop = _drop_args(p, seed, offset, offset_tensor)
+    given = out
+    out = _out(out, x.shape, rt, x.device, stream)
+    _call("moe_dropout", px, int(dt is torch.float32), pr, int(rt is torch.float32), x.numel(), *drop, out.data_ptr(),
+          _stream(stream))
+    _wrote(given)
+    return out
+
+
+def _rows_args(x, name="x"):
+    """T, d, whether x [T, d] is fp32, and its address."""
+    dt = _float_type(x.dtype, name)
+    if x.dim() != 2:
+        raise ValueError(f"{name} must be [T, d], got {tuple(x.shape)}")
+    T, d = x.shape
+    _fit(T=T, d=d)
+    return T, d, int(dt is torch.float32), _arg(x, dt, (T, d), name)
+
+
+def layer_norm(x, weight=None, bias=None, h=None, p: float = 0.0, seed: int = 0, offset: int = 0, offset_tensor=None,
+               eps: float = 1e-5, y=None, n=None, stats=None, stream=None):
+    """Layer norm of a residual stream after a block's output was added to it:
+
+        y = x + dropout(h)                      (p, seed, offset, offset_tensor as for ``dropout``)
+        n = weight * (y - mean) / std + bias    of y as it is stored
+
+    x [T, d] bf16 or fp32 (the stream), h [T, d] bf16 or None; weight and bias fp32 [d] (None: 1 and 0).  Returns
+    (y, n, stats): y of x's type (None without h: it is x), n bf16, stats fp32 [T, 2] with mean and 1 / std for the
+    gradient, ``layer_norm_backward``.  ``y`` may be x.  Not recorded by autograd."""
+    if _fast is not None and y is None and n is None and stats is None and stream is None:
+        r = _fast.layer_norm(x, weight, bias, h, p, seed, offset, offset_tensor, eps)
+        if r is not None:
+            return _done("moe_layer_norm", r)
+    T, d, f32, px = _rows_args(x)
+    ph = _opt(h, torch.bfloat16, (T, d), "h")
+    pw, pb = _opt(weight, torch.float32, (d,), "weight"), _opt(bias, torch.float32, (d,), "bias")
+    drop = _drop_args(p, seed, offset, offset_tensor)
+    given = (y if h is not None else None, n, stats)
+    y = _out(y, (T, d), x.dtype, x.device, stream, "y") if h is not None else None
+    n = _out(n, (T, d), torch.bfloat16, x.device, stream, "n")
+    stats = _out(stats, (T, 2), torch.float32, x.device, stream, "stats")
+    _call("moe_layer_norm", px, f32, ph, pw, pb, T, d, eps, *drop, _ptr(y), n.data_ptr(), stats.data_ptr(),
+          _stream(stream))
+    _wrote(*given)
+    return y, n, stats
+
+
+LAYER_NORM_GRADS = ("x", "h", "weight", "bias")
+
+
+def layer_norm_backward(x, stats, dn, dy=None, weight=None, bias=None, want_h: bool = False, p: float = 0.0,
+                        seed: int = 0, offset: int = 0, offset_tensor=None, workspace=None, stream=None):
+    """Gradients of ``layer_norm``, as a dict by the inputs' names: x (the stream's type), h (bf16; with ``want_h``),
+    weight and bias (fp32; for those that are given, None for the others; bias' values are not read).  x is the stream
+    that was normed (the forward call's y, or its x without h) and stats what that call returned; dn bf16 and dy (the
+    stream's type, or None for zero) [T, d]; p, seed, offset and offset_tensor as in the forward call."""
+    if _fast is not None and workspace is None and stream is None:
+        r = _fast.layer_norm_backward(x, stats, dn, dy, weight, bias, want_h, p, seed, offset, offset_tensor)
+        if r is not None:
+            return dict(zip(LAYER_NORM_GRADS, _done("moe_layer_norm_backward", r)))
+    T, d, f32, px = _rows_args(x)
+    ps, pn = _arg(stats, torch.float32, (T, 2), "stats"), _arg(dn, torch.bfloat16, (T, d), "dn")
+    py, pw = _opt(dy, x.dtype, (T, d), "dy"), _opt(weight, torch.float32, (d,), "weight")
+    _opt(bias, torch.float32, (d,), "bias")
+    drop = _drop_args(p, seed, offset, offset_tensor)
+    if workspace is None:
+        workspace = _empty((_layer_norm_workspace(T, d),), torch.uint8, x.device, stream)
+    g = dict.fromkeys(LAYER_NORM_GRADS)
+    g["x"] = _empty((T, d), x.dtype, x.device, stream)
+    if want_h:
+        g["h"] = _empty((T, d), torch.bfloat16, x.device, stream)
+    for name, t in (("weight", weight), ("bias", bias)):
+        if t is not None:
+            g[name] = _empty((d,), torch.float32, x.device, stream)
+    _call("moe_layer_norm_backward", px, f32, ps, pn, py, pw, T, d, *drop, g["x"].data_ptr(), _ptr(g["h"]),
+          _ptr(g["weight"]), _ptr(g["bias"]), *_scratch(workspace), _stream(stream))
+    return g
+
+
+@functools.lru_cache(maxsize=4096)
+def _layer_norm_workspace(T: int, d: int) -> int:
+    return int(load().moe_layer_norm_backward_workspace_size(T, d))
+
+
+def _ids_args(ids):
+    """The ids' address, whether they are int64, and their number."""
+    if ids.dtype not in (torch.int32, torch.int64):
+        raise ValueError(f"ids must be int32 or int64, got {ids.dtype}")
+    _fit(ids=ids.numel())
+    return _arg(ids, ids.dtype, ids.shape, "ids"), int(ids.dtype is torch.int64), ids.numel()
+
+
+def embed(ids, table, scale: float = 1.0, out=None, out_dtype=None, status=None, stream=None):
+    """scale * table[ids]: [*ids.shape, d] of ``out_dtype`` (bf16 or fp32; None: the table's type) from the table [V, d]
+    bf16 or fp32 and ids int32 or int64 of any shape.  An id outside [0, V) gives a row of zeros and sets
+    STATUS_BAD_TOKEN in ``status``.  Not recorded by autograd: the gradient is ``embed_backward``."""
+    if _fast is not None and out is None and stream is None:
+        r = _fast.embed(ids, table, scale, out_dtype is torch.float32 if out_dtype in _FLOATS else out_dtype, status)
+        if r is not None:
+            return _done("moe_embed", r)
+    V, d, f32, pt = _rows_args(table, "table")
+    pi, i64, T = _ids_args(ids)
+    out_dtype = _float_type(out.dtype if out is not None else out_dtype or table.dtype, "out")
+    given = out
+    out = _out(out, (*ids.shape, d), out_dtype, table.device, stream)
+    _call("moe_embed", pi, i64, pt, f32, T, V, d, scale, out.data_ptr(), int(out_dtype is torch.float32), _word(status),
+          _stream(stream))
+    _wrote(given)
+    return out
+
+
+@functools.lru_cache(maxsize=4096)
+def embed_backward_workspace_size(T: int, V: int, d: int) -> int:
+    """Bytes of workspace of ``embed_backward`` for T tokens."""
+    _fit(T=T, V=V, d=d)
+    return int(load().moe_embed_backward_workspace_size(T, V, d))
+
+
+def embed_backward(ids, dy, V: int, scale: float = 1.0, out=None, out_dtype=torch.float32, accumulate: bool = False,
+                   workspace=None, status=None, stream=None):
+    """Gradient of ``embed``'s table [V, d]: row v is scale times the sum of the rows of dy [*ids.shape, d] (bf16 or
+    fp32) whose id is v, zero where no id is; fp32 or bf16, or added to an fp32 ``out`` with ``accumulate``.  Summed in
+    fp32 in a fixed order.  Ids outside [0, V) are left out (STATUS_BAD_TOKEN in ``status``)."""
+    if _fast is not None and workspace is None and stream is None:
+        dtype = out_dtype if out is None else out.dtype
+        if dtype in _FLOATS:
+            r = _fast.embed_backward(ids, dy, V, scale, out, dtype is torch.float32, accumulate, status)
+            if r is not None:
+                return _done("moe_embed_backward", r)
+    pi, i64, T = _ids_args(ids)
+    dt = _float_type(dy.dtype, "dy")
+    if dy.dim() != ids.dim() + 1:
+        raise ValueError(f"dy must be [*ids.shape, d], got {tuple(dy.shape)} for ids {tuple(ids.shape)}")
+    d = dy.shape[-1]
+    _fit(V=V, d=d)
+    py = _arg(dy, dt, (*ids.shape, d), "dy")
+    if accumulate and out is None:
+        raise ValueError("accumulate adds to out: give out")
+    if V < 1:
+        raise ValueError(f"V = {V} must be at least 1")
+    out_dtype = _float_type(out.dtype if out is not None else out_dtype, "out")
+    given = out
+    out = _out(out, (V, d), out_dtype, dy.device, stream)
+    if workspace is None:
+        need = embed_backward_workspace_size(T, V, d)
+        if need:
+            workspace = _empty((need,), torch.uint8, dy.device, stream)
+    _call("moe_embed_backward", pi, i64, py, int(dt is torch.float32), T, V, d, scale, out.data_ptr(),
+          int(out_dtype is torch.float32), int(bool(accumulate)), *_scratch(workspace), _word(status), _stream(stream))
+    _wrote(given)
+    return out

@@ -273,7 +273,7 @@ struct EmbedArgs {
     int32_t* status;
 };
 cudaError_t launch_embed(const EmbedArgs& a, cudaStream_t s);
-size_t embed_backward_workspace(int T, int d);
+size_t embed_backward_workspace(int T, int V, int d);
 cudaError_t launch_embed_backward(const EmbedArgs& a, void* workspace, cudaStream_t s);
 cudaError_t launch_route_scores(const void* logits, bool bf16, const float* bias, int T, int E, int k, bool sigmoid,
                                 int n_group, int topk_group, bool renorm, float scale, int32_t* idx, float* w,

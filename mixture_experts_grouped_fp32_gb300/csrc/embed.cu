@@ -6,13 +6,18 @@
 // The gradient sorts the tokens by id (a stable counting sort) and adds up runs of equal ids: no atomic decides an
 // order, the same result on every run.
 //
-//   sort   The vocabulary is cut into slices, one for a block.  Every block reads all ids (T values from the L2, which
-//          costs less than a pass between blocks would), counts those below its slice and, warp by warp, those of each id
-//          in it; sums over the warps and ids then give each warp and id the place of its next token, and a second
-//          reading puts the tokens there.  Rows of the slice that no token has are zeroed in the same launch.
-//   sum    A group of threads takes a piece of kPiece sorted tokens and the columns eight a thread: runs that begin and
-//          end in it are written, the sums of those that go on beyond an end of it are left for
-//   join   which adds the pieces' sums of such a run in order.
+//   sort   The vocabulary is dealt out to the blocks.  Every block reads all ids (T values from the L2, which costs less
+//          than a pass between blocks would), counts those of the blocks before it and, warp by warp, those of each id of
+//          its own; sums over the warps and ids then give each warp and id the place of its next token, and a second
+//          reading puts the tokens there.
+//   sum    The sorted tokens are cut into pieces.  A group of threads takes a piece (and the columns eight a thread): it
+//          adds up the runs that begin in it, and follows the last one beyond the piece's end.  A run that covers a
+//          whole piece is long: its pieces' sums are left for the join.  Other blocks of the same launch zero the rows
+//          that no token has.
+//   join   adds the pieces' sums of a long run in order.
+//
+// Rows are taken in units of G = 8, 4, 2 or 1 elements, as width and addresses are aligned; neighbouring threads hold
+// neighbouring units.
 #include <algorithm>
 
 #include "stack_ops.cuh"
@@ -20,14 +25,108 @@
 namespace moe {
 namespace {
 
+// Where a thread's eight elements of a row lie: units of G, `step` elements apart, the first at `at`, `count` of them
+// in the row (tx threads to a stretch of 8 tx columns).
+template <int G>
+struct Columns {
+    int at, step, count;
+    __device__ __forceinline__ Columns(int chunk, int tx, int x, int d) {
+        at = chunk * 8 * tx + x * G;
+        step = tx * G;
+        count = min(8 / G, max(0, (d - at + step - 1) / step));
+    }
+};
+// A thread's elements of a row as they were loaded: a register for each load's word, so that nothing waits for a load
+// before the values are used.
+template <typename X, int G>
+struct Units;
+template <int G>
+struct Units<__nv_bfloat16, G> {
+    uint32_t w[G == 1 ? 8 : 4];
+    __device__ __forceinline__ void load(int j, const __nv_bfloat16* q) {
+        if constexpr (G == 8) {
+            const uint4 u = __ldcs(reinterpret_cast<const uint4*>(q));
+            w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
+        } else if constexpr (G == 4) {
+            const uint2 u = __ldcs(reinterpret_cast<const uint2*>(q));
+            w[2 * j] = u.x, w[2 * j + 1] = u.y;
+        } else if constexpr (G == 2) {
+            w[j] = __ldcs(reinterpret_cast<const unsigned int*>(q));
+        } else {
+            w[j] = __ldcs(reinterpret_cast<const unsigned short*>(q));
+        }
+    }
+    __device__ __forceinline__ Vec8 values() const {
+        Vec8 v;
+        if constexpr (G == 1) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v.v[j] = __uint_as_float(w[j] << 16);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) unpack_bf16x2(w[j], v.v[2 * j], v.v[2 * j + 1]);
+        }
+        return v;
+    }
+};
+template <int G>
+struct Units<float, G> {
+    Vec8 v;
+    __device__ __forceinline__ void load(int j, const float* q) {
+        if constexpr (G == 8) {
+            v = load8(q, 0);
+        } else if constexpr (G == 4) {
+            const float4 u = __ldcs(reinterpret_cast<const float4*>(q));
+            v.v[4 * j] = u.x, v.v[4 * j + 1] = u.y, v.v[4 * j + 2] = u.z, v.v[4 * j + 3] = u.w;
+        } else if constexpr (G == 2) {
+            const float2 u = __ldcs(reinterpret_cast<const float2*>(q));
+            v.v[2 * j] = u.x, v.v[2 * j + 1] = u.y;
+        } else {
+            v.v[j] = __ldcs(q);
+        }
+    }
+    __device__ __forceinline__ Vec8 values() const { return v; }
+};
+// Without a branch, so that the loads of several rows are under way together: in place of a unit behind the row the last
+// one is loaded again (count >= 1), and not written anywhere.
+template <int G, typename X>
+__device__ __forceinline__ void fetch(Units<X, G>& r, const X* p, const Columns<G>& c) {
+#pragma unroll
+    for (int j = 0; j < 8 / G; ++j) r.load(j, p + min(j, c.count - 1) * c.step);
+}
+template <int G>
+__device__ __forceinline__ void write(__nv_bfloat16* p, const Vec8& v, const Columns<G>& c) {
+#pragma unroll
+    for (int j = 0; j < 8 / G; ++j)
+        if (j < c.count) {
+            __nv_bfloat16* q = p + j * c.step;
+            if constexpr (G == 8) store8(q, 0, v);
+            else if constexpr (G == 4)
+                *reinterpret_cast<uint2*>(q) = make_uint2(pack_bf16x2(v.v[4 * j], v.v[4 * j + 1]), pack_bf16x2(v.v[4 * j + 2], v.v[4 * j + 3]));
+            else if constexpr (G == 2) *reinterpret_cast<uint32_t*>(q) = pack_bf16x2(v.v[2 * j], v.v[2 * j + 1]);
+            else put(q, v.v[j]);
+        }
+}
+template <int G>
+__device__ __forceinline__ void write(float* p, const Vec8& v, const Columns<G>& c) {
+#pragma unroll
+    for (int j = 0; j < 8 / G; ++j)
+        if (j < c.count) {
+            float* q = p + j * c.step;
+            if constexpr (G == 8) store8(q, 0, v);
+            else if constexpr (G == 4)
+                *reinterpret_cast<float4*>(q) = make_float4(v.v[4 * j], v.v[4 * j + 1], v.v[4 * j + 2], v.v[4 * j + 3]);
+            else if constexpr (G == 2) *reinterpret_cast<float2*>(q) = make_float2(v.v[2 * j], v.v[2 * j + 1]);
+            else *q = v.v[j];
+        }
+}
+
 template <typename I>
-__device__ __forceinline__ int id_at(const I* ids, size_t t, int V) {  // -1: none of the table
-    const long long v = static_cast<long long>(__ldg(ids + t));
+__device__ __forceinline__ int id_of(I v, int V) {  // -1: none of the table
     return v >= 0 && v < V ? static_cast<int>(v) : -1;
 }
 
-// blockDim.x threads to a row's vectors, blockDim.y rows side by side.
-template <typename I, typename X, typename O, bool ALIGNED>
+// blockDim.x threads to a row's columns, blockDim.y rows side by side, two stretches of columns a thread.
+template <typename I, typename X, typename O, int G>
 __global__ void __launch_bounds__(256)
 embed_kernel(const I* __restrict__ ids, const X* __restrict__ table, int T, int V, int d, float scale,
              O* __restrict__ out, int32_t* status) {
@@ -35,42 +134,50 @@ embed_kernel(const I* __restrict__ ids, const X* __restrict__ table, int T, int 
     pdl_trigger();
     const size_t t = static_cast<size_t>(blockIdx.x) * blockDim.y + threadIdx.y;
     if (t >= static_cast<size_t>(T)) return;
-    const int v = id_at(ids, t, V), d8 = (d + 7) / 8;
+    const int v = id_of<I>(__ldg(ids + t), V);
     if (v < 0 && threadIdx.x == 0 && blockIdx.y == 0) flag_status(status, MOE_STATUS_BAD_TOKEN);
-    const int per = 2 * blockDim.x, c0 = blockIdx.y * per + threadIdx.x;
-    Raw8<X> r[2];
+    const Columns<G> c[2] = {Columns<G>(2 * blockIdx.y, blockDim.x, threadIdx.x, d),
+                             Columns<G>(2 * blockIdx.y + 1, blockDim.x, threadIdx.x, d)};
+    Units<X, G> r[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+        if (c[k].count > 0) fetch<G>(r[k], table + static_cast<size_t>(max(v, 0)) * d + c[k].at, c[k]);
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-        const int c = c0 + k * blockDim.x;
-        r[k] = Raw8<X>{};
-        if (c < d8 && v >= 0) fetch_raw<ALIGNED>(r[k], table + static_cast<size_t>(v) * d + 8 * c, min(8, d - 8 * c));
-    }
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        const int c = c0 + k * blockDim.x;
-        if (c >= d8) break;
-        Vec8 o = values(r[k]);
+        if (c[k].count == 0) break;
+        Vec8 o = r[k].values();
 #pragma unroll
         for (int j = 0; j < 8; ++j) o.v[j] = v >= 0 ? o.v[j] * scale : 0.0f;
-        put8<ALIGNED>(out + t * d + 8 * c, o, min(8, d - 8 * c));
+        write<G>(out + t * d + c[k].at, o, c[k]);
     }
 }
 
 // ---------------------------------------------------------------------------------------------
 // The gradient.
 // ---------------------------------------------------------------------------------------------
-constexpr int kPiece = 32;         // sorted tokens of a piece
+constexpr int kMostPiece = 32;
 constexpr int kSortWarps = 32;
 constexpr int kMostSlice = 1600;   // ids of a slice: 32 warps' counts and the places fill 211 KB of shared memory
 constexpr int kSms = 152;          // of a GB300
+constexpr int kThreads = 256;      // of a block of the sums, at the most
+constexpr int kZeroWords = 16;     // 16-byte words that a thread of the other blocks looks at
 
-int slices_of(int V) { return std::max(std::min(V, kSms), (V - 1) / kMostSlice + 1); }
+// log2 of the sort's blocks: 128 of them (the time is that of reading all ids, whatever their number), more for
+// vocabularies whose slices would be too large, fewer where there are fewer ids.
+int slice_bits(int V) {
+    int bits = 7;
+    while ((V - 1) >> bits >= kMostSlice) ++bits;
+    while (bits > 0 && (1 << bits) > V) --bits;
+    return bits;
+}
 
 struct Workspace {
-    int32_t* found;  // tokens with an id of the table
-    int32_t* order;  // [T] tokens sorted by id, then by place
-    int32_t* id;     // [T] their ids
-    float* part;     // [pieces, 2, d] sums of the runs that begin before a piece, and that go on behind it
+    int32_t* found;    // tokens with an id of the table
+    int32_t* order;    // [T] tokens sorted by id, then by place
+    int32_t* id;       // [T] their ids
+    float* part;       // [pieces, 2, d] sums of the long runs that begin before a piece, and that begin in it
+    uint8_t* present;  // [V] whether a token has the id
+    int32_t* more;     // [pieces] of the long run that begins in a piece: how many pieces it goes on for, else 0
 };
 
 // Sum over the block's earlier threads and the block's total (1024 threads).
@@ -97,40 +204,49 @@ __device__ __forceinline__ int block_scan(int v, int* warp_sums, int* total) {
     return before + inc - v;
 }
 
-template <typename I, typename O, bool ALIGNED>
+// An id as 32 bits: one outside [0, 2^31) as 2^32 - 1.
+__device__ __forceinline__ uint32_t word_of(int32_t v) { return static_cast<uint32_t>(v) | static_cast<uint32_t>(v >> 31); }
+__device__ __forceinline__ uint32_t word_of(long long v) { return v >> 31 == 0 ? static_cast<uint32_t>(v) : ~0u; }
+
+// Block r of 2^bits takes the ids with v mod 2^bits = r (a vocabulary's frequent tokens are often neighbours: like this
+// they are spread), counted as v >> bits; the order of the ids is that of (v mod 2^bits, v >> bits).
+template <typename I>
 __global__ void __launch_bounds__(1024)
-embed_sort_kernel(const I* __restrict__ ids, int T, int V, int d, int slice, bool zero, Workspace ws, O* __restrict__ out,
-                  int32_t* status) {
-    extern __shared__ int32_t counts[];  // [warps][slice], then [slice] tokens of an id
+embed_sort_kernel(const I* __restrict__ ids, int T, int V, int slice, int bits, int piece, Workspace ws, int32_t* status) {
+    extern __shared__ int32_t counts[];  // [warps][slice]
     __shared__ int32_t warp_sums[32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int lo = static_cast<int>(min(static_cast<long long>(V), static_cast<long long>(blockIdx.x) * slice));
-    const int n = min(slice, V - lo);
+    const uint32_t r = blockIdx.x, vocabulary = V, blocks = gridDim.x;
+    const int n = r < vocabulary ? static_cast<int>((vocabulary - 1 - r) >> bits) + 1 : 0;
     int32_t* mine = counts + warp * slice;
-    int32_t* totals = counts + kSortWarps * slice;
     for (int i = tid; i < kSortWarps * slice; i += 1024) counts[i] = 0;
     pdl_wait();
     pdl_trigger();
     __syncthreads();
-    // A warp's tokens: a run of them, 32 at a time.
-    const size_t per = (static_cast<size_t>(T) + kSortWarps * 32 - 1) / (kSortWarps * 32) * 32;
-    const size_t t0 = warp * per, t1 = min(t0 + per, static_cast<size_t>(T));
+    // A warp's tokens: a run of them, 32 at a time and the loads of eight times 32 together.
+    const unsigned per = (static_cast<unsigned>(T) + kSortWarps * 32 - 1) / (kSortWarps * 32) * 32;
+    const unsigned t0 = min(warp * per, static_cast<unsigned>(T)), t1 = min(t0 + per, static_cast<unsigned>(T));
+    constexpr int kAhead = 8;
+    auto each = [&](auto&& work) {  // work(token, its id as a word, the block that takes it)
+        const I* p = ids + t0 + lane;
+        for (unsigned t = t0; t < t1; t += 32 * kAhead, p += 32 * kAhead) {
+            const int left = t1 - t;  // tokens
+            uint32_t v[kAhead];
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) v[u] = 32 * u + lane < left ? word_of(__ldg(p + 32 * u)) : vocabulary;
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u)
+                if (32 * u < left) work(t + 32 * u + lane, v[u], v[u] < vocabulary ? v[u] & (blocks - 1) : blocks);
+        }
+    };
     int below = 0;
     bool bad = false;
-    for (size_t t = t0; t < t1; t += 32) {
-        const bool there = t + lane < t1;
-        const int v = there ? id_at(ids, t + lane, V) : V;
-        bad |= v < 0;
-        below += v >= 0 && v < lo;
-        const int b = v - lo;
-        const bool in = v >= 0 && b >= 0 && b < n;
-        const unsigned hits = __ballot_sync(0xffffffffu, in);
-        if (hits == 0) continue;
-        const unsigned same = __match_any_sync(0xffffffffu, in ? b : -1);
-        if (in && lane == __ffs(same) - 1) mine[b] += __popc(same);
-        __syncwarp();
-    }
-    if (bad && blockIdx.x == 0) flag_status(status, MOE_STATUS_BAD_TOKEN);
+    each([&](unsigned t, uint32_t v, uint32_t block) {
+        if (r == 0) bad |= block == blocks && t < t1;
+        below += block < r;
+        if (block == r) atomicAdd(mine + (v >> bits), 1);
+    });
+    if (bad) flag_status(status, MOE_STATUS_BAD_TOKEN);
     __syncthreads();
     int all_below, own;
     block_scan(below, warp_sums, &all_below);
@@ -139,187 +255,285 @@ embed_sort_kernel(const I* __restrict__ ids, int T, int V, int d, int slice, boo
     int sum = 0;
     for (int b = b0; b < b1; ++b) {
         int c = 0;
+#pragma unroll 8
         for (int w = 0; w < kSortWarps; ++w) c += counts[w * slice + b];
-        totals[b] = c;
+        ws.present[(static_cast<size_t>(b) << bits) + r] = c != 0;
         sum += c;
     }
     int at = all_below + block_scan(sum, warp_sums, &own);
-    for (int b = b0; b < b1; ++b)
-        for (int w = 0; w < kSortWarps; ++w) {
-            const int c = counts[w * slice + b];
-            counts[w * slice + b] = at;
-            at += c;
-        }
     if (blockIdx.x == gridDim.x - 1 && tid == 0) *ws.found = all_below + own;
+    if (own == 0) return;
+    // (a piece's word is that of the block that holds its last token: a run that goes on behind the piece holds it)
+    for (int q = all_below / piece + tid; q < (all_below + own) / piece; q += 1024) ws.more[q] = 0;
     __syncthreads();
-    if (own > 0)
-        for (size_t t = t0; t < t1; t += 32) {
-            const bool there = t + lane < t1;
-            const int v = there ? id_at(ids, t + lane, V) : V;
-            const int b = v - lo;
-            const bool in = v >= 0 && b >= 0 && b < n;
-            const unsigned hits = __ballot_sync(0xffffffffu, in);
-            if (hits == 0) continue;
-            const unsigned same = __match_any_sync(0xffffffffu, in ? b : -1);
-            if (in) {
-                const int place = mine[b] + __popc(same & ((1u << lane) - 1));
-                ws.order[place] = static_cast<int32_t>(t + lane);
-                ws.id[place] = v;
+    if (sum > 0)
+        for (int b = b0; b < b1; ++b) {
+            const int start = at;
+#pragma unroll 8
+            for (int w = 0; w < kSortWarps; ++w) {
+                const int c = counts[w * slice + b];
+                counts[w * slice + b] = at;
+                at += c;
             }
-            __syncwarp();
-            if (in && lane == __ffs(same) - 1) mine[b] += __popc(same);
-            __syncwarp();
+            const int first = start / piece;
+            if (at - (start + piece - 1) / piece * piece >= piece && (at - 1) / piece > first)
+                ws.more[first] = (at - 1) / piece - first;
         }
-    if (!zero) return;
-    const int d8 = (d + 7) / 8;
-    for (int b = warp; b < n; b += kSortWarps) {  // a warp to a row
-        if (totals[b]) continue;
-        O* row = out + static_cast<size_t>(lo + b) * d;
-        for (int c = lane; c < d8; c += 32) put8<ALIGNED>(row + 8 * c, Vec8{}, min(8, d - 8 * c));
-    }
+    __syncthreads();
+    each([&](unsigned t, uint32_t v, uint32_t block) {
+        const bool in = block == r;
+        unsigned hits = __ballot_sync(0xffffffffu, in);
+        if (hits == 0) return;
+        const uint32_t q = v >> bits;
+        unsigned same = 0;  // lanes with this lane's id: one distinct id after another, seldom more than one or two
+        while (hits) {
+            const uint32_t one = __shfl_sync(0xffffffffu, v, __ffs(hits) - 1);
+            const unsigned m = __ballot_sync(0xffffffffu, v == one);
+            if (v == one) same = m;
+            hits &= ~m;
+        }
+        if (in) {
+            const int place = mine[q] + __popc(same & ((1u << lane) - 1));
+            ws.order[place] = static_cast<int32_t>(t);
+            ws.id[place] = static_cast<int32_t>(v);
+        }
+        __syncwarp();
+        if (in && lane == __ffs(same) - 1) mine[q] += __popc(same);
+        __syncwarp();
+    });
 }
 
-__device__ __forceinline__ void red_add4(float* p, float a, float b, float c, float e) {
-    asm volatile("red.relaxed.gpu.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(p), "f"(a), "f"(b), "f"(c), "f"(e)
-                 : "memory");
+// One addition to an element and call: no order matters.
+template <int G>
+__device__ __forceinline__ void add_to(float* p, const Vec8& v, const Columns<G>& c) {
+    constexpr int W = G < 4 ? G : 4;  // elements of one instruction
+#pragma unroll
+    for (int j = 0; j < 8 / W; ++j)
+        if (j * W / G < c.count) {
+            float* q = p + (j * W / G) * c.step + (j * W) % G;
+            const float* x = v.v + j * W;
+            if constexpr (W == 4)
+                asm volatile("red.relaxed.gpu.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(q), "f"(x[0]), "f"(x[1]),
+                             "f"(x[2]), "f"(x[3])
+                             : "memory");
+            else if constexpr (W == 2)
+                asm volatile("red.relaxed.gpu.global.add.v2.f32 [%0], {%1, %2};" ::"l"(q), "f"(x[0]), "f"(x[1]) : "memory");
+            else
+                asm volatile("red.relaxed.gpu.global.add.f32 [%0], %1;" ::"l"(q), "f"(x[0]) : "memory");
+        }
 }
-
-template <bool ALIGNED, typename O>
-__device__ __forceinline__ void finish(O* p, const Vec8& v, float scale, int count, bool add) {
+template <int G, typename O>
+__device__ __forceinline__ void finish(O* p, const Vec8& v, float scale, const Columns<G>& c, bool add) {
     Vec8 o;
 #pragma unroll
     for (int j = 0; j < 8; ++j) o.v[j] = v.v[j] * scale;
     if constexpr (sizeof(O) == 4) {
-        if (add) {  // one addition to an element and call: no order matters
-            if (ALIGNED) {
-                red_add4(p, o.v[0], o.v[1], o.v[2], o.v[3]);
-                red_add4(p + 4, o.v[4], o.v[5], o.v[6], o.v[7]);
-            } else {
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    if (j < count) atomicAdd(p + j, o.v[j]);
-            }
-            return;
-        }
+        if (add) return add_to<G>(p, o, c);
     }
-    put8<ALIGNED>(p, o, count);
+    write<G>(p, o, c);
 }
 
-template <typename X, typename O, bool ALIGNED>
-__global__ void __launch_bounds__(256)
-embed_sum_kernel(const X* __restrict__ dy, int d, float scale, bool add, Workspace ws, O* __restrict__ out) {
-    const int d8 = (d + 7) / 8, c = blockIdx.y * blockDim.x + threadIdx.x;
+struct SumArgs {
+    int V, d, piece, pieces, chunks;  // tokens of a piece, pieces of the T tokens, stretches of columns
+    int sum_blocks;                   // blocks that sum; the others zero
+    float scale;
+    bool add;
+};
+
+template <typename X, typename O, int G>
+__global__ void __launch_bounds__(kThreads)
+embed_sum_kernel(const X* __restrict__ dy, SumArgs a, Workspace ws, O* __restrict__ out) {
+    __shared__ int32_t s_id[32 * (2 * kMostPiece + 1)], s_order[32 * 2 * kMostPiece];
+    const int d = a.d, P = a.piece, tx = blockDim.x, x = threadIdx.x;
     pdl_wait();
     pdl_trigger();
-    const int found = __ldg(ws.found);
-    const long long piece = static_cast<long long>(blockIdx.x) * blockDim.y + threadIdx.y;
-    const long long p0 = piece * kPiece;
-    if (p0 >= found || c >= d8) return;
-    const int len = static_cast<int>(min(static_cast<long long>(kPiece), found - p0));
-    const int count = min(8, d - 8 * c);
-    const int32_t *order = ws.order + p0, *id = ws.id + p0;
-    const int before = p0 > 0 ? __ldg(id - 1) : -1, behind = p0 + len < found ? __ldg(id + len) : -1;
-    float* part = ws.part + static_cast<size_t>(piece) * 2 * d + 8 * c;
-    Vec8 sum{};
-    int begun = 0;  // where in the piece the run began
-    constexpr int kAhead = 8;
-    for (int i0 = 0; i0 < len; i0 += kAhead) {
-        Raw8<X> r[kAhead];
-        int v[kAhead + 1];
+    if (blockIdx.x >= static_cast<unsigned>(a.sum_blocks)) {
+        // Rows without a token: the table's 16-byte words one after another, element by element where a word lies in
+        // more than one row (or the table is not aligned for it).
+        constexpr int E = 16 / sizeof(O);
+        const int threads = tx * blockDim.y, tid = threadIdx.y * tx + x;
+        const unsigned long long w0 = static_cast<unsigned long long>(blockIdx.x - a.sum_blocks) * (kZeroWords * threads) + tid;
+        const unsigned long long e0 = w0 * E;
+        long long row = static_cast<long long>(e0 / d);
+        int col = static_cast<int>(e0 - static_cast<unsigned long long>(row) * d);
+        const int step_rows = threads * E / d, step_cols = threads * E % d;
+        const bool words = (reinterpret_cast<uintptr_t>(out) & 15) == 0;
+        constexpr int kBatch = 8;  // words whose rows are looked up together
+#pragma unroll 1
+        for (int k = 0; k < kZeroWords; k += kBatch) {
+            long long rows[kBatch];
+            int cols[kBatch];
+            bool zero[kBatch];
 #pragma unroll
-        for (int u = 0; u < kAhead; ++u) {
-            v[u] = i0 + u < len ? __ldg(id + i0 + u) : -1;
-            r[u] = Raw8<X>{};
-            if (i0 + u < len)
-                fetch_raw<ALIGNED>(r[u], dy + static_cast<size_t>(__ldg(order + i0 + u)) * d + 8 * c, count);
+            for (int u = 0; u < kBatch; ++u) {
+                rows[u] = row;
+                cols[u] = col;
+                zero[u] = words && row < a.V && col + E <= d && !__ldg(ws.present + row);
+                row += step_rows;
+                col += step_cols;
+                if (col >= d) col -= d, ++row;
+            }
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) {
+                O* q = out + static_cast<size_t>(rows[u]) * d + cols[u];
+                if (zero[u]) {
+                    *reinterpret_cast<uint4*>(q) = make_uint4(0, 0, 0, 0);
+                } else if (rows[u] < a.V && !(words && cols[u] + E <= d)) {
+                    for (int i = 0; i < E && rows[u] < a.V; ++i) {
+                        if (!__ldg(ws.present + rows[u])) put(q + i, 0.0f);
+                        if (++cols[u] == d) cols[u] = 0, ++rows[u];
+                    }
+                }
+            }
         }
-        v[kAhead] = i0 + kAhead < len ? __ldg(id + i0 + kAhead) : -1;
+        return;
+    }
+    const int chunk = blockIdx.x % a.chunks;
+    const long long piece = static_cast<long long>(blockIdx.x / a.chunks) * blockDim.y + threadIdx.y, p0 = piece * P;
+    const int found = __ldg(ws.found);
+    int32_t *id = s_id + threadIdx.y * (2 * P + 1), *order = s_order + threadIdx.y * 2 * P;
+    // Ids from the token before the piece to the end of the next piece (-1 before all and behind all).
+    for (int k = x; k <= 2 * P; k += tx) {
+        const long long at = p0 - 1 + k;
+        id[k] = at >= 0 && at < found ? __ldg(ws.id + at) : -1;
+        if (k < 2 * P) order[k] = at + 1 < found ? __ldg(ws.order + at + 1) : 0;
+    }
+    const int two_back = p0 >= P && p0 < found ? __ldg(ws.id + p0 - P) : -1;  // the first of the piece before
+    __syncthreads();
+    const Columns<G> c(chunk, tx, x, d);
+    if (p0 >= found || c.count == 0) return;
+    const int len = static_cast<int>(min(static_cast<long long>(P), found - p0));
+    ++id;  // id[-1]: before the piece
+    auto end_of_run = [&](int v, int from, int to) {  // (tokens of an id are neighbours)
+        while (from < to) {
+            const int m = (from + to) / 2;
+            if (id[m] == v) from = m + 1;
+            else to = m;
+        }
+        return from;
+    };
+    // The run that comes from before: its share here if it is long, else the piece before has it all.
+    const int head = id[0], tail = id[len - 1];
+    const bool from_before = id[-1] == head;
+    const bool head_long = from_before && (two_back == head || (len == P && tail == head));
+    const int begin = from_before && !head_long ? end_of_run(head, 0, len) : 0;
+    // The run that goes on behind the piece: all of it, unless it is long.
+    int end = len;
+    bool tail_long = false;
+    if (len == P && id[P] == tail) {
+        if (head == tail || id[2 * P - 1] == tail) tail_long = true;
+        else end = end_of_run(tail, P, 2 * P);
+    }
+    float* part = ws.part + static_cast<size_t>(piece) * 2 * d + c.at;
+    Vec8 sum{};
+    constexpr int kAhead = sizeof(X) == 4 || G <= 2 ? 4 : 8;
+    for (int i0 = begin; i0 < end; i0 += kAhead) {
+        Units<X, G> r[kAhead];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u)  // (behind the end the last row again)
+            fetch<G>(r[u], dy + static_cast<size_t>(order[min(i0 + u, end - 1)]) * d + c.at, c);
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
             const int i = i0 + u;
-            if (i >= len) break;
-            const Vec8 x = values(r[u]);
+            if (i >= end) break;
+            const Vec8 row = r[u].values();
 #pragma unroll
-            for (int j = 0; j < 4; ++j) sum.set(j, add2(sum.pair(j), x.pair(j)));
-            const bool last = i + 1 == len;
-            if (!last && v[u + 1] == v[u]) continue;
-            if (begun == 0 && v[u] == before) put8<ALIGNED>(part, sum, count);
-            else if (last && v[u] == behind) put8<ALIGNED>(part + d, sum, count);
-            else finish<ALIGNED>(out + static_cast<size_t>(v[u]) * d + 8 * c, sum, scale, count, add);
+            for (int j = 0; j < 4; ++j) sum.set(j, add2(sum.pair(j), row.pair(j)));
+            const int v = id[i];
+            if (i + 1 < end && id[i + 1] == v) continue;
+            if (head_long && v == head) write<G>(part, sum, c);
+            else if (tail_long && v == tail) write<G>(part + d, sum, c);
+            else finish<G>(out + static_cast<size_t>(v) * d + c.at, sum, a.scale, c, a.add);
             sum = Vec8{};
-            begun = i + 1;
         }
     }
 }
 
-// Block (x, y): the run that goes on behind piece x; eight groups of 32 threads take a share of its pieces each.
-template <typename O, bool ALIGNED>
-__global__ void __launch_bounds__(256)
-embed_join_kernel(int d, float scale, bool add, Workspace ws, O* __restrict__ out) {
-    __shared__ float part[8][32][9];
-    const int d8 = (d + 7) / 8, c = blockIdx.y * 32 + threadIdx.x, g = threadIdx.y;
+// Long runs: a block takes those that begin in its kWindow pieces, kShares groups of 32 threads a share of a run's pieces
+// each.
+constexpr int kWindow = 8, kShares = 16;
+template <typename O, int G>
+__global__ void __launch_bounds__(32 * kShares) embed_join_kernel(SumArgs a, Workspace ws, O* __restrict__ out) {
+    __shared__ float share[kShares][32][9];
+    const int P = a.piece, d = a.d, g = threadIdx.y, lane = threadIdx.x;
+    const Columns<G> c(blockIdx.y, 32, lane, d);
     pdl_wait();
     pdl_trigger();
-    const int found = __ldg(ws.found);
-    const long long first = blockIdx.x, end = (first + 1) * kPiece;
-    if (end >= found) return;  // (no token behind the piece)
-    const int v = __ldg(ws.id + end);
-    if (__ldg(ws.id + end - 1) != v) return;
-    if (first > 0 && __ldg(ws.id + end - kPiece) == v && __ldg(ws.id + end - kPiece - 1) == v) return;  // begun before
-    // The run's last token, by bisection in the sorted ids.
-    long long a = end, b = found;
-    while (b - a > 1) {
-        const long long m = (a + b) / 2;
-        if (__ldg(ws.id + m) == v) a = m;
-        else b = m;
-    }
-    const long long pieces = a / kPiece - first;  // behind the first
-    const int count = min(8, d - 8 * c);
-    Vec8 sum{};
-    if (c < d8) {
-        const float* p = ws.part + static_cast<size_t>(first) * 2 * d + 8 * c;
-        const long long per = (pieces + 8) / 8, k0 = g * per, k1 = min(k0 + per, pieces + 1);
-#pragma unroll 4
-        for (long long k = k0; k < k1; ++k) {
-            Raw8<float> r;
-            fetch_raw<ALIGNED>(r, k == 0 ? p + d : p + static_cast<size_t>(k) * 2 * d, count);
-            const Vec8 x = values(r);
+    const long long found = __ldg(ws.found);
+    const long long piece = static_cast<long long>(blockIdx.x) * kWindow + lane;
+    const int goes_on = lane < kWindow && (piece + 1) * P < found ? __ldg(ws.more + piece) : 0;
+    unsigned todo = __ballot_sync(0xffffffffu, goes_on > 0);
+    while (todo) {  // (the same in all warps)
+        const int k = __ffs(todo) - 1, more = __shfl_sync(0xffffffffu, goes_on, k);
+        todo &= todo - 1;
+        const long long first = static_cast<long long>(blockIdx.x) * kWindow + k;
+        const int value = __ldg(ws.id + (first + 1) * P);
+        Vec8 sum{};
+        const float* p = ws.part + static_cast<size_t>(first) * 2 * d + c.at;
+        const int per = more / kShares + 1, k0 = g * per, k1 = c.count > 0 ? min(k0 + per, more + 1) : k0;
+#pragma unroll 8
+        for (int q = k0; q < k1; ++q) {
+            Units<float, G> r;
+            fetch<G>(r, q == 0 ? p + d : p + static_cast<size_t>(q) * 2 * d, c);
+            const Vec8 row = r.values();
 #pragma unroll
-            for (int j = 0; j < 8; ++j) sum.v[j] += x.v[j];
+            for (int j = 0; j < 8; ++j) sum.v[j] += row.v[j];
         }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) share[g][lane][j] = sum.v[j];
+        __syncthreads();
+        if (g == 0) {
+            for (int q = 1; q < kShares; ++q)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) sum.v[j] += share[q][lane][j];
+            finish<G>(out + static_cast<size_t>(value) * d + c.at, sum, a.scale, c, a.add);
+        }
+        __syncthreads();
     }
-#pragma unroll
-    for (int j = 0; j < 8; ++j) part[g][threadIdx.x][j] = sum.v[j];
-    __syncthreads();
-    if (g != 0 || c >= d8) return;
-    for (int k = 1; k < 8; ++k)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) sum.v[j] += part[k][threadIdx.x][j];
-    finish<ALIGNED>(out + static_cast<size_t>(v) * d + 8 * c, sum, scale, count, add);
 }
 
-bool vectors(int d, const void* a, const void* b) {
-    return d % 8 == 0 && ((reinterpret_cast<uintptr_t>(a) | reinterpret_cast<uintptr_t>(b)) & 15) == 0;
+// The largest unit that width and addresses allow: loads of up to 16 bytes.
+int unit_of(int d, const void* a, size_t a_size, const void* b, size_t b_size) {
+    for (int g = 8; g > 1; g /= 2)
+        if (d % g == 0 && reinterpret_cast<uintptr_t>(a) % std::min<size_t>(16, g * a_size) == 0 &&
+            reinterpret_cast<uintptr_t>(b) % std::min<size_t>(16, g * b_size) == 0)
+            return g;
+    return 1;
 }
-// Threads of a row's vectors (a power of two), so that 256 threads hold whole rows.
-int across(int vectors_of_row) {
-    int x = 8;
-    while (x < vectors_of_row && x < 256) x *= 2;
-    return x;
+// Threads of a row, eight columns each: a power of two up to 32, then the multiple of 32 that leaves fewest idle.
+int across(int eights) {
+    if (eights <= 8) return 8;
+    if (eights <= 16) return 16;
+    const int stretches = (eights + kThreads - 1) / kThreads;
+    return (eights + 32 * stretches - 1) / (32 * stretches) * 32;
 }
 constexpr size_t kAlign = 256;
 size_t up(size_t n) { return (n + kAlign - 1) / kAlign * kAlign; }
 
-template <typename I, typename X, typename O, bool ALIGNED>
+// Tokens of a piece: 32, fewer where that leaves less than three blocks of the sums to an SM (12001 tokens of 1028
+// columns: 30 us with 16, 33 with 32 or 8).
+int piece_of(int T, int d) {
+    const int d8 = (d + 7) / 8, tx = across(d8), ty = kThreads / tx, stretches = (d8 - 1) / tx + 1;
+    int piece = kMostPiece;
+    while (piece > 8 && static_cast<long long>(T) / (piece * ty) * stretches < 3 * kSms) piece /= 2;
+    return piece;
+}
+
+template <typename I, typename X, typename O, int G>
 cudaError_t forward_as(const EmbedArgs& a, cudaStream_t s) {
-    const int d8 = (a.d + 7) / 8, tx = across((d8 + 1) / 2), ty = 256 / tx;
+    const int d8 = (a.d + 7) / 8, tx = across((d8 + 1) / 2), ty = kThreads / tx;
     const dim3 grid((a.T - 1) / ty + 1, (d8 - 1) / (2 * tx) + 1);
-    return launch_k(kPdlTrain, embed_kernel<I, X, O, ALIGNED>, grid, dim3(tx, ty), 0, s, static_cast<const I*>(a.ids),
+    return launch_k(kPdlTrain, embed_kernel<I, X, O, G>, grid, dim3(tx, ty), 0, s, static_cast<const I*>(a.ids),
                     static_cast<const X*>(a.rows), a.T, a.V, a.d, a.scale, static_cast<O*>(a.out), a.status);
 }
 template <typename I, typename X, typename O>
 cudaError_t forward_io(const EmbedArgs& a, cudaStream_t s) {
-    return vectors(a.d, a.rows, a.out) ? forward_as<I, X, O, true>(a, s) : forward_as<I, X, O, false>(a, s);
+    switch (unit_of(a.d, a.rows, sizeof(X), a.out, sizeof(O))) {
+        case 8: return forward_as<I, X, O, 8>(a, s);
+        case 4: return forward_as<I, X, O, 4>(a, s);
+        case 2: return forward_as<I, X, O, 2>(a, s);
+        default: return forward_as<I, X, O, 1>(a, s);
+    }
 }
 template <typename I>
 cudaError_t forward_i(const EmbedArgs& a, cudaStream_t s) {
@@ -328,33 +542,52 @@ cudaError_t forward_i(const EmbedArgs& a, cudaStream_t s) {
     return a.out_fp32 ? forward_io<I, B, float>(a, s) : forward_io<I, B, B>(a, s);
 }
 
-template <typename I, typename O, bool ALIGNED>
-cudaError_t sort_as(const EmbedArgs& a, const Workspace& ws, cudaStream_t s) {
-    const int blocks = slices_of(a.V), slice = (a.V - 1) / blocks + 1;
-    const size_t smem = sizeof(int32_t) * (kSortWarps + 1) * slice;
-    const cudaError_t e = cudaFuncSetAttribute(embed_sort_kernel<I, O, ALIGNED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               static_cast<int>(sizeof(int32_t) * (kSortWarps + 1) * kMostSlice));
+template <typename I>
+cudaError_t sort(const EmbedArgs& a, const Workspace& ws, cudaStream_t s) {
+    const int bits = slice_bits(a.V), slice = ((a.V - 1) >> bits) + 1;
+    const cudaError_t e = cudaFuncSetAttribute(embed_sort_kernel<I>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               static_cast<int>(sizeof(int32_t) * kSortWarps * kMostSlice));
     if (e != cudaSuccess) return e;
-    return launch_k(kPdlTrain, embed_sort_kernel<I, O, ALIGNED>, dim3(blocks), dim3(1024), smem, s,
-                    static_cast<const I*>(a.ids), a.T, a.V, a.d, slice, !a.accumulate, ws, static_cast<O*>(a.out), a.status);
+    return launch_k(kPdlTrain, embed_sort_kernel<I>, dim3(1 << bits), dim3(1024), sizeof(int32_t) * kSortWarps * slice, s,
+                    static_cast<const I*>(a.ids), a.T, a.V, slice, bits, piece_of(a.T, a.d), ws, a.status);
 }
-template <typename X, typename O, bool ALIGNED>
+template <typename X, typename O, int G>
 cudaError_t sum_as(const EmbedArgs& a, const Workspace& ws, cudaStream_t s) {
-    cudaError_t e = a.ids64 ? sort_as<long long, O, ALIGNED>(a, ws, s) : sort_as<int32_t, O, ALIGNED>(a, ws, s);
+    const int d8 = (a.d + 7) / 8, tx = across(d8), ty = kThreads / tx;
+    SumArgs g;
+    g.V = a.V, g.d = a.d;
+    g.piece = piece_of(a.T, a.d);
+    g.pieces = (a.T - 1) / g.piece + 1;
+    g.chunks = (d8 - 1) / tx + 1;
+    g.sum_blocks = ((g.pieces - 1) / ty + 1) * g.chunks;
+    g.scale = a.scale;
+    g.add = a.accumulate;
+    const long long words = (static_cast<long long>(a.V) * a.d * static_cast<long long>(sizeof(O)) + 15) / 16;
+    const long long zero_blocks = a.accumulate ? 0 : (words - 1) / (kZeroWords * tx * ty) + 1;
+    cudaError_t e = launch_k(kPdlTrain, embed_sum_kernel<X, O, G>, dim3(static_cast<unsigned>(g.sum_blocks + zero_blocks)), dim3(tx, ty), 0, s,
+                             static_cast<const X*>(a.rows), g, ws, static_cast<O*>(a.out));
+    if (e != cudaSuccess || g.pieces == 1) return e;
+    return launch_k(kPdlTrain, embed_join_kernel<O, G>, dim3((g.pieces - 1) / kWindow + 1, (d8 + 31) / 32), dim3(32, kShares), 0, s,
+                    g, ws, static_cast<O*>(a.out));
+}
+template <typename X, typename O>
+cudaError_t sum_xo(const EmbedArgs& a, const Workspace& ws, cudaStream_t s) {
+    const cudaError_t e = a.ids64 ? sort<long long>(a, ws, s) : sort<int32_t>(a, ws, s);
     if (e != cudaSuccess) return e;
-    const int d8 = (a.d + 7) / 8, tx = across(d8), ty = 256 / tx, pieces = (a.T - 1) / kPiece + 1;
-    e = launch_k(kPdlTrain, embed_sum_kernel<X, O, ALIGNED>, dim3((pieces - 1) / ty + 1, (d8 - 1) / tx + 1), dim3(tx, ty), 0, s,
-                 static_cast<const X*>(a.rows), a.d, a.scale, a.accumulate, ws, static_cast<O*>(a.out));
-    if (e != cudaSuccess || pieces == 1) return e;
-    return launch_k(kPdlTrain, embed_join_kernel<O, ALIGNED>, dim3(pieces - 1, (d8 + 31) / 32), dim3(32, 8), 0, s, a.d,
-                    a.scale, a.accumulate, ws, static_cast<O*>(a.out));
+    switch (unit_of(a.d, a.rows, sizeof(X), a.out, sizeof(O))) {
+        case 8: return sum_as<X, O, 8>(a, ws, s);
+        case 4: return sum_as<X, O, 4>(a, ws, s);
+        case 2: return sum_as<X, O, 2>(a, ws, s);
+        default: return sum_as<X, O, 1>(a, ws, s);
+    }
 }
 
 }  // namespace
 
-size_t embed_backward_workspace(int T, int d) {
-    const size_t pieces = (static_cast<size_t>(T) + kPiece - 1) / kPiece;
-    return kAlign + 2 * up(sizeof(int32_t) * static_cast<size_t>(T)) + up(sizeof(float) * 2 * d * pieces);
+size_t embed_backward_workspace(int T, int V, int d) {
+    const size_t piece = piece_of(T, d), pieces = (static_cast<size_t>(T) + piece - 1) / piece;
+    return kAlign + 2 * up(sizeof(int32_t) * static_cast<size_t>(T)) + up(static_cast<size_t>(V)) +
+           up(sizeof(int32_t) * pieces) + up(sizeof(float) * 2 * d * pieces);
 }
 
 cudaError_t launch_embed(const EmbedArgs& a, cudaStream_t s) {
@@ -367,15 +600,13 @@ cudaError_t launch_embed_backward(const EmbedArgs& a, void* workspace, cudaStrea
     ws.found = reinterpret_cast<int32_t*>(p);
     ws.order = reinterpret_cast<int32_t*>(p += kAlign);
     ws.id = reinterpret_cast<int32_t*>(p += up(sizeof(int32_t) * static_cast<size_t>(a.T)));
-    ws.part = reinterpret_cast<float*>(p + up(sizeof(int32_t) * static_cast<size_t>(a.T)));
+    ws.present = reinterpret_cast<uint8_t*>(p += up(sizeof(int32_t) * static_cast<size_t>(a.T)));
+    ws.more = reinterpret_cast<int32_t*>(p += up(static_cast<size_t>(a.V)));
+    const int piece = piece_of(a.T, a.d);
+    ws.part = reinterpret_cast<float*>(p + up(sizeof(int32_t) * ((static_cast<size_t>(a.T) + piece - 1) / piece)));
     using B = __nv_bfloat16;
-    const bool al = vectors(a.d, a.rows, a.out);
-    if (a.rows_fp32) {
-        if (a.out_fp32) return al ? sum_as<float, float, true>(a, ws, s) : sum_as<float, float, false>(a, ws, s);
-        return al ? sum_as<float, B, true>(a, ws, s) : sum_as<float, B, false>(a, ws, s);
-    }
-    if (a.out_fp32) return al ? sum_as<B, float, true>(a, ws, s) : sum_as<B, float, false>(a, ws, s);
-    return al ? sum_as<B, B, true>(a, ws, s) : sum_as<B, B, false>(a, ws, s);
+    if (a.rows_fp32) return a.out_fp32 ? sum_xo<float, float>(a, ws, s) : sum_xo<float, B>(a, ws, s);
+    return a.out_fp32 ? sum_xo<B, float>(a, ws, s) : sum_xo<B, B>(a, ws, s);
 }
 
 }  // namespace moe

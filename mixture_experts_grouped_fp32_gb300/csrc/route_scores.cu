@@ -13,12 +13,13 @@
 //
 // The choice is that of the definition in 64 bits, whatever 32 bits make of it: without bias and groups the logits
 // themselves are compared; else c is computed in fp32, and where two neighbours of the order are closer than the
-// errors of their fp32 values (a few rows in a thousand), the token is done again in fp64.  So the choice does not
-// depend on how a compiler rounds an exp.  Equal c: the lower expert.
+// errors of their fp32 values (one row in a thousand of 256 experts), the token is done again in fp64.  So the choice
+// does not depend on how a compiler rounds an exp.  Equal c: the lower expert.
 //
-// LANES threads to a token (8 for up to 64 experts, else 32), each with EPL neighbouring experts of one group, so
-// that lower lanes hold lower experts and a tie goes to the lowest lane.  A choice is a maximum over the lanes of an
-// integer with the order of c (one instruction for a warp), and the lane that holds it looks for its next one.
+// LANES threads to a token (8 for up to 64 experts, else 32), each with up to EPL neighbouring experts of one group, so
+// that lower lanes hold lower experts and a tie goes to the lowest lane.  A lane sorts its experts once, as integers
+// with the order of c; a slot then costs one maximum over the lanes' first ones (one instruction for a warp) and a
+// shift in the lane that held it.  Which expert a slot's integer belongs to is looked up for all slots at once.
 // Bound by instructions, not by the T E logits that are read.
 #include <climits>
 #include <cmath>
@@ -30,12 +31,13 @@ namespace {
 
 constexpr int kWarps = 8;  // of a block
 constexpr unsigned kAll = 0xffffffffu;
-// Bounds on the relative error of an fp32 score.  expf is off by 2 units in the last place at the most (2.4e-7).
-//   sigmoid  the addition and the division half a unit each: 3.6e-7
-//   softmax  a term of the sum: expf and its argument's rounding, 6e-8 |l - top|, whose mean over the softmax is below
-//            6e-8 ln 256; up to 21 additions of 6e-8: 1.9e-6 for the sum, and expf and the division of the score itself
-//            (its argument's rounding is added where it is used)
-constexpr float kSigmoidOff = 4.5e-7f, kSoftmaxOff = 2.5e-6f;
+// Bounds on the error of the fp32 scores that the choice goes by, from the documented ones of __expf (2 + 1.173 |x| units
+// in the last place, 1.2e-7 each) and __fdividef (2 units), 6e-8 for each rounding.
+//   sigmoid  1 / (1 + e), e = exp(-l) is off by (1 - s) (2.4e-7 + 1.4e-7 |l|) of s; s (1 - s) |l| is below 0.28: with the
+//            addition and the division 5.5e-7 s + 4e-8
+//   softmax  a term of the sum by 2.4e-7 + 2e-7 |l - top| (its argument is rounded too), whose mean over the softmax is
+//            below 2.4e-7 + 2e-7 ln 256, up to 21 additions, the quotient: 3e-6 + 2e-7 |l - top| of s
+constexpr float kSigmoidRel = 5.5e-7f, kSigmoidAbs = 4e-8f, kSoftmaxRel = 3e-6f, kSoftmaxArg = 2e-7f;
 
 template <typename L>
 __device__ __forceinline__ float logit(const L* p) {
@@ -107,17 +109,15 @@ struct RouteArgs {
 };
 
 // ---------------------------------------------------------------------------------------------
-// The choice in fp64: c[] of each lane -> the slots' experts, slot j's in lane j.
+// The choice in fp64: slot j's expert in lane j.
 // ---------------------------------------------------------------------------------------------
-__device__ __forceinline__ bool before(double a, int ai, double b, int bi) {  // strict order; INT_MAX: none
-    if (ai == INT_MAX) return false;
-    if (bi == INT_MAX) return true;
-    const bool an = a != a, bn = b != b;
-    if (an != bn) return bn;
-    return a > b || ((a == b || an) && ai < bi);
+__device__ __forceinline__ unsigned long long ordered(double v) {
+    const long long u = __double_as_longlong(v + 0.0);
+    return v != v ? 1ull : static_cast<unsigned long long>(u ^ ((u >> 63) | static_cast<long long>(0x8000000000000000ull)));
 }
 template <int LANES, int EPL, typename L>
 __device__ __noinline__ int choose64(const L* row, const RouteArgs& a, const Place& p) {
+    using Key = unsigned long long;
     double c[EPL];
     float top = -INFINITY;
     bool nan = false;
@@ -143,61 +143,72 @@ __device__ __noinline__ int choose64(const L* row, const RouteArgs& a, const Pla
 #pragma unroll
         for (int i = 0; i < EPL; ++i) c[i] = top == -INFINITY && s == s ? 0.0 : c[i] / s;
     }
-    unsigned left = 0;  // bit i: expert i of this lane may be chosen
+    Key key[EPL];
 #pragma unroll
-    for (int i = 0; i < EPL; ++i)
-        if (i < p.count) {
-            left |= 1u << i;
-            if (a.bias) c[i] += static_cast<double>(__ldg(a.bias + p.first + i));
-        }
-    // The best of the lanes that differ in the bits below `lanes`, and its expert (INT_MAX: none).
-    auto best = [&](unsigned open, int lanes, double& v, int& e) {
-        v = 0.0;
-        e = INT_MAX;
+    for (int i = 0; i < EPL; ++i) {
+        if (i < p.count && a.bias) c[i] += static_cast<double>(__ldg(a.bias + p.first + i));
+        key[i] = i < p.count ? ordered(c[i]) : 0ull;
+    }
+    // The largest key of `lanes` neighbouring lanes, and the first lane and place that hold it.
+    auto best = [&](int lanes, Key& all, bool& mine, int& at) {
+        Key m = 0ull;
+        at = 0;
 #pragma unroll
         for (int i = 0; i < EPL; ++i)
-            if ((open >> i & 1u) && before(c[i], p.first + i, v, e)) {
-                v = c[i];
-                e = p.first + i;
+            if (key[i] > m) {
+                m = key[i];
+                at = i;
             }
-        for (int o = lanes / 2; o > 0; o >>= 1) {
-            const double ov = __shfl_xor_sync(kAll, v, o);
-            const int oe = __shfl_xor_sync(kAll, e, o);
-            if (before(ov, oe, v, e)) {
-                v = ov;
-                e = oe;
-            }
-        }
+        all = m;
+        for (int o = lanes / 2; o > 0; o >>= 1) all = max(all, __shfl_xor_sync(kAll, all, o));
+        const int lane = threadIdx.x & 31;
+        const unsigned has = __ballot_sync(kAll, m == all) >> (lane & ~(lanes - 1));
+        mine = (lane & (lanes - 1)) == __ffs(has) - 1;
+    };
+    auto take_out = [&](int at) {
+#pragma unroll
+        for (int i = 0; i < EPL; ++i)
+            if (i == at) key[i] = 0ull;
     };
     if (a.G > 1) {
+        Key kept_keys[EPL];
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) kept_keys[i] = key[i];
         const int q = min(a.E / a.G, max(1, a.k / a.kept));
-        unsigned open = left;
         double score = 0.0;
         for (int r = 0; r < q; ++r) {
-            double v;
-            int e;
-            best(open, p.per_group, v, e);
-            score += v;
-            if (e >= p.first && e < p.first + p.count) open &= ~(1u << (e - p.first));
+            Key all;
+            bool mine;
+            int at;
+            best(p.per_group, all, mine, at);
+            score += all == 1ull ? static_cast<double>(NAN)
+                                 : __longlong_as_double(static_cast<long long>(all >> 63 ? all ^ 0x8000000000000000ull : ~all));
+            if (mine) take_out(at);
         }
+        const Key own = ordered(score);
         int rank = 0;
         for (int g = 0; g < a.G; ++g) {
-            const double v = __shfl_sync(kAll, score, g * p.per_group, LANES);
-            rank += before(v, g, score, p.group) ? 1 : 0;
+            const Key v = __shfl_sync(kAll, own, g * p.per_group, LANES);
+            rank += v > own || (v == own && g < p.group);
         }
-        if (rank >= a.kept) left = 0;
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) key[i] = rank < a.kept ? kept_keys[i] : 0ull;
     }
-    int mine = 0;
+    int slot = 0;
     for (int j = 0; j < a.k; ++j) {
-        double v;
-        int e;
-        best(left, LANES, v, e);
-        if (e >= p.first && e < p.first + p.count) left &= ~(1u << (e - p.first));
-        if (p.sub == j) mine = e;
+        Key all;
+        bool mine;
+        int at;
+        best(LANES, all, mine, at);
+        const unsigned who = __ballot_sync(kAll, mine) >> (threadIdx.x & 31 & ~(LANES - 1));
+        const int e = __shfl_sync(kAll, p.first + at, __ffs(who) - 1, LANES);
+        if (mine) take_out(at);
+        if (p.sub == j) slot = e;
     }
-    return mine;
+    return slot;
 }
 
+// ---------------------------------------------------------------------------------------------
 // The weights of the chosen experts, slot j's in lane j (8 lanes at least): s from its logit.
 //   softmax     exp(l - top), renormalised over the slots, or over `sum` of the row
 //   sigmoid     1 / (1 + exp(-l)); renormalised by logarithms where the sum is too small for a float
@@ -231,6 +242,71 @@ __device__ __forceinline__ float share_of_chosen(float l, bool in, bool sig) {
     return Z > 0.0f ? e / Z : (Z != Z ? Z : 0.0f);
 }
 
+// Batcher's odd-even merge sort of a lane's keys, the largest first.
+template <int N>
+__device__ __forceinline__ void sort_falling(uint32_t (&k)[N]) {
+#pragma unroll
+    for (int p = 1; p < N; p *= 2)
+#pragma unroll
+        for (int q = p; q >= 1; q /= 2)
+#pragma unroll
+            for (int j = q % p; j + q < N; j += 2 * q)
+#pragma unroll
+                for (int i = 0; i < q; ++i)
+                    if (i + j + q < N && (i + j) / (2 * p) == (i + j + q) / (2 * p)) {
+                        const uint32_t hi = max(k[i + j], k[i + j + q]), lo = min(k[i + j], k[i + j + q]);
+                        k[i + j] = hi;
+                        k[i + j + q] = lo;
+                    }
+}
+template <int N>
+__device__ __forceinline__ void drop_first(uint32_t (&k)[N], bool mine) {
+#pragma unroll
+    for (int i = 0; i + 1 < N; ++i) k[i] = mine ? k[i + 1] : k[i];
+    k[N - 1] = mine ? 0u : k[N - 1];
+}
+// The value of a key (-inf of none, NaN as none: rows with NaN are done in fp64).
+__device__ __forceinline__ float key_value(uint32_t k) {
+    return k <= 1u ? -INFINITY : __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
+}
+
+// A lane's values of a row, four at a time where `vec` (all lanes' experts are fours of a row aligned for them).
+template <int EPL>
+__device__ __forceinline__ void read_row(float (&l)[EPL], const float* p, int count, bool vec, float none) {
+    if (EPL % 4 == 0 && vec) {
+#pragma unroll
+        for (int i = 0; i < EPL; i += 4) {
+            float4 v = make_float4(none, none, none, none);
+            if (i < count) v = __ldg(reinterpret_cast<const float4*>(p + i));
+            l[i] = v.x;
+            if (i + 3 < EPL) l[i + 1] = v.y, l[i + 2] = v.z, l[i + 3] = v.w;
+        }
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) l[i] = i < count ? __ldg(p + i) : none;
+}
+template <int EPL>
+__device__ __forceinline__ void read_row(float (&l)[EPL], const __nv_bfloat16* p, int count, bool vec, float none) {
+    if (EPL % 4 == 0 && vec) {
+#pragma unroll
+        for (int i = 0; i < EPL; i += 4) {
+            float v[4] = {none, none, none, none};
+            if (i < count) {
+                const uint2 u = __ldg(reinterpret_cast<const uint2*>(p + i));
+                unpack_bf16x2(u.x, v[0], v[1]);
+                unpack_bf16x2(u.y, v[2], v[3]);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (i + j < EPL) l[i + j] = v[j];
+        }
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) l[i] = i < count ? logit(p + i) : none;
+}
+
 template <int LANES, int EPL, typename L>
 __global__ void __launch_bounds__(kWarps * 32) route_scores_kernel(const L* __restrict__ logits, RouteArgs a) {
     pdl_wait();
@@ -238,6 +314,7 @@ __global__ void __launch_bounds__(kWarps * 32) route_scores_kernel(const L* __re
     constexpr int kTokens = 32 / LANES;
     const Place p(LANES, a.E, a.G);
     const int lane = threadIdx.x & 31, base = lane & ~(LANES - 1);  // the token's first lane
+    const unsigned own_lanes = LANES == 32 ? kAll : (1u << (LANES & 31)) - 1;
     const long long warp = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
     if (warp * kTokens >= a.T) return;  // whole warps leave
     const long long want = warp * kTokens + lane / LANES;
@@ -245,12 +322,17 @@ __global__ void __launch_bounds__(kWarps * 32) route_scores_kernel(const L* __re
     const size_t t = static_cast<size_t>(there ? want : a.T - 1);
     const L* row = logits + t * a.E;
     const bool plain = !a.bias && a.G == 1;  // the order of the logits themselves
+    const int size = a.E / a.G, each = (size + p.per_group - 1) / p.per_group;
+    const bool fours = ((size | each) & 3) == 0;
+    const auto words = reinterpret_cast<uintptr_t>(logits) | reinterpret_cast<uintptr_t>(a.bias) |
+                       reinterpret_cast<uintptr_t>(a.scores);
+    const bool vec = fours && (words & 15) == 0;
 
     float l[EPL];
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) l[i] = i < p.count ? logit(row + p.first + i) : -INFINITY;
+    read_row<EPL>(l, row + p.first, p.count, vec, -INFINITY);
     float top = 0.0f, total = 1.0f;
-    if (!a.sigmoid && (!plain || !a.renorm || a.scores)) {
+    const bool exactly = a.scores != nullptr;  // (scores that leave the kernel come from expf)
+    if (!a.sigmoid && (!plain || !a.renorm || exactly)) {
         top = -INFINITY;
 #pragma unroll
         for (int i = 0; i < EPL; ++i) top = fmaxf(top, l[i]);
@@ -266,121 +348,160 @@ __global__ void __launch_bounds__(kWarps * 32) route_scores_kernel(const L* __re
         return top == -INFINITY && total == 0.0f ? 0.0f : expf(v - top) / total;
     };
     uint32_t key[EPL];
-    if (plain && !a.scores) {
+    bool nan = false;
+    if (plain && !exactly) {
 #pragma unroll
         for (int i = 0; i < EPL; ++i) key[i] = i < p.count ? ordered(l[i]) : 0u;
     } else {
+        float c[EPL], b[EPL];
+        if (exactly) {
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) c[i] = score(l[i]);
+            float* out = a.scores + t * a.E + p.first;
+            if (there) {
+                if (EPL % 4 == 0 && vec) {
+#pragma unroll
+                    for (int i = 0; i + 3 < EPL; i += 4)
+                        if (i < p.count) *reinterpret_cast<float4*>(out + i) = make_float4(c[i], c[i + 1], c[i + 2], c[i + 3]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < EPL; ++i)
+                        if (i < p.count) out[i] = c[i];
+                }
+            }
+        } else if (a.sigmoid) {
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) c[i] = __fdividef(1.0f, 1.0f + __expf(-l[i]));
+        } else {
+            const float inv = 1.0f / total;
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) c[i] = top == -INFINITY && total == 0.0f ? 0.0f : __expf(l[i] - top) * inv;
+        }
+        if (a.bias) {
+            read_row<EPL>(b, a.bias + p.first, p.count, vec, 0.0f);
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) c[i] += b[i];
+        }
 #pragma unroll
         for (int i = 0; i < EPL; ++i) {
-            key[i] = 0u;
-            if (i < p.count) {
-                const float s = score(l[i]);
-                if (a.scores && there) a.scores[t * a.E + p.first + i] = s;
-                key[i] = ordered(plain ? l[i] : a.bias ? s + __ldg(a.bias + p.first + i) : s);
-            }
+            nan |= i < p.count && c[i] != c[i];
+            key[i] = i < p.count ? ordered(plain ? l[i] : c[i]) : 0u;
         }
     }
-    auto value = [](uint32_t k) {  // of a key above 1
-        return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
-    };
-    bool sure = true;  // the fp32 order is that of the definition
-    if (a.G > 1) {
+    bool sure = plain || !nan;  // the fp32 order is that of the definition
+    uint32_t first[EPL];
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) first[i] = key[i];
+    sort_falling<EPL>(first);
+    if (a.G > 1 && a.kept < a.G) {
         // A group's score: its q largest, all groups at once.
-        const int q = min(a.E / a.G, max(1, a.k / a.kept));
-        unsigned open = (1u << EPL) - 1;
-        float sum = 0.0f, size = 0.0f;
-        for (int r = 0; r < q; ++r) {
-            uint32_t m = 0;
-            int at = 0;
+        const int q = min(size, max(1, a.k / a.kept));
+        float sum, bulk;  // bulk: sum of sizes
+        if (q <= 2) {
+            float t1 = key_value(first[0]), t2 = EPL > 1 ? key_value(first[EPL > 1 ? 1 : 0]) : -INFINITY;
+            for (int o = p.per_group / 2; o > 0; o >>= 1) {
+                const float o1 = __shfl_xor_sync(kAll, t1, o), o2 = __shfl_xor_sync(kAll, t2, o);
+                t2 = fmaxf(fminf(t1, o1), fmaxf(t2, o2));
+                t1 = fmaxf(t1, o1);
+            }
+            sum = q == 2 ? t1 + t2 : t1;
+            bulk = fabsf(t1) + (q == 2 ? fabsf(t2) : 0.0f);
+        } else {
+            uint32_t rest[EPL];
 #pragma unroll
-            for (int i = 0; i < EPL; ++i)
-                if ((open >> i & 1u) && key[i] > m) {
-                    m = key[i];
-                    at = i;
-                }
-            uint32_t all = m;
-            for (int o = p.per_group / 2; o > 0; o >>= 1) all = max(all, __shfl_xor_sync(kAll, all, o));
-            // (of equal ones the lowest lane's is taken out)
-            const unsigned has = __ballot_sync(kAll, m == all) >> (lane & ~(p.per_group - 1));
-            if ((lane & (p.per_group - 1)) == __ffs(has) - 1) open &= ~(1u << at);
-            const float c = all > 1 ? value(all) : NAN;
-            sum += c;
-            size += fabsf(c);
-        }
-        // The error of sum: its scores' (see below; a softmax's add up to 1 at most), its additions'.
-        const float off = (a.sigmoid ? q * kSigmoidOff : kSoftmaxOff) + size * (q + 1) * 6e-8f;
-        int rank = 0;
-        const uint32_t mine = ordered(sum);
-        unsigned close = 0;  // groups whose scores may be in another order than their fp32 values
-        for (int g = 0; g < a.G; ++g) {
-            const float v = __shfl_sync(kAll, sum, g * p.per_group, LANES), vo = __shfl_sync(kAll, off, g * p.per_group, LANES);
-            const uint32_t u = ordered(v);
-            if (g != p.group) {
-                rank += u > mine || (u == mine && g < p.group);
-                if (!(fabsf(v - sum) > vo + off)) close |= 1u << g;
+            for (int i = 0; i < EPL; ++i) rest[i] = first[i];
+            sum = bulk = 0.0f;
+            for (int r = 0; r < q; ++r) {
+                uint32_t all = rest[0];
+                for (int o = p.per_group / 2; o > 0; o >>= 1) all = max(all, __shfl_xor_sync(kAll, all, o));
+                const unsigned has = __ballot_sync(kAll, rest[0] == all) >> (lane & ~(p.per_group - 1));
+                drop_first<EPL>(rest, (lane & (p.per_group - 1)) == __ffs(has) - 1);
+                sum += key_value(all);
+                bulk += fabsf(key_value(all));
             }
         }
-        const bool kept = p.group < a.G && rank < a.kept;
-        const unsigned lanes_kept = __ballot_sync(kAll, kept) >> base;
-        for (int g = 0; g < a.G; ++g)  // (only a kept one and another matter)
-            if ((close >> g & 1u) && ((lanes_kept >> (g * p.per_group) & 1u) != 0) != kept && p.group < a.G) sure = false;
-        if (!kept) {
-#pragma unroll
-            for (int i = 0; i < EPL; ++i) key[i] = 0u;
+        // The error of a sum: its scores' and its additions'.
+        const bool real = p.group < a.G;
+        bulk = __uint_as_float(lanes_max<LANES>(real ? __float_as_uint(bulk) : 0u));  // (positive: integers have their order)
+        const float off = (a.sigmoid ? q * (kSigmoidRel + kSigmoidAbs) : kSoftmaxRel + q * 0.37f * kSoftmaxArg) + bulk * (q + 1) * 6e-8f;
+        uint32_t g = real ? ordered(sum) : 0u, m = 0u;
+        bool kept = false;
+        for (int r = 0; r < a.kept; ++r) {
+            m = lanes_max<LANES>(g);
+            const bool eq = g == m;
+            if (__popc(__ballot_sync(kAll, eq) >> base & own_lanes) != p.per_group) sure = false;  // equal sums
+            kept |= eq;
+            g = eq ? 0u : g;
         }
+        if (!(key_value(m) - key_value(lanes_max<LANES>(g)) > 2.0f * off)) sure = false;
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) first[i] = kept ? first[i] : 0u;
     }
-    // The slots, one by one (and the first that is not chosen, to see that it is not).
-    const int rounds = plain ? a.k : a.k + 1;
-    float last = INFINITY, last_off = 0.0f, my_l = 0.0f;
-    int my_e = 0;
-    uint32_t m = 0;
-    int at = 0;
-    auto next = [&] {
-        m = 0;
-        at = 0;
-#pragma unroll
-        for (int i = 0; i < EPL; ++i)
-            if (key[i] > m) {
-                m = key[i];
-                at = i;
-            }
-    };
-    next();
+    // The slots: key, lane, and how often this key of this lane came before.
+    uint32_t my_key = 0u, last = 0u;
+    int my_lane = 0, my_rep = 0, last_lane = -1, rep = 0;
 #pragma unroll 1
-    for (int j = 0; j < rounds; ++j) {
-        const uint32_t all = lanes_max<LANES>(m);
-        const unsigned has = __ballot_sync(kAll, m == all) >> base;
-        const int winner = __ffs(LANES == 32 ? has : has & ((1u << (LANES & 31)) - 1)) - 1;
-        float wl = 0.0f;
-#pragma unroll
-        for (int i = 0; i < EPL; ++i)
-            if (i == at) wl = l[i];
-        wl = __shfl_sync(kAll, wl, winner, LANES);
-        const int e = __shfl_sync(kAll, p.first + at, winner, LANES);
-        if (j < a.k && p.sub == j) {
-            my_e = e;
-            my_l = wl;
+    for (int j = 0; j < a.k; ++j) {
+        const uint32_t all = lanes_max<LANES>(first[0]);
+        const int winner = __ffs(__ballot_sync(kAll, first[0] == all) >> base & own_lanes) - 1;
+        rep = all == last && winner == last_lane ? rep + 1 : 0;
+        last = all;
+        last_lane = winner;
+        if (p.sub == j) {
+            my_key = all;
+            my_lane = winner;
+            my_rep = rep;
         }
-        if (!plain) {
-            const float c = all > 1 ? value(all) : NAN, sc = a.bias ? fabsf(c - __ldg(a.bias + e)) : fabsf(c);
-            const float off = sc * (a.sigmoid ? kSigmoidOff : kSoftmaxOff + 6e-8f * fabsf(wl - top)) + fabsf(c) * 1.2e-7f + 1e-30f;
-            if (all != 0 && j > 0 && !(last - c > last_off + off)) sure = false;
-            last = c;
-            last_off = off;
-        }
-        if (p.sub == winner) {
-#pragma unroll
-            for (int i = 0; i < EPL; ++i)
-                if (i == at) key[i] = 0u;
-            next();
-        }
+        drop_first<EPL>(first, p.sub == winner);
     }
-    if (!plain && __any_sync(kAll, !sure)) {
-        const int e = choose64<LANES, EPL>(row, a, p);
-        my_e = e;
-        my_l = p.sub < a.k ? logit(row + e) : 0.0f;
+    int at = 0, seen = 0;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+        const uint32_t v = __shfl_sync(kAll, key[i], my_lane, LANES);
+        if (v == my_key) {
+            if (seen == my_rep) at = i;
+            ++seen;
+        }
     }
     const bool in = p.sub < a.k;
+    int my_e = __shfl_sync(kAll, p.first, my_lane, LANES) + at;
+    if (!in) my_e = 0;
+    float my_l = logit(row + my_e);
+    if (!plain) {
+        // Neighbours in the order have to be further apart than their errors; the last slot's is the best that is left.
+        auto error = [&](float c, int e, float v) {
+            const float s = a.bias ? fabsf(c - __ldg(a.bias + e)) : fabsf(c);
+            return (a.sigmoid ? s * kSigmoidRel + kSigmoidAbs : s * (kSoftmaxRel + kSoftmaxArg * fabsf(v - top)) + 1e-30f) +
+                   fabsf(c) * 1.2e-7f;
+        };
+        const float c = key_value(my_key), off = error(c, my_e, my_l);
+        const uint32_t left = lanes_max<LANES>(first[0]);
+        float left_off = 0.0f;
+        if (first[0] == left && left != 0u) {
+            int i_left = 0;
+            float v = 0.0f;
+#pragma unroll
+            for (int i = 0; i < EPL; ++i)
+                if (key[i] == left) {
+                    i_left = i;
+                    v = l[i];
+                }
+            left_off = error(key_value(left), p.first + i_left, v);
+        }
+        left_off = __uint_as_float(lanes_max<LANES>(__float_as_uint(left_off)));
+        float next_c = __shfl_down_sync(kAll, c, 1, LANES), next_off = __shfl_down_sync(kAll, off, 1, LANES);
+        if (p.sub == a.k - 1) {
+            next_c = key_value(left);
+            next_off = left_off;
+        }
+        const bool none_left = p.sub == a.k - 1 && left == 0u;
+        if (in && !none_left && !(c - next_c > off + next_off)) sure = false;
+        if (__any_sync(kAll, !sure)) {
+            my_e = choose64<LANES, EPL>(row, a, p);
+            if (!in) my_e = 0;
+            my_l = logit(row + my_e);
+        }
+    }
     float w;
     if (a.renorm) w = share_of_chosen(my_l, in, a.sigmoid);
     else w = in ? score(my_l) : 0.0f;
@@ -397,14 +518,14 @@ struct RouteGradArgs {
     float scale;
 };
 
+// Lane `sub` of a token has the experts sub, sub + LANES, ..: loads and stores of neighbouring lanes are neighbours.
 template <int LANES, int EPL, typename L>
 __global__ void __launch_bounds__(kWarps * 32)
 route_scores_backward_kernel(const L* __restrict__ logits, RouteGradArgs a, L* __restrict__ dlogits) {
     pdl_wait();
     pdl_trigger();
     constexpr int kTokens = 32 / LANES;
-    const Place p(LANES, a.E, 1);
-    const int lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 31, sub = lane & (LANES - 1);
     const long long warp = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
     if (warp * kTokens >= a.T) return;
     const long long want = warp * kTokens + lane / LANES;
@@ -414,93 +535,76 @@ route_scores_backward_kernel(const L* __restrict__ logits, RouteGradArgs a, L* _
     // Of all scores only those that a gradient reaches are needed: the chosen ones, but for a softmax that is not
     // renormalised or whose scores have a gradient of their own.
     const bool dense = a.dscores || (!a.sigmoid && !a.renorm);
-
+    float v[EPL], g[EPL];
+    if (dense) {
+        const float* ds = a.dscores + (a.per_token ? t * a.E : 0);
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) {
+            const int e = sub + i * LANES;
+            v[i] = e < a.E ? logit(row + e) : -INFINITY;
+            g[i] = e < a.E && a.dscores ? __ldg(ds + e) : 0.0f;
+        }
+    }
     // Slot j in lane j; an expert that there is none of takes part in nothing.
     int e = -1;
     float u = 0.0f, l = 0.0f;
-    if (a.dw && p.sub < a.k) {
-        e = __ldg(a.idx + t * a.k + p.sub);
+    if (a.dw && sub < a.k) {
+        e = __ldg(a.idx + t * a.k + sub);
+        u = a.scale * __ldg(a.dw + t * a.k + sub);
         if (e < 0 || e >= a.E) e = -1;
-        else {
-            u = a.scale * __ldg(a.dw + t * a.k + p.sub);
-            l = logit(row + e);
-        }
+        else l = logit(row + e);
     }
-    float direct = 0.0f;  // this slot's part of dl itself (not through D)
-    float D = u;
-    if (a.renorm) {  // d(share)/dl needs the shares alone: s (1/S) = r
+    // What a slot adds to its expert: to dl itself, or (a softmax that is not renormalised) to D.
+    float add = e >= 0 ? u : 0.0f;
+    const bool to_dl = a.sigmoid || a.renorm;
+    if (a.renorm) {  // d(share)/dl needs the shares alone: s / S = r
         const float r = share_of_chosen(l, e >= 0, a.sigmoid);
         const float mean = eight_sum(e >= 0 ? r * u : 0.0f);
-        direct = e >= 0 ? r * (u - mean) : 0.0f;
-        if (a.sigmoid) direct *= sigmoid(-l);
-        D = 0.0f;
+        add = e >= 0 ? r * (u - mean) : 0.0f;
+        if (a.sigmoid) add *= sigmoid(-l);
     } else if (a.sigmoid) {
-        direct = e >= 0 ? sigmoid(l) * sigmoid(-l) * u : 0.0f;
-        D = 0.0f;
+        add = e >= 0 ? sigmoid(l) * sigmoid(-l) * u : 0.0f;
     }
-    float g[EPL], s[EPL];
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) g[i] = 0.0f;
-    if (dense) {
-        float v[EPL];
-#pragma unroll
-        for (int i = 0; i < EPL; ++i) v[i] = i < p.count ? logit(row + p.first + i) : -INFINITY;
-        if (a.sigmoid) {
-#pragma unroll
-            for (int i = 0; i < EPL; ++i) s[i] = sigmoid(v[i]) * sigmoid(-v[i]);
-        } else {
-            float top = -INFINITY, total = 0.0f;
-#pragma unroll
-            for (int i = 0; i < EPL; ++i) top = fmaxf(top, v[i]);
-            top = lanes_max<LANES>(top);
-#pragma unroll
-            for (int i = 0; i < EPL; ++i) {
-                s[i] = i < p.count ? (top == -INFINITY && v[i] == v[i] ? 0.0f : expf(v[i] - top)) : 0.0f;
-                total += s[i];
-            }
-            total = lanes_sum<LANES>(total);
-            const float inv = total == 0.0f ? 0.0f : 1.0f / total;
-#pragma unroll
-            for (int i = 0; i < EPL; ++i) s[i] *= inv;
-        }
-        if (a.dscores) {
-            const float* ds = a.dscores + (a.per_token ? t * a.E : 0);
-#pragma unroll
-            for (int i = 0; i < EPL; ++i)
-                if (i < p.count) g[i] = __ldg(ds + p.first + i);
-        }
-        if (!a.sigmoid && !a.renorm && a.dw)
-            for (int j = 0; j < a.k; ++j) {
-                const int at = __shfl_sync(kAll, e, j, LANES) - p.first;
-                const float add = __shfl_sync(kAll, D, j, LANES);
-#pragma unroll
-                for (int i = 0; i < EPL; ++i)
-                    if (at == i && i < p.count) g[i] += add;
-            }
-        if (a.sigmoid) {
-#pragma unroll
-            for (int i = 0; i < EPL; ++i) g[i] *= s[i];
-        } else {
-            float mean = 0.0f;
-#pragma unroll
-            for (int i = 0; i < EPL; ++i) mean = fmaf(s[i], g[i], mean);
-            mean = lanes_sum<LANES>(mean);
-#pragma unroll
-            for (int i = 0; i < EPL; ++i) g[i] = s[i] * (g[i] - mean);
-        }
-    }
-    if (a.dw && (a.sigmoid || a.renorm))
+    auto scatter = [&] {
         for (int j = 0; j < a.k; ++j) {
-            const int at = __shfl_sync(kAll, e, j, LANES) - p.first;
-            const float add = __shfl_sync(kAll, direct, j, LANES);
+            const int at = __shfl_sync(kAll, e, j, LANES) - sub;
+            const float x = __shfl_sync(kAll, add, j, LANES);
 #pragma unroll
             for (int i = 0; i < EPL; ++i)
-                if (at == i && i < p.count) g[i] += add;
+                if (at == i * LANES) g[i] += x;
         }
+    };
+    if (!dense) {
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) g[i] = 0.0f;
+    } else if (a.sigmoid) {
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) g[i] *= sigmoid(v[i]) * sigmoid(-v[i]);
+    } else {
+        if (!to_dl) scatter();
+        float top = -INFINITY, total = 0.0f, mean = 0.0f;
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) top = fmaxf(top, v[i]);
+        top = lanes_max<LANES>(top);
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) {
+            const bool none = sub + i * LANES >= a.E || (top == -INFINITY && v[i] == v[i]);
+            v[i] = none ? 0.0f : expf(v[i] - top);
+            total += v[i];
+            mean = fmaf(v[i], g[i], mean);
+        }
+        total = lanes_sum<LANES>(total);
+        mean = lanes_sum<LANES>(mean);
+        const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+        mean *= inv;
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) g[i] = v[i] * inv * (g[i] - mean);
+    }
+    if (to_dl && a.dw) scatter();
     if (there)
 #pragma unroll
         for (int i = 0; i < EPL; ++i)
-            if (i < p.count) store_grad(dlogits + t * a.E + p.first + i, g[i]);
+            if (sub + i * LANES < a.E) store_grad(dlogits + t * a.E + sub + i * LANES, g[i]);
 }
 
 // Experts of a lane, at most: groups up to a power of two share the lanes.
@@ -512,39 +616,42 @@ int experts_per_lane(int lanes, int E, int G) {
     return (E / G + per - 1) / per;
 }
 
-#define MOE_BY_WIDTH(CALL)                                                                  \
-    do {                                                                                    \
-        const int n8 = E <= 64 ? experts_per_lane(8, E, G) : 1 << 30;                       \
-        if (n8 <= 2) return CALL(8, 2);                                                     \
-        if (n8 <= 8) return CALL(8, 8);                                                     \
-        const int n32 = experts_per_lane(32, E, G);                                         \
-        if (n32 <= 2) return CALL(32, 2);                                                   \
-        if (n32 <= 4) return CALL(32, 4);                                                   \
-        if (n32 <= 8 || G == 1) return CALL(32, 8);  /* (256 experts at most) */            \
-        MOE_WIDER(CALL)                                                                     \
-    } while (0)
-
+template <int LANES, int EPL, typename L>
+cudaError_t forward_with(const L* logits, const RouteArgs& a, cudaStream_t s) {
+    return launch_k(kPdlTrain, route_scores_kernel<LANES, EPL, L>, dim3((a.T - 1) / (kWarps * (32 / LANES)) + 1),
+                    dim3(kWarps * 32), 0, s, logits, a);
+}
 template <typename L>
 cudaError_t forward_as(const L* logits, const RouteArgs& a, cudaStream_t s) {
-    const int E = a.E, G = a.G;
-#define MOE_CALL(LANES, EPL)                                                                                              \
-    launch_k(kPdlTrain, route_scores_kernel<LANES, EPL, L>, dim3((a.T - 1) / (kWarps * (32 / LANES)) + 1), dim3(kWarps * 32), \
-             0, s, logits, a)
-#define MOE_WIDER(CALL) return CALL(32, 16);
-    MOE_BY_WIDTH(MOE_CALL);
-#undef MOE_WIDER
-#undef MOE_CALL
+    const int n8 = a.E <= 64 ? experts_per_lane(8, a.E, a.G) : 1 << 30, n32 = experts_per_lane(32, a.E, a.G);
+    if (n8 <= 2) return forward_with<8, 2>(logits, a, s);
+    if (n8 <= 8) return forward_with<8, 8>(logits, a, s);
+    if (n32 <= 2) return forward_with<32, 2>(logits, a, s);
+    if (n32 <= 4) return forward_with<32, 4>(logits, a, s);
+    if (n32 <= 8) return forward_with<32, 8>(logits, a, s);
+    return forward_with<32, 16>(logits, a, s);
+}
+template <int LANES, int EPL, typename L>
+cudaError_t backward_with(const L* logits, const RouteGradArgs& a, L* dlogits, cudaStream_t s) {
+    return launch_k(kPdlTrain, route_scores_backward_kernel<LANES, EPL, L>, dim3((a.T - 1) / (kWarps * (32 / LANES)) + 1),
+                    dim3(kWarps * 32), 0, s, logits, a, dlogits);
 }
 template <typename L>
 cudaError_t backward_as(const L* logits, const RouteGradArgs& a, L* dlogits, cudaStream_t s) {
-    const int E = a.E, G = 1;
-#define MOE_CALL(LANES, EPL)                                                                                       \
-    launch_k(kPdlTrain, route_scores_backward_kernel<LANES, EPL, L>, dim3((a.T - 1) / (kWarps * (32 / LANES)) + 1), \
-             dim3(kWarps * 32), 0, s, logits, a, dlogits)
-#define MOE_WIDER(CALL)
-    MOE_BY_WIDTH(MOE_CALL);
-#undef MOE_WIDER
-#undef MOE_CALL
+    if (a.E <= 64) {
+        if (a.E <= 8) return backward_with<8, 1>(logits, a, dlogits, s);
+        if (a.E <= 16) return backward_with<8, 2>(logits, a, dlogits, s);
+        if (a.E <= 32) return backward_with<8, 4>(logits, a, dlogits, s);
+        return backward_with<8, 8>(logits, a, dlogits, s);
+    }
+    switch ((a.E + 31) / 32) {
+        case 3: return backward_with<32, 3>(logits, a, dlogits, s);
+        case 4: return backward_with<32, 4>(logits, a, dlogits, s);
+        case 5: return backward_with<32, 5>(logits, a, dlogits, s);
+        case 6: return backward_with<32, 6>(logits, a, dlogits, s);
+        case 7: return backward_with<32, 7>(logits, a, dlogits, s);
+        default: return backward_with<32, 8>(logits, a, dlogits, s);
+    }
 }
 
 }  // namespace

@@ -208,7 +208,7 @@ int moe_embed(const void* ids, int ids_int64, const void* table, int table_fp32,
 
 size_t moe_embed_backward_workspace_size(int T, int V, int d) {
     if (check_embed("moe_embed_backward_workspace_size", T, V, d, 1.0f) != MOE_OK || T == 0) return 0;
-    return embed_backward_workspace(T, d);
+    return embed_backward_workspace(T, V, d);
 }
 
 int moe_embed_backward(const void* ids, int ids_int64, const void* dy, int dy_fp32, int T, int V, int d, float scale,
@@ -223,7 +223,7 @@ int moe_embed_backward(const void* ids, int ids_int64, const void* dy, int dy_fp
     if ((rc = check_aligned(name, {{ids, ids_int64 ? 8u : 4u}, {dy, dy_fp32 ? 4u : 2u}, {out, out_fp32 ? 4u : 2u}, {status, 4}})))
         return rc;
     if (!aligned_to(workspace, 16)) return fail(MOE_ERR_INVALID_ARG, "%s: workspace must be 16-byte aligned", name);
-    const size_t need = T ? embed_backward_workspace(T, d) : 0;
+    const size_t need = T ? embed_backward_workspace(T, V, d) : 0;
     if (T > 0 && (!workspace || workspace_bytes < need))
         return fail(MOE_ERR_WORKSPACE, "%s: workspace has %zu bytes, %zu needed", name, workspace ? workspace_bytes : 0, need);
     int sms;

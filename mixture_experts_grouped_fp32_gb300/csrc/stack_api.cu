@@ -18,6 +18,15 @@ int check_rows(const char* name, int T, int d) {
     return MOE_OK;
 }
 
+// A row whose width is no multiple of 8 takes an eight more than its values fill, of the 8192 that a cluster holds.
+int check_norm_rows(const char* name, int T, int d) {
+    const int rc = check_rows(name, T, d);
+    if (rc) return rc;
+    if (d > kMaxDim - 16 && d % 8)
+        return fail(MOE_ERR_INVALID_ARG, "%s: d = %d must be a multiple of 8 above %d", name, d, kMaxDim - 16);
+    return MOE_OK;
+}
+
 int check_drop(const char* name, double p, uint64_t seed, int64_t offset, const int64_t* offset_dev, DropArgs* a) {
     if (!drop_args(p, seed, offset, offset_dev, a))
         return fail(MOE_ERR_INVALID_ARG, "%s: p = %g outside [0, 1 - 2^-17)", name, p);
@@ -107,7 +116,7 @@ int moe_layer_norm(const void* x, int x_fp32, const void* h, const float* weight
                    float* stats, moe_stream_t stream) {
     const char* name = "moe_layer_norm";
     LayerNormArgs a{};
-    int rc = check_rows(name, T, d);
+    int rc = check_norm_rows(name, T, d);
     if (rc || (rc = check_drop(name, p, seed, offset, offset_dev, &a.drop))) return rc;
     if (!(eps >= 0.0f) || eps > 3.0e38f) return fail(MOE_ERR_INVALID_ARG, "%s: eps must be finite and not negative", name);
     if (T == 0) return ok();
@@ -124,11 +133,11 @@ int moe_layer_norm(const void* x, int x_fp32, const void* h, const float* weight
     a.stats = stats;
     int sms;
     if ((rc = check_device(&sms))) return rc;
-    return launched(launch_layer_norm(a, sms, static_cast<cudaStream_t>(stream)), "layer_norm");
+    return launched(launch_layer_norm(a, static_cast<cudaStream_t>(stream)), "layer_norm");
 }
 
 size_t moe_layer_norm_backward_workspace_size(int T, int d) {
-    if (check_rows("moe_layer_norm_backward_workspace_size", T, d) != MOE_OK) return 0;
+    if (check_norm_rows("moe_layer_norm_backward_workspace_size", T, d) != MOE_OK) return 0;
     return sizeof(float) * 2 * static_cast<size_t>(d) * layer_norm_blocks(T, d);
 }
 
@@ -138,7 +147,7 @@ int moe_layer_norm_backward(const void* x, int x_fp32, const float* stats, const
                             size_t workspace_bytes, moe_stream_t stream) {
     const char* name = "moe_layer_norm_backward";
     LayerNormArgs a{};
-    int rc = check_rows(name, T, d);
+    int rc = check_norm_rows(name, T, d);
     if (rc || (rc = check_drop(name, p, seed, offset, offset_dev, &a.drop))) return rc;
     const uintptr_t sx = x_fp32 ? 4 : 2;
     if ((rc = check_aligned(name, {{x, sx}, {dy, sx}, {dx, sx}, {dn, 2}, {dh, 2}, {weight, 4}, {dweight, 4}, {dbias, 4}, {stats, 8}})))

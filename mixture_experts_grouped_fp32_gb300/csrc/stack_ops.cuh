@@ -75,7 +75,7 @@ struct LayerNormArgs {
     float* partial;           // [layer_norm_blocks(T, d), 2, d]
 };
 int layer_norm_blocks(int T, int d);
-cudaError_t launch_layer_norm(const LayerNormArgs& a, int num_sms, cudaStream_t s);
+cudaError_t launch_layer_norm(const LayerNormArgs& a, cudaStream_t s);
 cudaError_t launch_layer_norm_backward(const LayerNormArgs& a, cudaStream_t s);
 
 // What a kernel keeps of its arguments.
@@ -97,20 +97,6 @@ struct Drop {
             v.v[2 * j] = (w[j] << 16) >= cut16 ? v.v[2 * j] * up : 0.0f;
             v.v[2 * j + 1] = w[j] >= cut16 ? v.v[2 * j + 1] * up : 0.0f;
         }
-    }
-    // The same for any first element: its eight numbers lie in two blocks.
-    __device__ __forceinline__ void apply_any(Vec8& v, uint64_t first) const {
-        const int shift = static_cast<int>(first & 7);
-        if (shift == 0) return apply(v, first);
-        const uint4 a = philox(key0, key1, first >> 3, offset), b = philox(key0, key1, (first >> 3) + 1, offset);
-        const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-        uint32_t m = 0;  // bit i: number i of the two blocks stays
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            m |= ((w[j] << 16) >= cut16 ? 1u : 0u) << (2 * j) | (w[j] >= cut16 ? 1u : 0u) << (2 * j + 1);
-        m >>= shift;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v.v[j] = (m >> j) & 1u ? v.v[j] * up : 0.0f;
     }
 };
 
@@ -160,6 +146,13 @@ __device__ __forceinline__ Vec8 values(const Raw8<__nv_bfloat16>& r) { return un
 __device__ __forceinline__ Vec8 values(const Raw8<float>& r) {
     return Vec8{{r.a.x, r.a.y, r.a.z, r.a.w, r.b.x, r.b.y, r.b.z, r.b.w}};
 }
+__device__ __forceinline__ void set_values(Raw8<__nv_bfloat16>& r, const Vec8& v) { r.q = pack8(v); }
+__device__ __forceinline__ void set_values(Raw8<float>& r, const Vec8& v) {
+    r.a = make_float4(v.v[0], v.v[1], v.v[2], v.v[3]);
+    r.b = make_float4(v.v[4], v.v[5], v.v[6], v.v[7]);
+}
+__device__ __forceinline__ float to_float(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ float to_float(float v) { return v; }
 // The values as they read after a store.
 __device__ __forceinline__ Vec8 rounded(const Vec8& v, const __nv_bfloat16*) { return unpack8(pack8(v)); }
 __device__ __forceinline__ Vec8 rounded(const Vec8& v, const float*) { return v; }
@@ -176,17 +169,4 @@ __device__ __forceinline__ void put8(X* p, const Vec8& v, int count) {
             if (j < count) put(p + j, v.v[j]);
     }
 }
-// Eight fp32 values of a vector that every row reads.
-template <bool ALIGNED>
-__device__ __forceinline__ Vec8 cached8(const float* p, int count) {
-    if constexpr (ALIGNED) {
-        return load8_cached(p, 0);
-    } else {
-        Vec8 v;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v.v[j] = j < count ? __ldg(p + j) : 0.0f;
-        return v;
-    }
-}
-
 }  // namespace moe

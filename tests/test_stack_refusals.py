@@ -58,7 +58,7 @@ def test_layer_norm(lib):
     def call(x=P, f32=1, h=None, w=None, b=None, T=4, d=16, eps=1e-5, p=0.0, at=None, y=P, n=P, st=P):
         return lib.moe_layer_norm(x, f32, h, w, b, T, d, eps, p, 1, 2, at, y, n, st, None)
     refused(lib, call, [
-        (dict(T=-1), "T = -1"), (dict(T=BIG), "T = "), (dict(d=0), "d = 0"), (dict(d=65537), "d = 65537"),
+        (dict(T=-1), "T = -1"), (dict(T=BIG), "T = "), (dict(d=0), "d = 0"), (dict(d=65537), "d = 65537"), (dict(d=65521), "multiple of 8"),
         (dict(eps=-1.0), "eps"), (dict(eps=NAN), "eps"), (dict(eps=INF), "eps"), (dict(h=P, p=1.0), "p = 1"),
         (dict(h=P, p=0.999999), "p = 0.999999"), (dict(h=P, p=-0.1), "p = -0.1"), (dict(h=P, p=NAN), "p = "), (dict(p=0.5), "belongs to h"),
         (dict(x=None), "null"), (dict(n=None), "null"), (dict(st=None), "null"), (dict(h=P, y=None), "null"),
@@ -71,7 +71,7 @@ def test_layer_norm(lib):
     def back(x=P, st=P, dn=P, dy=None, w=None, T=4, d=16, p=0.0, at=None, dx=P, dh=None, dw=None, db=None, ws=P, n=need):
         return lib.moe_layer_norm_backward(x, 1, st, dn, dy, w, T, d, p, 1, 2, at, dx, dh, dw, db, ws, n, None)
     refused(lib, back, [
-        (dict(T=-1), "T = -1"), (dict(d=70000), "d = 70000"), (dict(p=1.5), "p = 1.5"), (dict(x=None), "null"), (dict(st=None), "null"),
+        (dict(T=-1), "T = -1"), (dict(d=70000), "d = 70000"), (dict(d=65535), "multiple of 8"), (dict(p=1.5), "p = 1.5"), (dict(x=None), "null"), (dict(st=None), "null"),
         (dict(dn=None), "null"), (dict(dx=None), "null"), (dict(dy=TWO), "aligned"), (dict(dw=TWO), "aligned"),
         (dict(db=TWO), "aligned"), (dict(dh=ODD), "aligned"), (dict(st=FOUR), "aligned"), (dict(ws=FOUR), "aligned"), (dict(at=FOUR), "aligned")])
     refused(lib, back, [(dict(ws=None), "workspace"), (dict(n=need - 1), "workspace")], code=-3)

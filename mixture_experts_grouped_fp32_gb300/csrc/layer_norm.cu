@@ -10,11 +10,12 @@
 //
 // y is bf16 or fp32, h, n, dn and dh bf16, weight, bias, their gradients and the stats (mean, r) fp32.
 //
-// One pass over memory each way; bound by it.  Each thread holds eight values of a row.  The variance is the sum of
-// squared distances from the mean (no difference of large sums), so a row needs two sums one after the other; the
-// second of row k is taken in the same reduction as the first of row k + 1, one barrier a row, with the loads of row
-// k + 2 under way.  A row that is wider than a block's threads hold lies in the blocks of a cluster, which exchange
-// their warps' sums through each other's shared memory.
+// One pass over memory each way; bound by it.  Each thread holds eight values of a row, with the next rows on their way
+// into shared memory (cp.async: a thread copies just the words that it will use, so the ring of rows needs no barrier).
+// The variance is the sum of squared distances from the mean (no difference of large sums), so a row needs two sums one
+// after the other; the second of row k is taken in the same reduction as the first of row k + 1, one barrier a row.
+// The backward pass takes two rows at a time, whose four sums share a reduction.  A row that is wider than a block's
+// threads hold lies in the blocks of a cluster, which exchange their warps' sums through each other's shared memory.
 //
 // Rows of any width: the eights are those of the tensor in memory order, aligned whatever the row, so a row starts
 // in the middle of one (at s = t d mod 8) and its first and last eights are shared with its neighbours: loaded whole,
@@ -43,37 +44,92 @@ __device__ __forceinline__ float2 warp_sum2(float2 v) {
     return up ? make_float2(b, a) : make_float2(a, b);
 }
 
-// Sums over the threads that hold a row.  One barrier each; the buffers alternate, so that none is needed behind it.
-template <bool CLUSTER>
+// Four sums over a warp: lane l holds that of s[l / 8].
+__device__ __forceinline__ float warp_sum4(const float (&s)[4]) {
+    const bool up = threadIdx.x & 16, up8 = threadIdx.x & 8;
+    const float a = (up ? s[2] : s[0]) + __shfl_xor_sync(0xffffffffu, up ? s[0] : s[2], 16);
+    const float b = (up ? s[3] : s[1]) + __shfl_xor_sync(0xffffffffu, up ? s[1] : s[3], 16);
+    float v = (up8 ? b : a) + __shfl_xor_sync(0xffffffffu, up8 ? a : b, 8);
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+// N = 2 or 4 sums over the threads that hold a row.  One barrier each; the buffers alternate, so that none is needed
+// behind it.
+template <bool CLUSTER, int N>
 struct RowSums {
-    float2* red;  // [2][blocks of the cluster x warps]
+    float* red;  // [2][blocks of the cluster x warps][N]
     int warps, barrier, blocks, rank, parity = 0;
-    __device__ __forceinline__ RowSums(float2* red_, int warps_, int barrier_, int blocks_)
+    __device__ __forceinline__ RowSums(float* red_, int warps_, int barrier_, int blocks_)
         : red(red_), warps(warps_), barrier(barrier_), blocks(blocks_), rank(CLUSTER ? ptx::cluster_ctarank() : 0) {}
-    __device__ __forceinline__ float2 operator()(float2 v) {
-        v = warp_sum2(v);
-        if (!CLUSTER && warps == 1) return v;
-        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, all = CLUSTER ? blocks * warps : warps;
-        float2* buf = red + parity * all;
-        parity ^= 1;
-        if (CLUSTER) {
-            if (lane < blocks) {
-                const uint32_t to = ptx::map_to_cta(ptx::smem_u32(buf + rank * warps + warp), lane);
-                asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(to), "f"(v.x), "f"(v.y) : "memory");
-            }
-            ptx::cluster_arrive();
-            ptx::cluster_wait();
-            v = make_float2(0.0f, 0.0f);
-            for (int i = lane; i < all; i += 32) v = add2(v, buf[i]);
+    __device__ __forceinline__ void operator()(float (&s)[N]) {
+        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, all = (CLUSTER ? blocks : 1) * warps;
+        float mine;  // this lane's part of sum lane / (32 / N)
+        if constexpr (N == 4) {
+            mine = warp_sum4(s);
         } else {
-            if (lane == 0) buf[warp] = v;
-            if (barrier == 0) __syncthreads();
-            else asm volatile("bar.sync %0, %1;" ::"r"(barrier), "r"(warps * 32) : "memory");
-            v = lane < warps ? buf[lane] : make_float2(0.0f, 0.0f);
+            const float2 v = warp_sum2(make_float2(s[0], s[1]));
+            mine = lane & 16 ? v.y : v.x;
         }
-        return warp_sum2(v);
+        if (CLUSTER || warps > 1) {
+            float* buf = red + parity * all * N;
+            parity ^= 1;
+            if (CLUSTER) {
+                // Lane l sends sum l mod N to block l / N, and to those 32 / N further on.
+                const float v = __shfl_sync(0xffffffffu, mine, (lane & (N - 1)) * (32 / N));
+                for (int to = lane / N; to < blocks; to += 32 / N)
+                    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(ptx::map_to_cta(
+                                     ptx::smem_u32(buf + (rank * warps + warp) * N + (lane & (N - 1))), to)),
+                                 "f"(v)
+                                 : "memory");
+                ptx::cluster_arrive();
+                ptx::cluster_wait();
+            } else {
+                if (lane % (32 / N) == 0) buf[warp * N + lane / (32 / N)] = mine;
+                if (barrier == 0) __syncthreads();
+                else asm volatile("bar.sync %0, %1;" ::"r"(barrier), "r"(warps * 32) : "memory");
+            }
+            // Lane l adds up sum l mod N of the warps l / N, l / N + 32 / N, ..
+            mine = 0.0f;
+            for (int w = lane / N; w < all; w += 32 / N) mine += buf[w * N + (lane & (N - 1))];
+#pragma unroll
+            for (int o = 16; o >= N; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+#pragma unroll
+            for (int k = 0; k < N; ++k) s[k] = __shfl_sync(0xffffffffu, mine, k);
+        } else {
+#pragma unroll
+            for (int k = 0; k < N; ++k) s[k] = __shfl_sync(0xffffffffu, mine, k * (32 / N));
+        }
     }
 };
+
+// 16-byte words of eight values of X, and a thread's words in a ring of rows.
+template <typename X>
+constexpr int words() { return sizeof(X) == 4 ? 2 : 1; }
+__device__ __forceinline__ void copy_word(uint4* to, const void* from, int bytes) {  // zeros behind `bytes`
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(ptx::smem_u32(to)), "l"(from), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copy_word_l1(uint4* to, const void* from, int bytes) {  // (half a sector: through L1)
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 16, %2;" ::"r"(ptx::smem_u32(to)), "l"(from), "r"(bytes) : "memory");
+}
+template <typename X>
+__device__ __forceinline__ Vec8 ring8(const uint4* word, int nt) {  // (its words lie nt apart)
+    const uint4 a = word[0];
+    if constexpr (sizeof(X) == 2) {
+        return unpack8(a);
+    } else {
+        const uint4 b = word[nt];
+        return Vec8{{__uint_as_float(a.x), __uint_as_float(a.y), __uint_as_float(a.z), __uint_as_float(a.w),
+                     __uint_as_float(b.x), __uint_as_float(b.y), __uint_as_float(b.z), __uint_as_float(b.w)}};
+    }
+}
+// All but the newest `pending` groups of copies have landed.
+__device__ __forceinline__ void wait_copies(int pending) {
+    if (pending >= 3) ptx::cp_async_wait<3>();
+    else if (pending == 2) ptx::cp_async_wait<2>();
+    else ptx::cp_async_wait<1>();
+}
 
 // A thread's eight of a row: the columns c .. c + 7, of which those from lo to hi - 1 are the row's.
 template <bool EDGE>
@@ -86,16 +142,28 @@ struct Eight {
     }
     __device__ __forceinline__ bool some() const { return hi > lo; }
     __device__ __forceinline__ bool whole() const { return !EDGE || (lo == 0 && hi == 8); }
-    // `at`: the first value's place in the tensor of `total` values.  Values that are not the row's may be any.
+    // On their way to `word`, words nt apart.  `at`: the first value's place in the tensor of `total` values.  Values that
+    // are not the row's may be any.
     template <typename X>
-    __device__ __forceinline__ void load(Raw8<X>& r, const X* p, long long at, long long total) const {
-        if (!EDGE || (vec && at + 8 <= total)) {
-            fetch_raw<true>(r, p + at, 8);
+    __device__ __forceinline__ void copy(uint4* word, int nt, const X* p, long long at, long long total) const {
+        if (!EDGE || vec) {
+            const long long left = EDGE ? (total - at) * static_cast<long long>(sizeof(X)) : 32;  // bytes
+            if constexpr (sizeof(X) == 2) {
+                copy_word(word, p + at, static_cast<int>(min(left, 16ll)));
+            } else {
+                copy_word_l1(word, p + at, static_cast<int>(min(left, 16ll)));
+                copy_word_l1(word + nt, p + at + (left > 16 ? 4 : 0), static_cast<int>(max(0ll, min(left - 16, 16ll))));
+            }
         } else {
             Vec8 v;
 #pragma unroll
             for (int j = 0; j < 8; ++j) v.v[j] = j >= lo && j < hi ? to_float(p[at + j]) : 0.0f;
-            set_values(r, v);
+            if constexpr (sizeof(X) == 2) {
+                *word = pack8(v);
+            } else {
+                word[0] = make_uint4(__float_as_uint(v.v[0]), __float_as_uint(v.v[1]), __float_as_uint(v.v[2]), __float_as_uint(v.v[3]));
+                word[nt] = make_uint4(__float_as_uint(v.v[4]), __float_as_uint(v.v[5]), __float_as_uint(v.v[6]), __float_as_uint(v.v[7]));
+            }
         }
     }
     __device__ __forceinline__ void mask(Vec8& v) const {
@@ -135,74 +203,88 @@ struct Forward {
     void* y;
     __nv_bfloat16* n;
     float2* stats;
-    int blocks, vec, keep;  // blocks of a cluster; keep: the weights go through shared memory
+    int blocks, vec, stages, keep;  // blocks of a cluster; rows in the ring; keep: the weights lie behind the ring
 };
 
 template <typename X, bool H, bool EDGE, bool CLUSTER>
 __global__ void __launch_bounds__(1024, 1) layer_norm_kernel(Forward a) {
-    __shared__ float2 red[2 * (CLUSTER ? kMostBlocks * 32 : 32)];
-    extern __shared__ float4 kept[];  // weight and bias, two words a thread each
-    const int tid = threadIdx.x, nt = blockDim.x, d = a.d;
+    __shared__ float red[2 * 2 * (CLUSTER ? kMostBlocks * 32 : 32)];
+    extern __shared__ uint4 ring[];
+    constexpr int W = words<X>() + (H ? 1 : 0);
+    const int tid = threadIdx.x, nt = blockDim.x, d = a.d, S = a.stages;
     const float fd = static_cast<float>(d);  // divided by, so that a constant row has deviations of 0
     const X* x = static_cast<const X*>(a.x);
     X* y = static_cast<X*>(a.y);
     const long long T = a.T, total = T * d, step = gridDim.x / a.blocks, row0 = blockIdx.x / a.blocks;
+    const int rows = static_cast<int>((T - row0 - 1) / step) + 1;
     if (CLUSTER) ptx::cluster_arrive();  // (the other blocks' memory is there once all have begun)
     pdl_wait();
     pdl_trigger();
     if (CLUSTER) ptx::cluster_wait();
-    RowSums<CLUSTER> row_sum(red, nt >> 5, 0, a.blocks);
-    const Drop drop(a.drop);
+    RowSums<CLUSTER, 2> row_sum(red, nt >> 5, 0, a.blocks);
     const int shift = EDGE ? static_cast<int>(row0 * d & 7) : 0;
     const Eight<EDGE> e((CLUSTER ? row_sum.rank * nt : 0) + tid, shift, d, a.vec != 0);
     const bool some = e.some();
-    Raw8<X> xr;
-    Raw8<__nv_bfloat16> hr;
-    auto fetch = [&](long long t) {
-        if (some) {
-            e.load(xr, x, t * d + e.c, total);
-            if (H) e.load(hr, a.h, t * d + e.c, total);
+    long long in = row0 * d + e.c;  // the next row's place, of those that are copied
+    const long long row = step * d;
+    uint4* slot = ring + tid;  // the next row's words
+    uint4* const last = ring + (S - 1) * W * nt + tid;
+    int copied = 0;
+    auto fetch = [&] {
+        if (copied < rows && some) {
+            e.copy(slot, nt, x, in, total);
+            if (H) e.copy(slot + words<X>() * nt, nt, a.h, in, total);
         }
+        ptx::cp_async_commit();
+        in += row;
+        slot = slot == last ? ring + tid : slot + W * nt;
+        ++copied;
     };
-    auto take = [&](Vec8& row, long long t) {  // the stream's values from the raw ones, stored with H; their sum
-        if (!some) return 0.0f;
-        row = values(xr);
-        if (H) {
-            Vec8 hv = values(hr);
-            if (drop.on()) drop.apply(hv, t * d + e.c);
+    for (int k = 0; k < S; ++k) fetch();
+    float4* const kept = reinterpret_cast<float4*>(ring + S * W * nt) + tid;  // a thread's own words: no barrier
+    if (a.keep && some) {
+        const Vec8 w = e.column(a.weight, 1.0f), b = e.column(a.bias, 0.0f);
+        kept[0] = make_float4(w.v[0], w.v[1], w.v[2], w.v[3]);
+        kept[nt] = make_float4(w.v[4], w.v[5], w.v[6], w.v[7]);
+        kept[2 * nt] = make_float4(b.v[0], b.v[1], b.v[2], b.v[3]);
+        kept[3 * nt] = make_float4(b.v[4], b.v[5], b.v[6], b.v[7]);
+    }
+    auto kept8 = [&](int k) {
+        const float4 p = kept[2 * k * nt], q = kept[(2 * k + 1) * nt];
+        return Vec8{{p.x, p.y, p.z, p.w, q.x, q.y, q.z, q.w}};
+    };
+    const Drop drop(a.drop);
+    const uint4* word = ring + tid;  // the row that is taken next
+    auto take = [&](Vec8& v, long long at) {  // the stream's values, stored with H; their sum
+        float2 s = make_float2(0.0f, 0.0f);
+        if (some) {
+            v = ring8<X>(word, nt);
+            if (H) {
+                Vec8 hv = ring8<__nv_bfloat16>(word + words<X>() * nt, nt);
+                if (drop.on()) drop.apply(hv, at);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) row.set(j, add2(row.pair(j), hv.pair(j)));
-            row = rounded(row, static_cast<const X*>(nullptr));
-            e.store(y, t * d + e.c, row);
+                for (int j = 0; j < 4; ++j) v.set(j, add2(v.pair(j), hv.pair(j)));
+                v = rounded(v, static_cast<const X*>(nullptr));
+                e.store(y, at, v);
+            }
+            e.mask(v);
+            s = v.pair(0);
+#pragma unroll
+            for (int j = 1; j < 4; ++j) s = add2(s, v.pair(j));
         }
-        e.mask(row);
-        float2 s = row.pair(0);
-#pragma unroll
-        for (int j = 1; j < 4; ++j) s = add2(s, row.pair(j));
+        word = word == last ? ring + tid : word + W * nt;
         return s.x + s.y;
     };
     Vec8 cur, nxt;
-    fetch(row0);
-    if (a.keep && some) {
-        const Vec8 w = e.column(a.weight, 1.0f), b = e.column(a.bias, 0.0f);
-        kept[tid] = make_float4(w.v[0], w.v[1], w.v[2], w.v[3]);
-        kept[nt + tid] = make_float4(w.v[4], w.v[5], w.v[6], w.v[7]);
-        kept[2 * nt + tid] = make_float4(b.v[0], b.v[1], b.v[2], b.v[3]);
-        kept[3 * nt + tid] = make_float4(b.v[4], b.v[5], b.v[6], b.v[7]);
-    }
-    auto kept8 = [&](int k) {  // (a thread's own words: no barrier)
-        const float4 p = kept[2 * k * nt + tid], q = kept[(2 * k + 1) * nt + tid];
-        return Vec8{{p.x, p.y, p.z, p.w, q.x, q.y, q.z, q.w}};
-    };
-    float mean = take(cur, row0);
-    if (row0 + step < T) fetch(row0 + step);
-    mean = row_sum(make_float2(mean, 0.0f)).x / fd;
-    for (long long t = row0; t < T; t += step) {
-        float next_sum = 0.0f;
-        if (t + step < T) {
-            next_sum = take(nxt, t + step);
-            if (t + 2 * step < T) fetch(t + 2 * step);
-        }
+    long long at = row0 * d + e.c;
+    wait_copies(S - 1);
+    float s[2] = {0.0f, take(cur, at)};
+    row_sum(s);
+    for (int k = 0; k < rows; ++k, at += row) {
+        const float mean = s[1] / fd;
+        fetch();
+        wait_copies(S - 1);
+        s[1] = k + 1 < rows ? take(nxt, at + row) : 0.0f;
         float2 q = make_float2(0.0f, 0.0f);
         if (some) {
 #pragma unroll
@@ -211,19 +293,20 @@ __global__ void __launch_bounds__(1024, 1) layer_norm_kernel(Forward a) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) q = fma2(cur.pair(j), cur.pair(j), q);
         }
-        const float2 s = row_sum(make_float2(q.x + q.y, next_sum));
-        const float r = 1.0f / sqrtf(s.x / fd + a.eps);
-        if (tid == 0 && row_sum.rank == 0) a.stats[t] = make_float2(mean, r);
+        s[0] = q.x + q.y;
+        row_sum(s);
+        const float r = 1.0f / sqrtf(s[0] / fd + a.eps);
+        if (tid == 0 && row_sum.rank == 0) a.stats[row0 + k * step] = make_float2(mean, r);
         if (some) {
             const Vec8 w = a.keep ? kept8(0) : e.column(a.weight, 1.0f), b = a.keep ? kept8(1) : e.column(a.bias, 0.0f);
             Vec8 o;
 #pragma unroll
             for (int j = 0; j < 4; ++j) o.set(j, fma2(mul2(cur.pair(j), r), w.pair(j), b.pair(j)));
-            e.store(a.n, t * d + e.c, o);
+            e.store(a.n, at, o);
         }
-        mean = s.y / fd;
         cur = nxt;
     }
+    ptx::cp_async_wait_all();
 }
 
 struct Backward {
@@ -237,16 +320,16 @@ struct Backward {
     void* dx;
     __nv_bfloat16* dh;
     float* partial;  // [clusters, 2, d], or null
-    int blocks, vec;
+    int blocks, vec, stages;  // stages: pairs of rows in the ring
 };
 
-// One reduction a row.  The column sums dweight and dbias of the rows that a block visits stay in registers and are
+// Two rows at a time.  The column sums dweight and dbias of the rows that a block visits stay in registers and are
 // written once; rows that are narrower than the block lie side by side in it (threadIdx.y), each with its barrier, and
 // their sums are added up first.
 template <typename X, bool EDGE, bool CLUSTER>
 __global__ void __launch_bounds__(512, 1) layer_norm_backward_kernel(Backward a) {
-    __shared__ float2 red[2 * (CLUSTER ? kMostBlocks * 16 : 16)];
-    extern __shared__ float sums[];  // [rows side by side][8][threads of a row]
+    __shared__ float red[2 * 4 * (CLUSTER ? kMostBlocks * 16 : 16)];
+    extern __shared__ uint4 ring_all[];
     using B = __nv_bfloat16;
     const int tid = threadIdx.x, nt = blockDim.x, warps = nt >> 5, d = a.d, groups = CLUSTER ? 1 : blockDim.y, group = threadIdx.y;
     const float inv_d = 1.0f / static_cast<float>(d);
@@ -254,81 +337,113 @@ __global__ void __launch_bounds__(512, 1) layer_norm_backward_kernel(Backward a)
     X* dx = static_cast<X*>(a.dx);
     const long long T = a.T, total = T * d, clusters = gridDim.x / a.blocks, cluster = blockIdx.x / a.blocks;
     const long long row0 = cluster + clusters * group, step = clusters * groups;
+    const int rows = row0 < T ? static_cast<int>((T - row0 - 1) / step) + 1 : 0;
     if (CLUSTER) ptx::cluster_arrive();
     pdl_wait();
     pdl_trigger();
     if (CLUSTER) ptx::cluster_wait();
-    RowSums<CLUSTER> row_sum(red + (CLUSTER ? 0 : 2 * warps * group), warps, groups > 1 ? 1 + group : 0, a.blocks);
+    RowSums<CLUSTER, 4> row_sum(red + (CLUSTER ? 0 : 8 * warps * group), warps, groups > 1 ? 1 + group : 0, a.blocks);
     const Drop drop(a.drop);
     const int shift = EDGE ? static_cast<int>(cluster * d & 7) : 0;
     const Eight<EDGE> e((CLUSTER ? row_sum.rank * nt : 0) + tid, shift, d, a.vec != 0);
     const bool some = e.some();
-    Raw8<X> xr, er;
-    Raw8<B> nr;
-    float2 st = make_float2(0.0f, 0.0f);
-    auto fetch = [&](long long t) {
-        st = __ldg(a.stats + t);
-        if (some) {
-            const long long at = t * d + e.c;
-            e.load(xr, x, at, total);
-            e.load(nr, a.dn, at, total);
-            if (dy) e.load(er, dy, at, total);
+    // Words of a row: x, dn, dy.
+    constexpr int o_dn = words<X>(), o_dy = o_dn + 1;
+    const int W = o_dy + (dy ? words<X>() : 0), S = a.stages;
+    uint4* const ring = ring_all + group * (S * 2 * W * nt) + tid;
+    const long long row = step * d;
+    long long in = row0 * d + e.c;
+    int copied = 0, slot = 0;
+    float2 st[2] = {}, next[2] = {};
+    auto fetch = [&] {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            if (copied < rows && some) {
+                uint4* w = ring + (2 * slot + i) * W * nt;
+                e.copy(w, nt, x, in, total);
+                e.copy(w + o_dn * nt, nt, a.dn, in, total);
+                if (dy) e.copy(w + o_dy * nt, nt, dy, in, total);
+            }
+            in += row;
+            ++copied;
         }
+        ptx::cp_async_commit();
+        slot = slot + 1 == S ? 0 : slot + 1;
     };
+    auto read_stats = [&](int k) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            if (k + i < rows) next[i] = __ldg(a.stats + row0 + (k + i) * step);
+    };
+    for (int k = 0; k + 1 < S; ++k) fetch();
+    read_stats(0);
     const Vec8 w = some ? e.column(a.weight, 1.0f) : Vec8{};
     Vec8 sw{}, sb{};
-    if (row0 < T) fetch(row0);
-    for (long long t = row0; t < T; t += step) {
-        const float r = st.y, back = -st.x;
-        Vec8 yh, g, o;
-        float2 sg = make_float2(0.0f, 0.0f), sy = sg;
-        if (some) {
-            yh = values(xr);
-            Vec8 nv = values(nr);
-            e.mask(yh);
-            e.mask(nv);
-            o = dy ? values(er) : Vec8{};
+    long long at = row0 * d + e.c;
+    int now = 0;  // the slot of these rows
+    for (int k = 0; k < rows; k += 2, at += 2 * row) {
+        fetch();
+        st[0] = next[0], st[1] = next[1];
+        read_stats(k + 2);
+        wait_copies(S - 1);
+        const uint4* words_of[2] = {ring + 2 * now * W * nt, ring + (2 * now + 1) * W * nt};
+        now = now + 1 == S ? 0 : now + 1;
+        const bool two = k + 1 < rows;
+        Vec8 yh[2], g[2];
+        float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                yh.set(j, mul2(add2(yh.pair(j), make_float2(back, back)), r));
-                g.set(j, mul2(nv.pair(j), w.pair(j)));
-                sg = add2(sg, g.pair(j));
-                sy = fma2(g.pair(j), yh.pair(j), sy);
-                sw.set(j, fma2(nv.pair(j), yh.pair(j), sw.pair(j)));
-                sb.set(j, add2(sb.pair(j), nv.pair(j)));
-            }
-        }
-        if (t + step < T) fetch(t + step);
-        const float2 s = row_sum(make_float2(sg.x + sg.y, sy.x + sy.y));
-        const float mg = s.x * inv_d, my = s.y * inv_d;
-        if (some) {
-            const long long at = t * d + e.c;
+        for (int i = 0; i < 2; ++i)
+            if (some && (i == 0 || two)) {
+                const float r = st[i].y, back = -st[i].x;
+                float2 sg = make_float2(0.0f, 0.0f), sy = sg;
+                yh[i] = ring8<X>(words_of[i], nt);
+                Vec8 nv = ring8<B>(words_of[i] + o_dn * nt, nt);
+                e.mask(yh[i]);
+                e.mask(nv);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float2 b = fma2(yh.pair(j), make_float2(-my, -my), add2(g.pair(j), make_float2(-mg, -mg)));
-                o.set(j, fma2(b, r, o.pair(j)));
+                for (int j = 0; j < 4; ++j) {
+                    yh[i].set(j, mul2(add2(yh[i].pair(j), make_float2(back, back)), r));
+                    g[i].set(j, mul2(nv.pair(j), w.pair(j)));
+                    sg = add2(sg, g[i].pair(j));
+                    sy = fma2(g[i].pair(j), yh[i].pair(j), sy);
+                    sw.set(j, fma2(nv.pair(j), yh[i].pair(j), sw.pair(j)));
+                    sb.set(j, add2(sb.pair(j), nv.pair(j)));
+                }
+                s[2 * i] = sg.x + sg.y;
+                s[2 * i + 1] = sy.x + sy.y;
             }
-            e.store(dx, at, o);
-            if (a.dh) {
-                if (drop.on()) drop.apply(o, at);
-                e.store(a.dh, at, o);
+        row_sum(s);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            if (some && (i == 0 || two)) {
+                const float mg = s[2 * i] * inv_d, my = s[2 * i + 1] * inv_d;
+                Vec8 o = dy ? ring8<X>(words_of[i] + o_dy * nt, nt) : Vec8{};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float2 b = fma2(yh[i].pair(j), make_float2(-my, -my), add2(g[i].pair(j), make_float2(-mg, -mg)));
+                    o.set(j, fma2(b, st[i].y, o.pair(j)));
+                }
+                e.store(dx, at + i * row, o);
+                if (a.dh) {
+                    if (drop.on()) drop.apply(o, at + i * row);
+                    e.store(a.dh, at + i * row, o);
+                }
             }
-        }
     }
+    ptx::cp_async_wait_all();
     if (!a.partial) return;
     float* p = a.partial + static_cast<size_t>(cluster) * 2 * d;
     const Eight<EDGE> column(some ? (e.c + shift) / 8 : 0, shift, d, false);  // (the rows of `partial` start anywhere)
     auto write = [&](float* to, const Vec8& v) {
-        if (!EDGE) {
-            store8(to + e.c, 0, v);
-            return;
-        }
-        column.store(to, e.c, v);
+        if (!EDGE) store8(to + e.c, 0, v);
+        else column.store(to, e.c, v);
     };
     if (groups > 1) {
+        float* sums = reinterpret_cast<float*>(ring_all);  // [rows side by side][8][threads of a row], once all are done
 #pragma unroll
         for (int k = 0; k < 2; ++k) {  // dweight, then dbias
             const Vec8& own = k ? sb : sw;
+            __syncthreads();
 #pragma unroll
             for (int j = 0; j < 8; ++j) sums[(group * 8 + j) * nt + tid] = own.v[j];
             __syncthreads();
@@ -339,7 +454,6 @@ __global__ void __launch_bounds__(512, 1) layer_norm_backward_kernel(Backward a)
                     for (int j = 0; j < 8; ++j) v.v[j] += sums[(g * 8 + j) * nt + tid];
                 write(p + k * static_cast<size_t>(d), v);
             }
-            __syncthreads();
         }
     } else if (some) {
         write(p, sw);
@@ -401,12 +515,20 @@ Shape shape_of(int T, int d, bool bwd) {
     return s;
 }
 
+constexpr size_t kMostSmem = 200 * 1024;  // of the blocks of an SM, for their rings
+
+// Dynamic shared memory beyond what a launch gets unasked (48 KB with the static one).
+template <typename... KArgs>
+cudaError_t allow_smem(void (*kernel)(KArgs...), size_t smem) {
+    if (smem <= 39 * 1024) return cudaSuccess;
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kMostSmem));
+}
+
 template <typename... KArgs, typename... Args>
 cudaError_t launch_rows(void (*kernel)(KArgs...), const Shape& f, size_t smem, cudaStream_t s, Args&&... args) {
-    if (f.blocks > 8) {
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-        if (e != cudaSuccess) return e;
-    }
+    cudaError_t e = allow_smem(kernel, smem);
+    if (e == cudaSuccess && f.blocks > 8) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(f.clusters * f.blocks);
     cfg.blockDim = dim3(f.threads, f.groups);
@@ -423,26 +545,29 @@ cudaError_t launch_rows(void (*kernel)(KArgs...), const Shape& f, size_t smem, c
     return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
 }
 
+// Stages of a ring (2 to 4), each of `stage` bytes, beside `other` bytes, in a block of which `per_sm` share an SM.
+int stages_for(size_t stage, size_t other, int per_sm) {
+    const size_t fit = (kMostSmem / per_sm - other) / stage;
+    return fit >= 4 ? 4 : fit >= 3 ? 3 : 2;
+}
+
 template <typename X, bool H, bool EDGE>
 cudaError_t forward_as(Forward a, cudaStream_t s) {
     const Shape f = shape_of(a.T, a.d, false);
     a.blocks = f.blocks;
-    // Weights whose loads would be one by one are read once for all rows of a block.
-    a.keep = EDGE && a.T > f.clusters;
-    const size_t smem = a.keep ? sizeof(float4) * 4 * f.threads : 0;
+    a.keep = a.T > f.clusters;  // more than one row to a block: the weights are read once
+    const size_t stage = sizeof(uint4) * (words<X>() + (H ? 1 : 0)) * f.threads, weights = a.keep ? sizeof(float4) * 4 * f.threads : 0;
+    a.stages = a.keep ? stages_for(stage, weights, std::max(1, 1024 / f.threads)) : 2;
     const auto kernel = f.blocks > 1 ? layer_norm_kernel<X, H, EDGE, true> : layer_norm_kernel<X, H, EDGE, false>;
-    if (smem) {
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 64 * 1024);
-        if (e != cudaSuccess) return e;
-    }
-    return launch_rows(kernel, f, smem, s, a);
+    return launch_rows(kernel, f, stage * a.stages + weights, s, a);
 }
 template <typename X, bool EDGE>
 cudaError_t backward_as(Backward a, const Shape& f, cudaStream_t s) {
     a.blocks = f.blocks;
-    const size_t smem = f.groups > 1 && a.partial ? sizeof(float) * 8 * f.threads * f.groups : 0;
+    const size_t pair = sizeof(uint4) * 2 * (words<X>() * (a.dy ? 2 : 1) + 1) * f.threads * f.groups;
+    a.stages = stages_for(pair, 0, std::max(1, 512 / (f.threads * f.groups)));
     const auto kernel = f.blocks > 1 ? layer_norm_backward_kernel<X, EDGE, true> : layer_norm_backward_kernel<X, EDGE, false>;
-    return launch_rows(kernel, f, smem, s, a);
+    return launch_rows(kernel, f, pair * a.stages, s, a);
 }
 
 }  // namespace
@@ -451,7 +576,7 @@ cudaError_t backward_as(Backward a, const Shape& f, cudaStream_t s) {
 int layer_norm_blocks(int T, int d) { return T == 0 ? 0 : shape_of(T, d, true).clusters; }
 
 cudaError_t launch_layer_norm(const LayerNormArgs& g, cudaStream_t s) {
-    Forward a{g.x, g.h, g.weight, g.bias, g.T, g.d, g.eps, g.drop, g.y, g.n, reinterpret_cast<float2*>(g.stats), 1, 0, 0};
+    Forward a{g.x, g.h, g.weight, g.bias, g.T, g.d, g.eps, g.drop, g.y, g.n, reinterpret_cast<float2*>(g.stats), 1, 0, 2, 0};
     a.vec = aligned({g.x, g.h, g.y, g.n});
     const bool edge = g.d % 8 != 0 || !a.vec || !aligned({g.weight, g.bias});
     using B = __nv_bfloat16;
@@ -464,7 +589,7 @@ cudaError_t launch_layer_norm(const LayerNormArgs& g, cudaStream_t s) {
 }
 
 cudaError_t launch_layer_norm_backward(const LayerNormArgs& g, cudaStream_t s) {
-    Backward a{g.x, reinterpret_cast<const float2*>(g.stats), g.dn, g.dy, g.weight, g.T, g.d, g.drop, g.dx, g.dh, nullptr, 1, 0};
+    Backward a{g.x, reinterpret_cast<const float2*>(g.stats), g.dn, g.dy, g.weight, g.T, g.d, g.drop, g.dx, g.dh, nullptr, 1, 0, 2};
     const bool sums = g.dweight || g.dbias;
     if (sums) a.partial = g.partial;
     a.vec = aligned({g.x, g.dn, g.dy, g.dx, g.dh});

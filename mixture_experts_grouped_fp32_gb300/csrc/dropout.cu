@@ -14,7 +14,7 @@ constexpr int kThreads = 256, kPer = 2;  // vectors of a thread
 
 template <typename X, typename R, bool RES, bool ALIGNED>
 __global__ void __launch_bounds__(kThreads)
-dropout_kernel(const X* x, const R* residual, size_t n, DropArgs args, R* out) {
+dropout_kernel(const X* x, const R* residual, size_t n, const __grid_constant__ DropArgs args, R* out) {
     pdl_wait();
     pdl_trigger();
     const Drop drop(args);

@@ -207,12 +207,13 @@ struct Forward {
 };
 
 template <typename X, bool H, bool EDGE, bool CLUSTER>
-__global__ void __launch_bounds__(1024, 1) layer_norm_kernel(Forward a) {
+__global__ void __launch_bounds__(1024, 1) layer_norm_kernel(const __grid_constant__ Forward a) {
     __shared__ float red[2 * 2 * (CLUSTER ? kMostBlocks * 32 : 32)];
     extern __shared__ uint4 ring[];
     constexpr int W = words<X>() + (H ? 1 : 0);
     const int tid = threadIdx.x, nt = blockDim.x, d = a.d, S = a.stages;
-    const float fd = static_cast<float>(d);  // divided by, so that a constant row has deviations of 0
+    // The mean is divided for, so that a constant row has deviations of 0.
+    const float fd = static_cast<float>(d), inv_d = 1.0f / fd;
     const X* x = static_cast<const X*>(a.x);
     X* y = static_cast<X*>(a.y);
     const long long T = a.T, total = T * d, step = gridDim.x / a.blocks, row0 = blockIdx.x / a.blocks;
@@ -295,7 +296,7 @@ __global__ void __launch_bounds__(1024, 1) layer_norm_kernel(Forward a) {
         }
         s[0] = q.x + q.y;
         row_sum(s);
-        const float r = 1.0f / sqrtf(s[0] / fd + a.eps);
+        const float r = rsqrtf(s[0] * inv_d + a.eps);
         if (tid == 0 && row_sum.rank == 0) a.stats[row0 + k * step] = make_float2(mean, r);
         if (some) {
             const Vec8 w = a.keep ? kept8(0) : e.column(a.weight, 1.0f), b = a.keep ? kept8(1) : e.column(a.bias, 0.0f);
@@ -327,7 +328,7 @@ struct Backward {
 // written once; rows that are narrower than the block lie side by side in it (threadIdx.y), each with its barrier, and
 // their sums are added up first.
 template <typename X, bool EDGE, bool CLUSTER>
-__global__ void __launch_bounds__(512, 1) layer_norm_backward_kernel(Backward a) {
+__global__ void __launch_bounds__(512, 1) layer_norm_backward_kernel(const __grid_constant__ Backward a) {
     __shared__ float red[2 * 4 * (CLUSTER ? kMostBlocks * 16 : 16)];
     extern __shared__ uint4 ring_all[];
     using B = __nv_bfloat16;

@@ -6,18 +6,20 @@
 // its number is at least `cut` = p 65536 (rounded); those that stay are multiplied by 65536 / (65536 - cut), the
 // inverse of the probability itself, so that the expectation is exact for the p that is used.
 //
-// Sixteen bits an element: a block of ten rounds costs about 80 issue slots, ten for each of eight elements; with 32
-// bits it would be twenty, and a bf16 dropout (4 bytes an element) would wait for the arithmetic, not for the memory.
+// Sixteen bits an element: a block of ten rounds serves eight elements; with 32 bits it would be four, and a bf16 dropout
+// (4 bytes an element) would wait for the arithmetic, not for the memory.  The rounds' keys come with the kernel's
+// arguments, as operands of their instructions.
 #pragma once
 
 #include "train_util.cuh"
 
 namespace moe {
 
+constexpr int kRounds = 10;
 struct DropArgs {
     uint32_t cut;  // 0: everything stays
     float up;
-    uint32_t key0, key1;
+    uint32_t key[kRounds][2];  // of each round
     uint64_t offset;
     const int64_t* offset_dev;  // added to the offset, or null
 };
@@ -29,25 +31,25 @@ inline bool drop_args(double p, uint64_t seed, int64_t offset, const int64_t* of
     if (cut > 65535) return false;
     a->cut = static_cast<uint32_t>(cut);
     a->up = static_cast<float>(65536.0 / (65536 - cut));
-    a->key0 = static_cast<uint32_t>(seed);
-    a->key1 = static_cast<uint32_t>(seed >> 32);
+    for (uint32_t r = 0; r < kRounds; ++r) {
+        a->key[r][0] = static_cast<uint32_t>(seed) + r * 0x9E3779B9u;
+        a->key[r][1] = static_cast<uint32_t>(seed >> 32) + r * 0xBB67AE85u;
+    }
     a->offset = static_cast<uint64_t>(offset);
     a->offset_dev = offset_dev;
     return true;
 }
 
-__device__ __forceinline__ uint4 philox(uint32_t k0, uint32_t k1, uint64_t block, uint64_t offset) {
+__device__ __forceinline__ uint4 philox(const DropArgs& a, uint64_t block, uint64_t offset) {
     uint32_t c0 = static_cast<uint32_t>(block), c1 = static_cast<uint32_t>(block >> 32);
     uint32_t c2 = static_cast<uint32_t>(offset), c3 = static_cast<uint32_t>(offset >> 32);
 #pragma unroll
-    for (int r = 0; r < 10; ++r) {
-        const uint64_t a = static_cast<uint64_t>(c0) * 0xD2511F53u, b = static_cast<uint64_t>(c2) * 0xCD9E8D57u;
-        c0 = static_cast<uint32_t>(b >> 32) ^ c1 ^ k0;
-        c1 = static_cast<uint32_t>(b);
-        c2 = static_cast<uint32_t>(a >> 32) ^ c3 ^ k1;
-        c3 = static_cast<uint32_t>(a);
-        k0 += 0x9E3779B9u;
-        k1 += 0xBB67AE85u;
+    for (int r = 0; r < kRounds; ++r) {
+        const uint64_t m0 = static_cast<uint64_t>(c0) * 0xD2511F53u, m1 = static_cast<uint64_t>(c2) * 0xCD9E8D57u;
+        c0 = static_cast<uint32_t>(m1 >> 32) ^ c1 ^ a.key[r][0];
+        c1 = static_cast<uint32_t>(m1);
+        c2 = static_cast<uint32_t>(m0 >> 32) ^ c3 ^ a.key[r][1];
+        c3 = static_cast<uint32_t>(m0);
     }
     return make_uint4(c0, c1, c2, c3);
 }
@@ -78,19 +80,20 @@ int layer_norm_blocks(int T, int d);
 cudaError_t launch_layer_norm(const LayerNormArgs& a, cudaStream_t s);
 cudaError_t launch_layer_norm_backward(const LayerNormArgs& a, cudaStream_t s);
 
-// What a kernel keeps of its arguments.
+// A kernel's use of its arguments (which it must hold as a parameter: the keys are read from there).
 struct Drop {
-    uint32_t cut16, key0, key1;  // cut << 16
-    float up;
+    const DropArgs& args;
+    uint32_t cut16;  // cut << 16
     uint64_t offset;
     __device__ __forceinline__ explicit Drop(const DropArgs& a)
-        : cut16(a.cut << 16), key0(a.key0), key1(a.key1), up(a.up),
+        : args(a), cut16(a.cut << 16),
           offset(a.offset + (a.offset_dev && a.cut ? static_cast<uint64_t>(__ldg(a.offset_dev)) : 0)) {}
     __device__ __forceinline__ bool on() const { return cut16 != 0; }
     // The eight elements from `first` on (a multiple of 8): zeroed or scaled.  What is dropped is 0 whatever it was,
     // an infinity or a NaN too.
     __device__ __forceinline__ void apply(Vec8& v, uint64_t first) const {
-        const uint4 q = philox(key0, key1, first >> 3, offset);
+        const uint4 q = philox(args, first >> 3, offset);
+        const float up = args.up;
         const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {

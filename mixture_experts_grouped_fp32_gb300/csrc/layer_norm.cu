@@ -124,40 +124,38 @@ __device__ __forceinline__ Vec8 ring8(const uint4* word, int nt) {  // (its word
                      __uint_as_float(b.x), __uint_as_float(b.y), __uint_as_float(b.z), __uint_as_float(b.w)}};
     }
 }
-// All but the newest `pending` groups of copies have landed.
-__device__ __forceinline__ void wait_copies(int pending) {
-    if (pending >= 3) ptx::cp_async_wait<3>();
-    else if (pending == 2) ptx::cp_async_wait<2>();
-    else ptx::cp_async_wait<1>();
-}
-
-// A thread's eight of a row: the columns c .. c + 7, of which those from lo to hi - 1 are the row's.
+// A thread's eight of a row: the columns c .. c + 7, of which those from lo to hi - 1 are the row's.  `base` below is
+// where the row's first eight begins in a tensor of `total` values (the same for all threads of a row), `off` the
+// thread's from there.
 template <bool EDGE>
 struct Eight {
+    unsigned off;
     int c, lo, hi;
     bool vec;  // the tensors are aligned for vectors
-    __device__ __forceinline__ Eight(int q, int shift, int d, bool vectors) : c(8 * q - shift), vec(vectors) {
+    __device__ __forceinline__ Eight(int q, int shift, int d, bool vectors) : off(8 * q), c(8 * q - shift), vec(vectors) {
         lo = EDGE ? max(0, -c) : 0;
         hi = min(8, d - c);
     }
     __device__ __forceinline__ bool some() const { return hi > lo; }
     __device__ __forceinline__ bool whole() const { return !EDGE || (lo == 0 && hi == 8); }
-    // On their way to `word`, words nt apart.  `at`: the first value's place in the tensor of `total` values.  Values that
-    // are not the row's may be any.
+    // On their way to `word`, words nt apart.  Values that are not the row's may be any.
     template <typename X>
-    __device__ __forceinline__ void copy(uint4* word, int nt, const X* p, long long at, long long total) const {
+    __device__ __forceinline__ void copy(uint4* word, int nt, const X* p, long long base, long long total) const {
+        const X* from = p + base + off;
         if (!EDGE || vec) {
-            const long long left = EDGE ? (total - at) * static_cast<long long>(sizeof(X)) : 32;  // bytes
+            // (only the tensor's last eight can reach behind its end: zeros are put there)
+            const bool inside = !EDGE || base + off + 8 <= total;
+            const int left = inside ? 32 : static_cast<int>(total - base - off) * static_cast<int>(sizeof(X));  // bytes
             if constexpr (sizeof(X) == 2) {
-                copy_word(word, p + at, static_cast<int>(min(left, 16ll)));
+                copy_word(word, from, min(left, 16));
             } else {
-                copy_word_l1(word, p + at, static_cast<int>(min(left, 16ll)));
-                copy_word_l1(word + nt, p + at + (left > 16 ? 4 : 0), static_cast<int>(max(0ll, min(left - 16, 16ll))));
+                copy_word_l1(word, from, min(left, 16));
+                copy_word_l1(word + nt, left > 16 ? from + 4 : from, max(0, min(left - 16, 16)));
             }
         } else {
             Vec8 v;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v.v[j] = j >= lo && j < hi ? to_float(p[at + j]) : 0.0f;
+            for (int j = 0; j < 8; ++j) v.v[j] = j >= lo && j < hi ? to_float(from[j]) : 0.0f;
             if constexpr (sizeof(X) == 2) {
                 *word = pack8(v);
             } else {
@@ -174,13 +172,14 @@ struct Eight {
         }
     }
     template <typename X>
-    __device__ __forceinline__ void store(X* p, long long at, const Vec8& v) const {
+    __device__ __forceinline__ void store(X* p, long long base, const Vec8& v) const {
+        X* to = p + base + off;
         if (!EDGE || (vec && whole())) {
-            store8(p + at, 0, v);
+            store8(to, 0, v);
         } else {
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-                if (j >= lo && j < hi) put(p + at + j, v.v[j]);
+                if (j >= lo && j < hi) put(to + j, v.v[j]);
         }
     }
     // Of a vector over the columns, or `none` without it.
@@ -203,20 +202,25 @@ struct Forward {
     void* y;
     __nv_bfloat16* n;
     float2* stats;
-    int blocks, vec, stages, keep;  // blocks of a cluster; rows in the ring; keep: the weights lie behind the ring
+    int blocks, vec, keep;  // blocks of a cluster; keep: the weights lie behind the ring
 };
+
+constexpr int kStages = 3;  // rows in the forward pass' ring
+// Pairs of rows in the backward pass' (512 threads: 144 KB, 160 KB with an fp32 stream).
+template <typename X>
+constexpr int pair_stages() { return sizeof(X) == 4 ? 2 : 3; }
 
 template <typename X, bool H, bool EDGE, bool CLUSTER>
 __global__ void __launch_bounds__(1024, 1) layer_norm_kernel(const __grid_constant__ Forward a) {
     __shared__ float red[2 * 2 * (CLUSTER ? kMostBlocks * 32 : 32)];
     extern __shared__ uint4 ring[];
     constexpr int W = words<X>() + (H ? 1 : 0);
-    const int tid = threadIdx.x, nt = blockDim.x, d = a.d, S = a.stages;
+    const int tid = threadIdx.x, nt = blockDim.x, d = a.d;
     // The mean is divided for, so that a constant row has deviations of 0.
     const float fd = static_cast<float>(d), inv_d = 1.0f / fd;
     const X* x = static_cast<const X*>(a.x);
     X* y = static_cast<X*>(a.y);
-    const long long T = a.T, total = T * d, step = gridDim.x / a.blocks, row0 = blockIdx.x / a.blocks;
+    const long long T = a.T, total = T * d, step = gridDim.x / a.blocks, row0 = blockIdx.x / a.blocks, row = step * d;
     const int rows = static_cast<int>((T - row0 - 1) / step) + 1;
     if (CLUSTER) ptx::cluster_arrive();  // (the other blocks' memory is there once all have begun)
     pdl_wait();
@@ -226,11 +230,12 @@ __global__ void __launch_bounds__(1024, 1) layer_norm_kernel(const __grid_consta
     const int shift = EDGE ? static_cast<int>(row0 * d & 7) : 0;
     const Eight<EDGE> e((CLUSTER ? row_sum.rank * nt : 0) + tid, shift, d, a.vec != 0);
     const bool some = e.some();
-    long long in = row0 * d + e.c;  // the next row's place, of those that are copied
-    const long long row = step * d;
-    uint4* slot = ring + tid;  // the next row's words
-    uint4* const last = ring + (S - 1) * W * nt + tid;
+    long long in = row0 * d - shift, out = in;  // where the row to copy next begins, and the one to write
     int copied = 0;
+    uint4* const first = ring + tid;
+    uint4* slot = first;  // the words of the row to copy next, of the row to take next
+    const uint4* word = first;
+    uint4* const last = first + (kStages - 1) * W * nt;
     auto fetch = [&] {
         if (copied < rows && some) {
             e.copy(slot, nt, x, in, total);
@@ -238,11 +243,12 @@ __global__ void __launch_bounds__(1024, 1) layer_norm_kernel(const __grid_consta
         }
         ptx::cp_async_commit();
         in += row;
-        slot = slot == last ? ring + tid : slot + W * nt;
+        slot = slot == last ? first : slot + W * nt;
         ++copied;
     };
-    for (int k = 0; k < S; ++k) fetch();
-    float4* const kept = reinterpret_cast<float4*>(ring + S * W * nt) + tid;  // a thread's own words: no barrier
+#pragma unroll
+    for (int k = 0; k < kStages; ++k) fetch();
+    float4* const kept = reinterpret_cast<float4*>(ring + kStages * W * nt) + tid;  // a thread's own words: no barrier
     if (a.keep && some) {
         const Vec8 w = e.column(a.weight, 1.0f), b = e.column(a.bias, 0.0f);
         kept[0] = make_float4(w.v[0], w.v[1], w.v[2], w.v[3]);
@@ -255,41 +261,41 @@ __global__ void __launch_bounds__(1024, 1) layer_norm_kernel(const __grid_consta
         return Vec8{{p.x, p.y, p.z, p.w, q.x, q.y, q.z, q.w}};
     };
     const Drop drop(a.drop);
-    const uint4* word = ring + tid;  // the row that is taken next
-    auto take = [&](Vec8& v, long long at) {  // the stream's values, stored with H; their sum
+    auto take = [&](Vec8& v, long long base) {  // the stream's values, stored with H; their sum
         float2 s = make_float2(0.0f, 0.0f);
         if (some) {
             v = ring8<X>(word, nt);
             if (H) {
                 Vec8 hv = ring8<__nv_bfloat16>(word + words<X>() * nt, nt);
-                if (drop.on()) drop.apply(hv, at);
+                if (drop.on()) drop.apply(hv, base + e.off);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) v.set(j, add2(v.pair(j), hv.pair(j)));
                 v = rounded(v, static_cast<const X*>(nullptr));
-                e.store(y, at, v);
+                e.store(y, base, v);
             }
             e.mask(v);
             s = v.pair(0);
 #pragma unroll
             for (int j = 1; j < 4; ++j) s = add2(s, v.pair(j));
         }
-        word = word == last ? ring + tid : word + W * nt;
+        word = word == last ? first : word + W * nt;
         return s.x + s.y;
     };
     Vec8 cur, nxt;
-    long long at = row0 * d + e.c;
-    wait_copies(S - 1);
-    float s[2] = {0.0f, take(cur, at)};
+    ptx::cp_async_wait<kStages - 1>();
+    float s[2] = {0.0f, take(cur, out)};
     row_sum(s);
-    for (int k = 0; k < rows; ++k, at += row) {
+    float2* stats = a.stats + row0;
+    for (int k = 0; k < rows; ++k) {
         const float mean = s[1] / fd;
         fetch();
-        wait_copies(S - 1);
-        s[1] = k + 1 < rows ? take(nxt, at + row) : 0.0f;
+        ptx::cp_async_wait<kStages - 1>();
+        s[1] = k + 1 < rows ? take(nxt, out + row) : 0.0f;
         float2 q = make_float2(0.0f, 0.0f);
         if (some) {
+            const float2 back = make_float2(-mean, -mean);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) cur.set(j, add2(cur.pair(j), make_float2(-mean, -mean)));
+            for (int j = 0; j < 4; ++j) cur.set(j, add2(cur.pair(j), back));
             e.mask(cur);
 #pragma unroll
             for (int j = 0; j < 4; ++j) q = fma2(cur.pair(j), cur.pair(j), q);
@@ -297,14 +303,16 @@ __global__ void __launch_bounds__(1024, 1) layer_norm_kernel(const __grid_consta
         s[0] = q.x + q.y;
         row_sum(s);
         const float r = rsqrtf(s[0] * inv_d + a.eps);
-        if (tid == 0 && row_sum.rank == 0) a.stats[row0 + k * step] = make_float2(mean, r);
+        if (tid == 0 && row_sum.rank == 0) *stats = make_float2(mean, r);
+        stats += step;
         if (some) {
             const Vec8 w = a.keep ? kept8(0) : e.column(a.weight, 1.0f), b = a.keep ? kept8(1) : e.column(a.bias, 0.0f);
             Vec8 o;
 #pragma unroll
             for (int j = 0; j < 4; ++j) o.set(j, fma2(mul2(cur.pair(j), r), w.pair(j), b.pair(j)));
-            e.store(a.n, at, o);
+            e.store(a.n, out, o);
         }
+        out += row;
         cur = nxt;
     }
     ptx::cp_async_wait_all();
@@ -321,7 +329,7 @@ struct Backward {
     void* dx;
     __nv_bfloat16* dh;
     float* partial;  // [clusters, 2, d], or null
-    int blocks, vec, stages;  // stages: pairs of rows in the ring
+    int blocks, vec;
 };
 
 // Two rows at a time.  The column sums dweight and dbias of the rows that a block visits stay in registers and are
@@ -349,18 +357,19 @@ __global__ void __launch_bounds__(512, 1) layer_norm_backward_kernel(const __gri
     const Eight<EDGE> e((CLUSTER ? row_sum.rank * nt : 0) + tid, shift, d, a.vec != 0);
     const bool some = e.some();
     // Words of a row: x, dn, dy.
-    constexpr int o_dn = words<X>(), o_dy = o_dn + 1;
-    const int W = o_dy + (dy ? words<X>() : 0), S = a.stages;
-    uint4* const ring = ring_all + group * (S * 2 * W * nt) + tid;
+    constexpr int o_dn = words<X>(), o_dy = o_dn + 1, W = o_dy + words<X>(), S = pair_stages<X>();
     const long long row = step * d;
-    long long in = row0 * d + e.c;
-    int copied = 0, slot = 0;
-    float2 st[2] = {}, next[2] = {};
+    long long in = row0 * d - shift, out = in;  // where the row to copy next begins, and the one to write
+    uint4* const first = ring_all + group * (S * 2 * W * nt) + tid;
+    uint4* const last = first + (S - 1) * 2 * W * nt;
+    uint4* slot = first;  // the words of the rows to copy next, of the rows to work on
+    const uint4* word = first;
+    int copied = 0;
     auto fetch = [&] {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             if (copied < rows && some) {
-                uint4* w = ring + (2 * slot + i) * W * nt;
+                uint4* w = slot + i * W * nt;
                 e.copy(w, nt, x, in, total);
                 e.copy(w + o_dn * nt, nt, a.dn, in, total);
                 if (dy) e.copy(w + o_dy * nt, nt, dy, in, total);
@@ -369,44 +378,48 @@ __global__ void __launch_bounds__(512, 1) layer_norm_backward_kernel(const __gri
             ++copied;
         }
         ptx::cp_async_commit();
-        slot = slot + 1 == S ? 0 : slot + 1;
+        slot = slot == last ? first : slot + 2 * W * nt;
     };
-    auto read_stats = [&](int k) {
+    float2 st[2] = {}, next[2] = {};
+    const float2* stats = a.stats + row0;  // of the rows to read next
+    int stats_left = rows;
+    auto read_stats = [&] {
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-            if (k + i < rows) next[i] = __ldg(a.stats + row0 + (k + i) * step);
+        for (int i = 0; i < 2; ++i) {
+            if (stats_left > 0) next[i] = __ldg(stats);
+            stats += step;
+            --stats_left;
+        }
     };
+#pragma unroll
     for (int k = 0; k + 1 < S; ++k) fetch();
-    read_stats(0);
+    read_stats();
     const Vec8 w = some ? e.column(a.weight, 1.0f) : Vec8{};
     Vec8 sw{}, sb{};
-    long long at = row0 * d + e.c;
-    int now = 0;  // the slot of these rows
-    for (int k = 0; k < rows; k += 2, at += 2 * row) {
+    for (int k = 0; k < rows; k += 2) {
         fetch();
         st[0] = next[0], st[1] = next[1];
-        read_stats(k + 2);
-        wait_copies(S - 1);
-        const uint4* words_of[2] = {ring + 2 * now * W * nt, ring + (2 * now + 1) * W * nt};
-        now = now + 1 == S ? 0 : now + 1;
+        read_stats();
+        ptx::cp_async_wait<S - 1>();
         const bool two = k + 1 < rows;
         Vec8 yh[2], g[2];
         float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int i = 0; i < 2; ++i)
             if (some && (i == 0 || two)) {
-                const float r = st[i].y, back = -st[i].x;
-                float2 sg = make_float2(0.0f, 0.0f), sy = sg;
-                yh[i] = ring8<X>(words_of[i], nt);
-                Vec8 nv = ring8<B>(words_of[i] + o_dn * nt, nt);
+                const float r = st[i].y;
+                const float2 back = make_float2(-st[i].x, -st[i].x);
+                float2 sg, sy;
+                yh[i] = ring8<X>(word + i * W * nt, nt);
+                Vec8 nv = ring8<B>(word + (i * W + o_dn) * nt, nt);
                 e.mask(yh[i]);
                 e.mask(nv);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    yh[i].set(j, mul2(add2(yh[i].pair(j), make_float2(back, back)), r));
+                    yh[i].set(j, mul2(add2(yh[i].pair(j), back), r));
                     g[i].set(j, mul2(nv.pair(j), w.pair(j)));
-                    sg = add2(sg, g[i].pair(j));
-                    sy = fma2(g[i].pair(j), yh[i].pair(j), sy);
+                    sg = j ? add2(sg, g[i].pair(j)) : g[i].pair(j);
+                    sy = j ? fma2(g[i].pair(j), yh[i].pair(j), sy) : mul2(g[i].pair(j), yh[i].pair(j));
                     sw.set(j, fma2(nv.pair(j), yh[i].pair(j), sw.pair(j)));
                     sb.set(j, add2(sb.pair(j), nv.pair(j)));
                 }
@@ -415,21 +428,30 @@ __global__ void __launch_bounds__(512, 1) layer_norm_backward_kernel(const __gri
             }
         row_sum(s);
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+        for (int i = 0; i < 2; ++i) {
             if (some && (i == 0 || two)) {
-                const float mg = s[2 * i] * inv_d, my = s[2 * i + 1] * inv_d;
-                Vec8 o = dy ? ring8<X>(words_of[i] + o_dy * nt, nt) : Vec8{};
+                // (r taken into the means: r (g - mg - yh my) + dy)
+                const float r = st[i].y, mg = -s[2 * i] * inv_d * r, my = -s[2 * i + 1] * inv_d * r;
+                Vec8 o;
+                if (dy) {
+                    o = ring8<X>(word + (i * W + o_dy) * nt, nt);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float2 b = fma2(yh[i].pair(j), make_float2(-my, -my), add2(g[i].pair(j), make_float2(-mg, -mg)));
-                    o.set(j, fma2(b, st[i].y, o.pair(j)));
+                    for (int j = 0; j < 4; ++j) o.set(j, add2(o.pair(j), make_float2(mg, mg)));
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) o.v[j] = mg;
                 }
-                e.store(dx, at + i * row, o);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) o.set(j, fma2(g[i].pair(j), r, fma2(yh[i].pair(j), my, o.pair(j))));
+                e.store(dx, out, o);
                 if (a.dh) {
-                    if (drop.on()) drop.apply(o, at + i * row);
-                    e.store(a.dh, at + i * row, o);
+                    if (drop.on()) drop.apply(o, out + e.off);
+                    e.store(a.dh, out, o);
                 }
             }
+            out += row;
+        }
+        word = word == last ? first : word + 2 * W * nt;
     }
     ptx::cp_async_wait_all();
     if (!a.partial) return;
@@ -437,7 +459,7 @@ __global__ void __launch_bounds__(512, 1) layer_norm_backward_kernel(const __gri
     const Eight<EDGE> column(some ? (e.c + shift) / 8 : 0, shift, d, false);  // (the rows of `partial` start anywhere)
     auto write = [&](float* to, const Vec8& v) {
         if (!EDGE) store8(to + e.c, 0, v);
-        else column.store(to, e.c, v);
+        else column.store(to - shift, 0, v);
     };
     if (groups > 1) {
         float* sums = reinterpret_cast<float*>(ring_all);  // [rows side by side][8][threads of a row], once all are done
@@ -516,7 +538,7 @@ Shape shape_of(int T, int d, bool bwd) {
     return s;
 }
 
-constexpr size_t kMostSmem = 200 * 1024;  // of the blocks of an SM, for their rings
+constexpr size_t kMostSmem = 216 * 1024;  // of a block's ring and weights (1024 threads: 208 KB)
 
 // Dynamic shared memory beyond what a launch gets unasked (48 KB with the static one).
 template <typename... KArgs>
@@ -546,29 +568,22 @@ cudaError_t launch_rows(void (*kernel)(KArgs...), const Shape& f, size_t smem, c
     return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
 }
 
-// Stages of a ring (2 to 4), each of `stage` bytes, beside `other` bytes, in a block of which `per_sm` share an SM.
-int stages_for(size_t stage, size_t other, int per_sm) {
-    const size_t fit = (kMostSmem / per_sm - other) / stage;
-    return fit >= 4 ? 4 : fit >= 3 ? 3 : 2;
-}
-
 template <typename X, bool H, bool EDGE>
 cudaError_t forward_as(Forward a, cudaStream_t s) {
     const Shape f = shape_of(a.T, a.d, false);
     a.blocks = f.blocks;
     a.keep = a.T > f.clusters;  // more than one row to a block: the weights are read once
-    const size_t stage = sizeof(uint4) * (words<X>() + (H ? 1 : 0)) * f.threads, weights = a.keep ? sizeof(float4) * 4 * f.threads : 0;
-    a.stages = a.keep ? stages_for(stage, weights, std::max(1, 1024 / f.threads)) : 2;
+    const size_t words_of_row = words<X>() + (H ? 1 : 0);
+    const size_t smem = sizeof(uint4) * f.threads * (kStages * words_of_row + (a.keep ? 4 : 0));
     const auto kernel = f.blocks > 1 ? layer_norm_kernel<X, H, EDGE, true> : layer_norm_kernel<X, H, EDGE, false>;
-    return launch_rows(kernel, f, stage * a.stages + weights, s, a);
+    return launch_rows(kernel, f, smem, s, a);
 }
 template <typename X, bool EDGE>
 cudaError_t backward_as(Backward a, const Shape& f, cudaStream_t s) {
     a.blocks = f.blocks;
-    const size_t pair = sizeof(uint4) * 2 * (words<X>() * (a.dy ? 2 : 1) + 1) * f.threads * f.groups;
-    a.stages = stages_for(pair, 0, std::max(1, 512 / (f.threads * f.groups)));
+    const size_t smem = sizeof(uint4) * pair_stages<X>() * 2 * (2 * words<X>() + 1) * f.threads * f.groups;
     const auto kernel = f.blocks > 1 ? layer_norm_backward_kernel<X, EDGE, true> : layer_norm_backward_kernel<X, EDGE, false>;
-    return launch_rows(kernel, f, pair * a.stages, s, a);
+    return launch_rows(kernel, f, smem, s, a);
 }
 
 }  // namespace
@@ -577,7 +592,7 @@ cudaError_t backward_as(Backward a, const Shape& f, cudaStream_t s) {
 int layer_norm_blocks(int T, int d) { return T == 0 ? 0 : shape_of(T, d, true).clusters; }
 
 cudaError_t launch_layer_norm(const LayerNormArgs& g, cudaStream_t s) {
-    Forward a{g.x, g.h, g.weight, g.bias, g.T, g.d, g.eps, g.drop, g.y, g.n, reinterpret_cast<float2*>(g.stats), 1, 0, 2, 0};
+    Forward a{g.x, g.h, g.weight, g.bias, g.T, g.d, g.eps, g.drop, g.y, g.n, reinterpret_cast<float2*>(g.stats), 1, 0, 0};
     a.vec = aligned({g.x, g.h, g.y, g.n});
     const bool edge = g.d % 8 != 0 || !a.vec || !aligned({g.weight, g.bias});
     using B = __nv_bfloat16;
@@ -590,7 +605,7 @@ cudaError_t launch_layer_norm(const LayerNormArgs& g, cudaStream_t s) {
 }
 
 cudaError_t launch_layer_norm_backward(const LayerNormArgs& g, cudaStream_t s) {
-    Backward a{g.x, reinterpret_cast<const float2*>(g.stats), g.dn, g.dy, g.weight, g.T, g.d, g.drop, g.dx, g.dh, nullptr, 1, 0, 2};
+    Backward a{g.x, reinterpret_cast<const float2*>(g.stats), g.dn, g.dy, g.weight, g.T, g.d, g.drop, g.dx, g.dh, nullptr, 1, 0};
     const bool sums = g.dweight || g.dbias;
     if (sums) a.partial = g.partial;
     a.vec = aligned({g.x, g.dn, g.dy, g.dx, g.dh});

@@ -138,7 +138,7 @@ int moe_layer_norm(const void* x, int x_fp32, const void* h, const float* weight
 
 size_t moe_layer_norm_backward_workspace_size(int T, int d) {
     if (check_norm_rows("moe_layer_norm_backward_workspace_size", T, d) != MOE_OK) return 0;
-    return sizeof(float) * 2 * static_cast<size_t>(d) * layer_norm_blocks(T, d);
+    return sizeof(float) * 2 * static_cast<size_t>(layer_norm_width(d)) * layer_norm_blocks(T, d);
 }
 
 int moe_layer_norm_backward(const void* x, int x_fp32, const float* stats, const void* dn, const void* dy,

@@ -74,9 +74,10 @@ struct LayerNormArgs {
     void* dx;
     __nv_bfloat16* dh;
     float *dweight, *dbias;
-    float* partial;           // [layer_norm_blocks(T, d), 2, d]
+    float* partial;           // [layer_norm_blocks(T, d), 2, layer_norm_width(d)]
 };
 int layer_norm_blocks(int T, int d);
+int layer_norm_width(int d);
 cudaError_t launch_layer_norm(const LayerNormArgs& a, cudaStream_t s);
 cudaError_t launch_layer_norm_backward(const LayerNormArgs& a, cudaStream_t s);
 

@@ -18,8 +18,8 @@
 //
 // LANES threads to a token (8 for up to 64 experts, else 32), each with up to EPL neighbouring experts of one group, so
 // that lower lanes hold lower experts and a tie goes to the lowest lane.  A lane sorts its experts once, as integers
-// with the order of c; a slot then costs one maximum over the lanes' first ones (one instruction for a warp) and a
-// shift in the lane that held it.  Which expert a slot's integer belongs to is looked up for all slots at once.
+// with the order of c; a slot then costs one maximum over the lanes' first ones (one instruction for a warp), and the
+// lane that held it reads its next one.  Which expert a slot's integer belongs to is looked up for all slots at once.
 // Bound by instructions, not by the T E logits that are read.
 #include <climits>
 #include <cmath>
@@ -55,6 +55,8 @@ __device__ __forceinline__ uint32_t ordered(float v) {
     const uint32_t u = __float_as_uint(v + 0.0f);
     return v != v ? 1u : u ^ (static_cast<uint32_t>(static_cast<int32_t>(u) >> 31) | 0x80000000u);
 }
+
+__device__ __forceinline__ float sigmoid(float l) { return 1.0f / (1.0f + expf(-l)); }
 
 template <int LANES>
 __device__ __forceinline__ float lanes_sum(float v) {
@@ -109,100 +111,152 @@ struct RouteArgs {
 };
 
 // ---------------------------------------------------------------------------------------------
-// The choice in fp64: slot j's expert in lane j.
+// The choice in fp64: slot j's expert in lane j.  Only the experts that the fp32 values leave in question are computed
+// again, a lane's one after another: in each group those that may be of its q largest, and then in the kept groups those
+// that may be of the k largest.  (Seldom run, so kept small: cold instructions take as long as the arithmetic.)
 // ---------------------------------------------------------------------------------------------
 __device__ __forceinline__ unsigned long long ordered(double v) {
     const long long u = __double_as_longlong(v + 0.0);
     return v != v ? 1ull : static_cast<unsigned long long>(u ^ ((u >> 63) | static_cast<long long>(0x8000000000000000ull)));
 }
+__device__ __forceinline__ double key_value64(unsigned long long k) {
+    return k == 1ull ? static_cast<double>(NAN) : __longlong_as_double(static_cast<long long>(k >> 63 ? k ^ 0x8000000000000000ull : ~k));
+}
+struct Exact {
+    int E, k, G, kept, sigmoid;
+};
 template <int LANES, int EPL, typename L>
-__device__ __noinline__ int choose64(const L* row, const RouteArgs& a, const Place& p) {
+__device__ __noinline__ int choose64(const L* row, const float* bias, Exact a) {
     using Key = unsigned long long;
-    double c[EPL];
+    const Place p(LANES, a.E, a.G);
+    const int lane = threadIdx.x & 31;
     float top = -INFINITY;
     bool nan = false;
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) {
-        const float l = i < p.count ? logit(row + p.first + i) : -INFINITY;
-        c[i] = l;
-        nan |= l != l;
+    double total = 1.0;
+#pragma unroll 1
+    for (int i = 0; i < p.count; ++i) {
+        const float l = logit(row + p.first + i);
+        nan |= l != l || (bias && bias[p.first + i] != bias[p.first + i]);
         top = fmaxf(top, l);
     }
-    if (a.sigmoid) {
-#pragma unroll
-        for (int i = 0; i < EPL; ++i) c[i] = 1.0 / (1.0 + exp(-c[i]));
-    } else {
+    if (!a.sigmoid) {
         top = lanes_max<LANES>(top);
-        double s = nan ? static_cast<double>(NAN) : 0.0;
-#pragma unroll
-        for (int i = 0; i < EPL; ++i) {
-            c[i] = top == -INFINITY ? 0.0 : exp(c[i] - static_cast<double>(top));
-            s += i < p.count ? c[i] : 0.0;
+        nan |= top == INFINITY;
+        total = nan ? static_cast<double>(NAN) : 0.0;
+#pragma unroll 2
+        for (int i = 0; i < p.count; ++i) {
+            const float l = logit(row + p.first + i);
+            if (top > -INFINITY) total += exp(static_cast<double>(l) - static_cast<double>(top));
         }
-        s = lanes_sum<LANES>(s);
-#pragma unroll
-        for (int i = 0; i < EPL; ++i) c[i] = top == -INFINITY && s == s ? 0.0 : c[i] / s;
+        total = lanes_sum<LANES>(total);
     }
-    Key key[EPL];
+    auto exactly = [&](int e) {
+        const float l = logit(row + e);
+        double c;
+        if (a.sigmoid) c = 1.0 / (1.0 + exp(-static_cast<double>(l)));
+        else c = top == -INFINITY && total == total ? 0.0 : exp(static_cast<double>(l) - static_cast<double>(top)) / total;
+        return bias ? c + static_cast<double>(__ldg(bias + e)) : c;
+    };
+    // In fp32, and how far off that may be.
+    float c[EPL], size = 0.0f, score = 0.0f;
+    const float inv = 1.0f / static_cast<float>(total);
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
-        if (i < p.count && a.bias) c[i] += static_cast<double>(__ldg(a.bias + p.first + i));
-        key[i] = i < p.count ? ordered(c[i]) : 0ull;
+        c[i] = -INFINITY;
+        if (i < p.count) {
+            const float l = logit(row + p.first + i), s = a.sigmoid ? sigmoid(l) : top == -INFINITY ? 0.0f : expf(l - top) * inv;
+            c[i] = bias ? s + __ldg(bias + p.first + i) : s;
+            size = fmaxf(size, fabsf(c[i]));
+            score = fmaxf(score, s);
+        }
     }
-    // The largest key of `lanes` neighbouring lanes, and the first lane and place that hold it.
-    auto best = [&](int lanes, Key& all, bool& mine, int& at) {
+    const float off = a.sigmoid ? kSigmoidRel + kSigmoidAbs : kSoftmaxRel * lanes_max<LANES>(score) + 0.37f * kSoftmaxArg;
+    const float margin = 2.0f * (off + 1.2e-7f * lanes_max<LANES>(size));
+    nan = __any_sync(kAll, nan);  // then every expert of the warp's tokens is in question
+    Key key[EPL];
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) key[i] = 0ull;
+    unsigned open = (1u << p.count) - 1, known = 0u;  // experts that may be chosen; that are computed
+    // The n-th largest fp32 value of the open experts of `lanes` lanes.
+    auto nth = [&](int n, int lanes) {
+        unsigned left = open;
+        uint32_t all = 0u;
+#pragma unroll 1
+        for (int r = 0; r < n; ++r) {
+            uint32_t m = 0u;
+            int at = 0;
+#pragma unroll
+            for (int i = 0; i < EPL; ++i)
+                if ((left >> i & 1u) && ordered(c[i]) > m) {
+                    m = ordered(c[i]);
+                    at = i;
+                }
+            all = m;
+            for (int o = lanes / 2; o > 0; o >>= 1) all = max(all, __shfl_xor_sync(kAll, all, o));
+            const unsigned has = __ballot_sync(kAll, m == all) >> (lane & ~(lanes - 1));
+            if ((lane & (lanes - 1)) == __ffs(has) - 1) left &= ~(1u << at);
+        }
+        return all <= 1u ? -INFINITY : __uint_as_float(all & 0x80000000u ? all ^ 0x80000000u : ~all);
+    };
+    auto compute = [&](float from) {  // the open experts whose fp32 value is `from` at least
+        unsigned todo = 0u;
+#pragma unroll
+        for (int i = 0; i < EPL; ++i)
+            if (((open & ~known) >> i & 1u) && (nan || !(c[i] < from))) todo |= 1u << i;
+        known |= todo;
+#pragma unroll 1
+        while (__any_sync(kAll, todo != 0u)) {
+            const int at = todo ? __ffs(todo) - 1 : -1;
+            const Key v = todo ? ordered(exactly(p.first + at)) : 0ull;
+            todo &= todo - 1;
+#pragma unroll
+            for (int i = 0; i < EPL; ++i)
+                if (i == at) key[i] = v;
+        }
+    };
+    // The largest key of `lanes` neighbouring lanes, taken out where the first lane and place hold it (that expert, there).
+    unsigned out = 0u;
+    auto best = [&](int lanes, bool& mine, int& at) {
         Key m = 0ull;
         at = 0;
 #pragma unroll
         for (int i = 0; i < EPL; ++i)
-            if (key[i] > m) {
+            if (((open & ~out) >> i & 1u) && key[i] > m) {
                 m = key[i];
                 at = i;
             }
-        all = m;
+        Key all = m;
         for (int o = lanes / 2; o > 0; o >>= 1) all = max(all, __shfl_xor_sync(kAll, all, o));
-        const int lane = threadIdx.x & 31;
         const unsigned has = __ballot_sync(kAll, m == all) >> (lane & ~(lanes - 1));
         mine = (lane & (lanes - 1)) == __ffs(has) - 1;
+        if (mine) out |= 1u << at;
+        return all;
     };
-    auto take_out = [&](int at) {
-#pragma unroll
-        for (int i = 0; i < EPL; ++i)
-            if (i == at) key[i] = 0ull;
-    };
-    if (a.G > 1) {
-        Key kept_keys[EPL];
-#pragma unroll
-        for (int i = 0; i < EPL; ++i) kept_keys[i] = key[i];
+    bool mine;
+    int at;
+    if (a.kept < a.G) {
         const int q = min(a.E / a.G, max(1, a.k / a.kept));
-        double score = 0.0;
-        for (int r = 0; r < q; ++r) {
-            Key all;
-            bool mine;
-            int at;
-            best(p.per_group, all, mine, at);
-            score += all == 1ull ? static_cast<double>(NAN)
-                                 : __longlong_as_double(static_cast<long long>(all >> 63 ? all ^ 0x8000000000000000ull : ~all));
-            if (mine) take_out(at);
-        }
-        const Key own = ordered(score);
+        compute(nth(q, p.per_group) - margin);
+        double sum = 0.0;
+#pragma unroll 1
+        for (int r = 0; r < q; ++r) sum += key_value64(best(p.per_group, mine, at));
+        const Key own = ordered(sum);
         int rank = 0;
+#pragma unroll 1
         for (int g = 0; g < a.G; ++g) {
             const Key v = __shfl_sync(kAll, own, g * p.per_group, LANES);
             rank += v > own || (v == own && g < p.group);
         }
-#pragma unroll
-        for (int i = 0; i < EPL; ++i) key[i] = rank < a.kept ? kept_keys[i] : 0ull;
+        if (rank >= a.kept || p.group >= a.G) open = 0u;
+        out = 0u;
     }
+    compute(nth(a.k, LANES) - margin);
     int slot = 0;
+#pragma unroll 1
     for (int j = 0; j < a.k; ++j) {
-        Key all;
-        bool mine;
-        int at;
-        best(LANES, all, mine, at);
-        const unsigned who = __ballot_sync(kAll, mine) >> (threadIdx.x & 31 & ~(LANES - 1));
+        best(LANES, mine, at);
+        const unsigned who = __ballot_sync(kAll, mine) >> (lane & ~(LANES - 1));
         const int e = __shfl_sync(kAll, p.first + at, __ffs(who) - 1, LANES);
-        if (mine) take_out(at);
         if (p.sub == j) slot = e;
     }
     return slot;
@@ -222,7 +276,6 @@ __device__ __forceinline__ float eight_max(float v) {
     for (int o = 4; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, o));
     return v;
 }
-__device__ __forceinline__ float sigmoid(float l) { return 1.0f / (1.0f + expf(-l)); }
 
 // Shares of the chosen scores in their sum (`in`: this lane has a slot), and 1 / sum for the gradient's use.
 __device__ __forceinline__ float share_of_chosen(float l, bool in, bool sig) {
@@ -258,12 +311,6 @@ __device__ __forceinline__ void sort_falling(uint32_t (&k)[N]) {
                         k[i + j] = hi;
                         k[i + j + q] = lo;
                     }
-}
-template <int N>
-__device__ __forceinline__ void drop_first(uint32_t (&k)[N], bool mine) {
-#pragma unroll
-    for (int i = 0; i + 1 < N; ++i) k[i] = mine ? k[i + 1] : k[i];
-    k[N - 1] = mine ? 0u : k[N - 1];
 }
 // The value of a key (-inf of none, NaN as none: rows with NaN are done in fp64).
 __device__ __forceinline__ float key_value(uint32_t k) {
@@ -309,6 +356,7 @@ __device__ __forceinline__ void read_row(float (&l)[EPL], const __nv_bfloat16* p
 
 template <int LANES, int EPL, typename L>
 __global__ void __launch_bounds__(kWarps * 32) route_scores_kernel(const L* __restrict__ logits, RouteArgs a) {
+    __shared__ uint32_t lists[kWarps][EPL][32];  // each lane's keys, the largest first (read by that lane alone)
     pdl_wait();
     pdl_trigger();
     constexpr int kTokens = 32 / LANES;
@@ -389,16 +437,25 @@ __global__ void __launch_bounds__(kWarps * 32) route_scores_kernel(const L* __re
         }
     }
     bool sure = plain || !nan;  // the fp32 order is that of the definition
-    uint32_t first[EPL];
+    uint32_t head;  // the largest that is left of this lane's keys, at `pos` of its list
+    float t1, t2;   // the largest two
+    {
+        uint32_t sorted[EPL];
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) first[i] = key[i];
-    sort_falling<EPL>(first);
+        for (int i = 0; i < EPL; ++i) sorted[i] = key[i];
+        sort_falling<EPL>(sorted);
+        head = sorted[0];
+        t1 = key_value(sorted[0]);
+        t2 = EPL > 1 ? key_value(sorted[EPL > 1 ? 1 : 0]) : -INFINITY;
+#pragma unroll
+        for (int i = 1; i < EPL; ++i) lists[threadIdx.x >> 5][i][lane] = sorted[i];
+    }
+    auto next_of = [&](int& pos) { return ++pos < EPL ? lists[threadIdx.x >> 5][pos][lane] : 0u; };
     if (a.G > 1 && a.kept < a.G) {
         // A group's score: its q largest, all groups at once.
         const int q = min(size, max(1, a.k / a.kept));
         float sum, bulk;  // bulk: sum of sizes
         if (q <= 2) {
-            float t1 = key_value(first[0]), t2 = EPL > 1 ? key_value(first[EPL > 1 ? 1 : 0]) : -INFINITY;
             for (int o = p.per_group / 2; o > 0; o >>= 1) {
                 const float o1 = __shfl_xor_sync(kAll, t1, o), o2 = __shfl_xor_sync(kAll, t2, o);
                 t2 = fmaxf(fminf(t1, o1), fmaxf(t2, o2));
@@ -407,15 +464,14 @@ __global__ void __launch_bounds__(kWarps * 32) route_scores_kernel(const L* __re
             sum = q == 2 ? t1 + t2 : t1;
             bulk = fabsf(t1) + (q == 2 ? fabsf(t2) : 0.0f);
         } else {
-            uint32_t rest[EPL];
-#pragma unroll
-            for (int i = 0; i < EPL; ++i) rest[i] = first[i];
+            uint32_t rest = head;
+            int pos = 0;
             sum = bulk = 0.0f;
             for (int r = 0; r < q; ++r) {
-                uint32_t all = rest[0];
+                uint32_t all = rest;
                 for (int o = p.per_group / 2; o > 0; o >>= 1) all = max(all, __shfl_xor_sync(kAll, all, o));
-                const unsigned has = __ballot_sync(kAll, rest[0] == all) >> (lane & ~(p.per_group - 1));
-                drop_first<EPL>(rest, (lane & (p.per_group - 1)) == __ffs(has) - 1);
+                const unsigned has = __ballot_sync(kAll, rest == all) >> (lane & ~(p.per_group - 1));
+                if ((lane & (p.per_group - 1)) == __ffs(has) - 1) rest = next_of(pos);
                 sum += key_value(all);
                 bulk += fabsf(key_value(all));
             }
@@ -434,26 +490,26 @@ __global__ void __launch_bounds__(kWarps * 32) route_scores_kernel(const L* __re
             g = eq ? 0u : g;
         }
         if (!(key_value(m) - key_value(lanes_max<LANES>(g)) > 2.0f * off)) sure = false;
-#pragma unroll
-        for (int i = 0; i < EPL; ++i) first[i] = kept ? first[i] : 0u;
+        head = kept ? head : 0u;
     }
-    // The slots: key, lane, and how often this key of this lane came before.
-    uint32_t my_key = 0u, last = 0u;
-    int my_lane = 0, my_rep = 0, last_lane = -1, rep = 0;
+    // The slots: key and lane.
+    uint32_t my_key = 0u;
+    int my_lane = 0, pos = 0;
 #pragma unroll 1
     for (int j = 0; j < a.k; ++j) {
-        const uint32_t all = lanes_max<LANES>(first[0]);
-        const int winner = __ffs(__ballot_sync(kAll, first[0] == all) >> base & own_lanes) - 1;
-        rep = all == last && winner == last_lane ? rep + 1 : 0;
-        last = all;
-        last_lane = winner;
+        const uint32_t all = lanes_max<LANES>(head);
+        const int winner = __ffs(__ballot_sync(kAll, head == all) >> base & own_lanes) - 1;
         if (p.sub == j) {
             my_key = all;
             my_lane = winner;
-            my_rep = rep;
         }
-        drop_first<EPL>(first, p.sub == winner);
+        if (p.sub == winner) head = next_of(pos);
     }
+    // How often a slot's key of its lane came before: equal ones follow one another.
+    const uint32_t key_before = __shfl_up_sync(kAll, my_key, 1, LANES);
+    const int lane_before = __shfl_up_sync(kAll, my_lane, 1, LANES);
+    const unsigned again = __ballot_sync(kAll, p.sub > 0 && my_key == key_before && my_lane == lane_before) >> base;
+    const int my_rep = __clz(~(again << (31 - p.sub)));
     int at = 0, seen = 0;
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
@@ -475,9 +531,9 @@ __global__ void __launch_bounds__(kWarps * 32) route_scores_kernel(const L* __re
                    fabsf(c) * 1.2e-7f;
         };
         const float c = key_value(my_key), off = error(c, my_e, my_l);
-        const uint32_t left = lanes_max<LANES>(first[0]);
+        const uint32_t left = lanes_max<LANES>(head);
         float left_off = 0.0f;
-        if (first[0] == left && left != 0u) {
+        if (head == left && left != 0u) {
             int i_left = 0;
             float v = 0.0f;
 #pragma unroll
@@ -497,7 +553,7 @@ __global__ void __launch_bounds__(kWarps * 32) route_scores_kernel(const L* __re
         const bool none_left = p.sub == a.k - 1 && left == 0u;
         if (in && !none_left && !(c - next_c > off + next_off)) sure = false;
         if (__any_sync(kAll, !sure)) {
-            my_e = choose64<LANES, EPL>(row, a, p);
+            my_e = choose64<LANES, EPL>(row, a.bias, Exact{a.E, a.k, a.G, a.kept, a.sigmoid});
             if (!in) my_e = 0;
             my_l = logit(row + my_e);
         }

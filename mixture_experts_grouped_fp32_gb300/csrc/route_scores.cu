@@ -21,6 +21,7 @@
 // with the order of c; a slot then costs one maximum over the lanes' first ones (one instruction for a warp), and the
 // lane that held it reads its next one.  Which expert a slot's integer belongs to is looked up for all slots at once.
 // Bound by instructions, not by the T E logits that are read.
+#include <algorithm>
 #include <climits>
 #include <cmath>
 
@@ -87,24 +88,35 @@ __device__ __forceinline__ uint32_t lanes_max(uint32_t v) {
     }
 }
 
-// Where a token's experts lie: lane `sub` of LANES has `count` of them from `first` on, all of group `group`.
-struct Place {
-    int sub, per_group, group, first, count;  // per_group: lanes of a group
-    __device__ __forceinline__ Place(int lanes, int E, int G) {
-        sub = threadIdx.x & (lanes - 1);
+// How a token's experts lie in its lanes: groups of `size` experts in 2^lanes_log2 lanes each, `each` to a lane.  Set on
+// the host (divisions).
+struct Layout {
+    int G, size, each, lanes_log2;
+    Layout() = default;
+    Layout(int lanes, int E, int groups) : G(groups), size(E / groups), lanes_log2(0) {
         int slots = 1;  // groups, up to a power of two
         while (slots < G) slots *= 2;
-        per_group = lanes / slots;
-        group = sub / per_group;
-        const int size = E / G, each = (size + per_group - 1) / per_group, at = (sub - group * per_group) * each;
-        first = group * size + at;
-        count = group < G ? max(0, min(each, size - at)) : 0;
+        while ((slots << (lanes_log2 + 1)) <= lanes) ++lanes_log2;
+        each = (size + (1 << lanes_log2) - 1) >> lanes_log2;
+    }
+};
+// Lane `sub` has `count` experts from `first` on, all of group `group`.
+struct Place {
+    int sub, per_group, group, first, count;  // per_group: lanes of a group
+    __device__ __forceinline__ Place(int lanes, const Layout& l) {
+        sub = threadIdx.x & (lanes - 1);
+        per_group = 1 << l.lanes_log2;
+        group = sub >> l.lanes_log2;
+        const int at = (sub & (per_group - 1)) * l.each;
+        first = group * l.size + at;
+        count = group < l.G ? max(0, min(l.each, l.size - at)) : 0;
     }
 };
 
 struct RouteArgs {
     const float* bias;
-    int T, E, k, sigmoid, G, kept, renorm;
+    Layout layout;
+    int T, E, k, q, sigmoid, G, kept, renorm;  // q: experts whose c make a group's score
     float scale;
     int32_t* idx;
     float *w, *scores;
@@ -122,13 +134,15 @@ __device__ __forceinline__ unsigned long long ordered(double v) {
 __device__ __forceinline__ double key_value64(unsigned long long k) {
     return k == 1ull ? static_cast<double>(NAN) : __longlong_as_double(static_cast<long long>(k >> 63 ? k ^ 0x8000000000000000ull : ~k));
 }
-struct Exact {
-    int E, k, G, kept, sigmoid;
-};
 template <int LANES, int EPL, typename L>
-__device__ __noinline__ int choose64(const L* row, const float* bias, Exact a) {
+__device__ __noinline__ int choose64(const L* row, const float* bias, int size, int each, int lanes_log2, int many, int sigmoid_) {
     using Key = unsigned long long;
-    const Place p(LANES, a.E, a.G);
+    struct {
+        int G, kept, k, q, sigmoid;
+    } a = {many & 63, many >> 6 & 63, many >> 12 & 15, many >> 16, sigmoid_};
+    Layout layout;
+    layout.G = a.G, layout.size = size, layout.each = each, layout.lanes_log2 = lanes_log2;
+    const Place p(LANES, layout);
     const int lane = threadIdx.x & 31;
     float top = -INFINITY;
     bool nan = false;
@@ -158,7 +172,7 @@ __device__ __noinline__ int choose64(const L* row, const float* bias, Exact a) {
         return bias ? c + static_cast<double>(__ldg(bias + e)) : c;
     };
     // In fp32, and how far off that may be.
-    float c[EPL], size = 0.0f, score = 0.0f;
+    float c[EPL], bulk = 0.0f, score = 0.0f;
     const float inv = 1.0f / static_cast<float>(total);
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
@@ -166,12 +180,12 @@ __device__ __noinline__ int choose64(const L* row, const float* bias, Exact a) {
         if (i < p.count) {
             const float l = logit(row + p.first + i), s = a.sigmoid ? sigmoid(l) : top == -INFINITY ? 0.0f : expf(l - top) * inv;
             c[i] = bias ? s + __ldg(bias + p.first + i) : s;
-            size = fmaxf(size, fabsf(c[i]));
+            bulk = fmaxf(bulk, fabsf(c[i]));
             score = fmaxf(score, s);
         }
     }
     const float off = a.sigmoid ? kSigmoidRel + kSigmoidAbs : kSoftmaxRel * lanes_max<LANES>(score) + 0.37f * kSoftmaxArg;
-    const float margin = 2.0f * (off + 1.2e-7f * lanes_max<LANES>(size));
+    const float margin = 2.0f * (off + 1.2e-7f * lanes_max<LANES>(bulk));
     nan = __any_sync(kAll, nan);  // then every expert of the warp's tokens is in question
     Key key[EPL];
 #pragma unroll
@@ -235,11 +249,10 @@ __device__ __noinline__ int choose64(const L* row, const float* bias, Exact a) {
     bool mine;
     int at;
     if (a.kept < a.G) {
-        const int q = min(a.E / a.G, max(1, a.k / a.kept));
-        compute(nth(q, p.per_group) - margin);
+        compute(nth(a.q, p.per_group) - margin);
         double sum = 0.0;
 #pragma unroll 1
-        for (int r = 0; r < q; ++r) sum += key_value64(best(p.per_group, mine, at));
+        for (int r = 0; r < a.q; ++r) sum += key_value64(best(p.per_group, mine, at));
         const Key own = ordered(sum);
         int rank = 0;
 #pragma unroll 1
@@ -360,7 +373,7 @@ __global__ void __launch_bounds__(kWarps * 32) route_scores_kernel(const L* __re
     pdl_wait();
     pdl_trigger();
     constexpr int kTokens = 32 / LANES;
-    const Place p(LANES, a.E, a.G);
+    const Place p(LANES, a.layout);
     const int lane = threadIdx.x & 31, base = lane & ~(LANES - 1);  // the token's first lane
     const unsigned own_lanes = LANES == 32 ? kAll : (1u << (LANES & 31)) - 1;
     const long long warp = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
@@ -370,8 +383,7 @@ __global__ void __launch_bounds__(kWarps * 32) route_scores_kernel(const L* __re
     const size_t t = static_cast<size_t>(there ? want : a.T - 1);
     const L* row = logits + t * a.E;
     const bool plain = !a.bias && a.G == 1;  // the order of the logits themselves
-    const int size = a.E / a.G, each = (size + p.per_group - 1) / p.per_group;
-    const bool fours = ((size | each) & 3) == 0;
+    const bool fours = ((a.layout.size | a.layout.each) & 3) == 0;
     const auto words = reinterpret_cast<uintptr_t>(logits) | reinterpret_cast<uintptr_t>(a.bias) |
                        reinterpret_cast<uintptr_t>(a.scores);
     const bool vec = fours && (words & 15) == 0;
@@ -453,7 +465,7 @@ __global__ void __launch_bounds__(kWarps * 32) route_scores_kernel(const L* __re
     auto next_of = [&](int& pos) { return ++pos < EPL ? lists[threadIdx.x >> 5][pos][lane] : 0u; };
     if (a.G > 1 && a.kept < a.G) {
         // A group's score: its q largest, all groups at once.
-        const int q = min(size, max(1, a.k / a.kept));
+        const int q = a.q;
         float sum, bulk;  // bulk: sum of sizes
         if (q <= 2) {
             for (int o = p.per_group / 2; o > 0; o >>= 1) {
@@ -525,26 +537,12 @@ __global__ void __launch_bounds__(kWarps * 32) route_scores_kernel(const L* __re
     float my_l = logit(row + my_e);
     if (!plain) {
         // Neighbours in the order have to be further apart than their errors; the last slot's is the best that is left.
-        auto error = [&](float c, int e, float v) {
-            const float s = a.bias ? fabsf(c - __ldg(a.bias + e)) : fabsf(c);
-            return (a.sigmoid ? s * kSigmoidRel + kSigmoidAbs : s * (kSoftmaxRel + kSoftmaxArg * fabsf(v - top)) + 1e-30f) +
-                   fabsf(c) * 1.2e-7f;
-        };
-        const float c = key_value(my_key), off = error(c, my_e, my_l);
+        const float inv = 1.0f / total, c = key_value(my_key), x = my_l - top;
         const uint32_t left = lanes_max<LANES>(head);
-        float left_off = 0.0f;
-        if (head == left && left != 0u) {
-            int i_left = 0;
-            float v = 0.0f;
-#pragma unroll
-            for (int i = 0; i < EPL; ++i)
-                if (key[i] == left) {
-                    i_left = i;
-                    v = l[i];
-                }
-            left_off = error(key_value(left), p.first + i_left, v);
-        }
-        left_off = __uint_as_float(lanes_max<LANES>(__float_as_uint(left_off)));
+        const float off = fabsf(c) * 1.2e-7f + (a.sigmoid ? kSigmoidRel + kSigmoidAbs
+                                                         : __expf(x) * inv * (kSoftmaxRel + kSoftmaxArg * fabsf(x)) + 1e-30f);
+        const float left_off = fabsf(key_value(left)) * 1.2e-7f +
+                               (a.sigmoid ? kSigmoidRel + kSigmoidAbs : inv * (kSoftmaxRel + 0.37f * kSoftmaxArg));
         float next_c = __shfl_down_sync(kAll, c, 1, LANES), next_off = __shfl_down_sync(kAll, off, 1, LANES);
         if (p.sub == a.k - 1) {
             next_c = key_value(left);
@@ -553,7 +551,8 @@ __global__ void __launch_bounds__(kWarps * 32) route_scores_kernel(const L* __re
         const bool none_left = p.sub == a.k - 1 && left == 0u;
         if (in && !none_left && !(c - next_c > off + next_off)) sure = false;
         if (__any_sync(kAll, !sure)) {
-            my_e = choose64<LANES, EPL>(row, a.bias, Exact{a.E, a.k, a.G, a.kept, a.sigmoid});
+            my_e = choose64<LANES, EPL>(row, a.bias, a.layout.size, a.layout.each, a.layout.lanes_log2,
+                                        a.G | a.kept << 6 | a.k << 12 | a.q << 16, a.sigmoid);
             if (!in) my_e = 0;
             my_l = logit(row + my_e);
         }
@@ -663,17 +662,15 @@ route_scores_backward_kernel(const L* __restrict__ logits, RouteGradArgs a, L* _
             if (sub + i * LANES < a.E) store_grad(dlogits + t * a.E + sub + i * LANES, g[i]);
 }
 
-// Experts of a lane, at most: groups up to a power of two share the lanes.
+// Experts of a lane; far too many where the lanes are fewer than the groups.
 int experts_per_lane(int lanes, int E, int G) {
     int slots = 1;
     while (slots < G) slots *= 2;
-    if (slots > lanes) return 1 << 30;
-    const int per = lanes / slots;
-    return (E / G + per - 1) / per;
+    return slots > lanes ? 1 << 30 : Layout(lanes, E, G).each;
 }
-
 template <int LANES, int EPL, typename L>
-cudaError_t forward_with(const L* logits, const RouteArgs& a, cudaStream_t s) {
+cudaError_t forward_with(const L* logits, RouteArgs a, cudaStream_t s) {
+    a.layout = Layout(LANES, a.E, a.G);
     return launch_k(kPdlTrain, route_scores_kernel<LANES, EPL, L>, dim3((a.T - 1) / (kWarps * (32 / LANES)) + 1),
                     dim3(kWarps * 32), 0, s, logits, a);
 }
@@ -715,7 +712,8 @@ cudaError_t backward_as(const L* logits, const RouteGradArgs& a, L* dlogits, cud
 cudaError_t launch_route_scores(const void* logits, bool bf16, const float* bias, int T, int E, int k, bool sigmoid,
                                 int n_group, int topk_group, bool renorm, float scale, int32_t* idx, float* w,
                                 float* scores, cudaStream_t s) {
-    const RouteArgs a{bias, T, E, k, sigmoid, n_group, topk_group, renorm, scale, idx, w, scores};
+    const RouteArgs a{bias, Layout(32, E, n_group), T, E, k, std::min(E / n_group, std::max(1, k / topk_group)), sigmoid, n_group,
+                      topk_group, renorm, scale, idx, w, scores};
     return bf16 ? forward_as(static_cast<const __nv_bfloat16*>(logits), a, s)
                 : forward_as(static_cast<const float*>(logits), a, s);
 }

@@ -57,6 +57,10 @@ __device__ __forceinline__ uint32_t ordered(float v) {
     return v != v ? 1u : u ^ (static_cast<uint32_t>(static_cast<int32_t>(u) >> 31) | 0x80000000u);
 }
 
+__device__ __forceinline__ unsigned long long ordered(double v) {
+    const long long u = __double_as_longlong(v + 0.0);
+    return v != v ? 1ull : static_cast<unsigned long long>(u ^ ((u >> 63) | static_cast<long long>(0x8000000000000000ull)));
+}
 __device__ __forceinline__ float sigmoid(float l) { return 1.0f / (1.0f + expf(-l)); }
 
 template <int LANES>
@@ -123,14 +127,76 @@ struct RouteArgs {
 };
 
 // ---------------------------------------------------------------------------------------------
-// The choice in fp64: slot j's expert in lane j.  Only the experts that the fp32 values leave in question are computed
+// The k best of a few experts in fp64: of those whose fp32 value is `from` at least (the k best are among them), at most
+// two to a lane; slot j's in lane j, or -1 in all lanes where there are more or a NaN.  `open`: this lane's may be chosen.
+// ---------------------------------------------------------------------------------------------
+template <int LANES, int EPL, typename L>
+__device__ __noinline__ int choose_few64(const L* row, const float* bias, int first, int count, bool open, float from,
+                                         float top, float inv, int sigmoid_) {
+    using Key = unsigned long long;
+    __shared__ int slots[kWarps][32];
+    const int lane = threadIdx.x & 31, sub = lane & (LANES - 1);
+    double total = 0.0;
+    unsigned todo = 0u;
+    bool few = true;
+#pragma unroll 2
+    for (int i = 0; i < count; ++i) {
+        const float l = logit(row + first + i), b = bias ? __ldg(bias + first + i) : 0.0f;
+        const float s = sigmoid_ ? sigmoid(l) : expf(l - top) * inv, c = s + b;
+        if (!sigmoid_) total += exp(static_cast<double>(l) - static_cast<double>(top));
+        if (open && !(c < from)) todo |= 1u << i;
+        few &= c == c;
+    }
+    if (!sigmoid_) total = lanes_sum<LANES>(total);
+    few &= __popc(todo) <= 2;
+    if (!__all_sync(kAll, few)) return -1;
+    Key key[2];
+    int id[2];
+#pragma unroll 1
+    for (int n = 0; n < 2; ++n) {
+        Key v = 0ull;
+        int e = -1;
+        if (todo) {
+            e = first + __ffs(todo) - 1;
+            todo &= todo - 1;
+            const double l = logit(row + e);
+            double c = exp(sigmoid_ ? -l : l - static_cast<double>(top));
+            c = sigmoid_ ? 1.0 / (1.0 + c) : c / total;
+            v = ordered(bias ? c + static_cast<double>(__ldg(bias + e)) : c);
+        }
+        if (n == 0) key[0] = v, id[0] = e;
+        else key[1] = v, id[1] = e;
+    }
+    // An expert's slot is the number of those before it.
+    int rank[2] = {0, 0};
+    unsigned some = __ballot_sync(kAll, id[0] >= 0);
+#pragma unroll
+    for (int o = LANES; o < 32; o *= 2) some |= some >> o | some << (32 - o);  // in any token of the warp
+    some &= LANES == 32 ? kAll : (1u << (LANES & 31)) - 1;
+    for (; some; some &= some - 1) {
+        const int from_lane = __ffs(some) - 1;
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+            const Key v = __shfl_sync(kAll, key[n], from_lane, LANES);
+            const int e = __shfl_sync(kAll, id[n], from_lane, LANES);
+#pragma unroll
+            for (int m = 0; m < 2; ++m) rank[m] += e >= 0 && (v > key[m] || (v == key[m] && e < id[m]));
+        }
+    }
+    slots[threadIdx.x >> 5][lane] = 0;
+    __syncwarp();
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+        if (id[m] >= 0 && rank[m] < 8 && rank[m] < LANES) slots[threadIdx.x >> 5][(lane & ~(LANES - 1)) + rank[m]] = id[m];
+    __syncwarp();
+    return sub < 8 ? slots[threadIdx.x >> 5][lane] : 0;
+}
+
+// ---------------------------------------------------------------------------------------------
+// The same of any, groups among them.  Only the experts that the fp32 values leave in question are computed
 // again, a lane's one after another: in each group those that may be of its q largest, and then in the kept groups those
 // that may be of the k largest.  (Seldom run, so kept small: cold instructions take as long as the arithmetic.)
 // ---------------------------------------------------------------------------------------------
-__device__ __forceinline__ unsigned long long ordered(double v) {
-    const long long u = __double_as_longlong(v + 0.0);
-    return v != v ? 1ull : static_cast<unsigned long long>(u ^ ((u >> 63) | static_cast<long long>(0x8000000000000000ull)));
-}
 __device__ __forceinline__ double key_value64(unsigned long long k) {
     return k == 1ull ? static_cast<double>(NAN) : __longlong_as_double(static_cast<long long>(k >> 63 ? k ^ 0x8000000000000000ull : ~k));
 }
@@ -449,6 +515,7 @@ __global__ void __launch_bounds__(kWarps * 32) route_scores_kernel(const L* __re
         }
     }
     bool sure = plain || !nan;  // the fp32 order is that of the definition
+    bool open = true;           // this lane's group is kept
     uint32_t head;  // the largest that is left of this lane's keys, at `pos` of its list
     float t1, t2;   // the largest two
     {
@@ -502,8 +569,10 @@ __global__ void __launch_bounds__(kWarps * 32) route_scores_kernel(const L* __re
             g = eq ? 0u : g;
         }
         if (!(key_value(m) - key_value(lanes_max<LANES>(g)) > 2.0f * off)) sure = false;
+        open = kept;
         head = kept ? head : 0u;
     }
+    const bool groups_sure = sure;
     // The slots: key and lane.
     uint32_t my_key = 0u;
     int my_lane = 0, pos = 0;
@@ -551,9 +620,16 @@ __global__ void __launch_bounds__(kWarps * 32) route_scores_kernel(const L* __re
         const bool none_left = p.sub == a.k - 1 && left == 0u;
         if (in && !none_left && !(c - next_c > off + next_off)) sure = false;
         if (__any_sync(kAll, !sure)) {
-            my_e = choose64<LANES, EPL>(row, a.bias, a.layout.size, a.layout.each, a.layout.lanes_log2,
-                                        a.G | a.kept << 6 | a.k << 12 | a.q << 16, a.sigmoid);
-            if (!in) my_e = 0;
+            int e = -1;
+            if (__all_sync(kAll, groups_sure)) {
+                const float least = __shfl_sync(kAll, c, a.k - 1, LANES);
+                const float most = fabsf(least) * 1.2e-7f + (a.sigmoid ? kSigmoidRel + kSigmoidAbs : inv * (kSoftmaxRel + 0.37f * kSoftmaxArg));
+                e = choose_few64<LANES, EPL>(row, a.bias, p.first, p.count, open, least - 2.1f * most, top, inv, a.sigmoid);
+            }
+            if (__any_sync(kAll, e < 0))
+                e = choose64<LANES, EPL>(row, a.bias, a.layout.size, a.layout.each, a.layout.lanes_log2,
+                                         a.G | a.kept << 6 | a.k << 12 | a.q << 16, a.sigmoid);
+            my_e = in ? e : 0;
             my_l = logit(row + my_e);
         }
     }

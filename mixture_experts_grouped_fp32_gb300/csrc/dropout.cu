@@ -10,7 +10,36 @@
 namespace moe {
 namespace {
 
-constexpr int kThreads = 256, kPer = 2;  // vectors of a thread
+constexpr int kThreads = 128, kPer = 2;  // vectors of eight of a thread
+
+// WHOLE: all vectors are there and aligned; else `count` elements one by one.
+template <typename X, typename R, bool RES, bool WHOLE>
+__device__ __forceinline__ void drop_vectors(const X* x, const R* residual, size_t first, size_t n, const Drop& drop, R* out) {
+    Raw8<X> xr[kPer];
+    Raw8<R> rr[kPer];
+    auto count = [&](int k) {
+        const size_t at = 8 * (first + k * kThreads);
+        return WHOLE ? 8 : at < n ? static_cast<int>(min(static_cast<size_t>(8), n - at)) : 0;
+    };
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+        const size_t at = 8 * (first + k * kThreads);
+        fetch_raw<WHOLE>(xr[k], x + at, count(k));
+        if (RES) fetch_raw<WHOLE>(rr[k], residual + at, count(k));
+    }
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+        const size_t at = 8 * (first + k * kThreads);
+        Vec8 v = values(xr[k]);
+        if (drop.on()) drop.apply(v, at);
+        if (RES) {
+            const Vec8 r = values(rr[k]);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v.set(j, add2(v.pair(j), r.pair(j)));
+        }
+        put8<WHOLE>(out + at, v, count(k));
+    }
+}
 
 template <typename X, typename R, bool RES, bool ALIGNED>
 __global__ void __launch_bounds__(kThreads)
@@ -18,37 +47,9 @@ dropout_kernel(const X* x, const R* residual, size_t n, const __grid_constant__ 
     pdl_wait();
     pdl_trigger();
     const Drop drop(args);
-    const size_t n8 = (n + 7) / 8;
-    const size_t first = static_cast<size_t>(blockIdx.x) * (kThreads * kPer) + threadIdx.x;
-    Raw8<X> xr[kPer];
-    Raw8<R> rr[kPer];
-    int count[kPer];
-#pragma unroll
-    for (int k = 0; k < kPer; ++k) {
-        const size_t i = first + k * kThreads;
-        count[k] = i < n8 ? static_cast<int>(min(static_cast<size_t>(8), n - 8 * i)) : 0;
-        if (count[k] == 8) {
-            fetch_raw<ALIGNED>(xr[k], x + 8 * i, 8);
-            if (RES) fetch_raw<ALIGNED>(rr[k], residual + 8 * i, 8);
-        } else if (count[k] > 0) {
-            fetch_raw<false>(xr[k], x + 8 * i, count[k]);
-            if (RES) fetch_raw<false>(rr[k], residual + 8 * i, count[k]);
-        }
-    }
-#pragma unroll
-    for (int k = 0; k < kPer; ++k) {
-        const size_t i = first + k * kThreads;
-        if (count[k] == 0) continue;
-        Vec8 v = values(xr[k]);
-        if (drop.on()) drop.apply(v, 8 * i);
-        if (RES) {
-            const Vec8 r = values(rr[k]);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v.v[j] += r.v[j];
-        }
-        if (count[k] == 8) put8<ALIGNED>(out + 8 * i, v, 8);
-        else put8<false>(out + 8 * i, v, count[k]);
-    }
+    const size_t begin = static_cast<size_t>(blockIdx.x) * (kThreads * kPer), first = begin + threadIdx.x;
+    if (ALIGNED && 8 * (begin + kThreads * kPer) <= n) drop_vectors<X, R, RES, true>(x, residual, first, n, drop, out);
+    else drop_vectors<X, R, RES, false>(x, residual, first, n, drop, out);
 }
 
 template <typename X, typename R, bool RES>

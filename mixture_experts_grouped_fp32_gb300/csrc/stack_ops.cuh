@@ -98,8 +98,8 @@ struct Drop {
         const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            v.v[2 * j] = (w[j] << 16) >= cut16 ? v.v[2 * j] * up : 0.0f;
-            v.v[2 * j + 1] = w[j] >= cut16 ? v.v[2 * j + 1] * up : 0.0f;
+            const float2 s = mul2(v.pair(j), up);
+            v.set(j, make_float2((w[j] << 16) >= cut16 ? s.x : 0.0f, w[j] >= cut16 ? s.y : 0.0f));
         }
     }
 };

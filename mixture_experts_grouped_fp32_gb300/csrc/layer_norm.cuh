@@ -18,6 +18,14 @@ namespace {
 constexpr int kSms = 152;  // of a GB300
 constexpr int kMostBlocks = 16;  // of a cluster
 
+// Two sums over a warp: lane l holds that of s[l / 16].
+__device__ __forceinline__ float warp_sum2(const float (&s)[2]) {
+    const bool up = threadIdx.x & 16;
+    float v = (up ? s[1] : s[0]) + __shfl_xor_sync(0xffffffffu, up ? s[0] : s[1], 16);
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
 // Four sums over a warp: lane l holds that of s[l / 8].
 __device__ __forceinline__ float warp_sum4(const float (&s)[4]) {
     const bool up = threadIdx.x & 16, up8 = threadIdx.x & 8;
@@ -36,7 +44,7 @@ __device__ __forceinline__ float lanes_sum(float v) {
     return v;
 }
 
-// N = 1 or 4 sums over the threads that hold a row.  One barrier each; the buffers alternate, so that none is needed
+// N = 1, 2 or 4 sums over the threads that hold a row.  One barrier each; the buffers alternate, so that none is needed
 // behind it.
 template <bool CLUSTER, int N>
 struct RowSums {
@@ -48,6 +56,7 @@ struct RowSums {
         const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, all = (CLUSTER ? blocks : 1) * warps;
         float mine;  // this lane's part of sum lane / (32 / N)
         if constexpr (N == 4) mine = warp_sum4(s);
+        else if constexpr (N == 2) mine = warp_sum2(s);
         else mine = warp_sum(s[0]);
         if (CLUSTER || warps > 1) {
             float* buf = red + parity * all * N;

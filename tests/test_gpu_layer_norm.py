@@ -48,7 +48,8 @@ def check_norm(y, weight, bias, n, stats, eps=EPS):
 
 
 SHAPES = [(1, 1), (3, 2), (2, 7), (5, 8), (9, 33), (4, 256), (7, 264), (700, 96), (33, 1000), (301, 1024), (5, 2891),
-          (160, 4096), (3, 4104), (1, 7168), (311, 7168), (6, 8190), (5, 8192), (2, 8200), (3, 16384), (2, 20001), (2, 65536)]
+          (160, 4096), (3, 4104), (1, 7168), (311, 7168), (6, 8190), (5, 8192), (400, 6091),
+          (1216, 2072), (1300, 2891), (2, 8200), (3, 16384), (2, 20001), (2, 65536)]
 
 
 @pytest.mark.parametrize("dt", [F32, BF16])

@@ -7,9 +7,9 @@
 // order, the same result on every run.
 //
 //   sort   The vocabulary is dealt out to the blocks.  Every block reads all ids (T values from the L2, which costs less
-//          than a pass between blocks would), counts those of the blocks before it and, warp by warp, those of each id of
-//          its own; sums over the warps and ids then give each warp and id the place of its next token, and a second
-//          reading puts the tokens there.
+//          than a pass between blocks would), counts those of the blocks before it and lists its own tokens, warp by
+//          warp, in shared memory.  Of these it counts each warp's of each id; sums over the warps and ids then give
+//          each warp and id the place of its next token, and the lists are gone through again to put the tokens there.
 //   sum    The sorted tokens are cut into pieces.  A group of threads takes a piece (and the columns eight a thread): it
 //          adds up the runs that begin in it, and follows the last one beyond the piece's end.  A run that covers a
 //          whole piece is long: its pieces' sums are left for the join.  Other blocks of the same launch zero the rows
@@ -157,7 +157,8 @@ embed_kernel(const I* __restrict__ ids, const X* __restrict__ table, int T, int 
 // ---------------------------------------------------------------------------------------------
 constexpr int kMostPiece = 32;
 constexpr int kSortWarps = 32;
-constexpr int kMostSlice = 1600;   // ids of a slice: 32 warps' counts and the places fill 211 KB of shared memory
+constexpr int kMostSlice = 1600;   // ids of a slice, whose counts of 32 warps take 205 KB of shared memory
+constexpr int kSortSmem = 220 << 10;  // what is left of it: the warps' lists
 constexpr int kSms = 152;          // of a GB300
 constexpr int kThreads = 256;      // of a block of the sums, at the most
 constexpr int kZeroWords = 16;     // 16-byte words that a thread of the other blocks looks at
@@ -176,7 +177,7 @@ struct Workspace {
     int32_t* order;    // [T] tokens sorted by id, then by place
     int32_t* id;       // [T] their ids
     float* part;       // [pieces, 2, d] sums of the long runs that begin before a piece, and that begin in it
-    uint8_t* present;  // [V] whether a token has the id
+    uint8_t* present;  // [V] whether a token has the id; null where that is not needed
     int32_t* more;     // [pieces] of the long run that begins in a piece: how many pieces it goes on for, else 0
 };
 
@@ -212,17 +213,18 @@ __device__ __forceinline__ uint32_t word_of(long long v) { return v >> 31 == 0 ?
 // they are spread), counted as v >> bits; the order of the ids is that of (v mod 2^bits, v >> bits).
 template <typename I>
 __global__ void __launch_bounds__(1024)
-embed_sort_kernel(const I* __restrict__ ids, int T, int V, int slice, int bits, int piece, Workspace ws, int32_t* status) {
-    extern __shared__ int32_t counts[];  // [warps][slice]
+embed_sort_kernel(const I* __restrict__ ids, int T, int V, int slice, int list, int bits, int piece, Workspace ws, int32_t* status) {
+    extern __shared__ int32_t counts[];  // [warps][slice], then the lists: [warps][list] {token, id}
     __shared__ int32_t warp_sums[32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t r = blockIdx.x, vocabulary = V, blocks = gridDim.x;
+    const unsigned before = (1u << lane) - 1;
     const int n = r < vocabulary ? static_cast<int>((vocabulary - 1 - r) >> bits) + 1 : 0;
     int32_t* mine = counts + warp * slice;
+    int2* own_list = reinterpret_cast<int2*>(counts + kSortWarps * slice) + warp * list;
     for (int i = tid; i < kSortWarps * slice; i += 1024) counts[i] = 0;
     pdl_wait();
     pdl_trigger();
-    __syncthreads();
     // A warp's tokens: a run of them, 32 at a time and the loads of eight times 32 together.
     const unsigned per = (static_cast<unsigned>(T) + kSortWarps * 32 - 1) / (kSortWarps * 32) * 32;
     const unsigned t0 = min(warp * per, static_cast<unsigned>(T)), t1 = min(t0 + per, static_cast<unsigned>(T));
@@ -239,17 +241,36 @@ embed_sort_kernel(const I* __restrict__ ids, int T, int V, int slice, int bits, 
                 if (32 * u < left) work(t + 32 * u + lane, v[u], v[u] < vocabulary ? v[u] & (blocks - 1) : blocks);
         }
     };
-    int below = 0;
+    int below = 0, len = 0;
     bool bad = false;
     each([&](unsigned t, uint32_t v, uint32_t block) {
         if (r == 0) bad |= block == blocks && t < t1;
         below += block < r;
-        if (block == r) atomicAdd(mine + (v >> bits), 1);
+        const unsigned hits = __ballot_sync(0xffffffffu, block == r);
+        if (hits) {
+            const int at = len + __popc(hits & before);
+            if (block == r && at < list) own_list[at] = make_int2(static_cast<int>(t), static_cast<int>(v));
+            len += __popc(hits);
+        }
     });
     if (bad) flag_status(status, MOE_STATUS_BAD_TOKEN);
-    __syncthreads();
+    // The block's tokens from the lists, or from the ids once more where a list was too short.
+    const bool listed = !__syncthreads_or(len > list);
+    auto each_own = [&](auto&& work) {  // work(token, its id as a word, whether the lane has one)
+        if (listed) {
+            for (int i = lane; i - lane < len; i += 32) {
+                const int2 e = i < len ? own_list[i] : make_int2(0, 0);
+                work(static_cast<unsigned>(e.x), static_cast<uint32_t>(e.y), i < len);
+            }
+        } else {
+            each([&](unsigned t, uint32_t v, uint32_t block) { work(t, v, block == r); });
+        }
+    };
+    each_own([&](unsigned, uint32_t v, bool in) {
+        if (in) atomicAdd(mine + (v >> bits), 1);
+    });
     int all_below, own;
-    block_scan(below, warp_sums, &all_below);
+    block_scan(below, warp_sums, &all_below);  // (its barriers are behind the counts, too)
     // Each id's places: those of the ids before it, then of the warps before one.
     const int ids_per = (n + 1023) / 1024, b0 = min(tid * ids_per, n), b1 = min(b0 + ids_per, n);
     int sum = 0;
@@ -257,7 +278,7 @@ embed_sort_kernel(const I* __restrict__ ids, int T, int V, int slice, int bits, 
         int c = 0;
 #pragma unroll 8
         for (int w = 0; w < kSortWarps; ++w) c += counts[w * slice + b];
-        ws.present[(static_cast<size_t>(b) << bits) + r] = c != 0;
+        if (ws.present) ws.present[(static_cast<size_t>(b) << bits) + r] = c != 0;
         sum += c;
     }
     int at = all_below + block_scan(sum, warp_sums, &own);
@@ -280,20 +301,19 @@ embed_sort_kernel(const I* __restrict__ ids, int T, int V, int slice, int bits, 
                 ws.more[first] = (at - 1) / piece - first;
         }
     __syncthreads();
-    each([&](unsigned t, uint32_t v, uint32_t block) {
-        const bool in = block == r;
+    each_own([&](unsigned t, uint32_t v, bool in) {
         unsigned hits = __ballot_sync(0xffffffffu, in);
         if (hits == 0) return;
         const uint32_t q = v >> bits;
-        unsigned same = 0;  // lanes with this lane's id: one distinct id after another, seldom more than one or two
+        unsigned same = 0;  // lanes with this lane's id: one distinct id after another
         while (hits) {
             const uint32_t one = __shfl_sync(0xffffffffu, v, __ffs(hits) - 1);
-            const unsigned m = __ballot_sync(0xffffffffu, v == one);
-            if (v == one) same = m;
+            const unsigned m = __ballot_sync(0xffffffffu, in && v == one);
+            if (in && v == one) same = m;
             hits &= ~m;
         }
         if (in) {
-            const int place = mine[q] + __popc(same & ((1u << lane) - 1));
+            const int place = mine[q] + __popc(same & before);
             ws.order[place] = static_cast<int32_t>(t);
             ws.id[place] = static_cast<int32_t>(v);
         }
@@ -334,7 +354,7 @@ __device__ __forceinline__ void finish(O* p, const Vec8& v, float scale, const C
 }
 
 struct SumArgs {
-    int V, d, piece, pieces, chunks;  // tokens of a piece, pieces of the T tokens, stretches of columns
+    int T, V, d, piece, pieces, chunks;  // tokens of a piece, pieces of the T tokens, stretches of columns
     int sum_blocks;                   // blocks that sum; the others zero
     float scale;
     bool add;
@@ -392,13 +412,16 @@ embed_sum_kernel(const X* __restrict__ dy, SumArgs a, Workspace ws, O* __restric
     const long long piece = static_cast<long long>(blockIdx.x / a.chunks) * blockDim.y + threadIdx.y, p0 = piece * P;
     const int found = __ldg(ws.found);
     int32_t *id = s_id + threadIdx.y * (2 * P + 1), *order = s_order + threadIdx.y * 2 * P;
-    // Ids from the token before the piece to the end of the next piece (-1 before all and behind all).
+    // Ids from the token before the piece to the end of the next piece (-1 before all and behind all).  All loads at
+    // once: what lies behind the tokens found is read, and not used.
     for (int k = x; k <= 2 * P; k += tx) {
         const long long at = p0 - 1 + k;
-        id[k] = at >= 0 && at < found ? __ldg(ws.id + at) : -1;
-        if (k < 2 * P) order[k] = at + 1 < found ? __ldg(ws.order + at + 1) : 0;
+        const int v = at >= 0 && at < a.T ? __ldg(ws.id + at) : -1, t = k < 2 * P && at + 1 < a.T ? __ldg(ws.order + at + 1) : 0;
+        id[k] = at < found ? v : -1;
+        if (k < 2 * P) order[k] = at + 1 < found ? t : 0;
     }
-    const int two_back = p0 >= P && p0 < found ? __ldg(ws.id + p0 - P) : -1;  // the first of the piece before
+    const int first_back = p0 >= P && p0 < a.T ? __ldg(ws.id + p0 - P) : -1;  // the first of the piece before
+    const int two_back = p0 < found ? first_back : -1;
     __syncthreads();
     const Columns<G> c(chunk, tx, x, d);
     if (p0 >= found || c.count == 0) return;
@@ -461,13 +484,16 @@ __global__ void __launch_bounds__(32 * kShares) embed_join_kernel(SumArgs a, Wor
     pdl_trigger();
     const long long found = __ldg(ws.found);
     const long long piece = static_cast<long long>(blockIdx.x) * kWindow + lane;
-    const int goes_on = lane < kWindow && (piece + 1) * P < found ? __ldg(ws.more + piece) : 0;
+    // (all loads at once: what lies behind the tokens found is read, and not used)
+    const bool whole = lane < kWindow && (piece + 1) * P < a.T;
+    const int pieces_more = whole ? __ldg(ws.more + piece) : 0, id = whole ? __ldg(ws.id + (piece + 1) * P) : 0;
+    const int goes_on = (piece + 1) * P < found ? pieces_more : 0;
     unsigned todo = __ballot_sync(0xffffffffu, goes_on > 0);
     while (todo) {  // (the same in all warps)
         const int k = __ffs(todo) - 1, more = __shfl_sync(0xffffffffu, goes_on, k);
         todo &= todo - 1;
         const long long first = static_cast<long long>(blockIdx.x) * kWindow + k;
-        const int value = __ldg(ws.id + (first + 1) * P);
+        const int value = __shfl_sync(0xffffffffu, id, k);
         Vec8 sum{};
         const float* p = ws.part + static_cast<size_t>(first) * 2 * d + c.at;
         const int per = more / kShares + 1, k0 = g * per, k1 = c.count > 0 ? min(k0 + per, more + 1) : k0;
@@ -545,17 +571,19 @@ cudaError_t forward_i(const EmbedArgs& a, cudaStream_t s) {
 template <typename I>
 cudaError_t sort(const EmbedArgs& a, const Workspace& ws, cudaStream_t s) {
     const int bits = slice_bits(a.V), slice = ((a.V - 1) >> bits) + 1;
-    const cudaError_t e = cudaFuncSetAttribute(embed_sort_kernel<I>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               static_cast<int>(sizeof(int32_t) * kSortWarps * kMostSlice));
+    const int counts = kSortWarps * slice, per = (a.T - 1) / (kSortWarps * 32) * 32 + 32;
+    const int list = std::min(per, (kSortSmem - 4 * counts) / (8 * kSortWarps));
+    const int smem = 4 * counts + 8 * kSortWarps * list;
+    const cudaError_t e = cudaFuncSetAttribute(embed_sort_kernel<I>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSortSmem);
     if (e != cudaSuccess) return e;
-    return launch_k(kPdlTrain, embed_sort_kernel<I>, dim3(1 << bits), dim3(1024), sizeof(int32_t) * kSortWarps * slice, s,
-                    static_cast<const I*>(a.ids), a.T, a.V, slice, bits, piece_of(a.T, a.d), ws, a.status);
+    return launch_k(kPdlTrain, embed_sort_kernel<I>, dim3(1 << bits), dim3(1024), smem, s,
+                    static_cast<const I*>(a.ids), a.T, a.V, slice, list, bits, piece_of(a.T, a.d), ws, a.status);
 }
 template <typename X, typename O, int G>
 cudaError_t sum_as(const EmbedArgs& a, const Workspace& ws, cudaStream_t s) {
     const int d8 = (a.d + 7) / 8, tx = across(d8), ty = kThreads / tx;
     SumArgs g;
-    g.V = a.V, g.d = a.d;
+    g.T = a.T, g.V = a.V, g.d = a.d;
     g.piece = piece_of(a.T, a.d);
     g.pieces = (a.T - 1) / g.piece + 1;
     g.chunks = (d8 - 1) / tx + 1;
@@ -602,6 +630,7 @@ cudaError_t launch_embed_backward(const EmbedArgs& a, void* workspace, cudaStrea
     ws.id = reinterpret_cast<int32_t*>(p += up(sizeof(int32_t) * static_cast<size_t>(a.T)));
     ws.present = reinterpret_cast<uint8_t*>(p += up(sizeof(int32_t) * static_cast<size_t>(a.T)));
     ws.more = reinterpret_cast<int32_t*>(p += up(static_cast<size_t>(a.V)));
+    if (a.accumulate) ws.present = nullptr;  // no row is zeroed
     const int piece = piece_of(a.T, a.d);
     ws.part = reinterpret_cast<float*>(p + up(sizeof(int32_t) * ((static_cast<size_t>(a.T) + piece - 1) / piece)));
     using B = __nv_bfloat16;

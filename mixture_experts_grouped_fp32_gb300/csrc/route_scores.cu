@@ -62,6 +62,10 @@ __device__ __forceinline__ unsigned long long ordered(double v) {
     return v != v ? 1ull : static_cast<unsigned long long>(u ^ ((u >> 63) | static_cast<long long>(0x8000000000000000ull)));
 }
 __device__ __forceinline__ float sigmoid(float l) { return 1.0f / (1.0f + expf(-l)); }
+__device__ __forceinline__ float sigmoid_slope(float l) {  // s (1 - s), small on both sides
+    const float e = expf(-fabsf(l)), q = 1.0f + e;
+    return e / (q * q);
+}
 
 template <int LANES>
 __device__ __forceinline__ float lanes_sum(float v) {
@@ -650,12 +654,32 @@ struct RouteGradArgs {
 };
 
 // Lane `sub` of a token has the experts sub, sub + LANES, ..: loads and stores of neighbouring lanes are neighbours.
-template <int LANES, int EPL, typename L>
+// Fours of a row.
+__device__ __forceinline__ void read4(float* v, const float* p) {
+    const float4 f = __ldg(reinterpret_cast<const float4*>(p));
+    v[0] = f.x, v[1] = f.y, v[2] = f.z, v[3] = f.w;
+}
+__device__ __forceinline__ void read4(float* v, const __nv_bfloat16* p) {
+    const uint2 u = __ldg(reinterpret_cast<const uint2*>(p));
+    unpack_bf16x2(u.x, v[0], v[1]);
+    unpack_bf16x2(u.y, v[2], v[3]);
+}
+__device__ __forceinline__ void store4(float* p, const float* v) {
+    *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+}
+__device__ __forceinline__ void store4(__nv_bfloat16* p, const float* v) {
+    *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+}
+
+// A lane has every LANES-th expert of its token, or (U = 4) every LANES-th four of them.  What the slots add to their
+// experts goes through shared memory.
+template <int LANES, int EPL, int U, typename L>
 __global__ void __launch_bounds__(kWarps * 32)
 route_scores_backward_kernel(const L* __restrict__ logits, RouteGradArgs a, L* __restrict__ dlogits) {
+    constexpr int kTokens = 32 / LANES;
+    __shared__ __align__(16) float sums[kWarps][kTokens][LANES * EPL];
     pdl_wait();
     pdl_trigger();
-    constexpr int kTokens = 32 / LANES;
     const int lane = threadIdx.x & 31, sub = lane & (LANES - 1);
     const long long warp = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
     if (warp * kTokens >= a.T) return;
@@ -663,17 +687,27 @@ route_scores_backward_kernel(const L* __restrict__ logits, RouteGradArgs a, L* _
     const bool there = want < a.T;
     const size_t t = static_cast<size_t>(there ? want : a.T - 1);
     const L* row = logits + t * a.E;
+    auto expert = [&](int i) { return (sub + i / U * LANES) * U + i % U; };
     // Of all scores only those that a gradient reaches are needed: the chosen ones, but for a softmax that is not
     // renormalised or whose scores have a gradient of their own.
     const bool dense = a.dscores || (!a.sigmoid && !a.renorm);
     float v[EPL], g[EPL];
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) g[i] = 0.0f;
     if (dense) {
         const float* ds = a.dscores + (a.per_token ? t * a.E : 0);
 #pragma unroll
-        for (int i = 0; i < EPL; ++i) {
-            const int e = sub + i * LANES;
-            v[i] = e < a.E ? logit(row + e) : -INFINITY;
-            g[i] = e < a.E && a.dscores ? __ldg(ds + e) : 0.0f;
+        for (int i = 0; i < EPL; i += U) {
+#pragma unroll
+            for (int j = 0; j < U; ++j) v[i + j] = -INFINITY;
+            if (expert(i) >= a.E) continue;
+            if constexpr (U == 4) {
+                read4(v + i, row + expert(i));
+                if (a.dscores) read4(g + i, ds + expert(i));
+            } else {
+                v[i] = logit(row + expert(i));
+                if (a.dscores) g[i] = __ldg(ds + expert(i));
+            }
         }
     }
     // Slot j in lane j; an expert that there is none of takes part in nothing.
@@ -694,32 +728,55 @@ route_scores_backward_kernel(const L* __restrict__ logits, RouteGradArgs a, L* _
         add = e >= 0 ? r * (u - mean) : 0.0f;
         if (a.sigmoid) add *= sigmoid(-l);
     } else if (a.sigmoid) {
-        add = e >= 0 ? sigmoid(l) * sigmoid(-l) * u : 0.0f;
+        add = e >= 0 ? sigmoid_slope(l) * u : 0.0f;
     }
+    float* sum = sums[threadIdx.x >> 5][lane / LANES];  // of the token's experts
     auto scatter = [&] {
-        for (int j = 0; j < a.k; ++j) {
-            const int at = __shfl_sync(kAll, e, j, LANES) - sub;
-            const float x = __shfl_sync(kAll, add, j, LANES);
+        if constexpr (U == 4) {
 #pragma unroll
-            for (int i = 0; i < EPL; ++i)
-                if (at == i * LANES) g[i] += x;
+            for (int i = 0; i < EPL; i += 4) *reinterpret_cast<float4*>(sum + expert(i)) = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        } else {
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) sum[expert(i)] = 0.0f;
+        }
+        __syncwarp();
+        // Whether an expert is in two slots (a caller's own choice): then one slot after another.
+        int* mark = reinterpret_cast<int*>(sum);
+        if (e >= 0) mark[e] = lane;
+        __syncwarp();
+        const bool first = e >= 0 && mark[e] == lane;
+        const bool twice = __any_sync(kAll, e >= 0 && !first);
+        __syncwarp();
+        if (first) sum[e] = twice ? 0.0f : add;
+        __syncwarp();
+        if (twice)
+            for (int j = 0; j < a.k; ++j) {
+                if (sub == j && e >= 0) sum[e] += add;
+                __syncwarp();
+            }
+        if constexpr (U == 4) {
+#pragma unroll
+            for (int i = 0; i < EPL; i += 4) {
+                const float4 f = *reinterpret_cast<const float4*>(sum + expert(i));
+                g[i] += f.x, g[i + 1] += f.y, g[i + 2] += f.z, g[i + 3] += f.w;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) g[i] += sum[expert(i)];
         }
     };
-    if (!dense) {
+    if (dense && a.sigmoid) {
 #pragma unroll
-        for (int i = 0; i < EPL; ++i) g[i] = 0.0f;
-    } else if (a.sigmoid) {
-#pragma unroll
-        for (int i = 0; i < EPL; ++i) g[i] *= sigmoid(v[i]) * sigmoid(-v[i]);
-    } else {
-        if (!to_dl) scatter();
+        for (int i = 0; i < EPL; ++i) g[i] *= sigmoid_slope(v[i]);
+    } else if (dense) {
+        if (!to_dl && a.dw) scatter();
         float top = -INFINITY, total = 0.0f, mean = 0.0f;
 #pragma unroll
         for (int i = 0; i < EPL; ++i) top = fmaxf(top, v[i]);
         top = lanes_max<LANES>(top);
 #pragma unroll
         for (int i = 0; i < EPL; ++i) {
-            const bool none = sub + i * LANES >= a.E || (top == -INFINITY && v[i] == v[i]);
+            const bool none = expert(i) >= a.E || (top == -INFINITY && v[i] == v[i]);
             v[i] = none ? 0.0f : expf(v[i] - top);
             total += v[i];
             mean = fmaf(v[i], g[i], mean);
@@ -732,10 +789,13 @@ route_scores_backward_kernel(const L* __restrict__ logits, RouteGradArgs a, L* _
         for (int i = 0; i < EPL; ++i) g[i] = v[i] * inv * (g[i] - mean);
     }
     if (to_dl && a.dw) scatter();
-    if (there)
+    if (!there) return;
 #pragma unroll
-        for (int i = 0; i < EPL; ++i)
-            if (sub + i * LANES < a.E) store_grad(dlogits + t * a.E + sub + i * LANES, g[i]);
+    for (int i = 0; i < EPL; i += U) {
+        if (expert(i) >= a.E) continue;
+        if constexpr (U == 4) store4(dlogits + t * a.E + expert(i), g + i);
+        else store_grad(dlogits + t * a.E + expert(i), g[i]);
+    }
 }
 
 // Experts of a lane; far too many where the lanes are fewer than the groups.
@@ -760,27 +820,29 @@ cudaError_t forward_as(const L* logits, const RouteArgs& a, cudaStream_t s) {
     if (n32 <= 8) return forward_with<32, 8>(logits, a, s);
     return forward_with<32, 16>(logits, a, s);
 }
-template <int LANES, int EPL, typename L>
+template <int LANES, int EPL, int U, typename L>
 cudaError_t backward_with(const L* logits, const RouteGradArgs& a, L* dlogits, cudaStream_t s) {
-    return launch_k(kPdlTrain, route_scores_backward_kernel<LANES, EPL, L>, dim3((a.T - 1) / (kWarps * (32 / LANES)) + 1),
+    return launch_k(kPdlTrain, route_scores_backward_kernel<LANES, EPL, U, L>, dim3((a.T - 1) / (kWarps * (32 / LANES)) + 1),
                     dim3(kWarps * 32), 0, s, logits, a, dlogits);
 }
 template <typename L>
 cudaError_t backward_as(const L* logits, const RouteGradArgs& a, L* dlogits, cudaStream_t s) {
-    if (a.E <= 64) {
-        if (a.E <= 8) return backward_with<8, 1>(logits, a, dlogits, s);
-        if (a.E <= 16) return backward_with<8, 2>(logits, a, dlogits, s);
-        if (a.E <= 32) return backward_with<8, 4>(logits, a, dlogits, s);
-        return backward_with<8, 8>(logits, a, dlogits, s);
+    // Fours where the experts are fours and the tensors aligned for them.
+    if (a.E % 4 == 0 && (reinterpret_cast<uintptr_t>(logits) | reinterpret_cast<uintptr_t>(dlogits)) % (4 * sizeof(L)) == 0 &&
+        reinterpret_cast<uintptr_t>(a.dscores) % 16 == 0) {
+        if (a.E <= 32) return backward_with<8, 4, 4>(logits, a, dlogits, s);
+        if (a.E <= 64) return backward_with<8, 8, 4>(logits, a, dlogits, s);
+        if (a.E <= 128) return backward_with<16, 8, 4>(logits, a, dlogits, s);
+        if (a.E <= 192) return backward_with<16, 12, 4>(logits, a, dlogits, s);
+        return backward_with<16, 16, 4>(logits, a, dlogits, s);
     }
-    switch ((a.E + 31) / 32) {
-        case 3: return backward_with<32, 3>(logits, a, dlogits, s);
-        case 4: return backward_with<32, 4>(logits, a, dlogits, s);
-        case 5: return backward_with<32, 5>(logits, a, dlogits, s);
-        case 6: return backward_with<32, 6>(logits, a, dlogits, s);
-        case 7: return backward_with<32, 7>(logits, a, dlogits, s);
-        default: return backward_with<32, 8>(logits, a, dlogits, s);
-    }
+    if (a.E <= 8) return backward_with<8, 1, 1>(logits, a, dlogits, s);
+    if (a.E <= 16) return backward_with<8, 2, 1>(logits, a, dlogits, s);
+    if (a.E <= 32) return backward_with<8, 4, 1>(logits, a, dlogits, s);
+    if (a.E <= 64) return backward_with<8, 8, 1>(logits, a, dlogits, s);
+    if (a.E <= 128) return backward_with<32, 4, 1>(logits, a, dlogits, s);
+    if (a.E <= 192) return backward_with<32, 6, 1>(logits, a, dlogits, s);
+    return backward_with<32, 8, 1>(logits, a, dlogits, s);
 }
 
 }  // namespace

@@ -164,7 +164,8 @@ def gradient(logits, idx, dw, ds, scoring, renorm, scale):
 
 @pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("renorm", [True, False])
-@pytest.mark.parametrize("T,E,k", [(1, 1, 1), (3, 2, 2), (5, 8, 2), (33, 17, 3), (129, 64, 8), (7, 65, 8), (257, 256, 8), (64, 250, 4)])
+@pytest.mark.parametrize("T,E,k", [(1, 1, 1), (3, 2, 2), (5, 8, 2), (33, 17, 3), (129, 64, 8), (7, 65, 8), (257, 256, 8), (64, 250, 4),
+                                   (65, 28, 4), (33, 100, 4), (130, 160, 6), (31, 188, 8), (9, 150, 5), (17, 240, 8)])
 def test_backward(moe, T, E, k, scoring, renorm):
     g = torch.Generator("cuda").manual_seed(T + E)
     for dt in (F32, BF16):
@@ -218,9 +219,10 @@ def test_backward_is_the_slope_of_forward(moe):
                 assert (slope - grad[:, e]).abs().le((2.0 ** -10 + h * h) * size).all()
 
 
-def test_experts_given_twice_and_out_of_range(moe):
-    l, dw = torch.randn(4, 10, device="cuda"), torch.randn(4, 3, device="cuda")
-    idx = torch.tensor([[1, 1, 1], [2, -1, 10], [-1, 99, -7], [9, 0, 9]], dtype=torch.int32, device="cuda")
+@pytest.mark.parametrize("E", [10, 12, 100, 130])
+def test_experts_given_twice_and_out_of_range(moe, E):
+    l, dw = torch.randn(4, E, device="cuda"), torch.randn(4, 3, device="cuda")
+    idx = torch.tensor([[1, 1, 1], [2, -1, E], [-1, E + 89, -7], [9, 0, 9]], dtype=torch.int32, device="cuda")
     for scoring in ("softmax", "sigmoid"):
         for renorm in (True, False):
             got = moe.route_scores_backward(l, idx, dw, scoring=scoring, renormalize=renorm)

@@ -361,6 +361,14 @@ bool real(PyObject* o, float* out) {
 }
 bool one_of(ScalarType t) { return t == BF16 || t == F32; }
 
+// Whether an object is true; false is returned for one that has no answer (the Python function reports it).
+bool truth(PyObject* o, bool* out) {
+    const int v = PyObject_IsTrue(o);
+    if (v < 0) PyErr_Clear();
+    *out = v > 0;
+    return v >= 0;
+}
+
 // "softmax" 0, "sigmoid" 1, anything else -1.
 int scoring_of(PyObject* o) {
     if (!PyUnicode_Check(o)) return -1;
@@ -381,9 +389,10 @@ PyObject* route_scores(PyObject*, PyObject* const* a, Py_ssize_t n) {
             Py_RETURN_NONE;
         const void *pl = c.plain(*l, l->scalar_type()), *pb = c.opt(a[3], F32, {E});
         if (!c.ok) Py_RETURN_NONE;
-        const bool renorm = PyObject_IsTrue(a[6]);
+        bool renorm, want;
+        if (!truth(a[6], &renorm) || !truth(a[8], &want)) Py_RETURN_NONE;
         at::Tensor idx = make({T, k}, I32, *l), w = make({T, k}, F32, *l), scores;
-        if (PyObject_IsTrue(a[8])) scores = make({T, E}, F32, *l);
+        if (want) scores = make({T, E}, F32, *l);
         const int rc = unlocked([&] {
             return lib.moe_route_scores(pl, l->scalar_type() == BF16, static_cast<const float*>(pb), T, E, k, how, groups,
                                         kept, renorm, scale, static_cast<int32_t*>(ptr(idx)), static_cast<float*>(ptr(w)),
@@ -416,7 +425,8 @@ PyObject* route_scores_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const bool per_token = ds && ds->dim() == 2;
         const void* ps = per_token ? c.at(a[3], F32, {T, E}) : c.opt(a[3], F32, {E});
         if (!c.ok) Py_RETURN_NONE;
-        const bool renorm = PyObject_IsTrue(a[5]);
+        bool renorm;
+        if (!truth(a[5], &renorm)) Py_RETURN_NONE;
         at::Tensor out = make({T, E}, l->scalar_type(), *l);
         const int rc = unlocked([&] {
             return lib.moe_route_scores_backward(pl, l->scalar_type() == BF16, static_cast<const int32_t*>(pi),
@@ -499,9 +509,11 @@ PyObject* layer_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
         c.opt(a[5], F32, {d});
         Dropping drop;
         if (!c.ok || !drop.read(c, a + 7)) Py_RETURN_NONE;
+        bool want_h;
+        if (!truth(a[6], &want_h)) Py_RETURN_NONE;
         const size_t need = lib.moe_layer_norm_backward_workspace_size(T, d);
         at::Tensor ws = make({static_cast<int64_t>(need)}, ScalarType::Byte, *x), dx = make({T, d}, type, *x), dh, dw, db;
-        if (PyObject_IsTrue(a[6])) dh = make({T, d}, BF16, *x);
+        if (want_h) dh = make({T, d}, BF16, *x);
         if (a[4] != Py_None) dw = make({d}, F32, *x);
         if (a[5] != Py_None) db = make({d}, F32, *x);
         const int rc = unlocked([&] {
@@ -560,7 +572,8 @@ PyObject* embed_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
         int V;
         float scale;
         if (!integer(a[2], &V) || V < 1 || !real(a[3], &scale)) Py_RETURN_NONE;
-        const bool f32 = PyObject_IsTrue(a[5]), acc = PyObject_IsTrue(a[6]);
+        bool f32, acc;
+        if (!truth(a[5], &f32) || !truth(a[6], &acc)) Py_RETURN_NONE;
         const void* py = c.plain(*dy, dy->scalar_type());
         c.opt(a[4], f32 ? F32 : BF16, {V, d});
         void* st = c.opt(a[7], I32, {1});

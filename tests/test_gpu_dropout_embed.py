@@ -240,3 +240,17 @@ def test_graphs_other_streams_and_no_tokens(moe):
     kept = out.clone()
     moe.embed_backward(none, dy[:0], 50, out=out, accumulate=True)
     assert torch.equal(out, kept)
+
+
+def test_other_types_are_refused(moe):
+    ids, dy = torch.zeros(4, dtype=torch.int64, device="cuda"), torch.ones(4, 8, device="cuda")
+    for dt in (torch.float16, torch.float64):
+        for call in (lambda: moe.embed_backward(ids, dy.to(dt), 5), lambda: moe.embed(ids, dy.to(dt)),
+                     lambda: moe.embed(ids, dy, out_dtype=dt), lambda: moe.embed_backward(ids, dy, 5, out_dtype=dt),
+                     lambda: moe.dropout(dy.to(dt), 0.1, 0), lambda: moe.dropout(dy, 0.1, 0, residual=dy.to(dt)),
+                     lambda: moe.layer_norm(dy.to(dt)), lambda: moe.layer_norm(dy, h=dy.to(dt)),
+                     lambda: moe.route_scores(dy.to(dt), 2)):
+            with pytest.raises((ValueError, TypeError)):
+                call()
+    with pytest.raises((ValueError, TypeError)):
+        moe.embed_backward(ids.to(torch.int16), dy, 5)

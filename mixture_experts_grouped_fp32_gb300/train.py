@@ -20,11 +20,12 @@ With ``norm="layer"`` the blocks have layer norms before them and nothing after:
     n    = w_pre[l + 1] * (x - mean(x)) / std(x) + b_pre[l + 1]     in one kernel with the addition
 
 ``dropout`` (either norm) zeroes elements of c; the masks are functions of the seed, the block and
-``mask_number`` on the device, which ``step`` counts up, so that the backward pass has the forward pass'
-and a replayed graph has new ones.  ``router`` replaces the softmax router by ``moe.route_scores`` and its
+``mask_number`` on the device, which every forward pass counts up and keeps, so that its backward pass has the
+same masks and a replayed graph new ones.  ``router`` replaces the softmax router by ``moe.route_scores`` and its
 gradient: scoring, n_group, topk_group, renormalize and scale as for that call; bias_rate, the step by which
-a bias that steers the choice follows the experts' loads (there is one if it is not 0); balance, the weight of
-a loss E * sum_e load_e * mean score_e on each block.  With ``vocab`` the stack reads tokens:
+a bias that steers the choice follows the experts' loads of the last forward pass (there is one if it is not 0);
+balance, the weight of a loss E * sum_e load_e * mean score_e on each block.  ``forward(x, train=False)`` drops
+nothing and records no loads.  With ``vocab`` the stack reads tokens:
 x = scale * w_embed[ids], and ids take the place of x in ``forward``.
 
 Parameters are fp32 with bf16 copies of the expert weights for the products; ``step`` updates both in
@@ -84,7 +85,7 @@ class MoEStack:
     def _scoring(self):
         return {k: self.router[k] for k in ("scoring", "renormalize", "scale")}
 
-    def _experts(self, n, p, w, l=0):
+    def _experts(self, n, p, w, l=0, train=True):
         """The routed experts of block l: (c bf16 [T, d], what the backward pass needs)."""
         logits = n.float() @ p["w_router"]
         if self.router is None:
@@ -93,7 +94,7 @@ class MoEStack:
             idx, wt, _ = moe.route_scores(logits, self.top_k, bias=self.biases[l], n_group=self.router["n_group"],
                                           topk_group=self.router["topk_group"], **self._scoring())
         counts, offsets, _, dest, rows = moe.permute(idx, n, self.E, status=self.status)
-        if self.router is not None:
+        if self.router is not None and train:
             self.loads[l].copy_(counts)
         where = dest.view(-1).long()
         w_rows = torch.empty(where.numel(), dtype=torch.float32, device=n.device)
@@ -102,11 +103,11 @@ class MoEStack:
         h = moe.swiglu(gu, w_rows)
         y = moe.grouped_mm(h, w["w_down"], offsets, out_dtype=torch.float32, status=self.status)
         c = moe.combine(y, torch.ones_like(wt), dest, status=self.status)
-        return c, (n, idx, wt, offsets, dest, where, rows, w_rows, gu, logits)
+        return c, (n, idx, wt, offsets, dest, where, rows, w_rows, gu, logits, counts)
 
-    def _experts_backward(self, dc, saved, p, w, l=0):
+    def _experts_backward(self, dc, saved, p, w):
         """(gradient of n as bf16, gradients of the block's router and expert weights)."""
-        n, idx, wt, offsets, dest, where, rows, w_rows, gu, logits = saved
+        n, idx, wt, offsets, dest, where, rows, w_rows, gu, logits, counts = saved
         dy = moe.permute(idx, dc, self.E, status=self.status)[4]  # dc's rows in the experts' order
         dh = moe.grouped_mm(dy, w["w_down"], offsets, transpose_b=True, status=self.status)
         dgu, dw_rows, h = moe.swiglu_backward(gu, dh, w_rows, want_h=True)
@@ -121,20 +122,24 @@ class MoEStack:
             d_logits = torch.zeros(n.shape[0], self.E, device=n.device).scatter_(1, idx.long(), d_chosen)
         else:
             T = n.shape[0]  # (the loss' load is a number: its gradient goes through the scores)
-            dscores = self.loads[l] * (self.router["balance"] * self.E / (T * T * self.top_k)) if \
+            dscores = counts * (self.router["balance"] * self.E / (T * T * self.top_k)) if \
                 self.router["balance"] and T else None
             d_logits = moe.route_scores_backward(logits, idx, dw, dscores, **self._scoring())
         g["w_router"] = n.float().t() @ d_logits
         return (dn.float() + d_logits @ p["w_router"].t()).bfloat16(), g
 
     # ----------------------------------------------------------------------------------------------
-    def _masks(self, l):
-        """The dropout of block l's output."""
-        return dict(p=self.p, seed=self.seed, offset=l, offset_tensor=self.mask_number)
+    def _masks(self, l, number):
+        """The dropout of block l's output; number: the forward pass' mask_number, None for no dropout."""
+        return dict(p=0.0, seed=0) if number is None else dict(p=self.p, seed=self.seed, offset=l, offset_tensor=number)
 
-    def forward(self, x):
+    def forward(self, x, train: bool = True):
         """x [T, d] fp32 or bf16 (the residual stream's type), or ids [T] int32 or int64 with ``vocab`` (an fp32 stream)
         -> (x after the last block, saved)."""
+        number = None
+        if self.p and train:
+            number = self.mask_number.clone()
+            self.mask_number.add_(self.layers)
         ids = None
         if self.vocab is not None:
             ids, x = x, moe.embed(x, self.params[0]["w_embed"], self.embed_scale, status=self.status)
@@ -145,18 +150,19 @@ class MoEStack:
         else:
             _, n = moe.block_norm(x, self.params[0]["w_pre"], eps=self.eps)
         for l, (p, w) in enumerate(zip(self.params, self.weights)):
-            c, kept = self._experts(n, p, w, l)
+            c, kept = self._experts(n, p, w, l, train)
             nxt = self.params[l + 1] if l + 1 < self.layers else None
             if layer:
-                saved.append((x, stats, kept, ids))
+                saved.append((x, stats, kept, ids, number))
                 if nxt is None:
-                    x = moe.dropout(c, residual=x, **self._masks(l))
+                    x = moe.dropout(c, residual=x, **self._masks(l, number))
                 else:
-                    x, n, stats = moe.layer_norm(x, nxt["w_pre"], nxt["b_pre"], h=c, eps=self.eps, **self._masks(l))
+                    x, n, stats = moe.layer_norm(x, nxt["w_pre"], nxt["b_pre"], h=c, eps=self.eps,
+                                                 **self._masks(l, number))
                 continue
-            if self.p:
-                c = moe.dropout(c, **self._masks(l))
-            saved.append((x, c, kept, ids))
+            if number is not None:
+                c = moe.dropout(c, **self._masks(l, number))
+            saved.append((x, c, kept, ids, number))
             x, n = moe.block_norm(x, nxt and nxt["w_pre"], h=c, w_post=p["w_post"], gate=p["gate"],
                                   res_scale=p["res_scale"], eps=self.eps)
         return x, saved
@@ -171,13 +177,14 @@ class MoEStack:
         return dx, grads
 
     def _backward_layer(self, dx, saved, grads):
-        last = self.layers - 1
-        dc = moe.dropout(dx.bfloat16(), **self._masks(last))
+        number = saved[0][4]
+        dc = moe.dropout(dx.bfloat16(), **self._masks(self.layers - 1, number))
         for l in reversed(range(self.layers)):
             p, w = self.params[l], self.weights[l]
-            x, stats, kept, _ = saved[l]
-            dn, ge = self._experts_backward(dc, kept, p, w, l)
-            g = moe.layer_norm_backward(x, stats, dn, dx, p["w_pre"], p["b_pre"], want_h=l > 0, **self._masks(l - 1))
+            x, stats, kept = saved[l][:3]
+            dn, ge = self._experts_backward(dc, kept, p, w)
+            g = moe.layer_norm_backward(x, stats, dn, dx, p["w_pre"], p["b_pre"], want_h=l > 0,
+                                        **self._masks(l - 1, number))
             dx, dc = g["x"], g["h"]
             grads[l].update(ge, w_pre=g["weight"], b_pre=g["bias"])
         return dx
@@ -186,7 +193,7 @@ class MoEStack:
         dn = None
         for l in reversed(range(self.layers)):
             p, w = self.params[l], self.weights[l]
-            x, c, kept, _ = saved[l]
+            x, c, kept = saved[l][:3]
             nxt = self.params[l + 1]["w_pre"] if l + 1 < self.layers else None
             g = moe.block_norm_backward(x, dx, dn, w_pre=nxt, h=c, w_post=p["w_post"], gate=p["gate"],
                                         res_scale=p["res_scale"], eps=self.eps)
@@ -194,8 +201,9 @@ class MoEStack:
                 grads[l + 1]["w_pre"] = g["w_pre"]
             dx = g["x"]
             grads[l].update({k: g[k] for k in ("w_post", "gate", "res_scale")})
-            dc = moe.dropout(g["h"], **self._masks(l)) if self.p else g["h"]
-            dn, ge = self._experts_backward(dc, kept, p, w, l)
+            number = saved[l][4]
+            dc = g["h"] if number is None else moe.dropout(g["h"], **self._masks(l, number))
+            dn, ge = self._experts_backward(dc, kept, p, w)
             grads[l].update(ge)
         g = moe.block_norm_backward(saved[0][0], dx, dn, w_pre=self.params[0]["w_pre"], eps=self.eps)
         grads[0]["w_pre"] = g["w_pre"]
@@ -205,8 +213,6 @@ class MoEStack:
              weight_decay: float = 0.1, factors=None):
         """One AdamW step on every parameter and its bf16 copy; ``factors`` as for ``moe.adamw_step``."""
         self.step_number.add_(1)
-        if self.p:
-            self.mask_number.add_(self.layers)
         for bias, load in zip(self.biases, self.loads):
             if bias is not None:  # towards the experts that have fewer tokens than the mean
                 bias.add_(torch.sign(load.sum() / self.E - load), alpha=self.router["bias_rate"])

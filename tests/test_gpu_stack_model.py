@@ -102,6 +102,32 @@ def test_stack_against_64_bits(T, d, f, E, k, options):
             assert load.sum() == T * k and torch.equal(torch.sign(b - old), torch.sign(load.sum() / E - load))
 
 
+@pytest.mark.parametrize("norm", ["rms", "layer"])
+def test_other_passes_between_a_forward_pass_and_its_backward_pass(norm):
+    """The masks and loads of a pass are its own; one that does not train changes neither."""
+    from mixture_experts_grouped_fp32_gb300.train import MoEStack
+    new = lambda: MoEStack(2, 64, 64, 8, 2, norm=norm, dropout=0.25, router=dict(balance=0.5, bias_rate=0.1))
+    g = torch.Generator("cuda").manual_seed(2)
+    x, other, dx = (torch.randn(T, 64, generator=g, device="cuda") for T in (40, 70, 40))
+    a, b = new(), new()
+    ya, saved = a.forward(x)
+    want = a.backward(dx, saved)
+    yb, saved = b.forward(x)
+    assert torch.equal(ya, yb)
+    loads = [t.clone() for t in b.loads]
+    plain = b.forward(other, train=False)[0]
+    assert all(torch.equal(s, t) for s, t in zip(loads, b.loads)) and b.mask_number.item() == 2
+    assert torch.equal(plain, b.forward(other, train=False)[0])
+    trained = b.forward(other)[0]
+    assert b.mask_number.item() == 4 and not torch.equal(plain, trained) and not torch.equal(trained, b.forward(other)[0])
+    got = b.backward(dx, saved)
+    assert torch.equal(got[0], want[0])
+    for s, t in zip(got[1], want[1]):
+        assert all(torch.equal(s[k], t[k]) for k in t)
+    out, saved = b.forward(x, train=False)
+    assert all(torch.isfinite(v).all() for s in b.backward(dx, saved)[1] for v in s.values())
+
+
 def test_options_that_there_are_not():
     from mixture_experts_grouped_fp32_gb300.train import MoEStack
     with pytest.raises(ValueError, match="norm must be"):

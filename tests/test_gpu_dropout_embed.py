@@ -43,14 +43,15 @@ def test_the_generator_gives_the_published_vectors():
         0xD16CFE09, 0x94FDCCEB, 0x5001E420, 0x24126EA1]
 
 
-def stays(n, p, seed, offset):
+def stays(n, p, seed, offset, first=0):
+    """Of the elements from ``first`` (a multiple of 8) to n - 1."""
     m = 0xFFFFFFFF
     key, off = (seed & m, seed >> 32), offset % 2 ** 64
     out = []
-    for b in range((n + 7) // 8):
+    for b in range(first // 8, (n + 7) // 8):
         for w in philox(key, (b & m, b >> 32, off & m, off >> 32)):
             out += [w & 0xFFFF, w >> 16]
-    return torch.tensor(out[:n], device="cuda") >= round(p * 65536)
+    return torch.tensor(out[:n - first], device="cuda") >= round(p * 65536)
 
 
 @pytest.mark.parametrize("n", [1, 7, 8, 9, 1000, 4096 + 5, 12345])
@@ -254,3 +255,24 @@ def test_other_types_are_refused(moe):
                 call()
     with pytest.raises((ValueError, TypeError)):
         moe.embed_backward(ids.to(torch.int16), dy, 5)
+
+
+def test_more_than_a_warp_lists(moe):
+    """Half of many tokens with one id, in small and in wide vocabularies (whole numbers: exact in any order), and all."""
+    g = torch.Generator("cuda").manual_seed(12)
+    for V in (40, 190_000):
+        ids = torch.randint(0, V, (70_001,), generator=g, device="cuda")
+        ids[torch.rand(70_001, generator=g, device="cuda") < 0.5] = 17
+        dy = torch.randint(-4, 5, (70_001, 8), generator=g, device="cuda").float()
+        for i in (ids, ids.int(), torch.full_like(ids, 17)):
+            want = torch.zeros(V, 8, device="cuda").index_add_(0, i, dy)
+            assert torch.equal(moe.embed_backward(i, dy, V), want)
+            assert torch.equal(moe.embed_backward(i, dy, V, out=want.clone(), accumulate=True), 2 * want)
+
+
+def test_elements_beyond_32_bits(moe):
+    n = 2 ** 32 + 43
+    x = torch.ones(n, dtype=BF16, device="cuda")
+    assert moe.dropout(x, 0.5, 3, 4, out=x) is x
+    for first, last in ((0, 64), (2 ** 31 - 32, 2 ** 31 + 32), (2 ** 32 - 32, n)):
+        assert torch.equal(x[first:last].ne(0), stays(last, 0.5, 3, 4, first)), first

@@ -201,3 +201,23 @@ def test_unaligned_tensors_in_place_and_no_rows(moe):
     assert y.shape == (0, 48) and n.shape == (0, 48) and stats.shape == (0, 2)
     grads = moe.layer_norm_backward(e, stats, n, weight=torch.ones(48, device="cuda"), bias=torch.ones(48, device="cuda"))
     assert grads["weight"].eq(0).all() and grads["bias"].eq(0).all() and grads["x"].shape == (0, 48)
+
+
+@pytest.mark.parametrize("T,d", [(600_001, 3581), (524_500, 4104)])
+def test_elements_beyond_32_bits(moe, T, d):
+    """The first and the last rows of more than 2^31 elements."""
+    g = torch.Generator("cuda").manual_seed(d)
+    assert T * d > 2 ** 31
+    x, dn = torch.zeros(T, d, dtype=BF16, device="cuda"), torch.zeros(T, d, dtype=BF16, device="cuda")
+    w = randn(g, d, scale=0.2, mean=1)
+    ends = [*range(9), *range(T - 9, T)]
+    x[ends], dn[ends] = randn(g, 18, d, dtype=BF16, scale=2, mean=0.5), randn(g, 18, d, dtype=BF16)
+    _, n, stats = moe.layer_norm(x, w)
+    check_norm(x[ends], w, None, n[ends], stats[ends])
+    assert n[9:T - 9].count_nonzero() == 0
+    del n
+    got = moe.layer_norm_backward(x, stats, dn, None, w)
+    dx, size, dw, dw_size, _, _ = backward(x[ends], stats[ends], dn[ends], None, w)
+    assert (got["x"][ends].to(D) - dx).abs().le(2.0 ** -8 * dx.abs() + 2.0 ** -17 * size).all()
+    assert got["x"][9:T - 9].count_nonzero() == 0
+    assert (got["weight"].to(D) - dw).abs().le(2.0 ** -17 * dw_size).all()

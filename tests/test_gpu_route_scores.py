@@ -254,3 +254,19 @@ def test_unaligned_logits(moe):
     assert l.data_ptr() % 4 == 2
     a, b = moe.route_scores(l, 3, "sigmoid", want_scores=True), moe.route_scores(l.clone(), 3, "sigmoid", want_scores=True)
     assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+def test_logits_beyond_32_bits(moe):
+    T, E = 2 ** 31 // 256 + 100, 256
+    l, ends = torch.zeros(T, E, dtype=BF16, device="cuda"), [*range(20), *range(T - 50, T)]
+    l[ends] = torch.randn(70, E, device="cuda").bfloat16()
+    bias = torch.randn(E, device="cuda") * 0.1
+    idx, w, _ = moe.route_scores(l, 8, "sigmoid", bias, 8, 4)
+    want = moe.route_scores(l[ends], 8, "sigmoid", bias, 8, 4)
+    assert torch.equal(idx[ends], want[0]) and torch.equal(w[ends], want[1])
+    assert idx[20:T - 50].eq(idx[20]).all()
+    dw = torch.zeros(T, 8, device="cuda")
+    dw[ends] = torch.randn(70, 8, device="cuda")
+    got = moe.route_scores_backward(l, idx, dw, scoring="sigmoid")
+    assert torch.equal(got[ends], moe.route_scores_backward(l[ends], idx[ends], dw[ends], scoring="sigmoid"))
+    assert got[20:T - 50].count_nonzero() == 0

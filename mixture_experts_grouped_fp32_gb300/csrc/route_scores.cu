@@ -32,12 +32,13 @@ namespace {
 
 constexpr int kWarps = 8;  // of a block
 constexpr unsigned kAll = 0xffffffffu;
-// Bounds on the error of the fp32 scores that the choice goes by, from the documented ones of __expf (2 + 1.173 |x| units
-// in the last place, 1.2e-7 each) and __fdividef (2 units), 6e-8 for each rounding.
+// Bounds on the error of the fp32 scores that the choice goes by: 2.4e-7 of a value for the instructions 2^x and 1 / x
+// (over all floats they are off by 1.5e-7 and 1.0e-7 at the most), 6e-8 for each rounding.
 //   sigmoid  1 / (1 + e), e = exp(-l) is off by (1 - s) (2.4e-7 + 1.4e-7 |l|) of s; s (1 - s) |l| is below 0.28: with the
 //            addition and the division 5.5e-7 s + 4e-8
 //   softmax  a term of the sum by 2.4e-7 + 2e-7 |l - top| (its argument is rounded too), whose mean over the softmax is
 //            below 2.4e-7 + 2e-7 ln 256, up to 21 additions, the quotient: 3e-6 + 2e-7 |l - top| of s
+// Values below 2^-126 count as 0 there.
 constexpr float kSigmoidRel = 5.5e-7f, kSigmoidAbs = 4e-8f, kSoftmaxRel = 3e-6f, kSoftmaxArg = 2e-7f;
 
 template <typename L>
@@ -57,11 +58,26 @@ __device__ __forceinline__ uint32_t ordered(float v) {
     return v != v ? 1u : u ^ (static_cast<uint32_t>(static_cast<int32_t>(u) >> 31) | 0x80000000u);
 }
 
+// The same of a score with its bias, where NaN is dealt with elsewhere and -0 cannot be.
+__device__ __forceinline__ uint32_t ordered_score(float v) {
+    const uint32_t u = __float_as_uint(v);
+    return u ^ (static_cast<uint32_t>(static_cast<int32_t>(u) >> 31) | 0x80000000u);
+}
 __device__ __forceinline__ unsigned long long ordered(double v) {
     const long long u = __double_as_longlong(v + 0.0);
     return v != v ? 1ull : static_cast<unsigned long long>(u ^ ((u >> 63) | static_cast<long long>(0x8000000000000000ull)));
 }
 __device__ __forceinline__ float sigmoid(float l) { return 1.0f / (1.0f + expf(-l)); }
+__device__ __forceinline__ float quick_exp(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x * 1.4426950408889634f));
+    return r;
+}
+__device__ __forceinline__ float quick_inverse(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
 __device__ __forceinline__ float sigmoid_slope(float l) {  // s (1 - s), small on both sides
     const float e = expf(-fabsf(l)), q = 1.0f + e;
     return e / (q * q);
@@ -131,69 +147,79 @@ struct RouteArgs {
 };
 
 // ---------------------------------------------------------------------------------------------
-// The k best of a few experts in fp64: of those whose fp32 value is `from` at least (the k best are among them), at most
-// two to a lane; slot j's in lane j, or -1 in all lanes where there are more or a NaN.  `open`: this lane's may be chosen.
+// The k best of a few experts in fp64, for the tokens of the warp that are `unsure`: of the experts whose fp32 value is
+// `from` at least (the k best are among them), one to a lane; slot j's in lane j, or -1 in all lanes where they are more
+// than 32 or one is NaN.  `open`: this lane's may be chosen.
 // ---------------------------------------------------------------------------------------------
 template <int LANES, int EPL, typename L>
-__device__ __noinline__ int choose_few64(const L* row, const float* bias, int first, int count, bool open, float from,
-                                         float top, float inv, int sigmoid_) {
+__device__ __noinline__ int choose_few64(const L* logits, size_t t, int E, const float* bias, int first, int count, bool open,
+                                         bool unsure, float from, float top, float inv, int sigmoid_) {
     using Key = unsigned long long;
-    __shared__ int slots[kWarps][32];
-    const int lane = threadIdx.x & 31, sub = lane & (LANES - 1);
-    double total = 0.0;
+    __shared__ int list[kWarps][32];
+    constexpr int kTokens = 32 / LANES;
+    int* const own = list[threadIdx.x >> 5];
+    const int lane = threadIdx.x & 31;
     unsigned todo = 0u;
     bool few = true;
+    if (unsure && open) {
 #pragma unroll 2
-    for (int i = 0; i < count; ++i) {
-        const float l = logit(row + first + i), b = bias ? __ldg(bias + first + i) : 0.0f;
-        const float s = sigmoid_ ? sigmoid(l) : expf(l - top) * inv, c = s + b;
-        if (!sigmoid_) total += exp(static_cast<double>(l) - static_cast<double>(top));
-        if (open && !(c < from)) todo |= 1u << i;
-        few &= c == c;
-    }
-    if (!sigmoid_) total = lanes_sum<LANES>(total);
-    few &= __popc(todo) <= 2;
-    if (!__all_sync(kAll, few)) return -1;
-    Key key[2];
-    int id[2];
-#pragma unroll 1
-    for (int n = 0; n < 2; ++n) {
-        Key v = 0ull;
-        int e = -1;
-        if (todo) {
-            e = first + __ffs(todo) - 1;
-            todo &= todo - 1;
-            const double l = logit(row + e);
-            double c = exp(sigmoid_ ? -l : l - static_cast<double>(top));
-            c = sigmoid_ ? 1.0 / (1.0 + c) : c / total;
-            v = ordered(bias ? c + static_cast<double>(__ldg(bias + e)) : c);
+        for (int i = 0; i < count; ++i) {
+            const float l = logit(logits + t * E + first + i), b = bias ? __ldg(bias + first + i) : 0.0f;
+            const float c = (sigmoid_ ? quick_inverse(1.0f + quick_exp(-l)) : quick_exp(l - top) * inv) + b;
+            if (!(c < from)) todo |= 1u << i;
+            few &= c == c;
         }
-        if (n == 0) key[0] = v, id[0] = e;
-        else key[1] = v, id[1] = e;
+    }
+    const int n = __popc(todo);
+    int upto = n;
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+        const int v = __shfl_up_sync(kAll, upto, o);
+        if (lane >= o) upto += v;
+    }
+    const int all = __shfl_sync(kAll, upto, 31);
+    if (!__all_sync(kAll, few) || all > 32) return -1;
+    for (int at = upto - n; todo; todo &= todo - 1) own[at++] = (first + __ffs(todo) - 1) | (lane / LANES) << 16;
+    __syncwarp();
+    const int e = lane < all ? own[lane] & 0xffff : 0, token = lane < all ? own[lane] >> 16 : -1;
+    const size_t my_t = __shfl_sync(kAll, static_cast<unsigned long long>(t), max(token, 0) * LANES);
+    const double my_top = __shfl_sync(kAll, top, max(token, 0) * LANES);
+    double total = 1.0;
+    if (!sigmoid_) {
+        const unsigned which = __ballot_sync(kAll, unsure);
+#pragma unroll 1
+        for (int u = 0; u < kTokens; ++u) {
+            if (!(which >> (u * LANES) & 1u)) continue;
+            const L* row = logits + __shfl_sync(kAll, static_cast<unsigned long long>(t), u * LANES) * E;
+            const double row_top = __shfl_sync(kAll, top, u * LANES);
+            double sum = 0.0;
+#pragma unroll 4
+            for (int i = lane; i < E; i += 32) sum += exp(logit(row + i) - row_top);
+            sum = lanes_sum<32>(sum);
+            if (token == u) total = sum;
+        }
+    }
+    Key key = 0ull;
+    if (token >= 0) {
+        const double l = logit(logits + my_t * E + e);
+        double c = exp(sigmoid_ ? -l : l - my_top);
+        c = (sigmoid_ ? 1.0 : c) / (sigmoid_ ? 1.0 + c : total);
+        key = ordered(bias ? c + static_cast<double>(__ldg(bias + e)) : c);
     }
     // An expert's slot is the number of those before it.
-    int rank[2] = {0, 0};
-    unsigned some = __ballot_sync(kAll, id[0] >= 0);
-#pragma unroll
-    for (int o = LANES; o < 32; o *= 2) some |= some >> o | some << (32 - o);  // in any token of the warp
-    some &= LANES == 32 ? kAll : (1u << (LANES & 31)) - 1;
-    for (; some; some &= some - 1) {
-        const int from_lane = __ffs(some) - 1;
-#pragma unroll
-        for (int n = 0; n < 2; ++n) {
-            const Key v = __shfl_sync(kAll, key[n], from_lane, LANES);
-            const int e = __shfl_sync(kAll, id[n], from_lane, LANES);
-#pragma unroll
-            for (int m = 0; m < 2; ++m) rank[m] += e >= 0 && (v > key[m] || (v == key[m] && e < id[m]));
-        }
+    int rank = 0;
+#pragma unroll 1
+    for (int i = 0; i < all; ++i) {
+        const Key v = __shfl_sync(kAll, key, i);
+        const int other = __shfl_sync(kAll, e, i);
+        rank += __shfl_sync(kAll, token, i) == token && (v > key || (v == key && other < e));
     }
-    slots[threadIdx.x >> 5][lane] = 0;
     __syncwarp();
-#pragma unroll
-    for (int m = 0; m < 2; ++m)
-        if (id[m] >= 0 && rank[m] < 8 && rank[m] < LANES) slots[threadIdx.x >> 5][(lane & ~(LANES - 1)) + rank[m]] = id[m];
+    own[lane] = 0;
     __syncwarp();
-    return sub < 8 ? slots[threadIdx.x >> 5][lane] : 0;
+    if (token >= 0 && rank < 8) own[token * LANES + rank] = e;
+    __syncwarp();
+    return own[lane];
 }
 
 // ---------------------------------------------------------------------------------------------
@@ -439,7 +465,8 @@ __device__ __forceinline__ void read_row(float (&l)[EPL], const __nv_bfloat16* p
 
 template <int LANES, int EPL, typename L>
 __global__ void __launch_bounds__(kWarps * 32) route_scores_kernel(const L* __restrict__ logits, RouteArgs a) {
-    __shared__ uint32_t lists[kWarps][EPL][32];  // each lane's keys, the largest first (read by that lane alone)
+    __shared__ uint2 slots[kWarps][32];          // of each token up to 8: key, and place in the lists
+    __shared__ uint32_t lists[kWarps][EPL][32];  // each lane's keys, the largest first, then 0 (read by that lane alone)
     pdl_wait();
     pdl_trigger();
     constexpr int kTokens = 32 / LANES;
@@ -460,7 +487,7 @@ __global__ void __launch_bounds__(kWarps * 32) route_scores_kernel(const L* __re
 
     float l[EPL];
     read_row<EPL>(l, row + p.first, p.count, vec, -INFINITY);
-    float top = 0.0f, total = 1.0f;
+    float top = 0.0f, total = 1.0f, c[EPL];
     const bool exactly = a.scores != nullptr;  // (scores that leave the kernel come from expf)
     if (!a.sigmoid && (!plain || !a.renorm || exactly)) {
         top = -INFINITY;
@@ -468,9 +495,20 @@ __global__ void __launch_bounds__(kWarps * 32) route_scores_kernel(const L* __re
         for (int i = 0; i < EPL; ++i) top = fmaxf(top, l[i]);
         top = lanes_max<LANES>(top);
         total = 0.0f;
+        // (weights that are parts of the sum have it from expf, too)
+        if (a.renorm && !exactly) {
 #pragma unroll
-        for (int i = 0; i < EPL; ++i)
-            if (i < p.count) total += top == -INFINITY && l[i] == l[i] ? 0.0f : expf(l[i] - top);
+            for (int i = 0; i < EPL; ++i) {
+                c[i] = i < p.count && !(top == -INFINITY && l[i] == l[i]) ? quick_exp(l[i] - top) : 0.0f;
+                total += c[i];
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) {
+                c[i] = i < p.count && !(top == -INFINITY && l[i] == l[i]) ? expf(l[i] - top) : 0.0f;
+                total += c[i];
+            }
+        }
         total = lanes_sum<LANES>(total);
     }
     auto score = [&](float v) {
@@ -483,7 +521,7 @@ __global__ void __launch_bounds__(kWarps * 32) route_scores_kernel(const L* __re
 #pragma unroll
         for (int i = 0; i < EPL; ++i) key[i] = i < p.count ? ordered(l[i]) : 0u;
     } else {
-        float c[EPL], b[EPL];
+        float b[EPL];
         if (exactly) {
 #pragma unroll
             for (int i = 0; i < EPL; ++i) c[i] = score(l[i]);
@@ -501,22 +539,24 @@ __global__ void __launch_bounds__(kWarps * 32) route_scores_kernel(const L* __re
             }
         } else if (a.sigmoid) {
 #pragma unroll
-            for (int i = 0; i < EPL; ++i) c[i] = __fdividef(1.0f, 1.0f + __expf(-l[i]));
+            for (int i = 0; i < EPL; ++i) c[i] = quick_inverse(1.0f + quick_exp(-l[i]));
         } else {
-            const float inv = 1.0f / total;
+            const float inv = total == 0.0f ? 0.0f : 1.0f / total;
 #pragma unroll
-            for (int i = 0; i < EPL; ++i) c[i] = top == -INFINITY && total == 0.0f ? 0.0f : __expf(l[i] - top) * inv;
+            for (int i = 0; i < EPL; ++i) c[i] *= inv;
         }
         if (a.bias) {
             read_row<EPL>(b, a.bias + p.first, p.count, vec, 0.0f);
 #pragma unroll
             for (int i = 0; i < EPL; ++i) c[i] += b[i];
         }
+        float all = 0.0f;  // NaN where one of them is (or infinities of both signs are there)
 #pragma unroll
         for (int i = 0; i < EPL; ++i) {
-            nan |= i < p.count && c[i] != c[i];
-            key[i] = i < p.count ? ordered(plain ? l[i] : c[i]) : 0u;
+            all += i < p.count ? c[i] : 0.0f;
+            key[i] = i < p.count ? (plain ? ordered(l[i]) : ordered_score(c[i])) : 0u;
         }
+        nan = all != all;
     }
     bool sure = plain || !nan;  // the fp32 order is that of the definition
     bool open = true;           // this lane's group is kept
@@ -531,9 +571,10 @@ __global__ void __launch_bounds__(kWarps * 32) route_scores_kernel(const L* __re
         t1 = key_value(sorted[0]);
         t2 = EPL > 1 ? key_value(sorted[EPL > 1 ? 1 : 0]) : -INFINITY;
 #pragma unroll
-        for (int i = 1; i < EPL; ++i) lists[threadIdx.x >> 5][i][lane] = sorted[i];
+        for (int i = 1; i < EPL; ++i) lists[threadIdx.x >> 5][i - 1][lane] = sorted[i];
+        lists[threadIdx.x >> 5][EPL - 1][lane] = 0u;
     }
-    auto next_of = [&](int& pos) { return ++pos < EPL ? lists[threadIdx.x >> 5][pos][lane] : 0u; };
+    auto next_of = [&](int& pos) { return lists[threadIdx.x >> 5][min(pos++, EPL - 1)][lane]; };
     if (a.G > 1 && a.kept < a.G) {
         // A group's score: its q largest, all groups at once.
         const int q = a.q;
@@ -563,38 +604,43 @@ __global__ void __launch_bounds__(kWarps * 32) route_scores_kernel(const L* __re
         const bool real = p.group < a.G;
         bulk = __uint_as_float(lanes_max<LANES>(real ? __float_as_uint(bulk) : 0u));  // (positive: integers have their order)
         const float off = (a.sigmoid ? q * (kSigmoidRel + kSigmoidAbs) : kSoftmaxRel + q * 0.37f * kSoftmaxArg) + bulk * (q + 1) * 6e-8f;
-        uint32_t g = real ? ordered(sum) : 0u, m = 0u;
-        bool kept = false;
-        for (int r = 0; r < a.kept; ++r) {
-            m = lanes_max<LANES>(g);
-            const bool eq = g == m;
-            if (__popc(__ballot_sync(kAll, eq) >> base & own_lanes) != p.per_group) sure = false;  // equal sums
-            kept |= eq;
-            g = eq ? 0u : g;
-        }
-        if (!(key_value(m) - key_value(lanes_max<LANES>(g)) > 2.0f * off)) sure = false;
+        const uint32_t g = real ? ordered(sum) : 0u;
+        int rank = 0;  // groups with a larger sum
+#pragma unroll 4
+        for (int o = 0; o < a.G; ++o) rank += __shfl_sync(kAll, g, o << a.layout.lanes_log2, LANES) > g;
+        const bool kept = real && rank < a.kept;
+        const int many = __popc(__ballot_sync(kAll, kept) >> base & own_lanes);  // more than asked for where sums are equal
+        const float least = key_value(~lanes_max<LANES>(kept ? ~g : 0u)), next = key_value(lanes_max<LANES>(kept ? 0u : g));
+        if (many != a.kept << a.layout.lanes_log2 || !(least - next > 2.0f * off)) sure = false;
         open = kept;
         head = kept ? head : 0u;
     }
     const bool groups_sure = sure;
-    // The slots: key and lane.
-    uint32_t my_key = 0u;
-    int my_lane = 0, pos = 0;
+    // The slots: the lane whose key is the largest writes its key and where it took it from.
+    const uint32_t* const list = &lists[threadIdx.x >> 5][0][0];
+    int place = lane;
 #pragma unroll 1
     for (int j = 0; j < a.k; ++j) {
         const uint32_t all = lanes_max<LANES>(head);
         const int winner = __ffs(__ballot_sync(kAll, head == all) >> base & own_lanes) - 1;
-        if (p.sub == j) {
-            my_key = all;
-            my_lane = winner;
+        if (p.sub == winner) {
+            slots[threadIdx.x >> 5][base + j] = make_uint2(all, place);
+            head = list[min(place, 32 * (EPL - 1) + lane)];
+            place += 32;
         }
-        if (p.sub == winner) head = next_of(pos);
     }
-    // How often a slot's key of its lane came before: equal ones follow one another.
-    const uint32_t key_before = __shfl_up_sync(kAll, my_key, 1, LANES);
-    const int lane_before = __shfl_up_sync(kAll, my_lane, 1, LANES);
-    const unsigned again = __ballot_sync(kAll, p.sub > 0 && my_key == key_before && my_lane == lane_before) >> base;
-    const int my_rep = __clz(~(again << (31 - p.sub)));
+    __syncwarp();
+    const uint2 slot = slots[threadIdx.x >> 5][base + min(p.sub, a.k - 1)];
+    const uint32_t my_key = slot.x;
+    const int my_lane = slot.y & (LANES - 1);
+    // How often a slot's key of its lane came before: equal ones follow one another.  (Equal scores are done in fp64.)
+    int my_rep = 0;
+    if (plain) {
+        const uint32_t key_before = __shfl_up_sync(kAll, my_key, 1, LANES);
+        const int lane_before = __shfl_up_sync(kAll, my_lane, 1, LANES);
+        const unsigned again = __ballot_sync(kAll, p.sub > 0 && my_key == key_before && my_lane == lane_before) >> base;
+        my_rep = __clz(~(again << (31 - p.sub)));
+    }
     int at = 0, seen = 0;
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
@@ -613,7 +659,7 @@ __global__ void __launch_bounds__(kWarps * 32) route_scores_kernel(const L* __re
         const float inv = 1.0f / total, c = key_value(my_key), x = my_l - top;
         const uint32_t left = lanes_max<LANES>(head);
         const float off = fabsf(c) * 1.2e-7f + (a.sigmoid ? kSigmoidRel + kSigmoidAbs
-                                                         : __expf(x) * inv * (kSoftmaxRel + kSoftmaxArg * fabsf(x)) + 1e-30f);
+                                                         : quick_exp(x) * inv * (kSoftmaxRel + kSoftmaxArg * fabsf(x)) + 1e-30f);
         const float left_off = fabsf(key_value(left)) * 1.2e-7f +
                                (a.sigmoid ? kSigmoidRel + kSigmoidAbs : inv * (kSoftmaxRel + 0.37f * kSoftmaxArg));
         float next_c = __shfl_down_sync(kAll, c, 1, LANES), next_off = __shfl_down_sync(kAll, off, 1, LANES);
@@ -623,17 +669,19 @@ __global__ void __launch_bounds__(kWarps * 32) route_scores_kernel(const L* __re
         }
         const bool none_left = p.sub == a.k - 1 && left == 0u;
         if (in && !none_left && !(c - next_c > off + next_off)) sure = false;
-        if (__any_sync(kAll, !sure)) {
+        const unsigned unsure = __ballot_sync(kAll, !sure);
+        if (unsure) {
+            const bool mine = unsure >> base & own_lanes;  // the token is
             int e = -1;
             if (__all_sync(kAll, groups_sure)) {
                 const float least = __shfl_sync(kAll, c, a.k - 1, LANES);
                 const float most = fabsf(least) * 1.2e-7f + (a.sigmoid ? kSigmoidRel + kSigmoidAbs : inv * (kSoftmaxRel + 0.37f * kSoftmaxArg));
-                e = choose_few64<LANES, EPL>(row, a.bias, p.first, p.count, open, least - 2.1f * most, top, inv, a.sigmoid);
+                e = choose_few64<LANES, EPL>(logits, t, a.E, a.bias, p.first, p.count, open, mine, least - 2.1f * most, top, inv, a.sigmoid);
             }
             if (__any_sync(kAll, e < 0))
                 e = choose64<LANES, EPL>(row, a.bias, a.layout.size, a.layout.each, a.layout.lanes_log2,
                                          a.G | a.kept << 6 | a.k << 12 | a.q << 16, a.sigmoid);
-            my_e = in ? e : 0;
+            if (in && mine) my_e = e;
             my_l = logit(row + my_e);
         }
     }

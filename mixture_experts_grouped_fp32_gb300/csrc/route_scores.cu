@@ -603,7 +603,8 @@ __global__ void __launch_bounds__(kWarps * 32) route_scores_kernel(const L* __re
         // The error of a sum: its scores' and its additions'.
         const bool real = p.group < a.G;
         bulk = __uint_as_float(lanes_max<LANES>(real ? __float_as_uint(bulk) : 0u));  // (positive: integers have their order)
-        const float off = (a.sigmoid ? q * (kSigmoidRel + kSigmoidAbs) : kSoftmaxRel + q * 0.37f * kSoftmaxArg) + bulk * (q + 1) * 6e-8f;
+        const float inv = 1.0f / total;  // (no score is above it)
+        const float off = (a.sigmoid ? q * (kSigmoidRel + kSigmoidAbs) : fminf(1.0f, q * inv) * kSoftmaxRel + q * inv * 0.37f * kSoftmaxArg) + bulk * (q + 1) * 6e-8f;
         const uint32_t g = real ? ordered(sum) : 0u;
         int rank = 0;  // groups with a larger sum
 #pragma unroll 4

@@ -633,7 +633,8 @@ MOE_API int moe_dropout(const void* x, int x_fp32, const void* residual, int res
  *   n = weight * (y - mean) / std + bias,  mean = mean of y,  std = sqrt(mean of (y - mean)^2 + eps)
  * of y as it is stored, after its rounding.  x, y [T,d] bf16, or fp32 with x_fp32 = 1;  h, n [T,d] bf16;  weight, bias
  * [d] fp32 (NULL: 1, 0);  stats [T,2] fp32 out: mean and 1 / std, 8-byte aligned.  1 <= d <= 65536 (above 65520 a
- * multiple of 8), eps >= 0; p and what follows it as for moe_dropout (p = 0 without h).  y may be x; other outputs must not overlap the inputs. */
+ * multiple of 8), eps >= 0; p and what follows it as for moe_dropout (p = 0 without h).  y may be x; other outputs must
+ * not overlap the inputs. */
 MOE_API int moe_layer_norm(const void* x, int x_fp32, const void* h, const float* weight, const float* bias, int T,
                            int d, float eps, double p, uint64_t seed, int64_t offset, const int64_t* offset_dev, void* y,
                            void* n, float* stats, moe_stream_t stream);

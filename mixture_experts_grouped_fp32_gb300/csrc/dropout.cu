@@ -2,7 +2,8 @@
 //
 // Elements are taken in memory order, eight to a thread and step, the random block of an element its index / 8: the
 // gradient is the same call on the gradient of the output.  One pass over memory, bound by it: the generator runs
-// while the loads are under way.
+// while the loads are under way.  8192 x 14336 bf16 74 us (6.3 TB/s, 94 % of the copy rate; 55 % of the issue slots, the
+// generator's); 64 x 256 1.5 us in a graph, 4 us called from Python, which is the call.
 #include <algorithm>
 
 #include "stack_ops.cuh"

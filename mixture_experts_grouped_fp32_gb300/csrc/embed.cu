@@ -16,6 +16,13 @@
 //          that no token has.
 //   join   adds the pieces' sums of a long run in order.
 //
+// What bounds it: the forward pass and the gradient of a whole table the memory (16384 tokens of 131072 x 4096, fp32 out:
+// 325 us, 2.1 GB written at 7 TB/s).  An addition to the gradient moves little and waits for three kernels of one
+// another (12001 tokens of 1028 columns, 50001 ids, Zipf 1.2: 24 us, about 8 the sort, 10 the sums, 6 the joins of the
+// most frequent ids).  The sort's time is that of reading all ids in every block once (50000 tokens 24 us with 8 columns;
+// with a second reading in place of the lists 37).  Zeroing in the sums' launch, in many small blocks, runs while the
+// others wait for their rows (a launch of its own before it held the next kernel back: +115 us).
+//
 // Rows are taken in units of G = 8, 4, 2 or 1 elements, as width and addresses are aligned; neighbouring threads hold
 // neighbouring units.
 #include <algorithm>

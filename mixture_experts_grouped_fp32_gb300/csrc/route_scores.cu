@@ -13,14 +13,19 @@
 //
 // The choice is that of the definition in 64 bits, whatever 32 bits make of it: without bias and groups the logits
 // themselves are compared; else c is computed in fp32, and where two neighbours of the order are closer than the
-// errors of their fp32 values (one row in a thousand of 256 experts), the token is done again in fp64.  So the choice
+// errors of their fp32 values (at most one row in a thousand of 256 experts), the token is done again in fp64.  So the choice
 // does not depend on how a compiler rounds an exp.  Equal c: the lower expert.
 //
 // LANES threads to a token (8 for up to 64 experts, else 32), each with up to EPL neighbouring experts of one group, so
 // that lower lanes hold lower experts and a tie goes to the lowest lane.  A lane sorts its experts once, as integers
 // with the order of c; a slot then costs one maximum over the lanes' first ones (one instruction for a warp), and the
 // lane that held it reads its next one.  Which expert a slot's integer belongs to is looked up for all slots at once.
-// Bound by instructions, not by the T E logits that are read.
+// Bound by instructions, not by the T E logits that are read: 780 of a warp for a token of 256 experts in 8 groups
+// (sigmoid, bias; 16384 tokens 17.9 us, 72 % of the issue slots while it runs, and the last contested token's fp64
+// behind the others), 10.3 us without groups and bias, 7.2 us for 64 experts (sigmoid, bias).
+//
+// The gradient takes eight or sixteen threads to a token where the experts are fours: fewer steps of a reduction, wide
+// loads (16001 x 160 softmax with all scores' gradient 6.2 us; with a warp to a token and one expert at a time 11.8).
 #include <algorithm>
 #include <climits>
 #include <cmath>

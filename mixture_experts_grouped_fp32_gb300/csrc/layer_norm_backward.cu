@@ -12,7 +12,7 @@
 // What bounds it: memory, with about 300 instructions to a warp's two eights close behind.  In a graph, with dh:
 // 8192 x 4096 bf16 57 us (86 % of the copy rate), 2932 x 8192 44 us (80 %).  Rows of odd widths pay for the masks and
 // the single values at both ends: 16000 x 2891 105 us (65 %).  In a cluster each row waits for the others' sums:
-// 1422 x 16384 65 us (53 %).
+// 1422 x 16384 58 us (59 %).
 #include "layer_norm.cuh"
 
 namespace moe {
@@ -255,7 +255,16 @@ Shape backward_shape(int T, int d) {
     // rows at a time win where a block has few of them (160 x 3261 8.2 us, not 9.3) and for narrow rows (1000 x 1024 7.7
     // us, not 10.3).
     s.vpt = eights > most || (eights > most / 2 && T >= 8 * kSms) ? 2 : 1;
-    while (s.blocks < kMostBlocks && s.blocks * most * s.vpt < eights) s.blocks *= 2;
+    auto blocks_of = [&](int threads) {
+        int b = 1;
+        while (b < kMostBlocks && b * threads * s.vpt < eights) b *= 2;
+        return b;
+    };
+    // Clusters of twice the blocks of half the threads, two blocks to an SM, where these are mostly filled: one row's
+    // exchange runs while the other's threads work (4000 x 12288 139 -> 131 us, x 16384 164 -> 145; 1422 x 9739, whose
+    // threads would be 60 % filled, 57 -> 63).
+    const int half = blocks_of(most / 2);
+    s.blocks = half > 2 && 4 * eights >= 3 * half * (most / 2) * s.vpt ? half : blocks_of(most);
     s.threads = ((eights + s.blocks * s.vpt - 1) / (s.blocks * s.vpt) + 31) / 32 * 32;
     s.groups = 1;
     int per_sm = std::min(32, most / s.threads);
@@ -263,6 +272,7 @@ Shape backward_shape(int T, int d) {
         s.groups = std::max(1, std::min({per_sm, s.threads == 32 ? 16 : 8, (T - 1) / kSms + 1}));
         per_sm = std::max(1, most / (s.threads * s.groups));
     }
+    if (s.blocks > 1) per_sm = std::min(per_sm, 2);
     s.clusters = clusters_for((T - 1) / s.groups + 1, per_sm, s.blocks);
     if (s.groups > 1 && d % 8) s.clusters = (s.clusters + 7) / 8 * 8;
     return s;

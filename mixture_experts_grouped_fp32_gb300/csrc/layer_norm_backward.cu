@@ -299,7 +299,7 @@ cudaError_t launch_layer_norm_backward(const LayerNormArgs& g, cudaStream_t s) {
     const bool sums = g.dweight || g.dbias;
     if (sums) a.partial = g.partial;
     a.vec = aligned({g.x, g.dn, g.dy, g.dx, g.dh});
-    const bool edge = g.d % 8 != 0 || !a.vec || !aligned({g.weight});
+    const bool edge = g.d % 8 != 0 || !a.vec || !aligned({g.weight}, 31);
     const Shape f = backward_shape(g.T, g.d);
     using B = __nv_bfloat16;
     const cudaError_t e = g.x_fp32 ? (edge ? backward_as<float, true>(a, f, s) : backward_as<float, false>(a, f, s))

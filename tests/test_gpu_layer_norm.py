@@ -184,6 +184,19 @@ def test_same_result_on_every_run_and_in_graphs(moe):
     assert all(torch.equal(a, b) for a, b in zip(first, kept)) and not torch.equal(kept[0], moe.layer_norm(x, w, w, h=h, p=0.2, seed=5, offset=2)[0])
 
 
+def test_weights_off_the_widest_loads(moe):
+    g = torch.Generator("cuda").manual_seed(14)
+    flat, x = randn(g, 4 * 4200, scale=0.2, mean=1), randn(g, 40, 4096, dtype=BF16)
+    dn = randn(g, 40, 4096, dtype=BF16)
+    for off in (1, 2, 4, 12):
+        w, b = flat[off:off + 4096], flat[8400 + off:8400 + off + 4096]
+        _, n, stats = moe.layer_norm(x, w, b)
+        check_norm(x, w, b, n, stats)
+        got = moe.layer_norm_backward(x, stats, dn, None, w)["x"]
+        dx, size = backward(x, stats, dn, None, w)[:2]
+        assert (got.to(D) - dx).abs().le(2.0 ** -8 * dx.abs() + 2.0 ** -17 * size).all()
+
+
 def test_unaligned_tensors_in_place_and_no_rows(moe):
     g = torch.Generator("cuda").manual_seed(4)
     flat = randn(g, 1 + 6 * 48, dtype=BF16)

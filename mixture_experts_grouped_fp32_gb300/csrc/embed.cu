@@ -367,7 +367,8 @@ struct SumArgs {
     bool add;
 };
 
-template <typename X, typename O, int G>
+// AHEAD: the lines of what is added to are fetched ahead.
+template <typename X, typename O, int G, bool AHEAD>
 __global__ void __launch_bounds__(kThreads)
 embed_sum_kernel(const X* __restrict__ dy, SumArgs a, Workspace ws, O* __restrict__ out) {
     __shared__ int32_t s_id[32 * (2 * kMostPiece + 1)], s_order[32 * 2 * kMostPiece];
@@ -462,6 +463,12 @@ embed_sum_kernel(const X* __restrict__ dy, SumArgs a, Workspace ws, O* __restric
 #pragma unroll
         for (int u = 0; u < kAhead; ++u)  // (behind the end the last row again)
             fetch<G>(r[u], dy + static_cast<size_t>(order[min(i0 + u, end - 1)]) * d + c.at, c);
+        // What is added to on its way into the L2 (a lane for 128 bytes).
+        if (AHEAD && x % (32 / G) == 0)
+            for (int i = i0; i < min(i0 + kAhead, end); ++i)
+                if (i + 1 == end || id[i + 1] != id[i])
+                    for (int j = 0; j < c.count; ++j)
+                        asm volatile("prefetch.global.L2 [%0];" ::"l"(out + static_cast<size_t>(id[i]) * d + c.at + j * c.step));
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
             const int i = i0 + u;
@@ -597,9 +604,16 @@ cudaError_t sum_as(const EmbedArgs& a, const Workspace& ws, cudaStream_t s) {
     g.sum_blocks = ((g.pieces - 1) / ty + 1) * g.chunks;
     g.scale = a.scale;
     g.add = a.accumulate;
+    // An addition in the L2 waits for its line.  Fetched ahead where the rows are more than the 129 MB L2 holds: 16384
+    // tokens of 128256 x 4096 140 -> 126 us; where they may be in it the requests cost (12001 of 50001 x 1028 24 -> 27 us).
+    const bool ahead = a.accumulate && 4ll * std::min(a.T, a.V) * a.d > (129ll << 20);
     const long long words = (static_cast<long long>(a.V) * a.d * static_cast<long long>(sizeof(O)) + 15) / 16;
     const long long zero_blocks = a.accumulate ? 0 : (words - 1) / (kZeroWords * tx * ty) + 1;
-    cudaError_t e = launch_k(kPdlTrain, embed_sum_kernel<X, O, G>, dim3(static_cast<unsigned>(g.sum_blocks + zero_blocks)), dim3(tx, ty), 0, s,
+    auto kernel = embed_sum_kernel<X, O, G, false>;
+    if constexpr (sizeof(O) == 4) {
+        if (ahead) kernel = embed_sum_kernel<X, O, G, true>;
+    }
+    cudaError_t e = launch_k(kPdlTrain, kernel, dim3(static_cast<unsigned>(g.sum_blocks + zero_blocks)), dim3(tx, ty), 0, s,
                              static_cast<const X*>(a.rows), g, ws, static_cast<O*>(a.out));
     if (e != cudaSuccess || g.pieces == 1) return e;
     return launch_k(kPdlTrain, embed_join_kernel<O, G>, dim3((g.pieces - 1) / kWindow + 1, (d8 + 31) / 32), dim3(32, kShares), 0, s,
@@ -609,8 +623,11 @@ template <typename X, typename O>
 cudaError_t sum_xo(const EmbedArgs& a, const Workspace& ws, cudaStream_t s) {
     const cudaError_t e = a.ids64 ? sort<long long>(a, ws, s) : sort<int32_t>(a, ws, s);
     if (e != cudaSuccess) return e;
-    switch (unit_of(a.d, a.rows, sizeof(X), a.out, sizeof(O))) {
-        case 8: return sum_as<X, O, 8>(a, ws, s);
+    const int unit = unit_of(a.d, a.rows, sizeof(X), a.out, sizeof(O));
+    if constexpr (sizeof(X) == 2) {
+        if (unit == 8) return sum_as<X, O, 8>(a, ws, s);
+    }
+    switch (std::min(unit, 4)) {  // (fp32 rows: 15261 x 4864 65 us, 79 as eights)
         case 4: return sum_as<X, O, 4>(a, ws, s);
         case 2: return sum_as<X, O, 2>(a, ws, s);
         default: return sum_as<X, O, 1>(a, ws, s);

@@ -270,6 +270,35 @@ def test_more_than_a_warp_lists(moe):
             assert torch.equal(moe.embed_backward(i, dy, V, out=want.clone(), accumulate=True), 2 * want)
 
 
+@pytest.mark.parametrize("d", [2048, 2052, 2050, 2051])
+def test_additions_to_more_than_the_cache_holds(moe, d):
+    g = torch.Generator("cuda").manual_seed(d)
+    V, T = 20_000, 25_000
+    ids = torch.randint(0, V, (T,), generator=g, device="cuda")
+    ids[:3000] = 5
+    out = torch.randint(-4, 5, (V, d), generator=g, device="cuda").float()
+    for dt in (F32, BF16):
+        dy = torch.randint(-4, 5, (T, d), generator=g, device="cuda").to(dt)
+        want = out.clone().index_add_(0, ids, dy.float())
+        assert torch.equal(moe.embed_backward(ids, dy, V, out=out.clone(), accumulate=True), want)
+
+
+@pytest.mark.parametrize("off", [1, 2, 4, 8])
+def test_rows_off_the_widest_loads(moe, off):
+    """Tables, rows and gradients that begin at any multiple of their elements."""
+    g = torch.Generator("cuda").manual_seed(off)
+    ids = torch.randint(0, 30, (200,), generator=g, device="cuda")
+    for dt in (F32, BF16):
+        flat = torch.randint(-4, 5, (off + 200 * 64,), generator=g, device="cuda").to(dt)
+        dy, table = flat[off:].view(200, 64), flat[off:off + 30 * 64].view(30, 64)
+        assert torch.equal(moe.embed(ids, table), table[ids])
+        want = torch.zeros(30, 64, device="cuda").index_add_(0, ids, dy.float())
+        assert torch.equal(moe.embed_backward(ids, dy, 30), want)
+        out = torch.zeros(off + 30 * 64, device="cuda")[off:].view(30, 64)
+        assert torch.equal(moe.embed_backward(ids, dy, 30, out=out), want)
+        assert torch.equal(moe.embed_backward(ids, dy, 30, out=out, accumulate=True), 2 * want)
+
+
 def test_elements_beyond_32_bits(moe):
     n = 2 ** 32 + 43
     x = torch.ones(n, dtype=BF16, device="cuda")

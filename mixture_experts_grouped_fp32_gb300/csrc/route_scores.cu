@@ -27,6 +27,7 @@
 // The gradient takes eight or sixteen threads to a token where the experts are fours: fewer steps of a reduction, wide
 // loads (16001 x 160 softmax with all scores' gradient 6.2 us; with a warp to a token and one expert at a time 11.8).
 #include <algorithm>
+#include <cfloat>
 #include <climits>
 #include <cmath>
 
@@ -583,41 +584,44 @@ __global__ void __launch_bounds__(kWarps * 32) route_scores_kernel(const L* __re
     if (a.G > 1 && a.kept < a.G) {
         // A group's score: its q largest, all groups at once.
         const int q = a.q;
-        float sum, bulk;  // bulk: sum of sizes
+        float sum = 0.0f, bulk = 0.0f;  // bulk: sum of sizes
+        auto add = [&](float v) {  // a mask of the lowest float counts as -1e30 (the sum is a number), one of -inf is exact
+            const float low = fmaxf(v, -1e30f);
+            sum += v == -INFINITY ? v : low;
+            bulk += v == -INFINITY ? 0.0f : fabsf(low);
+        };
         if (q <= 2) {
             for (int o = p.per_group / 2; o > 0; o >>= 1) {
                 const float o1 = __shfl_xor_sync(kAll, t1, o), o2 = __shfl_xor_sync(kAll, t2, o);
                 t2 = fmaxf(fminf(t1, o1), fmaxf(t2, o2));
                 t1 = fmaxf(t1, o1);
             }
-            sum = q == 2 ? t1 + t2 : t1;
-            bulk = fabsf(t1) + (q == 2 ? fabsf(t2) : 0.0f);
+            add(t1);
+            if (q == 2) add(t2);
         } else {
             uint32_t rest = head;
             int pos = 0;
-            sum = bulk = 0.0f;
             for (int r = 0; r < q; ++r) {
                 uint32_t all = rest;
                 for (int o = p.per_group / 2; o > 0; o >>= 1) all = max(all, __shfl_xor_sync(kAll, all, o));
                 const unsigned has = __ballot_sync(kAll, rest == all) >> (lane & ~(p.per_group - 1));
                 if ((lane & (p.per_group - 1)) == __ffs(has) - 1) rest = next_of(pos);
-                sum += key_value(all);
-                bulk += fabsf(key_value(all));
+                add(key_value(all));
             }
         }
         // The error of a sum: its scores' and its additions'.
         const bool real = p.group < a.G;
-        bulk = __uint_as_float(lanes_max<LANES>(real ? __float_as_uint(bulk) : 0u));  // (positive: integers have their order)
         const float inv = 1.0f / total;  // (no score is above it)
-        const float off = (a.sigmoid ? q * (kSigmoidRel + kSigmoidAbs) : fminf(1.0f, q * inv) * kSoftmaxRel + q * inv * 0.37f * kSoftmaxArg) + bulk * (q + 1) * 6e-8f;
+        const float off = (a.sigmoid ? q * (kSigmoidRel + kSigmoidAbs) : fminf(1.0f, q * inv) * kSoftmaxRel + q * inv * 0.37f * kSoftmaxArg) +
+                          bulk * (q + 2) * 6e-8f;
         const uint32_t g = real ? ordered(sum) : 0u;
         int rank = 0;  // groups with a larger sum
 #pragma unroll 4
         for (int o = 0; o < a.G; ++o) rank += __shfl_sync(kAll, g, o << a.layout.lanes_log2, LANES) > g;
         const bool kept = real && rank < a.kept;
         const int many = __popc(__ballot_sync(kAll, kept) >> base & own_lanes);  // more than asked for where sums are equal
-        const float least = key_value(~lanes_max<LANES>(kept ? ~g : 0u)), next = key_value(lanes_max<LANES>(kept ? 0u : g));
-        if (many != a.kept << a.layout.lanes_log2 || !(least - next > 2.0f * off)) sure = false;
+        const uint32_t least = ~lanes_max<LANES>(kept ? ~ordered(sum - off) : 0u), next = lanes_max<LANES>(real && !kept ? ordered(sum + off) : 0u);
+        if (many != a.kept << a.layout.lanes_log2 || least <= next || least <= 1u) sure = false;
         open = kept;
         head = kept ? head : 0u;
     }
@@ -662,11 +666,11 @@ __global__ void __launch_bounds__(kWarps * 32) route_scores_kernel(const L* __re
     float my_l = logit(row + my_e);
     if (!plain) {
         // Neighbours in the order have to be further apart than their errors; the last slot's is the best that is left.
-        const float inv = 1.0f / total, c = key_value(my_key), x = my_l - top;
+        const float inv = 1.0f / total, c = key_value(my_key), x = my_l - top, e = quick_exp(x);  // (e |x| is below 0.37)
         const uint32_t left = lanes_max<LANES>(head);
         const float off = fabsf(c) * 1.2e-7f + (a.sigmoid ? kSigmoidRel + kSigmoidAbs
-                                                         : quick_exp(x) * inv * (kSoftmaxRel + kSoftmaxArg * fabsf(x)) + 1e-30f);
-        const float left_off = fabsf(key_value(left)) * 1.2e-7f +
+                                                         : inv * (e * kSoftmaxRel + kSoftmaxArg * fminf(e * fabsf(x), 0.37f)) + 1e-30f);
+        const float left_off = fabsf(fmaxf(key_value(left), -FLT_MAX)) * 1.2e-7f +
                                (a.sigmoid ? kSigmoidRel + kSigmoidAbs : inv * (kSoftmaxRel + 0.37f * kSoftmaxArg));
         float next_c = __shfl_down_sync(kAll, c, 1, LANES), next_off = __shfl_down_sync(kAll, off, 1, LANES);
         if (p.sub == a.k - 1) {

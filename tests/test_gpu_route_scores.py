@@ -132,6 +132,25 @@ def test_masked_experts_and_empty_rows(moe):
                 assert d.isfinite().all() and d[1].eq(0).all()
 
 
+@pytest.mark.parametrize("low", [-INF, torch.finfo(F32).min, -1e9])
+def test_experts_masked_by_the_bias_or_the_logits(moe, low):
+    g = torch.Generator("cuda").manual_seed(6)
+    for E, groups, kept, k in ((256, 8, 4, 8), (64, 4, 2, 3), (160, 8, 8, 6), (32, 8, 2, 6)):
+        logits = torch.randn(300, E, generator=g, device="cuda")
+        bias = torch.randn(E, generator=g, device="cuda") * 0.1
+        for gone in (torch.arange(0, E, 3), torch.arange(0, E // groups), torch.arange(0, E - k), torch.arange(1, E)):
+            b, l = bias.clone(), logits.clone()
+            b[gone.cuda()] = low
+            l[:, gone.cuda()] = low
+            for scoring in ("softmax", "sigmoid"):
+                for x, y in ((logits, b), (l, bias), (l, None)):
+                    for n, m in ((1, 1), (groups, kept)):
+                        idx, w, _ = moe.route_scores(x, k, scoring, y, n, m)
+                        ridx, rw, _ = reference(x, k, scoring, y, n, m, True, 1.0)
+                        assert torch.equal(idx.cpu().long(), ridx)
+                        assert (w.cpu().to(D) - rw).abs().le(2.0 ** -18 * rw + 2.0 ** -126).all()
+
+
 def test_nan_ranks_last_and_reaches_its_weights(moe):
     l = torch.randn(3, 12, device="cuda")
     l[0, 2] = NAN

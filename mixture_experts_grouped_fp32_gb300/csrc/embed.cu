@@ -165,7 +165,7 @@ embed_kernel(const I* __restrict__ ids, const X* __restrict__ table, int T, int 
 constexpr int kMostPiece = 32;
 constexpr int kSortWarps = 32;
 constexpr int kMostSlice = 1600;   // ids of a slice, whose counts of 32 warps take 205 KB of shared memory
-constexpr int kSortSmem = 220 << 10;  // what is left of it: the warps' lists
+constexpr int kSortSmem = 220 << 10;  // of a block of the sort: the counts, then the warps' lists
 constexpr int kSms = 152;          // of a GB300
 constexpr int kThreads = 256;      // of a block of the sums, at the most
 constexpr int kZeroWords = 16;     // 16-byte words that a thread of the other blocks looks at

@@ -150,11 +150,6 @@ __device__ __forceinline__ Vec8 values(const Raw8<__nv_bfloat16>& r) { return un
 __device__ __forceinline__ Vec8 values(const Raw8<float>& r) {
     return Vec8{{r.a.x, r.a.y, r.a.z, r.a.w, r.b.x, r.b.y, r.b.z, r.b.w}};
 }
-__device__ __forceinline__ void set_values(Raw8<__nv_bfloat16>& r, const Vec8& v) { r.q = pack8(v); }
-__device__ __forceinline__ void set_values(Raw8<float>& r, const Vec8& v) {
-    r.a = make_float4(v.v[0], v.v[1], v.v[2], v.v[3]);
-    r.b = make_float4(v.v[4], v.v[5], v.v[6], v.v[7]);
-}
 __device__ __forceinline__ float to_float(__nv_bfloat16 v) { return __bfloat162float(v); }
 __device__ __forceinline__ float to_float(float v) { return v; }
 // The values as they read after a store.

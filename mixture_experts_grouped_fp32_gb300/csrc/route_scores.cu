@@ -523,44 +523,45 @@ __global__ void __launch_bounds__(kWarps * 32) route_scores_kernel(const L* __re
     };
     uint32_t key[EPL];
     bool nan = false;
-    if (plain && !exactly) {
+    if (exactly) {
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) c[i] = score(l[i]);
+        float* out = a.scores + t * a.E + p.first;
+        if (there) {
+            if (EPL % 4 == 0 && vec) {
+#pragma unroll
+                for (int i = 0; i + 3 < EPL; i += 4)
+                    if (i < p.count) *reinterpret_cast<float4*>(out + i) = make_float4(c[i], c[i + 1], c[i + 2], c[i + 3]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < EPL; ++i)
+                    if (i < p.count) out[i] = c[i];
+            }
+        }
+    }
+    if (plain) {
 #pragma unroll
         for (int i = 0; i < EPL; ++i) key[i] = i < p.count ? ordered(l[i]) : 0u;
     } else {
         float b[EPL];
-        if (exactly) {
-#pragma unroll
-            for (int i = 0; i < EPL; ++i) c[i] = score(l[i]);
-            float* out = a.scores + t * a.E + p.first;
-            if (there) {
-                if (EPL % 4 == 0 && vec) {
-#pragma unroll
-                    for (int i = 0; i + 3 < EPL; i += 4)
-                        if (i < p.count) *reinterpret_cast<float4*>(out + i) = make_float4(c[i], c[i + 1], c[i + 2], c[i + 3]);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < EPL; ++i)
-                        if (i < p.count) out[i] = c[i];
-                }
-            }
-        } else if (a.sigmoid) {
+        if (a.bias) read_row<EPL>(b, a.bias + p.first, p.count, vec, 0.0f);
+        if (!exactly && a.sigmoid) {
 #pragma unroll
             for (int i = 0; i < EPL; ++i) c[i] = quick_inverse(1.0f + quick_exp(-l[i]));
-        } else {
+        } else if (!exactly) {
             const float inv = total == 0.0f ? 0.0f : 1.0f / total;
 #pragma unroll
             for (int i = 0; i < EPL; ++i) c[i] *= inv;
         }
         if (a.bias) {
-            read_row<EPL>(b, a.bias + p.first, p.count, vec, 0.0f);
 #pragma unroll
             for (int i = 0; i < EPL; ++i) c[i] += b[i];
         }
-        float all = 0.0f;  // NaN where one of them is (or infinities of both signs are there)
+        float all = 0.0f;  // NaN where one of them is (or infinities of both signs are there); no expert's c is 0
 #pragma unroll
         for (int i = 0; i < EPL; ++i) {
-            all += i < p.count ? c[i] : 0.0f;
-            key[i] = i < p.count ? (plain ? ordered(l[i]) : ordered_score(c[i])) : 0u;
+            all += c[i];
+            key[i] = i < p.count ? ordered_score(c[i]) : 0u;
         }
         nan = all != all;
     }

@@ -305,3 +305,25 @@ def test_elements_beyond_32_bits(moe):
     assert moe.dropout(x, 0.5, 3, 4, out=x) is x
     for first, last in ((0, 64), (2 ** 31 - 32, 2 ** 31 + 32), (2 ** 32 - 32, n)):
         assert torch.equal(x[first:last].ne(0), stays(last, 0.5, 3, 4, first)), first
+
+
+def test_two_streams_at_once(moe):
+    g = torch.Generator("cuda").manual_seed(15)
+    sets = [(torch.randint(0, 3000, (5000,), generator=g, device="cuda") // (i + 1), torch.randn(5000, 264 + i, generator=g, device="cuda"))
+            for i in range(2)]
+
+    def both(ids, dy):
+        d = moe.embed_backward(ids, dy, 3000)
+        return [d, moe.embed(ids, d), moe.dropout(dy, 0.3, 9, residual=dy)]
+    want = [both(*s) for s in sets]
+    streams = [torch.cuda.Stream() for _ in sets]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    got = [[], []]
+    for _ in range(3):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(both(*sets[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(a, b) for r in got[i] for a, b in zip(r, want[i]))

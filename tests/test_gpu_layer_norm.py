@@ -234,3 +234,34 @@ def test_elements_beyond_32_bits(moe, T, d):
     assert (got["x"][ends].to(D) - dx).abs().le(2.0 ** -8 * dx.abs() + 2.0 ** -17 * size).all()
     assert got["x"][9:T - 9].count_nonzero() == 0
     assert (got["weight"].to(D) - dw).abs().le(2.0 ** -17 * dw_size).all()
+
+
+@pytest.mark.parametrize("T,d", [(50, 256), (1300, 2891), (40, 8200), (90, 12288), (30, 16384), (3, 65536)])
+def test_two_streams_at_once_and_a_replayed_graph(moe, T, d):
+    g = torch.Generator("cuda").manual_seed(d)
+    sets = [(randn(g, T, d, dtype=BF16), randn(g, T, d, dtype=BF16), randn(g, d)) for _ in range(2)]
+
+    def both(x, h, w, stream=None):
+        y, n, stats = moe.layer_norm(x, w, w, h=h, p=0.25, seed=3, stream=stream)
+        return [y, n, stats, *moe.layer_norm_backward(y, stats, h, x, w, w, True, 0.25, 3, stream=stream).values()]
+    want = [both(*s) for s in sets]
+    streams = [torch.cuda.Stream() for _ in sets]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    got = [[], []]
+    for _ in range(3):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(both(*sets[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(a, b) for r in got[i] for a, b in zip(r, want[i]))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        kept = [both(*s) for s in sets]
+    for r in kept:
+        for t in r:
+            t.zero_()
+    for _ in range(2):
+        graph.replay()
+    assert all(torch.equal(a, b) for r, v in zip(kept, want) for a, b in zip(r, v))

@@ -289,3 +289,33 @@ def test_logits_beyond_32_bits(moe):
     got = moe.route_scores_backward(l, idx, dw, scoring="sigmoid")
     assert torch.equal(got[ends], moe.route_scores_backward(l[ends], idx[ends], dw[ends], scoring="sigmoid"))
     assert got[20:T - 50].count_nonzero() == 0
+
+
+@pytest.mark.parametrize("E,k,groups,kept", [(64, 6, 1, 1), (256, 8, 8, 4), (100, 3, 1, 1)])
+def test_two_streams_at_once_and_a_replayed_graph(moe, E, k, groups, kept):
+    g = torch.Generator("cuda").manual_seed(E)
+    sets = [torch.randn(2000, E, generator=g, device="cuda") for _ in range(2)]
+    sets[1][:, 1] = sets[1][:, 0]  # (contested rows)
+    bias, dw = torch.randn(E, generator=g, device="cuda") * 0.1, torch.randn(2000, k, generator=g, device="cuda")
+
+    def both(l):
+        idx, w, s = moe.route_scores(l, k, "softmax", bias, groups, kept, want_scores=True)
+        return [idx, w, s, moe.route_scores_backward(l, idx, dw, bias, "softmax")]
+    want = [both(l) for l in sets]
+    streams = [torch.cuda.Stream() for _ in sets]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    got = [[], []]
+    for _ in range(3):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(both(sets[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(a, b) for r in got[i] for a, b in zip(r, want[i]))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        kept_outputs = both(sets[0])
+    sets[0].copy_(sets[1])
+    graph.replay()
+    assert all(torch.equal(a, b) for a, b in zip(kept_outputs, want[1]))

@@ -247,18 +247,19 @@ __device__ __noinline__ int choose64(const L* row, const float* bias, int size, 
     const Place p(LANES, layout);
     const int lane = threadIdx.x & 31;
     float top = -INFINITY;
-    bool nan = false;
+    bool bad = false, nan = false;  // a logit is NaN (or +inf: a softmax over it is NaN throughout); one of c is
     double total = 1.0;
 #pragma unroll 1
     for (int i = 0; i < p.count; ++i) {
         const float l = logit(row + p.first + i);
-        nan |= l != l || (bias && bias[p.first + i] != bias[p.first + i]);
+        bad |= l != l;
+        nan |= bias && bias[p.first + i] != bias[p.first + i];  // (of that expert alone)
         top = fmaxf(top, l);
     }
     if (!a.sigmoid) {
         top = lanes_max<LANES>(top);
-        nan |= top == INFINITY;
-        total = nan ? static_cast<double>(NAN) : 0.0;
+        bad |= top == INFINITY;
+        total = bad ? static_cast<double>(NAN) : 0.0;
 #pragma unroll 2
         for (int i = 0; i < p.count; ++i) {
             const float l = logit(row + p.first + i);
@@ -288,7 +289,7 @@ __device__ __noinline__ int choose64(const L* row, const float* bias, int size, 
     }
     const float off = a.sigmoid ? kSigmoidRel + kSigmoidAbs : kSoftmaxRel * lanes_max<LANES>(score) + 0.37f * kSoftmaxArg;
     const float margin = 2.0f * (off + 1.2e-7f * lanes_max<LANES>(bulk));
-    nan = __any_sync(kAll, nan);  // then every expert of the warp's tokens is in question
+    nan = __any_sync(kAll, nan || bad);  // then every expert of the warp's tokens is in question
     Key key[EPL];
 #pragma unroll
     for (int i = 0; i < EPL; ++i) key[i] = 0ull;

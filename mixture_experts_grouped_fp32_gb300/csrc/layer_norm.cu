@@ -9,9 +9,11 @@
 // One pass over memory; bound by it.  A thread holds its values of a row in registers, with those of its next row on
 // their way into shared memory (cp.async: a thread copies just the words that it will use, so no barrier is needed for
 // them).  The variance is the sum of squared distances from the mean (no difference of large sums): two reductions,
-// one after the other, which other blocks of the SM fill.  Rows of up to 256 values are eight lanes' each, rows of up
-// to 1024 eights a block's; wider ones lie in the blocks of a cluster, which exchange their warps' sums through each
-// other's shared memory.
+// one after the other, which other blocks of the SM fill.  The second one also sums the distances themselves, which is
+// what the first was off by: the mean is then right to its own rounding, and a constant row's distances are 0 (without
+// that 1000.1 gave n = 0.02 for some widths; it costs 0 to 4 %, 8192 x 4096 bf16 26.9 -> 27.7 us, and 0.1 us of a token).
+// Rows of up to 256 values are eight lanes' each, rows of up to 1024 eights a block's; wider ones lie in the blocks of a
+// cluster, which exchange their warps' sums through each other's shared memory.
 #include "layer_norm.cuh"
 
 namespace moe {
@@ -35,15 +37,14 @@ struct Forward {
 template <typename X, bool H, bool EDGE, int VPT, int LANES, bool CLUSTER>
 __global__ void __launch_bounds__(LANES == 32 ? 1024 / VPT : 256, LANES == 32 ? VPT : 3)
 layer_norm_kernel(const __grid_constant__ Forward a) {
-    __shared__ float red[2 * (CLUSTER ? kMostBlocks * 32 / VPT : 32 / VPT)];
+    __shared__ float red[2 * 2 * (CLUSTER ? kMostBlocks * 32 / VPT : 32 / VPT)];
     constexpr bool SIDE = LANES < 32;
     extern __shared__ uint4 next_row[];
     constexpr int W = words<X>() + (H ? 1 : 0);
     // An fp32 stream with h is at the memory's rate, which falls when the weights come faster (8192 x 7168 106 -> 120 us).
     constexpr bool WIDE = W < 3;
     const int tid = threadIdx.x, nt = blockDim.x, d = a.d;  // (of a row)
-    // The mean is divided for, so that a constant row has deviations of 0.
-    const float fd = static_cast<float>(d), inv_d = 1.0f / fd;
+    const float inv_d = 1.0f / static_cast<float>(d);
     const X* x = static_cast<const X*>(a.x);
     X* y = static_cast<X*>(a.y);
     const long long T = a.T, total = T * d, side = SIDE ? blockDim.y : 1, step = gridDim.x / a.blocks * side;
@@ -55,12 +56,13 @@ layer_norm_kernel(const __grid_constant__ Forward a) {
     pdl_wait();
     pdl_trigger();
     if (CLUSTER) ptx::cluster_wait();
-    RowSums<CLUSTER, 1> row_sums(red, nt >> 5, 0, a.blocks);
-    auto row_sum = [&](float v) {
-        if (SIDE) return lanes_sum<LANES>(v);
-        float s[1] = {v};
-        row_sums(s);
-        return s[0];
+    RowSums<CLUSTER, 2> row_sums(red, nt >> 5, 0, a.blocks);
+    auto sum_row = [&](auto& s) {
+        if constexpr (SIDE) {
+            for (float& v : s) v = lanes_sum<LANES>(v);
+        } else {
+            row_sums(s);
+        }
     };
     const int shift = EDGE ? static_cast<int>(row0 * d & 7) : 0, q0 = (CLUSTER ? row_sums.rank * nt * VPT : 0) + tid;
     auto eight = [&](int v) { return Eight<EDGE>(q0 + v * nt, shift, d, a.vec != 0); };
@@ -123,9 +125,11 @@ layer_norm_kernel(const __grid_constant__ Forward a) {
             }
         }
         if (k + 1 < own) fetch(at + row);
-        const float mean = row_sum(sum.x + sum.y) / fd;
-        const float2 back = make_float2(-mean, -mean);
-        sum = make_float2(0.0f, 0.0f);
+        float about[1] = {sum.x + sum.y};  // the mean, but for the errors of its sum
+        sum_row(about);
+        about[0] *= inv_d;
+        float2 back = make_float2(-about[0], -about[0]), square = make_float2(0.0f, 0.0f);
+        sum = square;
 #pragma unroll
         for (int v = 0; v < VPT; ++v) {
             const Eight<EDGE> e = eight(v);
@@ -134,10 +138,21 @@ layer_norm_kernel(const __grid_constant__ Forward a) {
                 for (int j = 0; j < 4; ++j) val[v].set(j, add2(val[v].pair(j), back));
                 e.mask(val[v]);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) sum = fma2(val[v].pair(j), val[v].pair(j), sum);
+                for (int j = 0; j < 4; ++j) {
+                    sum = add2(sum, val[v].pair(j));
+                    square = fma2(val[v].pair(j), val[v].pair(j), square);
+                }
             }
         }
-        const float r = rsqrtf(row_sum(sum.x + sum.y) * inv_d + a.eps);
+        // The mean with the mean of what it leaves, and the variance about that.  `shift_by` is what the distances change by,
+        // exactly where the mean is not near 0 (a difference of close floats): those of a constant row become 0, and its
+        // mean the constant.
+        float second[2] = {sum.x + sum.y, square.x + square.y};
+        sum_row(second);
+        const float left = second[0] * inv_d, mean = about[0] + left, shift_by = mean - about[0];
+        const float var = second[1] * inv_d - shift_by * (2.0f * left - shift_by);
+        const float r = rsqrtf((var < 0.0f ? 0.0f : var) + a.eps);  // (NaN stays)
+        back = make_float2(-shift_by, -shift_by);
         if (here && tid == 0 && row_sums.rank == 0) *stats = make_float2(mean, r);
         stats += step;
 #pragma unroll
@@ -156,7 +171,7 @@ layer_norm_kernel(const __grid_constant__ Forward a) {
                 }
                 Vec8 o;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) o.set(j, fma2(mul2(val[v].pair(j), r), w.pair(j), b.pair(j)));
+                for (int j = 0; j < 4; ++j) o.set(j, fma2(mul2(add2(val[v].pair(j), back), r), w.pair(j), b.pair(j)));
                 e.store(a.n, at, o);
             }
         }

@@ -44,22 +44,24 @@ __device__ __forceinline__ float lanes_sum(float v) {
     return v;
 }
 
-// N = 1, 2 or 4 sums over the threads that hold a row.  One barrier each; the buffers alternate, so that none is needed
-// behind it.
-template <bool CLUSTER, int N>
+// N = 1, 2 or 4 sums (MOST at the most) over the threads that hold a row.  One barrier each; the buffers alternate, so
+// that none is needed behind it.
+template <bool CLUSTER, int MOST>
 struct RowSums {
-    float* red;  // [2][blocks of the cluster x warps][N]
+    float* red;  // [2][blocks of the cluster x warps][MOST]
     int warps, barrier, blocks, rank, parity = 0;
     __device__ __forceinline__ RowSums(float* red_, int warps_, int barrier_, int blocks_)
         : red(red_), warps(warps_), barrier(barrier_), blocks(blocks_), rank(CLUSTER ? ptx::cluster_ctarank() : 0) {}
+    template <int N>
     __device__ __forceinline__ void operator()(float (&s)[N]) {
+        static_assert(N <= MOST);
         const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, all = (CLUSTER ? blocks : 1) * warps;
         float mine;  // this lane's part of sum lane / (32 / N)
         if constexpr (N == 4) mine = warp_sum4(s);
         else if constexpr (N == 2) mine = warp_sum2(s);
         else mine = warp_sum(s[0]);
         if (CLUSTER || warps > 1) {
-            float* buf = red + parity * all * N;
+            float* buf = red + parity * all * MOST;
             parity ^= 1;
             if (CLUSTER) {
                 // Lane l sends sum l mod N to block l / N, and to those 32 / N further on.

@@ -178,7 +178,9 @@ class MoEStack:
 
     def _backward_layer(self, dx, saved, grads):
         number = saved[0][4]
-        dc = moe.dropout(dx.bfloat16(), **self._masks(self.layers - 1, number))
+        # (dropped in the stream's type: rounded to bf16 once)
+        dc = dx if number is None else moe.dropout(dx, **self._masks(self.layers - 1, number))
+        dc = dc.bfloat16()
         for l in reversed(range(self.layers)):
             p, w = self.params[l], self.weights[l]
             x, stats, kept = saved[l][:3]

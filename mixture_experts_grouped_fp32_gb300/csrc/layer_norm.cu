@@ -33,16 +33,14 @@ struct Forward {
 };
 
 // VPT eights to a thread, blockDim.x apart.  LANES: 32 and a block's threads for a row (or those of a cluster), or as many
-// lanes of a warp, blockDim.y rows side by side.
-template <typename X, bool H, bool EDGE, int VPT, int LANES, bool CLUSTER>
+// lanes of a warp, blockDim.y rows side by side.  WIDE: eight weights as one word.
+template <typename X, bool H, bool EDGE, int VPT, int LANES, bool CLUSTER, bool WIDE>
 __global__ void __launch_bounds__(LANES == 32 ? 1024 / VPT : 256, LANES == 32 ? VPT : 3)
 layer_norm_kernel(const __grid_constant__ Forward a) {
     __shared__ float red[2 * 2 * (CLUSTER ? kMostBlocks * 32 / VPT : 32 / VPT)];
     constexpr bool SIDE = LANES < 32;
     extern __shared__ uint4 next_row[];
     constexpr int W = words<X>() + (H ? 1 : 0);
-    // An fp32 stream with h is at the memory's rate, which falls when the weights come faster (8192 x 7168 106 -> 120 us).
-    constexpr bool WIDE = W < 3;
     const int tid = threadIdx.x, nt = blockDim.x, d = a.d;  // (of a row)
     const float inv_d = 1.0f / static_cast<float>(d);
     const X* x = static_cast<const X*>(a.x);
@@ -207,10 +205,10 @@ Shape forward_shape(int T, int d, int word_bytes, bool keep) {
     }
 }
 
-template <typename X, bool H, bool EDGE, int VPT, int LANES, bool CLUSTER>
+template <typename X, bool H, bool EDGE, int VPT, int LANES, bool CLUSTER, bool WIDE = true>
 cudaError_t forward_with(const Forward& a, const Shape& f, int word_bytes, cudaStream_t s) {
     const size_t smem = static_cast<size_t>(f.threads) * f.groups * VPT * (word_bytes + (a.keep ? 64 : 0));
-    return launch_rows(layer_norm_kernel<X, H, EDGE, VPT, LANES, CLUSTER>, f, smem, s, a);
+    return launch_rows(layer_norm_kernel<X, H, EDGE, VPT, LANES, CLUSTER, WIDE>, f, smem, s, a);
 }
 template <typename X, bool H, bool EDGE>
 cudaError_t forward_as(Forward a, cudaStream_t s) {
@@ -219,6 +217,14 @@ cudaError_t forward_as(Forward a, cudaStream_t s) {
     // Weights whose loads would be one by one are read once, where a block has more than one row after another.
     a.keep = EDGE && f.groups == 1 && a.T > f.clusters;
     a.blocks = f.blocks;
+    // Weights as two words of four: for an fp32 stream with h whose rows fill a block each, many to a block.  These streams
+    // are at the memory's rate, and slower where the weights come faster (us, as two words / as one, with dropout; the
+    // cause is not known):
+    //   8192 rows of   4096 70/73, 4608 84/82, 5120 81/88, 6144 125/113, 6656 100/108, 7168 105/119, 7680 114/128, 8192 127/139
+    //   2000 rows of   4096 17.8/16.6, 5120 23.0/22.6, 6656 28.4/27.3, 7168 30.2/29.7, 8192 33.5/34.8
+    // and rows in less than a block or in a cluster: 8192 x 512 11.7/11.1, x 10240 202/194, x 16384 314/305.
+    if constexpr (sizeof(X) == 4 && H && !EDGE)
+        if (f.blocks == 1 && f.vpt == 2 && a.d >= 5120 && a.T >= 8 * f.clusters) return forward_with<X, H, EDGE, 2, 32, false, false>(a, f, word_bytes, s);
     if (f.threads < 32) return forward_with<X, H, EDGE, 4, 8, false>(a, f, word_bytes, s);
     if (f.blocks > 1)
         return f.vpt == 2 ? forward_with<X, H, EDGE, 2, 32, true>(a, f, word_bytes, s) : forward_with<X, H, EDGE, 1, 32, true>(a, f, word_bytes, s);

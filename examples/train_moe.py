@@ -23,6 +23,8 @@ from mixture_experts_grouped_fp32_gb300.train import MoEStack  # noqa: E402
 def train(steps=50, tokens=512, layers=2, d=256, f=512, experts=8, top_k=2, state_bits=32, graph=False, lr=3e-3,
           norm="rms", dropout=0.0, scoring=None, groups=1, kept=1, bias_rate=0.0, balance=0.0, vocab=None, report=print):
     """Returns the losses of all steps (a device tensor is read once, at the end)."""
+    if scoring is None and (groups, kept, bias_rate, balance) != (1, 1, 0.0, 0.0):
+        raise ValueError("groups, kept, bias_rate and balance are options of a router by scores: give scoring")
     router = None if scoring is None else dict(scoring=scoring, n_group=groups, topk_group=kept, bias_rate=bias_rate,
                                                balance=balance)
     teacher = MoEStack(layers, d, f, experts, top_k, seed=1, norm=norm, vocab=vocab)

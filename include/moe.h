@@ -596,12 +596,15 @@ MOE_API int moe_adamw_step(const moe_adamw_tensor* tensors, int count, int param
  *   idx[t,.] = the top_k largest c among the kept groups' experts, falling (equal: lower id first)
  *   w[t,j]   = scale * s[idx[t,j]] / (renormalize ? sum_j' s[idx[t,j']] : 1)
  * The choice is the one of these formulas in 64-bit arithmetic: scores that fp32 cannot tell apart are computed
- * again in fp64.  Without bias and groups the logits themselves are compared (the same order).
+ * again in fp64, and so are equal ones (rows of equal logits take several times as long).  Without bias and groups the
+ * logits themselves are compared (the same order; NaN logits last).  moe_route_grouped and the forward calls that route by
+ * it choose by fp32 scores: where two scores are closer than fp32 rounding they may choose another expert.
  *   logits [T,E] fp32 or bf16;  bias [E] fp32 or NULL;  idx [T,top_k] int32 out;  w [T,top_k] fp32 out;
  *   scores [T,E] fp32 out (s; for a balancing loss), or NULL.
  * An expert with logit -inf has score 0; a token whose chosen scores are all 0 has weights 0 (that of a row of -inf
- * is such a token).  NaN: a c that is NaN ranks below every number, NaNs by ascending id; a softmax over a NaN or
- * over +inf is NaN throughout, and weights that it reaches are NaN.
+ * is such a token).  NaN: a c that is NaN ranks below every number, NaNs by ascending id, and a group whose sum is NaN
+ * below the others; a NaN in the bias is its own expert's alone; a softmax over a NaN or over +inf is NaN throughout,
+ * and weights that it reaches are NaN (renormalised ones are those of the chosen logits alone).
  * 1 <= E <= 256, 1 <= top_k <= 8, n_group in [1, 32] dividing E, 1 <= topk_group <= n_group, top_k <= topk_group *
  * E / n_group, scale finite. */
 MOE_API int moe_route_scores(const void* logits, int logits_bf16, const float* bias, int T, int E, int top_k,
@@ -643,7 +646,7 @@ MOE_API int moe_layer_norm(const void* x, int x_fp32, const void* h, const float
  * (moe_layer_norm's y, or its x without h) and its stats:
  *   dx [T,d] (the stream's type): the whole gradient of the stream before the addition, x's;
  *   dh [T,d] bf16, or NULL: dropout(dx), with the forward call's p, seed and offset;
- *   dweight, dbias [d] fp32, or NULL: sums over the rows in a fixed order, written, not added to.
+ *   dweight, dbias [d] fp32, or NULL: sums over the rows, in fp32 and in a fixed order, written, not added to.
  * dx may be dy.  workspace: 16-byte aligned, moe_layer_norm_backward_workspace_size(T, d) bytes. */
 MOE_API size_t moe_layer_norm_backward_workspace_size(int T, int d);
 MOE_API int moe_layer_norm_backward(const void* x, int x_fp32, const float* stats, const void* dn, const void* dy,

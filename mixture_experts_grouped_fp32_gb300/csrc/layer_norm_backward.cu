@@ -7,12 +7,14 @@
 // next eights on their way into shared memory (cp.async).  A row that is wider than a block's threads hold lies in the
 // blocks of a cluster, which exchange their warps' sums through each other's shared memory.  The column sums of a
 // block's rows are written once, and a second kernel adds the blocks in a fixed order: no atomics, the same result on
-// every run.
+// every run.  They are fp32 sums of a block's rows one after another: off by as many 2^-24 of the terms' sizes at the most
+// as a block has rows (8192 x 4096 27, 16384 x 65536 1024; by about the root of that in earnest), and by some 40 more for
+// the join.  A second sum for each column would cost the registers that hold two eights.
 //
 // What bounds it: memory, with about 300 instructions to a warp's two eights close behind.  In a graph, with dh:
-// 8192 x 4096 bf16 57 us (86 % of the copy rate), 2932 x 8192 44 us (80 %).  Rows of odd widths pay for the masks and
-// the single values at both ends: 16000 x 2891 105 us (65 %).  In a cluster each row waits for the others' sums:
-// 1422 x 16384 58 us (59 %).
+// 8192 x 4096 bf16 57 us (86 % of the copy rate), fp32 84 us (94 %), 2932 x 8192 bf16 44 us (80 %).  Rows of odd widths
+// pay for the masks and the single values at both ends: 16000 x 2891 105 us (65 %).  In a cluster each row waits for the
+// others' sums: 1422 x 16384 bf16 58 us (59 %), 4000 x 12288 fp32 160 us (73 %).
 #include "layer_norm.cuh"
 
 namespace moe {

@@ -13,15 +13,18 @@
 //
 // The choice is that of the definition in 64 bits, whatever 32 bits make of it: without bias and groups the logits
 // themselves are compared; else c is computed in fp32, and where two neighbours of the order are closer than the
-// errors of their fp32 values (at most one row in a thousand of 256 experts), the token is done again in fp64.  So the choice
-// does not depend on how a compiler rounds an exp.  Equal c: the lower expert.
+// errors of their fp32 values, the token is done again in fp64.  So the choice does not depend on how a compiler rounds an
+// exp.  Equal c: the lower expert.  Of random fp32 logits over 256 experts 0.03 to 0.15 % of the rows are done again.
+// Equal scores are too, though no precision tells them apart: of bf16 logits without a bias (in groups), or with a bias
+// of zeros, that is every third row (16384 x 256, sigmoid 30 us, softmax 76; of fp32 logits 19 and 23), and where half of
+// the rows are zeros, every one of those (150 and 220 us).  With a bias of unequal values they are no more than in fp32.
 //
 // LANES threads to a token (8 for up to 64 experts, else 32), each with up to EPL neighbouring experts of one group, so
 // that lower lanes hold lower experts and a tie goes to the lowest lane.  A lane sorts its experts once, as integers
 // with the order of c; a slot then costs one maximum over the lanes' first ones (one instruction for a warp), and the
 // lane that held it reads its next one.  Which expert a slot's integer belongs to is looked up for all slots at once.
 // Bound by instructions, not by the T E logits that are read: 780 of a warp for a token of 256 experts in 8 groups
-// (sigmoid, bias; 16384 tokens 17.9 us, 72 % of the issue slots while it runs, and the last contested token's fp64
+// (sigmoid, bias; 16384 tokens 16 to 19 us, 72 % of the issue slots while it runs, and the last contested token's fp64
 // behind the others), 10.3 us without groups and bias, 7.2 us for 64 experts (sigmoid, bias).
 //
 // The gradient takes eight or sixteen threads to a token where the experts are fours: fewer steps of a reduction, wide
@@ -145,7 +148,7 @@ struct Place {
 
 struct RouteArgs {
     const float* bias;
-    Layout layout;
+    Layout layout;  // set at the launch, by the lanes of a token
     int T, E, k, q, sigmoid, G, kept, renorm;  // q: experts whose c make a group's score
     float scale;
     int32_t* idx;
@@ -713,7 +716,6 @@ struct RouteGradArgs {
     float scale;
 };
 
-// Lane `sub` of a token has the experts sub, sub + LANES, ..: loads and stores of neighbouring lanes are neighbours.
 // Fours of a row.
 __device__ __forceinline__ void read4(float* v, const float* p) {
     const float4 f = __ldg(reinterpret_cast<const float4*>(p));
@@ -910,7 +912,7 @@ cudaError_t backward_as(const L* logits, const RouteGradArgs& a, L* dlogits, cud
 cudaError_t launch_route_scores(const void* logits, bool bf16, const float* bias, int T, int E, int k, bool sigmoid,
                                 int n_group, int topk_group, bool renorm, float scale, int32_t* idx, float* w,
                                 float* scores, cudaStream_t s) {
-    const RouteArgs a{bias, Layout(32, E, n_group), T, E, k, std::min(E / n_group, std::max(1, k / topk_group)), sigmoid, n_group,
+    const RouteArgs a{bias, Layout(), T, E, k, std::min(E / n_group, std::max(1, k / topk_group)), sigmoid, n_group,
                       topk_group, renorm, scale, idx, w, scores};
     return bf16 ? forward_as(static_cast<const __nv_bfloat16*>(logits), a, s)
                 : forward_as(static_cast<const float*>(logits), a, s);

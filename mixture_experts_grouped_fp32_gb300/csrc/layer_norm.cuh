@@ -177,7 +177,7 @@ struct Eight {
         }
     }
     // Of a vector over the columns (32-byte aligned unless EDGE), or `none` without it.  WIDE: as one word.  Two touch every
-    // sector twice, and the L1 bounds what reads little else (8192 x 4096 bf16 without h 39 us, not 27).
+    // sector twice, and the L1 bounds what reads little else (8192 x 4096 bf16 without h 34 us, not 28).
     template <bool WIDE = true>
     __device__ __forceinline__ Vec8 column(const float* p, float none) const {
         Vec8 v;

@@ -24,7 +24,7 @@
 // with the order of c; a slot then costs one maximum over the lanes' first ones (one instruction for a warp), and the
 // lane that held it reads its next one.  Which expert a slot's integer belongs to is looked up for all slots at once.
 // Bound by instructions, not by the T E logits that are read: 780 of a warp for a token of 256 experts in 8 groups
-// (sigmoid, bias; 16384 tokens 16 to 19 us, 72 % of the issue slots while it runs, and the last contested token's fp64
+// (sigmoid, bias; 16384 tokens 16 to 23 us by the inputs, 72 % of the issue slots while it runs, and the last contested token's fp64
 // behind the others), 10.3 us without groups and bias, 7.2 us for 64 experts (sigmoid, bias).
 //
 // The gradient takes eight or sixteen threads to a token where the experts are fours: fewer steps of a reduction, wide
@@ -587,13 +587,13 @@ __global__ void __launch_bounds__(kWarps * 32) route_scores_kernel(const L* __re
     }
     auto next_of = [&](int& pos) { return lists[threadIdx.x >> 5][min(pos++, EPL - 1)][lane]; };
     if (a.G > 1 && a.kept < a.G) {
-        // A group's score: its q largest, all groups at once.
+        // A group's score: its q largest, all groups at once.  In eighths, exact but below 2^-123: the sum of up to eight
+        // masks of the lowest float is a number, too.  A mask of -inf has no error.
         const int q = a.q;
         float sum = 0.0f, bulk = 0.0f;  // bulk: sum of sizes
-        auto add = [&](float v) {  // a mask of the lowest float counts as -1e30 (the sum is a number), one of -inf is exact
-            const float low = fmaxf(v, -1e30f);
-            sum += v == -INFINITY ? v : low;
-            bulk += v == -INFINITY ? 0.0f : fabsf(low);
+        auto add = [&](float v) {
+            sum = fmaf(v, 0.125f, sum);
+            bulk += v == -INFINITY ? 0.0f : fabsf(v) * 0.125f;
         };
         if (q <= 2) {
             for (int o = p.per_group / 2; o > 0; o >>= 1) {
@@ -617,8 +617,8 @@ __global__ void __launch_bounds__(kWarps * 32) route_scores_kernel(const L* __re
         // The error of a sum: its scores' and its additions'.
         const bool real = p.group < a.G;
         const float inv = 1.0f / total;  // (no score is above it)
-        const float off = (a.sigmoid ? q * (kSigmoidRel + kSigmoidAbs) : fminf(1.0f, q * inv) * kSoftmaxRel + q * inv * 0.37f * kSoftmaxArg) +
-                          bulk * (q + 2) * 6e-8f;
+        const float off = 0.125f * (a.sigmoid ? q * (kSigmoidRel + kSigmoidAbs) : fminf(1.0f, q * inv) * kSoftmaxRel + q * inv * 0.37f * kSoftmaxArg) +
+                          bulk * ((q + 2) * 6e-8f);
         const uint32_t g = real ? ordered(sum) : 0u;
         int rank = 0;  // groups with a larger sum
 #pragma unroll 4
